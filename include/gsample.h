@@ -262,6 +262,137 @@ gsample_status gsample_gumbel_argmax_host(const void* logits, gsample_dtype dtyp
                                           int64_t* out_idx, void* workspace,
                                           gsample_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Logit constraints: the steps between a model's logits and the draw that
+ * "Softmax-free GPU sampling" (Background) lists ahead of the sampler: token
+ * bias and repetition / frequency / presence penalties, and grammar masks.
+ *
+ * For element v of row b, with x = logits[b, v] in binary32, the state row r
+ * and the row's parameters, the constrained logit is
+ *
+ *   if x == -inf:               -inf (a token masked upstream stays masked)
+ *   otherwise                   x = x + bias[r, v]
+ *     if history[r, v] != 0:    x = x > 0 ? x / repetition : x * repetition
+ *     with c = history & 0x7fffffff, if c > 0:
+ *                               x = (x - frequency * c) - presence
+ *   if the mask bit of v is 0:  -inf, whatever x is (NaN and +inf included)
+ *
+ * each operation rounded once to binary32. A repetition that is not finite or
+ * not > 0 counts as 1, a NaN frequency or presence as 0.
+ * ------------------------------------------------------------------------- */
+
+/* What each request has seen and the biases it asked for, on the device: the
+ * caller owns the three arrays, zeroes them once, and passes this struct (host
+ * memory, read during the call). State rows are a server's request slots; a
+ * batch row picks its own through `slot`.
+ *   history  int32 [rows, ld]: bits 0..30 count the token's appearances in the
+ *            output so far; bit 31 is set when it is in the prompt. The
+ *            repetition penalty applies to both, frequency and presence to the
+ *            output alone.
+ *   bias     float [rows, ld], or NULL: no biases.
+ *   touched  uint32 [rows, ld / 32]: bit v & 31 of word v >> 5 is set where
+ *            history or bias may be nonzero. Entries without it are not read
+ *            and hold zeros. The calls below keep it so.
+ *   rows >= 1; vocab = V of the logits; ld a multiple of 32, >= vocab
+ *   (gsample_logit_state_ld). history and bias are 16-byte aligned, touched
+ *   4-byte aligned.
+ * The layout is public: rows may be copied (a forked request), saved and
+ * restored by plain copies of the three arrays. Calls that write a state must
+ * be ordered (by stream or event) with every call that uses it. */
+typedef struct {
+  int32_t* history;
+  float* bias;
+  uint32_t* touched;
+  int64_t rows;
+  int64_t vocab;
+  int64_t ld;
+} gsample_logit_state;
+
+/* The constraints of a batch (host memory, read during the call; the arrays
+ * are device memory). Any part may be absent (NULL).
+ *   state       penalties and biases; NULL: neither.
+ *   slot        int32[B]: the state row of each batch row; a value outside
+ *               [0, rows) means no state for that row. NULL: row b uses state
+ *               row b (rows >= B).
+ *   repetition, frequency, presence   float[B]; NULL: 1, 0, 0.
+ *   mask        packed masks [mask_rows, mask_ld] of 32-bit words, bit v & 31
+ *               of word v >> 5 set where token v is allowed; mask_ld words
+ *               (>= ceil(V / 32)) from row to row. Bits at and past V are
+ *               ignored. 4-byte aligned.
+ *   mask_row    int32[B]: the mask row of each batch row; a value outside
+ *               [0, mask_rows) means no mask. NULL: row b uses mask row b
+ *               (mask_rows >= B). */
+typedef struct {
+  const gsample_logit_state* state;
+  const int32_t* slot;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const uint32_t* mask;
+  int64_t mask_rows;
+  int64_t mask_ld;
+  const int32_t* mask_row;
+} gsample_constraints;
+
+/* Which part of the history gsample_history_append extends. */
+typedef enum {
+  GSAMPLE_HISTORY_PROMPT = 0, /* sets bit 31 */
+  GSAMPLE_HISTORY_OUTPUT = 1  /* adds one to the count */
+} gsample_history_kind;
+
+/* Smallest ld of a state for vocabulary V: V rounded up to a multiple of 32. */
+int64_t gsample_logit_state_ld(int64_t V);
+
+/* Clears n state rows (history, bias and touched bits): those in slot[0..n)
+ * (device int32, values outside [0, rows) ignored), or the first n when slot
+ * is NULL. Reads the touched bits and writes only what they mark. */
+gsample_status gsample_state_reset(const gsample_logit_state* state, const int32_t* slot,
+                                   int64_t n, gsample_stream_t stream);
+
+/* Appends tokens to the history of n requests. Request i owns
+ * tokens[offsets[i] .. offsets[i + 1]) (device int64, offsets[0..n] not
+ * decreasing; positions outside [0, total) and outside every request are
+ * ignored), or tokens[i] alone when offsets is NULL (total == n: the indices a
+ * sampler just drew, say). slot as in gsample_state_reset. Token ids outside
+ * [0, vocab) are ignored (a sampler's -1 too). A slot or a token may appear
+ * more than once: every appearance counts. */
+gsample_status gsample_history_append(const gsample_logit_state* state, const int32_t* slot,
+                                      int64_t n, const int64_t* tokens, int64_t total,
+                                      const int64_t* offsets, gsample_history_kind kind,
+                                      gsample_stream_t stream);
+
+/* Sets bias[slot, tokens[j]] = values[j] for the lists of n requests (layout
+ * as in gsample_history_append). Other entries keep their values. A token
+ * named twice in one list takes the later value; a slot named by two requests
+ * of one call takes either request's value. state->bias must not be NULL. */
+gsample_status gsample_bias_set(const gsample_logit_state* state, const int32_t* slot, int64_t n,
+                                const int64_t* tokens, const float* values, int64_t total,
+                                const int64_t* offsets, gsample_stream_t stream);
+
+/* Writes the constrained logits of every row: out[b, v], rounded once to
+ * out_dtype, which is GSAMPLE_F32 or the logits' type; out_ld elements from
+ * row to row. In place (out == logits, same type and ld) it writes only the
+ * elements that change. Any other overlap of a row of out with a row of the
+ * logits returns GSAMPLE_ERR_INVALID_ARG. constraints == NULL converts. */
+gsample_status gsample_process_logits(const void* logits, gsample_dtype dtype, int64_t B,
+                                      int64_t V, int64_t ld,
+                                      const gsample_constraints* constraints, void* out,
+                                      gsample_dtype out_dtype, int64_t out_ld,
+                                      gsample_stream_t stream);
+
+/* gsample_gumbel_argmax on the constrained logits, which are not written
+ * anywhere and not rounded below binary32: the indices are those of
+ * gsample_process_logits with GSAMPLE_F32 followed by gsample_gumbel_argmax.
+ * A row whose mask leaves nothing gets -1. Everything else (greedy rows,
+ * workspace, validation, asynchrony) as gsample_gumbel_argmax. */
+gsample_status gsample_constrained_gumbel_argmax(const void* logits, gsample_dtype dtype,
+                                                 int64_t B, int64_t V, int64_t ld,
+                                                 const float* temperature, const uint64_t* seed,
+                                                 const uint64_t* offset,
+                                                 const gsample_constraints* constraints,
+                                                 int64_t* out_idx, void* workspace,
+                                                 gsample_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

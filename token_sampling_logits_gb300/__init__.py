@@ -13,6 +13,7 @@ All calls are asynchronous on ``torch.cuda.current_stream()``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -24,7 +25,8 @@ __all__ = [
     "GSampleError", "HlgParams", "PIVOT_TOP", "PIVOT_ENTROPY", "F32", "BF16", "F16",
     "lib", "library_path", "workspace_bytes", "workspace_init", "new_workspace", "argmax",
     "gumbel_argmax", "hlg_gumbel_argmax", "hlg_gumbel_argmax_rows", "hlg_rows_tensor",
-    "categorical", "filtered_gumbel_argmax", "status_string",
+    "categorical", "filtered_gumbel_argmax", "status_string", "LogitState", "new_logit_state",
+    "state_reset", "history_append", "bias_set", "process_logits", "constrained_gumbel_argmax",
 ]
 
 F32, BF16, F16 = 0, 1, 2
@@ -43,6 +45,17 @@ class _HlgParamsC(ctypes.Structure):
     _fields_ = [("m", ctypes.c_float), ("w", ctypes.c_float), ("beta_t", ctypes.c_float),
                 ("beta_h", ctypes.c_float), ("pivot_offset", ctypes.c_float),
                 ("pivot_mode", ctypes.c_int32)]
+
+
+class _StateC(ctypes.Structure):
+    _fields_ = [("history", _vp), ("bias", _vp), ("touched", _vp), ("rows", _i64),
+                ("vocab", _i64), ("ld", _i64)]
+
+
+class _ConstraintsC(ctypes.Structure):
+    _fields_ = [("state", ctypes.POINTER(_StateC)), ("slot", _vp), ("repetition", _vp),
+                ("frequency", _vp), ("presence", _vp), ("mask", _vp), ("mask_rows", _i64),
+                ("mask_ld", _i64), ("mask_row", _vp)]
 
 
 @dataclass(frozen=True)
@@ -118,6 +131,14 @@ def lib() -> ctypes.CDLL:
                                                   _vp, _vp, _vp]),
             "gsample_filtered_gumbel_argmax": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp,
                                                       _vp, _vp, _vp, _vp, _vp]),
+            "gsample_logit_state_ld": (_i64, [_i64]),
+            "gsample_state_reset": (_int, [_vp, _vp, _i64, _vp]),
+            "gsample_history_append": (_int, [_vp, _vp, _i64, _vp, _i64, _vp, _int, _vp]),
+            "gsample_bias_set": (_int, [_vp, _vp, _i64, _vp, _vp, _i64, _vp, _vp]),
+            "gsample_process_logits": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _int, _i64,
+                                              _vp]),
+            "gsample_constrained_gumbel_argmax": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp,
+                                                         _vp, _vp, _vp, _vp, _vp]),
             "gsample_debug_filtered_ex": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp,
                                                  _vp, _vp, _vp, _i32, _vp]),
         }
@@ -401,6 +422,216 @@ def hlg_gumbel_argmax_rows(logits, temperature, seed, offset, params, out=None, 
                                               S.data_ptr(), O.data_ptr(), params.data_ptr(),
                                               out.data_ptr(), ws.data_ptr(), _stream_ptr(dev))
     _check(st, "gsample_hlg_gumbel_argmax_rows")
+    return out
+
+
+# --------------------------------------------------------------------------
+# Logit constraints
+# --------------------------------------------------------------------------
+class LogitState:
+    """What each request slot has seen and its biases (gsample_logit_state): a
+    view of caller-owned tensors on one device, zeroed before first use.
+
+    history  int32 [rows, ld]: output count, bit 31 set for a prompt token.
+    bias     float32 [rows, ld], or None.
+    touched  int32 [rows, ld // 32]: bit v set where history or bias may be
+             nonzero.
+    ld is `vocab` rounded up to a multiple of 32 (or more). Rows may be copied
+    with plain tensor copies (all three tensors): to fork a request, say."""
+
+    def __init__(self, history, bias, touched, vocab: int):
+        torch = _torch()
+        if not history.is_cuda or history.dim() != 2 or history.dtype != torch.int32 or \
+                not history.is_contiguous():
+            raise ValueError("history must be a contiguous int32 CUDA tensor [rows, ld]")
+        rows, ld = history.shape
+        if ld % 32 or not 1 <= vocab <= ld:
+            raise ValueError("ld must be a multiple of 32 and at least vocab")
+        dev = history.device
+        if bias is not None and (bias.dtype != torch.float32 or bias.device != dev or
+                                 bias.shape != (rows, ld) or not bias.is_contiguous()):
+            raise ValueError("bias must be a contiguous float32 tensor [rows, ld] on history's "
+                             "device, or None")
+        if touched.dtype != torch.int32 or touched.device != dev or \
+                touched.shape != (rows, ld // 32) or not touched.is_contiguous():
+            raise ValueError("touched must be a contiguous int32 tensor [rows, ld // 32] on "
+                             "history's device")
+        self.history, self.bias, self.touched, self.vocab = history, bias, touched, int(vocab)
+        self.rows, self.ld, self.device = rows, ld, dev
+        self._c = _StateC(history.data_ptr(), None if bias is None else bias.data_ptr(),
+                          touched.data_ptr(), rows, self.vocab, ld)
+
+
+def new_logit_state(rows: int, vocab: int, device=None, bias: bool = True) -> LogitState:
+    """An empty state for `rows` request slots."""
+    torch = _torch()
+    ld = int(lib().gsample_logit_state_ld(vocab))
+    dev = device or "cuda"
+    return LogitState(torch.zeros((rows, ld), dtype=torch.int32, device=dev),
+                      torch.zeros((rows, ld), dtype=torch.float32, device=dev) if bias else None,
+                      torch.zeros((rows, ld // 32), dtype=torch.int32, device=dev), vocab)
+
+
+def _on(device):
+    """The tensors' device as the current one (the library launches there)."""
+    torch = _torch()
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _vector(x, n, dtype, device, name):
+    if x is not None and (x.dtype != dtype or x.device != device or x.dim() != 1 or
+                          (n is not None and x.shape[0] != n) or not x.is_contiguous()):
+        raise ValueError("%s must be a contiguous 1-D %s tensor%s on %s" %
+                         (name, dtype, "" if n is None else " of %d entries" % n, device))
+    return x
+
+
+def _lists(state, slots, tokens, offsets):
+    torch = _torch()
+    _vector(tokens, None, torch.int64, state.device, "tokens")
+    _vector(offsets, None, torch.int64, state.device, "offsets")
+    if offsets is not None and offsets.shape[0] < 1:
+        raise ValueError("offsets has one entry more than there are requests")
+    n = tokens.shape[0] if offsets is None else offsets.shape[0] - 1
+    _vector(slots, n, torch.int32, state.device, "slots")
+    return n
+
+
+def state_reset(state: LogitState, slots=None) -> None:
+    """Clears the state rows in `slots` (int32 device tensor), or all of them."""
+    _vector(slots, None, _torch().int32, state.device, "slots")
+    n = state.rows if slots is None else slots.shape[0]
+    with _on(state.device):
+        _check(lib().gsample_state_reset(ctypes.byref(state._c), _ptr(slots), n,
+                                         _stream_ptr(state.device)), "gsample_state_reset")
+
+
+def history_append(state: LogitState, tokens, slots=None, offsets=None,
+                   prompt: bool = False) -> None:
+    """Appends tokens (int64 device tensor) to the requests' histories: request
+    i owns tokens[offsets[i]:offsets[i + 1]], or tokens[i] alone without
+    offsets (the indices a sampler just drew). slots[i] (int32) is its state
+    row; without slots, row i. Ids outside the vocabulary are ignored."""
+    n = _lists(state, slots, tokens, offsets)
+    with _on(state.device):
+        _check(lib().gsample_history_append(ctypes.byref(state._c), _ptr(slots), n, _ptr(tokens),
+                                            tokens.shape[0], _ptr(offsets), 0 if prompt else 1,
+                                            _stream_ptr(state.device)), "gsample_history_append")
+
+
+def bias_set(state: LogitState, tokens, values, slots=None, offsets=None) -> None:
+    """Sets the biases of the listed tokens (lists as in history_append,
+    values float32). Other entries keep theirs."""
+    torch = _torch()
+    if state.bias is None:
+        raise ValueError("the state was made without biases")
+    n = _lists(state, slots, tokens, offsets)
+    _vector(values, tokens.shape[0], torch.float32, state.device, "values")
+    with _on(state.device):
+        _check(lib().gsample_bias_set(ctypes.byref(state._c), _ptr(slots), n, _ptr(tokens),
+                                      _ptr(values), tokens.shape[0], _ptr(offsets),
+                                      _stream_ptr(state.device)), "gsample_bias_set")
+
+
+def _constraints(B, V, dev, state, slots, repetition, frequency, presence, mask, mask_rows):
+    """The C struct, and the tensors it points into (to be kept until the call)."""
+    torch = _torch()
+    c = _ConstraintsC()
+    keep = []
+    if state is not None:
+        if state.device != dev or state.vocab != V:
+            raise ValueError("the state must be on the logits' device and of their vocabulary")
+        if slots is None and state.rows < B:
+            raise ValueError("without slots the state needs a row for every batch row")
+        c.state = ctypes.pointer(state._c)
+        c.slot = _ptr(_vector(slots, B, torch.int32, dev, "slots"))
+        for name, x in (("repetition", repetition), ("frequency", frequency),
+                        ("presence", presence)):
+            if x is not None:
+                x = _row_tensor(x, B, torch.float32, dev, name)
+                keep.append(x)
+                setattr(c, name, x.data_ptr())
+    elif slots is not None or repetition is not None or frequency is not None or \
+            presence is not None:
+        raise ValueError("slots and penalties need a state")
+    if mask is not None:
+        if mask.dtype != torch.int32 or mask.device != dev or mask.dim() != 2 or \
+                (mask.shape[1] > 1 and mask.stride(1) != 1) or mask.shape[1] < (V + 31) // 32:
+            raise ValueError("mask must be an int32 tensor [masks, >= ceil(V / 32)] with "
+                             "contiguous rows on the logits' device")
+        if mask_rows is None and mask.shape[0] < B:
+            raise ValueError("without mask_rows there must be a mask for every batch row")
+        if mask.shape[0] > 1 and mask.stride(0) < mask.shape[1]:
+            raise ValueError("mask rows must not overlap")
+        c.mask = mask.data_ptr()
+        c.mask_rows = mask.shape[0]
+        c.mask_ld = mask.stride(0) if mask.shape[0] > 1 else mask.shape[1]
+        c.mask_row = _ptr(_vector(mask_rows, B, torch.int32, dev, "mask_rows"))
+    elif mask_rows is not None:
+        raise ValueError("mask_rows needs a mask")
+    return c, keep
+
+
+def process_logits(logits, state: LogitState | None = None, slots=None, repetition=None,
+                   frequency=None, presence=None, mask=None, mask_rows=None, out=None,
+                   out_dtype=None):
+    """The constrained logits [B, V] (gsample_process_logits): biases,
+    repetition / frequency / presence penalties and grammar masks.
+
+    state       LogitState; slots (int32 [B]) names each row's state row, -1
+                for none (default: row b uses state row b).
+    repetition, frequency, presence   float32 [B] tensors or scalars.
+    mask        int32 [masks, >= ceil(V / 32)], bit v & 31 of word v >> 5 set
+                where token v is allowed; mask_rows (int32 [B]) names each
+                row's mask, -1 for none (default: row b uses mask b).
+    out         a [B, V] tensor with contiguous rows, in the logits' type or
+                float32; out=logits works in place. Default: a new tensor of
+                out_dtype (the logits' type, or torch.float32)."""
+    torch = _torch()
+    dt, B, V, ld = _logits_args(logits)
+    dev = logits.device
+    if out is None:
+        out = torch.empty((B, V), dtype=out_dtype or logits.dtype, device=dev)
+    elif out.device != dev or out.shape != (B, V) or (out_dtype or out.dtype) != out.dtype:
+        raise ValueError("out must be a [B, V] tensor on the logits' device, of out_dtype")
+    odt, _, _, out_ld = _logits_args(out)
+    if odt not in (F32, dt):
+        raise ValueError("out must be of the logits' type or float32")
+    c, keep = _constraints(B, V, dev, state, slots, repetition, frequency, presence, mask,
+                           mask_rows)
+    with _on(dev):
+        _check(lib().gsample_process_logits(logits.data_ptr(), dt, B, V, ld, ctypes.byref(c),
+                                            out.data_ptr(), odt, out_ld, _stream_ptr(dev)),
+               "gsample_process_logits")
+    return out
+
+
+def constrained_gumbel_argmax(logits, temperature, seed, offset, state: LogitState | None = None,
+                              slots=None, repetition=None, frequency=None, presence=None,
+                              mask=None, mask_rows=None, out=None, workspace=None):
+    """gumbel_argmax on the constrained logits (arguments as in process_logits
+    and gumbel_argmax), which are never written: the same indices as
+    gumbel_argmax(process_logits(..., out_dtype=torch.float32), ...). -1 for a
+    row whose constraints leave nothing."""
+    torch = _torch()
+    dt, B, V, ld, out, ws = _prepare(logits, out, workspace)
+    dev = logits.device
+    T = _row_tensor(temperature, B, torch.float32, dev, "temperature")
+    S = _row_tensor(seed, B, torch.int64, dev, "seed")
+    O = _row_tensor(offset, B, torch.int64, dev, "offset")
+    c, keep = _constraints(B, V, dev, state, slots, repetition, frequency, presence, mask,
+                           mask_rows)
+    with _on(dev):
+        _check(lib().gsample_constrained_gumbel_argmax(
+            logits.data_ptr(), dt, B, V, ld, T.data_ptr(), S.data_ptr(), O.data_ptr(),
+            ctypes.byref(c), out.data_ptr(), ws.data_ptr(), _stream_ptr(dev)),
+            "gsample_constrained_gumbel_argmax")
     return out
 
 

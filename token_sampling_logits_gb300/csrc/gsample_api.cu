@@ -519,6 +519,18 @@ gsample_status validate_gumbel_args(const void* logits, gsample_dtype dtype, int
   return device_info(&d);
 }
 
+gsample_status check_logits(const void* logits, gsample_dtype dtype, int64_t B, int64_t V,
+                            int64_t ld) {
+  return check_common(logits, dtype, B, V, ld, (const int64_t*)16, nullptr, false);
+}
+
+gsample_status current_device_sms(int* sms) {
+  const DeviceInfo* d = nullptr;
+  const gsample_status st = device_info(&d);
+  if (st == GSAMPLE_OK) *sms = d->sms;
+  return st;
+}
+
 }  // namespace gsample
 
 extern "C" {

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "gsample.h"
+#include "gsample_constrain.cuh"
 #include "gsample_device.cuh"
 
 namespace gsample {
@@ -148,6 +149,57 @@ gsample_status validate_gumbel_args(const void* logits, gsample_dtype dtype, int
                                     int64_t V, int64_t ld, const float* temperature,
                                     const uint64_t* seed, const uint64_t* offset,
                                     const int64_t* out_idx);
+
+// ---------------------------------------------------------------------------
+// Logit constraints (gsample_constrain.cu, gsample_constrain_api.cu)
+// ---------------------------------------------------------------------------
+// The writable view of a gsample_logit_state.
+struct StateArgs {
+  uint32_t* history;
+  float* bias;
+  uint32_t* touched;
+  int64_t rows, vocab, ld;
+};
+
+struct ProcessParams {
+  const char* logits;
+  char* out;
+  int64_t ld_bytes, out_ld_bytes;
+  int64_t B, V;
+  bool inplace;
+  ConstrainArgs con;
+};
+
+struct ConDrawParams {
+  const char* logits;
+  int64_t ld_bytes;
+  int64_t B;
+  int32_t V;
+  const float* temperature;
+  const uint64_t* seed;
+  const uint64_t* offset;
+  int64_t* out_idx;
+  ConstrainArgs con;
+};
+
+cudaError_t launch_state_reset(const StateArgs& s, const int32_t* slot, int64_t n, int sms,
+                               cudaStream_t stream);
+cudaError_t launch_history_append(const StateArgs& s, const int32_t* slot, int64_t n,
+                                  const int64_t* tokens, int64_t total, const int64_t* offsets,
+                                  bool prompt, int sms, cudaStream_t stream);
+cudaError_t launch_bias_set(const StateArgs& s, const int32_t* slot, int64_t n,
+                            const int64_t* tokens, const float* values, int64_t total,
+                            const int64_t* offsets, cudaStream_t stream);
+cudaError_t launch_process(const ProcessParams& p, int dtype, int out_dtype, int sms,
+                           cudaStream_t stream);
+cudaError_t launch_constrained_draw(const ConDrawParams& p, int dtype, cudaStream_t stream);
+
+// The host-side checks of the logits arguments and of the current device,
+// shared with gsample_api.cu. current_device_sms returns the status of the
+// device check and the number of its SMs.
+gsample_status check_logits(const void* logits, gsample_dtype dtype, int64_t B, int64_t V,
+                            int64_t ld);
+gsample_status current_device_sms(int* sms);
 
 cudaError_t launch_debug_philox(uint64_t seed, uint32_t row, uint64_t offset, int64_t group0,
                                 int64_t n, uint32_t* out, cudaStream_t stream);
