@@ -36,6 +36,8 @@ struct DeviceInfo {
   int hlg_cluster[6] = {0, 0, 0, 0, 0, 0};   // largest co-schedulable cluster, per (dtype, vec)
   int cat_cluster[6] = {0, 0, 0, 0, 0, 0};   // the same for the categorical baseline
   int rc_cluster[6] = {0, 0, 0, 0, 0, 0};    // the same for the small-batch sampler
+  int con_slots[6] = {0, 0, 0, 0, 0, 0};     // sample_slots of the constrained sampler
+  int con_cluster[6] = {0, 0, 0, 0, 0, 0};   // rc_cluster of the constrained sampler
   int filt_cluster[6] = {0, 0, 0, 0, 0, 0};  // the same for the top-k / top-p filter
 };
 
@@ -63,12 +65,14 @@ gsample_status device_info(const DeviceInfo** out) {
     if (d.supported) {
       for (int dt = 0; dt < 3; ++dt)
         for (int v = 0; v < 2; ++v) {
-          const int n = gsample::sample_ctas_per_sm(dt, v != 0);
-          if (n <= 0) {
+          const int n = gsample::sample_ctas_per_sm(dt, v != 0, false);
+          const int nc = gsample::sample_ctas_per_sm(dt, v != 0, true);
+          if (n <= 0 || nc <= 0) {
             cudaGetLastError();
             return GSAMPLE_ERR_CUDA;
           }
           d.sample_slots[dt * 2 + v] = n;
+          d.con_slots[dt * 2 + v] = nc;
           const int c = gsample::hlg_max_cluster(dt, v != 0, gsample::hlg_smem_limit());
           if (c <= 0) {
             cudaGetLastError();
@@ -81,12 +85,14 @@ gsample_status device_info(const DeviceInfo** out) {
             return GSAMPLE_ERR_CUDA;
           }
           d.cat_cluster[dt * 2 + v] = cc;
-          const int rc = gsample::rc_max_cluster(dt, v != 0);
-          if (rc <= 0) {
+          const int rc = gsample::rc_max_cluster(dt, v != 0, false);
+          const int rcc = gsample::rc_max_cluster(dt, v != 0, true);
+          if (rc <= 0 || rcc <= 0) {
             cudaGetLastError();
             return GSAMPLE_ERR_CUDA;
           }
           d.rc_cluster[dt * 2 + v] = rc;
+          d.con_cluster[dt * 2 + v] = rcc;
           const int fc = gsample::filter_max_cluster(dt, v != 0);
           if (fc <= 0) {
             cudaGetLastError();
@@ -219,7 +225,8 @@ bool vec_path(const void* logits, gsample_dtype dtype, int64_t ld) {
 // Fill SampleParams and choose the CTA count: one wave of CTAs (SMs x resident
 // CTAs per SM), fewer when the batch has too few units to give every thread one.
 void plan_sample(const DeviceInfo& d, const void* logits, gsample_dtype dtype, int64_t B,
-                 int64_t V, int64_t ld, int32_t ctas_override, SampleParams* p, bool* vec_out) {
+                 int64_t V, int64_t ld, int32_t ctas_override, SampleParams* p, bool* vec_out,
+                 bool constrained = false) {
   const bool vec = vec_path(logits, dtype, ld);
   const int epu = gsample::units_elems((int)dtype, vec);
   const int64_t nu = (V + epu - 1) / epu;
@@ -228,13 +235,14 @@ void plan_sample(const DeviceInfo& d, const void* logits, gsample_dtype dtype, i
   if (ctas_override > 0) {
     g = ctas_override;
   } else {
-    const int64_t slots = (int64_t)d.sms * d.sample_slots[(int)dtype * 2 + (vec ? 1 : 0)];
+    const int at = (int)dtype * 2 + (vec ? 1 : 0);
+    const int64_t slots = (int64_t)d.sms * (constrained ? d.con_slots[at] : d.sample_slots[at]);
     g = (total + kMinUnitsPerCta - 1) / kMinUnitsPerCta;
     if (g > slots) g = slots;
   }
   if (g > total) g = total;
   if (g < 1) g = 1;
-  std::memset(p, 0, sizeof *p);
+  *p = SampleParams{};
   p->logits = static_cast<const char*>(logits);
   p->ld_bytes = ld * elt_bytes(dtype);
   p->B = B;
@@ -258,7 +266,8 @@ gsample_status run_sample(const void* logits, gsample_dtype dtype, int64_t B, in
                           int64_t ld, const float* temperature, const uint64_t* seed,
                           const uint64_t* offset, int64_t* out_idx, void* workspace,
                           int32_t ctas_override, cudaStream_t stream,
-                          int32_t cluster_override = 0) {
+                          int32_t cluster_override = 0,
+                          const gsample::ConstrainArgs* con = nullptr) {
   gsample_status st = check_common(logits, dtype, B, V, ld, out_idx, workspace);
   if (st != GSAMPLE_OK || B == 0) return st;
   const DeviceInfo* d = nullptr;
@@ -270,17 +279,18 @@ gsample_status run_sample(const void* logits, gsample_dtype dtype, int64_t B, in
     const bool vec = vec_path(logits, dtype, ld);
     const int epu = gsample::units_elems((int)dtype, vec);
     const int64_t nu = (V + epu - 1) / epu;
-    const int max_cluster = d->rc_cluster[(int)dtype * 2 + (vec ? 1 : 0)];
+    const int at = (int)dtype * 2 + (vec ? 1 : 0);
+    const int max_cluster = con ? d->con_cluster[at] : d->rc_cluster[at];
+    const size_t limit = con ? gsample::rc_con_slice_limit() : gsample::rc_smem_limit();
     int cluster = cluster_override;
     if (cluster == 0 && B <= kClusterMaxRows) {
-      cluster = pick_cluster(gsample::rc_kernel, (int)dtype, vec, B, nu, max_cluster,
-                             kClusterUnitsPerCta, gsample::rc_smem_limit());
-      if ((nu + cluster - 1) / cluster * 16 > (int64_t)gsample::rc_smem_limit()) cluster = 0;
+      cluster = pick_cluster(con ? gsample::rc_con_kernel : gsample::rc_kernel, (int)dtype, vec, B,
+                             nu, max_cluster, kClusterUnitsPerCta, limit);
+      if ((nu + cluster - 1) / cluster * 16 > (int64_t)limit) cluster = 0;
     }
     if (cluster > 0) {
       if (cluster > 16 || cluster > max_cluster) return GSAMPLE_ERR_INVALID_ARG;
-      RowClusterParams q;
-      std::memset(&q, 0, sizeof q);
+      gsample::ConRowClusterParams q{};
       q.logits = static_cast<const char*>(logits);
       q.ld_bytes = ld * elt_bytes(dtype);
       q.B = B;
@@ -292,22 +302,36 @@ gsample_status run_sample(const void* logits, gsample_dtype dtype, int64_t B, in
       q.seed = seed;
       q.offset = offset;
       q.out_idx = out_idx;
-      if (gsample::launch_sample_cluster(q, (int)dtype, vec, stream) != cudaSuccess) {
+      cudaError_t e;
+      if (con) {
+        q.con = *con;
+        e = gsample::launch_sample_cluster(q, (int)dtype, vec, stream);
+      } else {
+        e = gsample::launch_sample_cluster(static_cast<const RowClusterParams&>(q), (int)dtype,
+                                           vec, stream);
+      }
+      if (e != cudaSuccess) {
         cudaGetLastError();
         return GSAMPLE_ERR_CUDA;
       }
       return GSAMPLE_OK;
     }
   }
-  SampleParams p;
+  gsample::ConSampleParams p{};
   bool vec = false;
-  plan_sample(*d, logits, dtype, B, V, ld, ctas_override, &p, &vec);
+  plan_sample(*d, logits, dtype, B, V, ld, ctas_override, &p, &vec, con != nullptr);
   p.temperature = temperature;
   p.seed = seed;
   p.offset = offset;
   p.out_idx = out_idx;
   p.ws = static_cast<WsRow*>(workspace);
-  const cudaError_t err = gsample::launch_sample(p, (int)dtype, vec, stream);
+  cudaError_t err;
+  if (con) {
+    p.con = *con;
+    err = gsample::launch_sample(p, (int)dtype, vec, stream);
+  } else {
+    err = gsample::launch_sample(static_cast<const SampleParams&>(p), (int)dtype, vec, stream);
+  }
   if (err != cudaSuccess) {
     cudaGetLastError();
     return GSAMPLE_ERR_CUDA;
@@ -522,6 +546,14 @@ gsample_status validate_gumbel_args(const void* logits, gsample_dtype dtype, int
 gsample_status check_logits(const void* logits, gsample_dtype dtype, int64_t B, int64_t V,
                             int64_t ld) {
   return check_common(logits, dtype, B, V, ld, (const int64_t*)16, nullptr, false);
+}
+
+gsample_status sample_constrained(const void* logits, gsample_dtype dtype, int64_t B, int64_t V,
+                                  int64_t ld, const float* temperature, const uint64_t* seed,
+                                  const uint64_t* offset, const ConstrainArgs& con,
+                                  int64_t* out_idx, void* workspace, cudaStream_t stream) {
+  return run_sample(logits, dtype, B, V, ld, temperature, seed, offset, out_idx, workspace, 0,
+                    stream, 0, &con);
 }
 
 gsample_status current_device_sms(int* sms) {

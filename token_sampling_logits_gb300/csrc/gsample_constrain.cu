@@ -1,8 +1,9 @@
 // Logit constraints ("Softmax-free GPU sampling: Gumbel-max categorical
 // sampling kernel", lablup/mlxcel issue #900, Background: the token bias and
 // the repetition / frequency / presence penalties ahead of the sampler; and
-// grammar masks): the per-request state, the kernel that writes the
-// constrained logits, and the draw from them.
+// grammar masks): the per-request state and the kernel that writes the
+// constrained logits. The draw from them is the samplers' own (sample_kernel
+// and sample_cluster_kernel with CON).
 #include <climits>
 #include <cstdint>
 
@@ -156,41 +157,6 @@ __global__ void __launch_bounds__(kConThreads) process_kernel(const ProcessParam
   }
 }
 
-// ---------------------------------------------------------------------------
-// The draw: one CTA a row.
-// ---------------------------------------------------------------------------
-template <int DT>
-__global__ void __launch_bounds__(kConThreads) constrained_draw_kernel(const ConDrawParams p) {
-  __shared__ unsigned long long red[kConThreads / 32];
-  pdl_wait_then_release();
-  const int64_t b = blockIdx.x;
-  const RowConstraints r = row_constraints(p.con, b);
-  const float T = __ldg(p.temperature + b);
-  const uint64_t sd = __ldg(p.seed + b), of = __ldg(p.offset + b);
-  const PhiloxRow ph = philox_row((uint32_t)b, (uint32_t)of, (uint32_t)(of >> 32), (uint32_t)sd,
-                                  (uint32_t)(sd >> 32));
-  const char* row = p.logits + b * p.ld_bytes;
-  float bs = -INFINITY;
-  int32_t bi = INT32_MAX;
-  for (int32_t g = threadIdx.x; g < (p.V + 3) / 4; g += kConThreads) {
-    const uint4 w = philox_row_1((uint32_t)g, ph);
-    for (int t = 0; t < 4; ++t) {
-      const int32_t v = 4 * g + t;
-      if (v >= p.V) break;
-      const float x = constrained_logit(load_one<DT>(row, v), v, r);
-      if (x > -INFINITY) take_better(T > 0.0f ? exact_score(x, word_of(w, t), T) : x, v, bs, bi);
-    }
-  }
-  warp_argmax(bs, bi);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = bi != INT32_MAX ? pack_key(bs, bi) : 0ull;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    unsigned long long k = 0ull;
-    for (int i = 0; i < kConThreads / 32; ++i) k = red[i] > k ? red[i] : k;
-    p.out_idx[b] = index_of_key(k);
-  }
-}
-
 // Launch with programmatic stream serialization, as every kernel here.
 template <typename... Params, typename... Args>
 cudaError_t launch(void (*fn)(Params...), int64_t blocks, int threads, cudaStream_t stream,
@@ -242,14 +208,6 @@ cudaError_t launch_process(const ProcessParams& p, int dtype, int out_dtype, int
     case 3: return launch(process_kernel<1, 1>, blocks, kConThreads, stream, p);
     case 4: return launch(process_kernel<2, 0>, blocks, kConThreads, stream, p);
     default: return launch(process_kernel<2, 2>, blocks, kConThreads, stream, p);
-  }
-}
-
-cudaError_t launch_constrained_draw(const ConDrawParams& p, int dtype, cudaStream_t stream) {
-  switch (dtype) {
-    case 0: return launch(constrained_draw_kernel<0>, p.B, kConThreads, stream, p);
-    case 1: return launch(constrained_draw_kernel<1>, p.B, kConThreads, stream, p);
-    default: return launch(constrained_draw_kernel<2>, p.B, kConThreads, stream, p);
   }
 }
 

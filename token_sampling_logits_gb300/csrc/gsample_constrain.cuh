@@ -14,6 +14,8 @@
 
 #include <cstdint>
 
+#include <cuda_bf16.h>
+
 #include "gsample_device.cuh"
 
 namespace gsample {
@@ -90,6 +92,134 @@ __device__ __forceinline__ float penalised(float x, uint32_t h, float bias,
   const uint32_t c = h & 0x7FFFFFFFu;
   if (c != 0u) y = __fsub_rn(__fsub_rn(y, __fmul_rn(r.freq, __uint2float_rn(c))), r.pres);
   return y;
+}
+
+// ---------------------------------------------------------------------------
+// Units in shared memory. The samplers hold rows as 16-byte units of EPU
+// elements: binary32 bits, or raw 16-bit values. Before a sampler looks at its
+// units, every masked element becomes -inf, and every touched one
+//   - its constrained value, in binary32 units;
+//   - in 16-bit units of a sampled row, that value rounded UP to the type: the
+//     pruning tests only need a bound from above, and the exact pass forms the
+//     value again from the logit (exact_touched);
+//   - in 16-bit units of a greedy row, -inf, after the binary32 value has been
+//     offered to the running best itself.
+// ---------------------------------------------------------------------------
+
+// The value of `y` rounded up to the 16-bit type (NaN, which is never drawn: -inf).
+template <int DT>
+__device__ __forceinline__ uint32_t bound_bits(float y) {
+  constexpr uint32_t ninf = DT == 1 ? 0xFF80u : 0xFC00u;
+  if (y != y) return ninf;
+  if constexpr (DT == 1) {
+    const __nv_bfloat16 h = __float2bfloat16_ru(y);
+    return *reinterpret_cast<const unsigned short*>(&h);
+  } else {
+    const __half h = __float2half_ru(y);
+    return *reinterpret_cast<const unsigned short*>(&h);
+  }
+}
+
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .u16 t;\n\tld.shared.u16 t, [%1];\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(v) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ void sts_u16(uint32_t a, uint32_t v) {
+  asm volatile("{\n\t.reg .u16 t;\n\tcvt.u16.u32 t, %1;\n\tst.shared.u16 [%0], t;\n\t}" ::"r"(a), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ void sts_f32(uint32_t a, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+
+// The touched and allowed elements of a thread's units u0, u0 + STRIDE, ... (at
+// shared addresses a0, a0 + 16 * STRIDE, ...): bit 8 * k + e of `todo` stands
+// for element e of the k-th unit. Four state words are fetched at a time, so a
+// usual tile (one or two touched elements a thread) costs one round trip.
+template <int DT, bool F32BITS, int EPU, int STRIDE>
+__device__ __forceinline__ void apply_touched(uint32_t a0, int32_t u0, uint64_t todo,
+                                              const RowConstraints& r, bool sampled, float& bs,
+                                              int32_t& bi) {
+  constexpr int N = 4;
+  while (todo != 0ull) {
+    uint32_t at[N], h[N];
+    int32_t v[N];
+    float b[N];
+    bool on[N];
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      on[q] = todo != 0ull;
+      const int j = on[q] ? __ffsll((long long)todo) - 1 : 0;
+      todo &= todo - 1ull;  // 0 stays 0
+      const int k = j >> 3, e = j & 7;
+      v[q] = (u0 + k * STRIDE) * EPU + e;
+      at[q] = a0 + (uint32_t)(k * STRIDE) * 16u + (uint32_t)e * (F32BITS ? 4u : 2u);
+      h[q] = on[q] ? __ldcg(r.history + v[q]) : 0u;
+      b[q] = on[q] && r.bias ? __ldcg(r.bias + v[q]) : 0.0f;
+    }
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      if (!on[q]) continue;
+      if constexpr (F32BITS) {
+        sts_f32(at[q], penalised(lds_f32(at[q]), h[q], b[q], r));
+      } else {
+        const float y = penalised(half_to_f32<DT>(lds_u16(at[q])), h[q], b[q], r);
+        if (sampled) {
+          sts_u16(at[q], bound_bits<DT>(y));
+        } else {
+          take_better(y, v[q], bs, bi);
+          sts_u16(at[q], DT == 1 ? 0xFF80u : 0xFC00u);
+        }
+      }
+    }
+  }
+}
+
+// A unit with the elements whose bit in `allowed` is clear set to -inf.
+template <int DT, bool F32BITS>
+__device__ __forceinline__ uint4 masked_unit(uint4 r, uint32_t allowed) {
+  uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (F32BITS) {
+      if (!((allowed >> i) & 1u)) w[i] = 0xFF800000u;
+    } else {
+      constexpr uint32_t ninf = DT == 1 ? 0xFF80u : 0xFC00u;
+      const uint32_t keep = ((allowed >> (2 * i)) & 1u ? 0xFFFFu : 0u) |
+                            ((allowed >> (2 * i)) & 2u ? 0xFFFF0000u : 0u);
+      w[i] = (w[i] & keep) | ((ninf * 0x10001u) & ~keep);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The constrained value of a touched element of a 16-bit row, from its logit.
+template <int DT>
+__device__ __forceinline__ float exact_touched(const char* row, int32_t v,
+                                               const RowConstraints& r) {
+  const float x = half_to_f32<DT>(__ldg(reinterpret_cast<const unsigned short*>(row) + v));
+  return penalised(x, __ldcg(r.history + v), r.bias ? __ldcg(r.bias + v) : 0.0f, r);
+}
+
+// The values of group g (elements 4 g .. 4 g + 3) of a 16-bit row whose touched
+// elements hold bounds: those get their exact values.
+template <int DT>
+__device__ __forceinline__ void exact_group(uint32_t g, float (&x)[4], const char* row,
+                                            const RowConstraints& r) {
+  if (!r.touched) return;
+  const uint32_t bits = (uint32_t)__ldcg(r.touched + (g >> 1)) >> (4u * (g & 1u));
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+    if (((bits >> t) & 1u) && x[t] > -INFINITY)
+      x[t] = exact_touched<DT>(row, (int32_t)(4u * g) + t, r);
 }
 
 // The N bits (N = 4 or 8) of a bit row that belong to the unit starting at

@@ -197,26 +197,13 @@ gsample_status gsample_constrained_gumbel_argmax(const void* logits, gsample_dty
                                                  int64_t* out_idx, void* workspace,
                                                  gsample_stream_t stream) {
   if (B > 0 && (!temperature || !seed || !offset)) return GSAMPLE_ERR_INVALID_ARG;
-  gsample::ConDrawParams p;
-  std::memset(&p, 0, sizeof p);
-  if (B > 0 && (!out_idx || !workspace || misaligned(out_idx, 8))) return GSAMPLE_ERR_INVALID_ARG;
   gsample_status st = gsample::check_logits(logits, dtype, B, V, ld);
   if (st != GSAMPLE_OK) return st;
-  if (B > 0 && misaligned(workspace, 16)) return GSAMPLE_ERR_WORKSPACE;
-  st = check_constraints(constraints, B, V, &p.con);
-  if (st != GSAMPLE_OK || B == 0) return st;
-  int sms = 0;
-  st = gsample::current_device_sms(&sms);
+  ConstrainArgs con;
+  st = check_constraints(constraints, B, V, &con);
   if (st != GSAMPLE_OK) return st;
-  p.logits = static_cast<const char*>(logits);
-  p.ld_bytes = ld * elt_bytes(dtype);
-  p.B = B;
-  p.V = (int32_t)V;
-  p.temperature = temperature;
-  p.seed = seed;
-  p.offset = offset;
-  p.out_idx = out_idx;
-  return launched(gsample::launch_constrained_draw(p, (int)dtype, (cudaStream_t)stream));
+  return gsample::sample_constrained(logits, dtype, B, V, ld, temperature, seed, offset, con,
+                                     out_idx, workspace, (cudaStream_t)stream);
 }
 
 }  // extern "C"

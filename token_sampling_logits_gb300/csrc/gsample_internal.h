@@ -40,6 +40,11 @@ struct SampleParams {
   WsRow* ws;
 };
 
+// The same launch, drawing from constrained logits.
+struct ConSampleParams : SampleParams {
+  ConstrainArgs con;
+};
+
 // One row's curve; the same layout as the public gsample_hlg_params.
 struct HlgRowParams {
   float m, w, beta_t, beta_h, pivot_offset;
@@ -82,6 +87,11 @@ struct RowClusterParams {
   int64_t* out_idx;
 };
 
+// The small-batch sampler drawing from constrained logits.
+struct ConRowClusterParams : RowClusterParams {
+  ConstrainArgs con;
+};
+
 // Top-k / top-p on the Gumbel path, after the plain sampler has written its
 // proposals into out_idx: one thread-block cluster of `cluster` CTAs per row
 // tests the proposal and, when it is rejected, replaces it by the Gumbel-max
@@ -114,9 +124,10 @@ cudaError_t launch_filter(const FilterParams& p, int dtype, bool vec, cudaStream
 inline int units_elems(int dtype, bool vec) { return vec ? (dtype == 0 ? 4 : 8) : 4; }
 
 // Occupancy-derived CTA slots per SM for the sampler kernel of (dtype, vec).
-int sample_ctas_per_sm(int dtype, bool vec);
+int sample_ctas_per_sm(int dtype, bool vec, bool constrained);
 size_t sample_smem_bytes(int dtype, bool vec);
 cudaError_t launch_sample(const SampleParams& p, int dtype, bool vec, cudaStream_t stream);
+cudaError_t launch_sample(const ConSampleParams& p, int dtype, bool vec, cudaStream_t stream);
 
 // HLG: the largest cluster size the device can co-schedule for this kernel and
 // the shared memory a CTA needs to hold `units_per_cta` units.
@@ -133,9 +144,15 @@ void* hlg_kernel_fn(int dtype, bool vec, bool resident, int* threads);
 
 // Small-batch sampler (one cluster per row): largest co-schedulable cluster,
 // per-CTA slice limit, launch.
-int rc_max_cluster(int dtype, bool vec);
+int rc_max_cluster(int dtype, bool vec, bool constrained);
 size_t rc_smem_limit();
 cudaError_t launch_sample_cluster(const RowClusterParams& p, int dtype, bool vec,
+                                  cudaStream_t stream);
+// The same drawing from constrained logits: the slice limit leaves room for
+// the slice's mask and touched bits.
+void* rc_con_kernel(int dtype, bool vec, bool resident, int* threads);
+size_t rc_con_slice_limit();
+cudaError_t launch_sample_cluster(const ConRowClusterParams& p, int dtype, bool vec,
                                   cudaStream_t stream);
 
 // Categorical baseline: largest co-schedulable cluster, per-CTA slice limit.
@@ -170,18 +187,6 @@ struct ProcessParams {
   ConstrainArgs con;
 };
 
-struct ConDrawParams {
-  const char* logits;
-  int64_t ld_bytes;
-  int64_t B;
-  int32_t V;
-  const float* temperature;
-  const uint64_t* seed;
-  const uint64_t* offset;
-  int64_t* out_idx;
-  ConstrainArgs con;
-};
-
 cudaError_t launch_state_reset(const StateArgs& s, const int32_t* slot, int64_t n, int sms,
                                cudaStream_t stream);
 cudaError_t launch_history_append(const StateArgs& s, const int32_t* slot, int64_t n,
@@ -192,7 +197,6 @@ cudaError_t launch_bias_set(const StateArgs& s, const int32_t* slot, int64_t n,
                             const int64_t* offsets, cudaStream_t stream);
 cudaError_t launch_process(const ProcessParams& p, int dtype, int out_dtype, int sms,
                            cudaStream_t stream);
-cudaError_t launch_constrained_draw(const ConDrawParams& p, int dtype, cudaStream_t stream);
 
 // The host-side checks of the logits arguments and of the current device,
 // shared with gsample_api.cu. current_device_sms returns the status of the
@@ -200,6 +204,12 @@ cudaError_t launch_constrained_draw(const ConDrawParams& p, int dtype, cudaStrea
 gsample_status check_logits(const void* logits, gsample_dtype dtype, int64_t B, int64_t V,
                             int64_t ld);
 gsample_status current_device_sms(int* sms);
+// The sampler of gsample_gumbel_argmax (its checks, plan and launch), drawing
+// from constrained logits.
+gsample_status sample_constrained(const void* logits, gsample_dtype dtype, int64_t B, int64_t V,
+                                  int64_t ld, const float* temperature, const uint64_t* seed,
+                                  const uint64_t* offset, const ConstrainArgs& con,
+                                  int64_t* out_idx, void* workspace, cudaStream_t stream);
 
 cudaError_t launch_debug_philox(uint64_t seed, uint32_t row, uint64_t offset, int64_t group0,
                                 int64_t n, uint32_t* out, cudaStream_t stream);

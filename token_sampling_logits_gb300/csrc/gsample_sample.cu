@@ -37,6 +37,7 @@
 
 #include <cuda_bf16.h>
 
+#include "gsample_constrain.cuh"
 #include "gsample_internal.h"
 
 namespace gsample {
@@ -306,6 +307,16 @@ __device__ __forceinline__ void raw_values(const RareRaw<DT, VEC>& r, float x[4]
   }
 }
 
+// What the exact pass needs besides the list: nothing, or, for constrained rows
+// of 16-bit units (whose touched elements hold bounds), the row.
+template <bool CON>
+struct ExactCtx {};
+template <>
+struct ExactCtx<true> {
+  const char* row;
+  RowConstraints c;
+};
+
 // Score the listed groups exactly (one per lane) against the current bound.
 // Out of line: it runs once per 32 listed groups, and keeping its logarithms
 // out of the tile loop keeps that loop's code small.
@@ -331,10 +342,33 @@ __device__ __noinline__ Best flush_rare_cold(const unsigned char* rbase, int rcn
   return Best{bs, bi};
 }
 
-template <int DT, bool VEC>
+template <int DT>
+__device__ __noinline__ Best flush_rare_constrained(const unsigned char* rbase, int rcnt, float T,
+                                                    float rT, PhiloxRow ph, Prune pr, float bs,
+                                                    int32_t bi, ExactCtx<true> ec) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  if (lane < rcnt) {
+    const uint32_t g = reinterpret_cast<const uint32_t*>(rbase)[lane];
+    float x[4];
+    raw_values<DT, true>(reinterpret_cast<const RareRaw<DT, true>*>(rbase + kRareRawOff)[lane], x);
+    exact_group<DT>(g, x, ec.row, ec.c);
+    const uint4 w = philox_row_1(g, ph);
+    score_group(g, x[0], x[1], x[2], x[3], w, pr, make_reach(pr, rT), T, &bs, &bi);
+  }
+  __syncwarp();
+  return Best{bs, bi};
+}
+
+template <int DT, bool VEC, bool CON>
 __device__ __forceinline__ void flush_rare(const unsigned char* rbase, int rcnt, const RowCtx& rc,
-                                           const Prune& pr, float& bs, int32_t& bi) {
-  const Best r = flush_rare_cold<DT, VEC>(rbase, rcnt, rc.T, rc.rT, rc.ph, pr, bs, bi);
+                                           const Prune& pr, float& bs, int32_t& bi,
+                                           const ExactCtx<CON>& ec) {
+  Best r;
+  if constexpr (CON && !Cfg<DT, VEC>::kF32Bits)
+    r = flush_rare_constrained<DT>(rbase, rcnt, rc.T, rc.rT, rc.ph, pr, bs, bi, ec);
+  else
+    r = flush_rare_cold<DT, VEC>(rbase, rcnt, rc.T, rc.rT, rc.ph, pr, bs, bi);
   bs = r.s;
   bi = r.i;
 }
@@ -349,11 +383,11 @@ __device__ __forceinline__ uint32_t lane_group(int i, int lane) {
 // Groups whose word test passed join the rare list: one round per set bit of
 // the lane's `need` mask. Bit j stands for tile-local group q[j], or, with N ==
 // 0, for the lane's j-th group of the tile.
-template <int DT, bool VEC, int N>
+template <int DT, bool VEC, int N, bool CON>
 __device__ __forceinline__ void append_rare(uint32_t need, const uint32_t* q, uint32_t stage,
                                             uint32_t g0, const RowCtx& rc, const Prune& pr,
                                             unsigned char* rbase, int& rcnt, float& bs,
-                                            int32_t& bi) {
+                                            int32_t& bi, const ExactCtx<CON>& ec) {
   using C = Cfg<DT, VEC>;
   const int lane = threadIdx.x & 31;
   const unsigned lt_mask = (1u << lane) - 1u;
@@ -362,7 +396,7 @@ __device__ __forceinline__ void append_rare(uint32_t need, const uint32_t* q, ui
     const unsigned m = __ballot_sync(0xFFFFFFFFu, has);
     const int n = __popc(m);
     if (rcnt + n > kRareCap) {
-      flush_rare<DT, VEC>(rbase, rcnt, rc, pr, bs, bi);
+      flush_rare<DT, VEC>(rbase, rcnt, rc, pr, bs, bi, ec);
       rcnt = 0;
     }
     if (has) {
@@ -406,12 +440,12 @@ __device__ __forceinline__ float group_max_at(uint32_t stage, uint32_t q) {
 
 // One batch of the compacted list: entries [base, base + 32 * N) below cnt,
 // N Philox blocks per lane side by side.
-template <int DT, bool VEC, int N>
+template <int DT, bool VEC, int N, bool CON>
 __device__ __forceinline__ void compact_batch(uint32_t stage, const unsigned short* clist, int base,
                                               int cnt, uint32_t g0, const RowCtx& rc,
                                               const Prune& pr, const ReachTest& rt,
                                               unsigned char* rbase, int& rcnt, float& bs,
-                                              int32_t& bi) {
+                                              int32_t& bi, const ExactCtx<CON>& ec) {
   const int lane = threadIdx.x & 31;
   uint32_t q[N], g[N], wt[N];
   bool valid[N];
@@ -436,7 +470,7 @@ __device__ __forceinline__ void compact_batch(uint32_t stage, const unsigned sho
   uint32_t need = 0;
 #pragma unroll
   for (int j = 0; j < N; ++j) need |= (valid[j] && max_word(w[j]) >= wt[j]) ? (1u << j) : 0u;
-  append_rare<DT, VEC, N>(need, q, stage, g0, rc, pr, rbase, rcnt, bs, bi);
+  append_rare<DT, VEC, N>(need, q, stage, g0, rc, pr, rbase, rcnt, bs, bi, ec);
 }
 
 #ifndef GSAMPLE_DENSE_NUM
@@ -456,11 +490,11 @@ __device__ __forceinline__ void compact_batch(uint32_t stage, const unsigned sho
 // only they get Philox, 128 per warp batch (a short last batch runs one or two
 // blocks per lane). Either way the word test follows, and the rare groups that
 // pass it join the rare list.
-template <int DT, bool VEC>
+template <int DT, bool VEC, bool CON>
 __device__ __forceinline__ void sampled_tile(uint32_t stage, uint32_t g0, const RowCtx& rc,
                                              const Prune& pr, unsigned char* rbase,
                                              unsigned short* clist, int& rcnt, float& bs,
-                                             int32_t& bi) {
+                                             int32_t& bi, const ExactCtx<CON>& ec) {
   using C = Cfg<DT, VEC>;
   constexpr int NG = kVPT * C::kGPU;  // groups per lane in a tile
   static_assert(NG % 4 == 0 && NG <= 32, "groups per lane must fill four-way Philox batches");
@@ -513,7 +547,7 @@ __device__ __forceinline__ void sampled_tile(uint32_t stage, uint32_t g0, const 
 #pragma unroll
       for (int j = 0; j < 4; ++j) need |= max_word(w[j]) >= wt[b + j] ? (1u << (b + j)) : 0u;
     }
-    append_rare<DT, VEC, 0>(need, nullptr, stage, g0, rc, pr, rbase, rcnt, bs, bi);
+    append_rare<DT, VEC, 0>(need, nullptr, stage, g0, rc, pr, rbase, rcnt, bs, bi, ec);
     return;
   }
 
@@ -540,20 +574,24 @@ __device__ __forceinline__ void sampled_tile(uint32_t stage, uint32_t g0, const 
   for (int base = 0; base < cnt; base += 128) {
     const int r = cnt - base;
     if (r > 64) {
-      compact_batch<DT, VEC, 4>(stage, clist, base, cnt, g0, rc, pr, rt, rbase, rcnt, bs, bi);
+      compact_batch<DT, VEC, 4>(stage, clist, base, cnt, g0, rc, pr, rt, rbase, rcnt, bs, bi, ec);
     } else if (r > 32) {
-      compact_batch<DT, VEC, 2>(stage, clist, base, cnt, g0, rc, pr, rt, rbase, rcnt, bs, bi);
+      compact_batch<DT, VEC, 2>(stage, clist, base, cnt, g0, rc, pr, rt, rbase, rcnt, bs, bi, ec);
     } else {
-      compact_batch<DT, VEC, 1>(stage, clist, base, cnt, g0, rc, pr, rt, rbase, rcnt, bs, bi);
+      compact_batch<DT, VEC, 1>(stage, clist, base, cnt, g0, rc, pr, rt, rbase, rcnt, bs, bi, ec);
     }
   }
   __syncwarp();  // the list is read before the next tile rewrites it
 }
 
-// Phase A: this lane's largest logit of the tile, scored exactly.
-template <int DT, bool VEC>
-__device__ __forceinline__ void lane_candidate(uint32_t stage, int32_t t0, int32_t t_hi,
-                                               const RowCtx& rc, float& bs, int32_t& bi) {
+// Phase A: this lane's largest logit of the tile, scored exactly. `touched`
+// marks the elements whose place in the tile holds a bound (bit 8 k + e:
+// element e of the lane's k-th unit); the result says whether the lane found
+// any candidate.
+template <int DT, bool VEC, bool CON>
+__device__ __forceinline__ bool lane_candidate(uint32_t stage, int32_t t0, int32_t t_hi,
+                                               const RowCtx& rc, float& bs, int32_t& bi,
+                                               uint64_t touched, const ExactCtx<CON>& ec) {
   using C = Cfg<DT, VEC>;
   const int lane = threadIdx.x & 31;
   float cm = -INFINITY;
@@ -568,7 +606,7 @@ __device__ __forceinline__ void lane_candidate(uint32_t stage, int32_t t0, int32
     }
   }
   GSAMPLE_COUNT(ck < 0 ? 0 : 1);
-  if (ck < 0) return;
+  if (ck < 0) return false;
   const uint4 ru = lds128(stage + (uint32_t)(ck * 32 + lane) * 16u);
   int ce = C::kEPU - 1;
 #pragma unroll
@@ -576,7 +614,11 @@ __device__ __forceinline__ void lane_candidate(uint32_t stage, int32_t t0, int32
     if (unit_elt<DT, VEC>(ru, e) == cm) ce = e;
   const int32_t i = (t0 + ck * 32 + lane) * C::kEPU + ce;
   const uint4 blk = philox_row_1((uint32_t)i >> 2, rc.ph);
+  if constexpr (CON && !C::kF32Bits) {
+    if ((touched >> (8 * ck + ce)) & 1ull) cm = exact_touched<DT>(ec.row, i, ec.c);
+  }
   take_better(exact_score(cm, word_of(blk, i & 3), rc.T), i, bs, bi);
+  return true;
 }
 
 // Warp-uniform cursor over this warp's tiles: row b, row-local units
@@ -652,6 +694,114 @@ __device__ __forceinline__ void issue_tile(const SampleParams& p, const TileCurs
   cp_async_commit();
 }
 
+// The mask and touched bits of a lane's units of a tile, one byte a unit.
+struct TileBits {
+  uint64_t allowed, touched;
+};
+
+// The same, as loaded for the tile after next: raw bytes, one register each,
+// so that nothing waits for them before they are packed.
+struct RawBits {
+  uint32_t allowed[kVPT], touched[kVPT];
+};
+
+template <int DT, bool VEC>
+__device__ __forceinline__ void load_bits(const TileCursor& c, const uint8_t* mask,
+                                          const uint8_t* touched, RawBits& r) {
+  constexpr int EPU = Cfg<DT, VEC>::kEPU;
+  static_assert(kVPT == 8, "eight units a lane: one byte each of a 64-bit word");
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < kVPT; ++k) {
+    const int32_t u = c.t0 + k * 32 + lane;
+    const bool in = c.valid && u < c.t_hi;
+    r.allowed[k] = !in ? 0u : mask ? (uint32_t)__ldcg(mask + (u * EPU >> 3)) : 0xFFu;
+    r.touched[k] = in && touched ? (uint32_t)__ldcg(touched + (u * EPU >> 3)) : 0u;
+  }
+}
+
+template <int DT, bool VEC>
+__device__ __forceinline__ TileBits pack_bits(const TileCursor& c, const RawBits& r) {
+  constexpr int EPU = Cfg<DT, VEC>::kEPU;
+  const int lane = threadIdx.x & 31;
+  TileBits b{0ull, 0ull};
+#pragma unroll
+  for (int k = 0; k < kVPT; ++k) {
+    uint32_t m = r.allowed[k], t = r.touched[k];
+    if constexpr (EPU == 4) {  // two units a byte
+      const int sh = ((c.t0 + k * 32 + lane) & 1) * 4;
+      m = (m >> sh) & 0xFu;
+      t = (t >> sh) & 0xFu;
+    }
+    b.allowed |= (uint64_t)m << (8 * k);
+    b.touched |= (uint64_t)(t & m) << (8 * k);
+  }
+  return b;
+}
+
+// issue_tile for constrained rows: units that the mask leaves nothing of are
+// not read, and a tile of such units alone is not even written to the stage.
+template <int DT, bool VEC>
+__device__ __forceinline__ void issue_tile_masked(const SampleParams& p, const TileCursor& c,
+                                                  uint64_t allowed, uint32_t stage,
+                                                  uint64_t pol) {
+  using C = Cfg<DT, VEC>;
+  if (__any_sync(0xFFFFFFFFu, allowed != 0ull)) {
+    const int lane = threadIdx.x & 31;
+    const char* row = p.logits + c.b * p.ld_bytes;
+#pragma unroll
+    for (int k = 0; k < kVPT; ++k) {
+      const int32_t u = c.t0 + k * 32 + lane;
+      const uint32_t dst = stage + (uint32_t)(k * 32 + lane) * 16u;
+      if (((allowed >> (8 * k)) & 0xFFull) == 0ull) {  // masked, or past the tile
+        sts128(dst, empty_unit<DT, VEC>());
+      } else if (VEC && (u + 1) * C::kEPU <= p.V) {
+        cp_async16(dst, row + (size_t)u * 16, pol);
+      } else {
+        sts128(dst, load_unit_sync<DT, VEC>(row, u, p.V));
+      }
+    }
+  }
+  cp_async_commit();
+}
+
+// The constraints of a landed tile, in place (see gsample_constrain.cuh).
+template <int DT, bool VEC>
+__device__ __forceinline__ void constrain_tile(uint32_t stage, int32_t t0, const TileBits& b,
+                                               const RowConstraints& rc, bool sampled, float& bs,
+                                               int32_t& bi) {
+  using C = Cfg<DT, VEC>;
+  const int lane = threadIdx.x & 31;
+  constexpr uint32_t kFull = (1u << C::kEPU) - 1u;
+  apply_touched<DT, C::kF32Bits, C::kEPU, 32>(stage + (uint32_t)lane * 16u, t0 + lane, b.touched,
+                                              rc, sampled, bs, bi);
+#pragma unroll
+  for (int k = 0; k < kVPT; ++k) {
+    const uint32_t m = (uint32_t)(b.allowed >> (8 * k)) & 0xFFu;
+    if (m != kFull && m != 0u) {  // 0: the unit was never read and holds -inf
+      const uint32_t a = stage + (uint32_t)(k * 32 + lane) * 16u;
+      sts128(a, masked_unit<DT, C::kF32Bits>(lds128(a), m));
+    }
+  }
+  __syncwarp();  // other lanes read the units
+}
+
+// Greedy over a constrained tile: the running best may already hold a touched
+// element of a higher index, so equal values compare indexes.
+template <int DT, bool VEC>
+__device__ __forceinline__ void greedy_unit_constrained(const uint4& r, int32_t u, float& bs,
+                                                        int32_t& bi) {
+  using C = Cfg<DT, VEC>;
+  const float m = unit_max<DT, VEC>(r);
+  if (m >= bs) {
+    int32_t e_first = C::kEPU - 1;
+#pragma unroll
+    for (int e = C::kEPU - 1; e >= 0; --e)
+      if (unit_elt<DT, VEC>(r, e) == m) e_first = e;
+    take_better(m, u * C::kEPU + e_first, bs, bi);
+  }
+}
+
 __device__ __forceinline__ float warp_max_f32(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
@@ -682,8 +832,12 @@ __device__ __forceinline__ int64_t split_point(const SampleParams& p, int64_t w)
   return b * NU + (la > 0 ? la : 0);
 }
 
-template <int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM) sample_kernel(const SampleParams p) {
+template <bool CON>
+using KernelParams = typename std::conditional<CON, ConSampleParams, SampleParams>::type;
+
+template <int DT, bool VEC, bool CON>
+__global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
+    sample_kernel(const KernelParams<CON> p) {
   using C = Cfg<DT, VEC>;
   extern __shared__ __align__(16) unsigned char smem[];
   pdl_wait_then_release();
@@ -702,10 +856,35 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM) sample_kern
   // Prologue: the first kStages - 1 tiles go in flight.
   TileCursor cur = segment_at(u_begin / NU, u_begin, u_end, NU, C::kTile);
   TileCursor ahead = cur;
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) {
-    issue_tile<DT, VEC>(p, ahead, ring + s * C::kTileBytes, pol);
+  // Constrained rows: the bits of the current tile and of the one in flight,
+  // the raw bytes of the one after (its units are requested by them), and the
+  // rows those belong to.
+  [[maybe_unused]] TileBits bits{0ull, 0ull}, bits_ahead{0ull, 0ull};
+  [[maybe_unused]] RawBits raw;
+  [[maybe_unused]] const uint8_t *mask_ahead = nullptr, *touched_ahead = nullptr;
+  [[maybe_unused]] ExactCtx<CON> ec;
+  if constexpr (CON) {
+    static_assert(kStages == 2, "one tile in flight: its bits are bits_ahead");
+    ec.row = p.logits + cur.b * p.ld_bytes;
+    ec.c = row_constraints(p.con, cur.b);
+    mask_ahead = ec.c.mask;
+    touched_ahead = ec.c.touched;
+    load_bits<DT, VEC>(ahead, mask_ahead, touched_ahead, raw);
+    bits_ahead = pack_bits<DT, VEC>(ahead, raw);
+    issue_tile_masked<DT, VEC>(p, ahead, bits_ahead.allowed, ring, pol);
     ahead = next_tile<C::kTile>(ahead, u_end, NU);
+    if (ahead.valid && ahead.b != cur.b) {
+      const RowConstraints n = row_constraints(p.con, ahead.b);
+      mask_ahead = n.mask;
+      touched_ahead = n.touched;
+    }
+    load_bits<DT, VEC>(ahead, mask_ahead, touched_ahead, raw);
+  } else {
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+      issue_tile<DT, VEC>(p, ahead, ring + s * C::kTileBytes, pol);
+      ahead = next_tile<C::kTile>(ahead, u_end, NU);
+    }
   }
 
   RowCtx rc = row_context(p, cur.b);
@@ -737,16 +916,42 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM) sample_kern
     // Refill the ring slot that the previous tile freed.
     int fill = slot + kStages - 1;
     if (fill >= kStages) fill -= kStages;
-    issue_tile<DT, VEC>(p, ahead, ring + fill * C::kTileBytes, pol);
-    ahead = next_tile<C::kTile>(ahead, u_end, NU);
+    if constexpr (CON) {
+      bits = bits_ahead;
+      bits_ahead = pack_bits<DT, VEC>(ahead, raw);
+      issue_tile_masked<DT, VEC>(p, ahead, bits_ahead.allowed, ring + fill * C::kTileBytes, pol);
+      const int64_t row = ahead.b;
+      ahead = next_tile<C::kTile>(ahead, u_end, NU);
+      if (ahead.valid && ahead.b != row) {
+        const RowConstraints n = row_constraints(p.con, ahead.b);
+        mask_ahead = n.mask;
+        touched_ahead = n.touched;
+      }
+      load_bits<DT, VEC>(ahead, mask_ahead, touched_ahead, raw);
+    } else {
+      issue_tile<DT, VEC>(p, ahead, ring + fill * C::kTileBytes, pol);
+      ahead = next_tile<C::kTile>(ahead, u_end, NU);
+    }
 
     const int32_t t0 = cur.t0, t_hi = cur.t_hi;
+    bool left = true;  // constrained rows: whether the tile may hold a candidate
+    if constexpr (CON) {
+      left = __any_sync(0xFFFFFFFFu, bits.allowed != 0ull);
+      if (left) constrain_tile<DT, VEC>(stage, t0, bits, ec.c, rc.T > 0.0f, bs, bi);
+    }
     if (rc.T > 0.0f) {
-      if (seg_first) {
-        lane_candidate<DT, VEC>(stage, t0, t_hi, rc, bs, bi);
-        seen = 0u;
-      } else {
-        seen = pending;
+      seen = seg_first ? 0u : pending;
+      // The first bound of the row's part: each lane's best of the first tile
+      // (for constrained rows, of the first tile that holds any candidate).
+      bool first = seg_first;
+      if constexpr (CON) {
+        const bool known = __any_sync(0xFFFFFFFFu, bi != INT32_MAX || seen != 0u);
+        first = left && (seg_first || !known);
+      }
+      if (first) {
+        const bool found =
+            lane_candidate<DT, VEC>(stage, t0, t_hi, rc, bs, bi, bits.touched, ec);
+        if constexpr (CON) left = __any_sync(0xFFFFFFFFu, found);
       }
       pending = __ldcg(&rc.ws->hint);
       // The best exact score this warp knows; publish it (fire-and-forget) if
@@ -757,13 +962,19 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM) sample_kern
       const float L = fmaxf(wbest, score_of_hint(seen));
       const Prune pr = make_prune(L, rc.T);
       pr_last = pr;
-      sampled_tile<DT, VEC>(stage, (uint32_t)t0 * C::kGPU, rc, pr, rbase,
-                            reinterpret_cast<unsigned short*>(rbase + kRareBytes), rcnt, bs, bi);
-    } else {
+      if (left)
+        sampled_tile<DT, VEC>(stage, (uint32_t)t0 * C::kGPU, rc, pr, rbase,
+                              reinterpret_cast<unsigned short*>(rbase + kRareBytes), rcnt, bs, bi,
+                              ec);
+    } else if (left) {
 #pragma unroll
       for (int k = 0; k < kVPT; ++k) {
         const int32_t u = t0 + k * 32 + lane;
-        greedy_unit<DT, VEC>(lds128(stage + (uint32_t)(k * 32 + lane) * 16u), u, bs, bi);
+        const uint4 r = lds128(stage + (uint32_t)(k * 32 + lane) * 16u);
+        if constexpr (CON)
+          greedy_unit_constrained<DT, VEC>(r, u, bs, bi);
+        else
+          greedy_unit<DT, VEC>(r, u, bs, bi);
       }
     }
     __syncwarp();  // every lane is done with this stage before it is refilled
@@ -777,7 +988,7 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM) sample_kern
       // to the row's ticket; the warp that brings the count to NU writes the
       // answer and clears the row's slot (checked one tile later).
       if (rcnt > 0) {
-        flush_rare<DT, VEC>(rbase, rcnt, rc, pr_last, bs, bi);
+        flush_rare<DT, VEC>(rbase, rcnt, rc, pr_last, bs, bi, ec);
         rcnt = 0;
       }
       warp_argmax(bs, bi);
@@ -792,6 +1003,10 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM) sample_kern
       cur = next_tile<C::kTile>(cur, u_end, NU);
       if (!cur.valid) break;
       rc = row_context_from(p, cur.b, next_params);
+      if constexpr (CON) {
+        ec.row = p.logits + cur.b * p.ld_bytes;
+        ec.c = row_constraints(p.con, cur.b);
+      }
       next_params = load_row_params(p, cur.b + 1);
       bs = -INFINITY;
       bi = INT32_MAX;
@@ -807,19 +1022,34 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM) sample_kern
 }
 
 template <int DT, bool VEC>
-void* kernel_ptr() {
-  return reinterpret_cast<void*>(&sample_kernel<DT, VEC>);
+void* kernel_ptr(bool constrained) {
+  return constrained ? reinterpret_cast<void*>(&sample_kernel<DT, VEC, true>)
+                     : reinterpret_cast<void*>(&sample_kernel<DT, VEC, false>);
 }
 
-void* select_kernel(int dtype, bool vec) {
+void* select_kernel(int dtype, bool vec, bool constrained) {
   switch (dtype * 2 + (vec ? 1 : 0)) {
-    case 0: return kernel_ptr<0, false>();
-    case 1: return kernel_ptr<0, true>();
-    case 2: return kernel_ptr<1, false>();
-    case 3: return kernel_ptr<1, true>();
-    case 4: return kernel_ptr<2, false>();
-    default: return kernel_ptr<2, true>();
+    case 0: return kernel_ptr<0, false>(constrained);
+    case 1: return kernel_ptr<0, true>(constrained);
+    case 2: return kernel_ptr<1, false>(constrained);
+    case 3: return kernel_ptr<1, true>(constrained);
+    case 4: return kernel_ptr<2, false>(constrained);
+    default: return kernel_ptr<2, true>(constrained);
   }
+}
+
+cudaError_t launch_kernel(void* fn, const SampleParams& p, void* param, int dtype, bool vec,
+                          cudaStream_t stream) {
+  void* args[] = {param};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sample_smem_bytes(dtype, vec);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
 }  // namespace
@@ -838,8 +1068,8 @@ size_t sample_smem_bytes(int dtype, bool vec) {
 // One-time per-device setup: raise the dynamic shared-memory limit of every
 // variant (a function attribute, so it is kept for the life of the context),
 // then report how many CTAs of the variant fit on one SM.
-int sample_ctas_per_sm(int dtype, bool vec) {
-  void* fn = select_kernel(dtype, vec);
+int sample_ctas_per_sm(int dtype, bool vec, bool constrained) {
+  void* fn = select_kernel(dtype, vec, constrained);
   const size_t smem = sample_smem_bytes(dtype, vec);
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
       cudaSuccess)
@@ -850,17 +1080,13 @@ int sample_ctas_per_sm(int dtype, bool vec) {
 }
 
 cudaError_t launch_sample(const SampleParams& p, int dtype, bool vec, cudaStream_t stream) {
-  void* fn = select_kernel(dtype, vec);
-  void* args[] = {const_cast<SampleParams*>(&p)};
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = sample_smem_bytes(dtype, vec);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1] = {pdl_attribute()};
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelExC(&cfg, fn, args);
+  return launch_kernel(select_kernel(dtype, vec, false), p, const_cast<SampleParams*>(&p), dtype,
+                       vec, stream);
+}
+
+cudaError_t launch_sample(const ConSampleParams& p, int dtype, bool vec, cudaStream_t stream) {
+  return launch_kernel(select_kernel(dtype, vec, true), p, const_cast<ConSampleParams*>(&p), dtype,
+                       vec, stream);
 }
 
 // ---------------------------------------------------------------------------

@@ -18,6 +18,9 @@
 
 #include <cstdint>
 
+#include <type_traits>
+
+#include "gsample_constrain.cuh"
 #include "gsample_internal.h"
 #include "gsample_slice.cuh"
 
@@ -61,6 +64,29 @@ __device__ __noinline__ RcBest rc_score_cold(uint32_t g, float x0, float x1, flo
   return RcBest{bs, bi};
 }
 
+// The same for a group of a constrained 16-bit row: its touched elements hold
+// bounds, and get their exact values first.
+template <int DT>
+__device__ __noinline__ RcBest rc_score_constrained(uint32_t g, float x0, float x1, float x2,
+                                                    float x3, uint4 w, Prune pr, ReachTest rt,
+                                                    float T, float bs, int32_t bi, const char* row,
+                                                    RowConstraints c) {
+  float x[4] = {x0, x1, x2, x3};
+  exact_group<DT>(g, x, row, c);
+  score_group(g, x[0], x[1], x[2], x[3], w, pr, rt, T, &bs, &bi);
+  return RcBest{bs, bi};
+}
+
+// Bytes of one bit row's words that cover a slice of `units` units, wherever
+// it starts.
+template <int DT, bool VEC>
+__host__ __device__ constexpr size_t slice_bit_bytes(int32_t units) {
+  return ((size_t)units * (VEC && DT != 0 ? 8 : 4) / 32 + 2) * 4;
+}
+
+template <bool CON>
+using RcKernelParams = typename std::conditional<CON, ConRowClusterParams, RowClusterParams>::type;
+
 // Block-wide (score, index) argmax as a packed key; every thread gets it.
 __device__ __forceinline__ unsigned long long rc_block_best(float s, int32_t i,
                                                             unsigned long long* red) {
@@ -73,8 +99,10 @@ __device__ __forceinline__ unsigned long long rc_block_best(float s, int32_t i,
   return k;
 }
 
-template <int DT, bool VEC, bool RESIDENT>
-__global__ void __launch_bounds__(kRcThreads, 1) sample_cluster_kernel(const RowClusterParams p) {
+template <int DT, bool VEC, bool RESIDENT, bool CON>
+__global__ void __launch_bounds__(kRcThreads, 1)
+    sample_cluster_kernel(const RcKernelParams<CON> p) {
+  static_assert(RESIDENT || !CON, "constrained slices are held on chip");
   using C = HCfg<DT, VEC>;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ unsigned long long s_red[kRcWarps];
@@ -127,7 +155,72 @@ __global__ void __launch_bounds__(kRcThreads, 1) sample_cluster_kernel(const Row
       cand_u = u;
     }
   };
-  if constexpr (RESIDENT) {
+  float bs = -INFINITY;
+  int32_t bi = INT32_MAX;
+  [[maybe_unused]] RowConstraints con;
+  [[maybe_unused]] const unsigned char* slice_touched = nullptr;  // byte of unit u at byte_of(u)
+  [[maybe_unused]] const int32_t w_lo = (int32_t)((int64_t)u_lo * C::kEPU >> 5);
+  [[maybe_unused]] auto byte_of = [&](int32_t u) { return (u * C::kEPU >> 3) - w_lo * 4; };
+  if constexpr (CON) {
+    // The slice and the words of its mask and touched bits are requested side
+    // by side; the words are shared by the CTA's threads.
+    for (int32_t u = u_lo + tid; u < u_hi; u += kRcThreads) {
+      const uint32_t dst = slice + (uint32_t)(u - u_lo) * 16u;
+      if (VEC && (u + 1) * C::kEPU <= p.V)
+        cp_async16(dst, row + (size_t)u * 16, pol);
+      else
+        sts128(dst, load_unit<DT, VEC>(row, u, p.V, pol));
+    }
+    cp_async_commit();
+    con = row_constraints(p.con, b);
+    unsigned char* mask_bytes = smem + (size_t)p.units_per_cta * 16;
+    unsigned char* touched_bytes = mask_bytes + slice_bit_bytes<DT, VEC>(p.units_per_cta);
+    slice_touched = touched_bytes;
+    if (u_lo < u_hi) {
+      const int64_t e_hi = (int64_t)u_hi * C::kEPU;
+      const int32_t words = (int32_t)(((e_hi < p.V ? e_hi : p.V) + 31) >> 5) - w_lo;
+      const uint32_t* mw = reinterpret_cast<const uint32_t*>(con.mask);
+      const uint32_t* tw = reinterpret_cast<const uint32_t*>(con.touched);
+#pragma unroll 4
+      for (int32_t w = tid; w < words; w += kRcThreads) {
+        const uint32_t m = mw ? __ldcg(mw + w_lo + w) : 0xFFFFFFFFu;
+        const uint32_t t = tw ? __ldcg(tw + w_lo + w) : 0u;
+        reinterpret_cast<uint32_t*>(mask_bytes)[w] = m;
+        reinterpret_cast<uint32_t*>(touched_bytes)[w] = t & m;
+      }
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    // Each thread constrains its own units, eight at a time, and takes their
+    // maxima.
+    for (int32_t u0 = u_lo + tid; u0 < u_hi; u0 += 8 * kRcThreads) {
+      constexpr uint32_t kFull = (1u << C::kEPU) - 1u;
+      uint64_t allowed = 0ull, touched = 0ull;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int32_t u = u0 + k * kRcThreads;
+        if (u >= u_hi) break;
+        const int sh = C::kEPU == 4 ? (u & 1) * 4 : 0;
+        allowed |= (uint64_t)((mask_bytes[byte_of(u)] >> sh) & kFull) << (8 * k);
+        touched |= (uint64_t)((touched_bytes[byte_of(u)] >> sh) & kFull) << (8 * k);
+      }
+      const uint32_t a0 = slice + (uint32_t)(u0 - u_lo) * 16u;
+      apply_touched<DT, C::kF32Bits, C::kEPU, kRcThreads>(a0, u0, touched, con, sampled, bs, bi);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int32_t u = u0 + k * kRcThreads;
+        if (u >= u_hi) break;
+        const uint32_t a = a0 + (uint32_t)(k * kRcThreads) * 16u;
+        const uint32_t m = (uint32_t)(allowed >> (8 * k)) & 0xFFu;
+        uint4 r = lds128(a);
+        if (m != kFull) {
+          r = masked_unit<DT, C::kF32Bits>(r, m);
+          sts128(a, r);
+        }
+        unit_max_of(u, r);
+      }
+    }
+  } else if constexpr (RESIDENT) {
     load_slice_then<DT, VEC, kRcThreads, GSAMPLE_RC_CHUNKS>(row, u_lo, u_hi, p.V, slice, pol,
                                                            unit_max_of);
   } else {
@@ -141,16 +234,25 @@ __global__ void __launch_bounds__(kRcThreads, 1) sample_cluster_kernel(const Row
       if (elt<DT, VEC>(r, e) == cand_x) cand_i = cand_u * C::kEPU + e;
   }
 
-  float bs = -INFINITY;
-  int32_t bi = INT32_MAX;
+  // Constrained slices without any candidate are not swept.
+  bool left = true;
+  if constexpr (CON) left = __syncthreads_or(cand_x > -INFINITY) != 0;
   if (!sampled) {
-    bs = cand_x;
-    bi = cand_x > -INFINITY ? cand_i : INT32_MAX;
-  } else {
+    if constexpr (CON) {
+      take_better(cand_x, cand_i, bs, bi);  // bs: touched elements of 16-bit units
+    } else {
+      bs = cand_x;
+      bi = cand_x > -INFINITY ? cand_i : INT32_MAX;
+    }
+  } else if (left) {
     const PhiloxRow ph = philox_row((uint32_t)b, (uint32_t)of, (uint32_t)(of >> 32), (uint32_t)sd,
                                     (uint32_t)(sd >> 32));
     if (cand_i != INT32_MAX && cand_x > -INFINITY) {
       const uint4 blk = philox_row_1((uint32_t)cand_i >> 2, ph);
+      if constexpr (CON && !C::kF32Bits) {
+        if ((slice_touched[byte_of(cand_u)] >> (cand_i - cand_u * C::kEPU)) & 1)
+          cand_x = exact_touched<DT>(row, cand_i, con);
+      }
       take_better(exact_score(cand_x, word_of(blk, cand_i & 3), T), cand_i, bs, bi);
     }
     const float L = score_of_key(rc_block_best(bs, bi, s_red));
@@ -199,7 +301,14 @@ __global__ void __launch_bounds__(kRcThreads, 1) sample_cluster_kernel(const Row
         if (ok[jj] && max_word(w[jj]) >= wt[jj]) {
           const uint4 rj = r[jj / C::kGPU];
           const int h = jj % C::kGPU;
-          if constexpr (DT != 0) {
+          if constexpr (CON && !C::kF32Bits) {
+            const RcBest sb = rc_score_constrained<DT>(
+                g[jj], elt<DT, VEC>(rj, 4 * h), elt<DT, VEC>(rj, 4 * h + 1),
+                elt<DT, VEC>(rj, 4 * h + 2), elt<DT, VEC>(rj, 4 * h + 3), w[jj], pr, rt, T, bs, bi,
+                row, con);
+            bs = sb.s;
+            bi = sb.i;
+          } else if constexpr (DT != 0) {
             // 16-bit rows: the exact scores out of line (measured faster at
             // B = 32-64); binary32 rows keep them inline (faster on the
             // small f32 sweeps).
@@ -234,7 +343,30 @@ __global__ void __launch_bounds__(kRcThreads, 1) sample_cluster_kernel(const Row
 
 template <int DT, bool VEC, bool RES>
 void* sk() {
-  return reinterpret_cast<void*>(&sample_cluster_kernel<DT, VEC, RES>);
+  return reinterpret_cast<void*>(&sample_cluster_kernel<DT, VEC, RES, false>);
+}
+
+template <int DT, bool VEC>
+void* sck() {
+  return reinterpret_cast<void*>(&sample_cluster_kernel<DT, VEC, true, true>);
+}
+
+void* select_rc_constrained(int dtype, bool vec) {
+  switch (dtype * 2 + (vec ? 1 : 0)) {
+    case 0: return sck<0, false>();
+    case 1: return sck<0, true>();
+    case 2: return sck<1, false>();
+    case 3: return sck<1, true>();
+    case 4: return sck<2, false>();
+    default: return sck<2, true>();
+  }
+}
+
+// Dynamic shared memory of a constrained CTA: its slice and two rows of bits.
+size_t con_smem_bytes(int dtype, bool vec, int32_t units) {
+  const size_t bits = vec && dtype != 0 ? slice_bit_bytes<1, true>(units)
+                                        : slice_bit_bytes<0, true>(units);
+  return (size_t)units * 16 + 2 * bits;
 }
 
 void* select_rc(int dtype, bool vec, bool resident) {
@@ -255,6 +387,9 @@ void* select_rc(int dtype, bool vec, bool resident) {
 }
 
 constexpr size_t kRcSmemLimit = 200 * 1024;
+// Slices of constrained rows: with two rows of bits (an eighth of the slice at
+// most) they stay within kRcSmemLimit.
+constexpr size_t kRcConSliceLimit = 176 * 1024;
 
 }  // namespace
 
@@ -265,9 +400,16 @@ void* rc_kernel(int dtype, bool vec, bool resident, int* threads) {
   return select_rc(dtype, vec, resident);
 }
 
-int rc_max_cluster(int dtype, bool vec) {
-  for (int res = 0; res < 2; ++res) {
-    void* fn = select_rc(dtype, vec, res != 0);
+size_t rc_con_slice_limit() { return kRcConSliceLimit; }
+
+void* rc_con_kernel(int dtype, bool vec, bool, int* threads) {
+  *threads = kRcThreads;
+  return select_rc_constrained(dtype, vec);
+}
+
+int rc_max_cluster(int dtype, bool vec, bool constrained) {
+  for (int res = constrained ? 1 : 0; res < 2; ++res) {
+    void* fn = constrained ? select_rc_constrained(dtype, vec) : select_rc(dtype, vec, res != 0);
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              res ? (int)kRcSmemLimit : 0) != cudaSuccess)
@@ -285,21 +427,19 @@ int rc_max_cluster(int dtype, bool vec) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int size = 0;
-  if (cudaOccupancyMaxPotentialClusterSize(&size, select_rc(dtype, vec, true), &cfg) !=
-      cudaSuccess)
-    return 0;
+  void* fn = constrained ? select_rc_constrained(dtype, vec) : select_rc(dtype, vec, true);
+  if (cudaOccupancyMaxPotentialClusterSize(&size, fn, &cfg) != cudaSuccess) return 0;
   return size;
 }
 
-cudaError_t launch_sample_cluster(const RowClusterParams& p, int dtype, bool vec,
-                                  cudaStream_t stream) {
-  const size_t need = (size_t)p.units_per_cta * 16;
-  const bool resident = need <= kRcSmemLimit;
-  void* fn = select_rc(dtype, vec, resident);
+namespace {
+
+cudaError_t launch_rc(void* fn, const RowClusterParams& p, void* param, size_t smem,
+                      cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.B * p.cluster));
   cfg.blockDim = dim3(kRcThreads);
-  cfg.dynamicSmemBytes = resident ? need : 0;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -309,8 +449,24 @@ cudaError_t launch_sample_cluster(const RowClusterParams& p, int dtype, bool vec
   attr[1] = pdl_attribute();
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  void* args[] = {const_cast<RowClusterParams*>(&p)};
+  void* args[] = {param};
   return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+}  // namespace
+
+cudaError_t launch_sample_cluster(const RowClusterParams& p, int dtype, bool vec,
+                                  cudaStream_t stream) {
+  const size_t need = (size_t)p.units_per_cta * 16;
+  const bool resident = need <= kRcSmemLimit;
+  return launch_rc(select_rc(dtype, vec, resident), p, const_cast<RowClusterParams*>(&p),
+                   resident ? need : 0, stream);
+}
+
+cudaError_t launch_sample_cluster(const ConRowClusterParams& p, int dtype, bool vec,
+                                  cudaStream_t stream) {
+  return launch_rc(select_rc_constrained(dtype, vec), p, const_cast<ConRowClusterParams*>(&p),
+                   con_smem_bytes(dtype, vec, p.units_per_cta), stream);
 }
 
 }  // namespace gsample
