@@ -140,20 +140,154 @@ __device__ __forceinline__ void store_one(char* row, int32_t i, float x) {
   }
 }
 
-template <int DT, int ODT>
+// The row kernel. Row b of the result is cut into units of N elements (N = 8
+// for 16-bit logits, 4 for binary32: 16 bytes of the logits) that start on
+// 16-byte boundaries of the RESULT, so that every full unit is stored with
+// 128-bit stores wherever the two rows start; the first and last unit may be
+// partial and go element by element. The logits of a full unit are one 128-bit
+// load where they are aligned too; otherwise the two aligned 16-byte pieces
+// that hold them, shifted together (both inside the row: units for which they
+// are not count as partial).
+//
+// Order of work in a thread: the mask and touched bits of its units, the units
+// that the mask leaves anything of (the others are never read), the masked
+// units' stores, and then the touched elements, four at a time, each written
+// over its place in the unit (the same thread wrote that, so the order holds).
+// In place, a unit is read and written only where the mask takes some but not
+// all of it, written only where it takes all, and touched elements are the only
+// traffic elsewhere.
+constexpr int kUnits = 4;  // units a thread
+
+__device__ __forceinline__ uint4 ld_unit(const char* p, uint64_t pol) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p), "l"(pol)
+               : "memory");
+  return v;
+}
+
+// 16 bytes at p, `a` (0 < a < 16) bytes past a 16-byte boundary.
+__device__ __forceinline__ uint4 ld_unit_shifted(const char* p, int a, uint64_t pol) {
+  const uint4 lo = ld_unit(p - a, pol), hi = ld_unit(p - a + 16, pol);
+  const int sh = (a & 3) * 8;
+  uint32_t w[5];
+  switch (a >> 2) {  // the same for a whole row
+    case 0: w[0] = lo.x; w[1] = lo.y; w[2] = lo.z; w[3] = lo.w; w[4] = hi.x; break;
+    case 1: w[0] = lo.y; w[1] = lo.z; w[2] = lo.w; w[3] = hi.x; w[4] = hi.y; break;
+    case 2: w[0] = lo.z; w[1] = lo.w; w[2] = hi.x; w[3] = hi.y; w[4] = hi.z; break;
+    default: w[0] = lo.w; w[1] = hi.x; w[2] = hi.y; w[3] = hi.z; w[4] = hi.w; break;
+  }
+  return make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
+                    __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
+}
+
+// The N bits of a bit row from bit e0 on; all of them lie inside the row.
+template <int N>
+__device__ __forceinline__ uint32_t bits_at(const uint8_t* bits, int32_t e0) {
+  const int sh = e0 & 7;
+  uint32_t v = __ldcg(bits + (e0 >> 3));
+  if (sh + N > 8) v |= (uint32_t)__ldcg(bits + (e0 >> 3) + 1) << 8;
+  return (v >> sh) & ((1u << N) - 1u);
+}
+
+template <int DT, int ODT, bool INPLACE>
 __global__ void __launch_bounds__(kConThreads) process_kernel(const ProcessParams p) {
+  constexpr int N = DT == 0 ? 4 : 8;
+  constexpr int ISZ = DT == 0 ? 4 : 2, OSZ = ODT == 0 ? 4 : 2;
+  constexpr uint32_t kFull = (1u << N) - 1u;
   pdl_wait_then_release();
-  const int64_t cpr = (p.V + kConThreads - 1) / kConThreads;
-  const bool inplace = p.inplace;
-  for (int64_t c = blockIdx.x; c < p.B * cpr; c += gridDim.x) {
-    const int64_t b = c / cpr;
-    const int64_t v = (c - b * cpr) * kConThreads + threadIdx.x;
-    if (v >= p.V) continue;
+  const uint64_t pol = evict_first_policy();
+  const int32_t V = (int32_t)p.V;
+  for (int64_t c = blockIdx.x; c < p.B * p.chunks_per_row; c += gridDim.x) {
+    const int64_t b = c / p.chunks_per_row;
+    const int32_t j0 = (int32_t)(c - b * p.chunks_per_row) * (kConThreads * kUnits) + threadIdx.x;
     const RowConstraints r = row_constraints(p.con, b);
-    const float x = load_one<DT>(p.logits + b * p.ld_bytes, (int32_t)v);
-    const float y = constrained_logit(x, (int32_t)v, r);
-    if (!inplace || __float_as_uint(x) != __float_as_uint(y))
-      store_one<ODT>(p.out + b * p.out_ld_bytes, (int32_t)v, y);
+    const char* in = p.logits + b * p.ld_bytes;
+    char* out = p.out + b * p.out_ld_bytes;
+    // Elements by which unit 0 starts before the row, and the misalignment of
+    // the logits of every unit.
+    const int32_t s = (int32_t)((uintptr_t)out & 15u) / OSZ;
+    const int a = (int)(((uintptr_t)in - (uintptr_t)(s * ISZ)) & 15u);
+    // Full units start in [lo, hi]: all N elements lie in the row, and every
+    // byte that is loaded for them (a multiple of ISZ before and after).
+    const int32_t lo = a / ISZ, hi = V - (a == 0 ? N : (32 - a) / ISZ);
+
+    int32_t e0[kUnits];
+    uint32_t allowed[kUnits], touched[kUnits];
+    bool full[kUnits];
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      // Past the row's last unit: V, which is neither full nor partial.
+      e0[k] = j0 + k * kConThreads < p.units_per_row ? (j0 + k * kConThreads) * N - s : V;
+      full[k] = e0[k] >= lo && e0[k] <= hi;
+      allowed[k] = full[k] ? (r.mask ? bits_at<N>(r.mask, e0[k]) : kFull) : 0u;
+      touched[k] = full[k] && r.touched ? bits_at<N>(r.touched, e0[k]) : 0u;
+    }
+    uint4 x[kUnits];
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      const char* q = in + (int64_t)e0[k] * ISZ;
+      if (allowed[k] != 0u && (!INPLACE || allowed[k] != kFull))
+        x[k] = a == 0 ? ld_unit(q, pol) : ld_unit_shifted(q, a, pol);
+    }
+    uint32_t todo = 0u;  // N bits a unit
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      if (!full[k]) continue;
+      todo |= (touched[k] & allowed[k]) << (N * k);
+      if (INPLACE && allowed[k] == kFull) continue;
+      const uint4 y = masked_unit<DT, DT == 0>(x[k], allowed[k]);
+      uint4* dst = reinterpret_cast<uint4*>(out + (int64_t)e0[k] * OSZ);
+      if constexpr (DT != 0 && ODT == 0) {
+        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[2 * i] = half_to_f32<DT>(w[i] & 0xFFFFu);
+          f[2 * i + 1] = half_to_f32<DT>(w[i] >> 16);
+        }
+        dst[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                            __float_as_uint(f[3]));
+        dst[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
+                            __float_as_uint(f[7]));
+      } else {
+        dst[0] = y;
+      }
+    }
+    static_assert(N * kUnits <= 32, "a thread's touched bits fit in one word");
+    while (todo != 0u) {
+      constexpr int M = 4;
+      int32_t v[M];
+      uint32_t h[M];
+      float bias[M], l[M];
+      bool on[M];
+#pragma unroll
+      for (int q = 0; q < M; ++q) {
+        on[q] = todo != 0u;
+        const int j = on[q] ? __ffs((int)todo) - 1 : 0;
+        todo &= todo - 1u;  // 0 stays 0
+        v[q] = (j0 + (j / N) * kConThreads) * N - s + j % N;
+        h[q] = on[q] ? __ldcg(r.history + v[q]) : 0u;
+        bias[q] = on[q] && r.bias ? __ldcg(r.bias + v[q]) : 0.0f;
+        l[q] = on[q] ? load_one<DT>(in, v[q]) : 0.0f;
+      }
+#pragma unroll
+      for (int q = 0; q < M; ++q)
+        if (on[q]) store_one<ODT>(out, v[q], penalised(l[q], h[q], bias[q], r));
+    }
+    // The partial units at the row's ends.
+#pragma unroll 1
+    for (int k = 0; k < kUnits; ++k) {
+      if (j0 + k * kConThreads >= p.units_per_row) break;
+      const int32_t e = (j0 + k * kConThreads) * N - s;
+      if (e >= lo && e <= hi) continue;
+      for (int32_t v = e < 0 ? 0 : e; v < e + N && v < V; ++v) {
+        const float l = load_one<DT>(in, v);
+        const float y = constrained_logit(l, v, r);
+        if (!INPLACE || __float_as_uint(l) != __float_as_uint(y)) store_one<ODT>(out, v, y);
+      }
+    }
   }
 }
 
@@ -198,16 +332,22 @@ cudaError_t launch_bias_set(const StateArgs& s, const int32_t* slot, int64_t n,
   return launch(bias_set_kernel, n, 32, stream, s, slot, tokens, values, total, offsets);
 }
 
-cudaError_t launch_process(const ProcessParams& p, int dtype, int out_dtype, int sms,
-                           cudaStream_t stream) {
-  const int64_t cpr = (p.V + kConThreads - 1) / kConThreads;
-  const int64_t blocks = blocks_for(p.B * cpr, 1, (int64_t)sms * 8);
-  switch (dtype * 2 + (out_dtype == 0 ? 0 : 1)) {
-    case 0: return launch(process_kernel<0, 0>, blocks, kConThreads, stream, p);
-    case 2: return launch(process_kernel<1, 0>, blocks, kConThreads, stream, p);
-    case 3: return launch(process_kernel<1, 1>, blocks, kConThreads, stream, p);
-    case 4: return launch(process_kernel<2, 0>, blocks, kConThreads, stream, p);
-    default: return launch(process_kernel<2, 2>, blocks, kConThreads, stream, p);
+cudaError_t launch_process(ProcessParams p, int dtype, int out_dtype, cudaStream_t stream) {
+  // One unit more than the elements need: the first may start before the row.
+  const int64_t n = dtype == 0 ? 4 : 8;
+  const int64_t units = (p.V + n - 1) / n + 1;
+  p.units_per_row = (int32_t)units;
+  p.chunks_per_row = (units + kConThreads * kUnits - 1) / (kConThreads * kUnits);
+  const int64_t blocks = blocks_for(p.B * p.chunks_per_row, 1, INT32_MAX);
+  switch (dtype * 4 + (out_dtype == 0 ? 0 : 2) + (p.inplace ? 1 : 0)) {
+    case 0: return launch(process_kernel<0, 0, false>, blocks, kConThreads, stream, p);
+    case 1: return launch(process_kernel<0, 0, true>, blocks, kConThreads, stream, p);
+    case 4: return launch(process_kernel<1, 0, false>, blocks, kConThreads, stream, p);
+    case 6: return launch(process_kernel<1, 1, false>, blocks, kConThreads, stream, p);
+    case 7: return launch(process_kernel<1, 1, true>, blocks, kConThreads, stream, p);
+    case 8: return launch(process_kernel<2, 0, false>, blocks, kConThreads, stream, p);
+    case 10: return launch(process_kernel<2, 2, false>, blocks, kConThreads, stream, p);
+    default: return launch(process_kernel<2, 2, true>, blocks, kConThreads, stream, p);
   }
 }
 
