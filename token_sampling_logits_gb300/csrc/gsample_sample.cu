@@ -307,16 +307,6 @@ __device__ __forceinline__ void raw_values(const RareRaw<DT, VEC>& r, float x[4]
   }
 }
 
-// What the exact pass needs besides the list: nothing, or, for constrained rows
-// of 16-bit units (whose touched elements hold bounds), the row.
-template <bool CON>
-struct ExactCtx {};
-template <>
-struct ExactCtx<true> {
-  const char* row;
-  RowConstraints c;
-};
-
 // Score the listed groups exactly (one per lane) against the current bound.
 // Out of line: it runs once per 32 listed groups, and keeping its logarithms
 // out of the tile loop keeps that loop's code small.
@@ -342,33 +332,10 @@ __device__ __noinline__ Best flush_rare_cold(const unsigned char* rbase, int rcn
   return Best{bs, bi};
 }
 
-template <int DT>
-__device__ __noinline__ Best flush_rare_constrained(const unsigned char* rbase, int rcnt, float T,
-                                                    float rT, PhiloxRow ph, Prune pr, float bs,
-                                                    int32_t bi, ExactCtx<true> ec) {
-  const int lane = threadIdx.x & 31;
-  __syncwarp();
-  if (lane < rcnt) {
-    const uint32_t g = reinterpret_cast<const uint32_t*>(rbase)[lane];
-    float x[4];
-    raw_values<DT, true>(reinterpret_cast<const RareRaw<DT, true>*>(rbase + kRareRawOff)[lane], x);
-    exact_group<DT>(g, x, ec.row, ec.c);
-    const uint4 w = philox_row_1(g, ph);
-    score_group(g, x[0], x[1], x[2], x[3], w, pr, make_reach(pr, rT), T, &bs, &bi);
-  }
-  __syncwarp();
-  return Best{bs, bi};
-}
-
-template <int DT, bool VEC, bool CON>
+template <int DT, bool VEC>
 __device__ __forceinline__ void flush_rare(const unsigned char* rbase, int rcnt, const RowCtx& rc,
-                                           const Prune& pr, float& bs, int32_t& bi,
-                                           const ExactCtx<CON>& ec) {
-  Best r;
-  if constexpr (CON && !Cfg<DT, VEC>::kF32Bits)
-    r = flush_rare_constrained<DT>(rbase, rcnt, rc.T, rc.rT, rc.ph, pr, bs, bi, ec);
-  else
-    r = flush_rare_cold<DT, VEC>(rbase, rcnt, rc.T, rc.rT, rc.ph, pr, bs, bi);
+                                           const Prune& pr, float& bs, int32_t& bi) {
+  const Best r = flush_rare_cold<DT, VEC>(rbase, rcnt, rc.T, rc.rT, rc.ph, pr, bs, bi);
   bs = r.s;
   bi = r.i;
 }
@@ -383,11 +350,11 @@ __device__ __forceinline__ uint32_t lane_group(int i, int lane) {
 // Groups whose word test passed join the rare list: one round per set bit of
 // the lane's `need` mask. Bit j stands for tile-local group q[j], or, with N ==
 // 0, for the lane's j-th group of the tile.
-template <int DT, bool VEC, int N, bool CON>
+template <int DT, bool VEC, int N>
 __device__ __forceinline__ void append_rare(uint32_t need, const uint32_t* q, uint32_t stage,
                                             uint32_t g0, const RowCtx& rc, const Prune& pr,
                                             unsigned char* rbase, int& rcnt, float& bs,
-                                            int32_t& bi, const ExactCtx<CON>& ec) {
+                                            int32_t& bi) {
   using C = Cfg<DT, VEC>;
   const int lane = threadIdx.x & 31;
   const unsigned lt_mask = (1u << lane) - 1u;
@@ -396,7 +363,7 @@ __device__ __forceinline__ void append_rare(uint32_t need, const uint32_t* q, ui
     const unsigned m = __ballot_sync(0xFFFFFFFFu, has);
     const int n = __popc(m);
     if (rcnt + n > kRareCap) {
-      flush_rare<DT, VEC>(rbase, rcnt, rc, pr, bs, bi, ec);
+      flush_rare<DT, VEC>(rbase, rcnt, rc, pr, bs, bi);
       rcnt = 0;
     }
     if (has) {
@@ -440,12 +407,12 @@ __device__ __forceinline__ float group_max_at(uint32_t stage, uint32_t q) {
 
 // One batch of the compacted list: entries [base, base + 32 * N) below cnt,
 // N Philox blocks per lane side by side.
-template <int DT, bool VEC, int N, bool CON>
+template <int DT, bool VEC, int N>
 __device__ __forceinline__ void compact_batch(uint32_t stage, const unsigned short* clist, int base,
                                               int cnt, uint32_t g0, const RowCtx& rc,
                                               const Prune& pr, const ReachTest& rt,
                                               unsigned char* rbase, int& rcnt, float& bs,
-                                              int32_t& bi, const ExactCtx<CON>& ec) {
+                                              int32_t& bi) {
   const int lane = threadIdx.x & 31;
   uint32_t q[N], g[N], wt[N];
   bool valid[N];
@@ -470,7 +437,7 @@ __device__ __forceinline__ void compact_batch(uint32_t stage, const unsigned sho
   uint32_t need = 0;
 #pragma unroll
   for (int j = 0; j < N; ++j) need |= (valid[j] && max_word(w[j]) >= wt[j]) ? (1u << j) : 0u;
-  append_rare<DT, VEC, N>(need, q, stage, g0, rc, pr, rbase, rcnt, bs, bi, ec);
+  append_rare<DT, VEC, N>(need, q, stage, g0, rc, pr, rbase, rcnt, bs, bi);
 }
 
 #ifndef GSAMPLE_DENSE_NUM
@@ -490,11 +457,11 @@ __device__ __forceinline__ void compact_batch(uint32_t stage, const unsigned sho
 // only they get Philox, 128 per warp batch (a short last batch runs one or two
 // blocks per lane). Either way the word test follows, and the rare groups that
 // pass it join the rare list.
-template <int DT, bool VEC, bool CON>
+template <int DT, bool VEC>
 __device__ __forceinline__ void sampled_tile(uint32_t stage, uint32_t g0, const RowCtx& rc,
                                              const Prune& pr, unsigned char* rbase,
                                              unsigned short* clist, int& rcnt, float& bs,
-                                             int32_t& bi, const ExactCtx<CON>& ec) {
+                                             int32_t& bi) {
   using C = Cfg<DT, VEC>;
   constexpr int NG = kVPT * C::kGPU;  // groups per lane in a tile
   static_assert(NG % 4 == 0 && NG <= 32, "groups per lane must fill four-way Philox batches");
@@ -547,7 +514,7 @@ __device__ __forceinline__ void sampled_tile(uint32_t stage, uint32_t g0, const 
 #pragma unroll
       for (int j = 0; j < 4; ++j) need |= max_word(w[j]) >= wt[b + j] ? (1u << (b + j)) : 0u;
     }
-    append_rare<DT, VEC, 0>(need, nullptr, stage, g0, rc, pr, rbase, rcnt, bs, bi, ec);
+    append_rare<DT, VEC, 0>(need, nullptr, stage, g0, rc, pr, rbase, rcnt, bs, bi);
     return;
   }
 
@@ -574,24 +541,21 @@ __device__ __forceinline__ void sampled_tile(uint32_t stage, uint32_t g0, const 
   for (int base = 0; base < cnt; base += 128) {
     const int r = cnt - base;
     if (r > 64) {
-      compact_batch<DT, VEC, 4>(stage, clist, base, cnt, g0, rc, pr, rt, rbase, rcnt, bs, bi, ec);
+      compact_batch<DT, VEC, 4>(stage, clist, base, cnt, g0, rc, pr, rt, rbase, rcnt, bs, bi);
     } else if (r > 32) {
-      compact_batch<DT, VEC, 2>(stage, clist, base, cnt, g0, rc, pr, rt, rbase, rcnt, bs, bi, ec);
+      compact_batch<DT, VEC, 2>(stage, clist, base, cnt, g0, rc, pr, rt, rbase, rcnt, bs, bi);
     } else {
-      compact_batch<DT, VEC, 1>(stage, clist, base, cnt, g0, rc, pr, rt, rbase, rcnt, bs, bi, ec);
+      compact_batch<DT, VEC, 1>(stage, clist, base, cnt, g0, rc, pr, rt, rbase, rcnt, bs, bi);
     }
   }
   __syncwarp();  // the list is read before the next tile rewrites it
 }
 
-// Phase A: this lane's largest logit of the tile, scored exactly. `touched`
-// marks the elements whose place in the tile holds a bound (bit 8 k + e:
-// element e of the lane's k-th unit); the result says whether the lane found
-// any candidate.
-template <int DT, bool VEC, bool CON>
+// Phase A: this lane's largest logit of the tile, scored exactly. Says whether
+// the lane found any candidate.
+template <int DT, bool VEC>
 __device__ __forceinline__ bool lane_candidate(uint32_t stage, int32_t t0, int32_t t_hi,
-                                               const RowCtx& rc, float& bs, int32_t& bi,
-                                               uint64_t touched, const ExactCtx<CON>& ec) {
+                                               const RowCtx& rc, float& bs, int32_t& bi) {
   using C = Cfg<DT, VEC>;
   const int lane = threadIdx.x & 31;
   float cm = -INFINITY;
@@ -614,9 +578,6 @@ __device__ __forceinline__ bool lane_candidate(uint32_t stage, int32_t t0, int32
     if (unit_elt<DT, VEC>(ru, e) == cm) ce = e;
   const int32_t i = (t0 + ck * 32 + lane) * C::kEPU + ce;
   const uint4 blk = philox_row_1((uint32_t)i >> 2, rc.ph);
-  if constexpr (CON && !C::kF32Bits) {
-    if ((touched >> (8 * ck + ce)) & 1ull) cm = exact_touched<DT>(ec.row, i, ec.c);
-  }
   take_better(exact_score(cm, word_of(blk, i & 3), rc.T), i, bs, bi);
   return true;
 }
@@ -694,96 +655,188 @@ __device__ __forceinline__ void issue_tile(const SampleParams& p, const TileCurs
   cp_async_commit();
 }
 
-// The mask and touched bits of a lane's units of a tile, one byte a unit.
-struct TileBits {
-  uint64_t allowed, touched;
-};
+// ---------------------------------------------------------------------------
+// Constrained rows. A tile's elements fall into three kinds by their mask and
+// touched bits: masked ones, which do not exist; touched ones, which wait in a
+// per-warp list with their logit, history word and bias until they are scored
+// one a lane; and the rest, which go through the tile as they are. Only the
+// last kind needs the stage: touched and masked places of it are set to -inf.
+// A tile with few elements left (a grammar that allows a few tokens) has all of
+// them listed and is not loaded at all.
+//
+// The list's three words an entry are gathered with cp.async, issued when the
+// tile has been swept and used after the next one, so no lane waits for them
+// but at the end of a row's part.
+//
+// Split points lie on multiples of 8 units of the row (32 or 64 elements), so a
+// tile's bits are whole words: lane l holds words l and, for 16-bit units (64
+// words a tile), l + 32.
+// ---------------------------------------------------------------------------
+constexpr int kListCap = 128;     // entries of a warp's list
+constexpr int kListFlush = 32;    // scored from this many on
+constexpr int kFewLeft = 64;      // a tile with at most this many elements left is listed whole
+constexpr int kConListBytes = kListCap * 16;  // element, logit word, history word, bias
 
-// The same, as loaded for the tile after next: raw bytes, one register each,
-// so that nothing waits for them before they are packed.
-struct RawBits {
-  uint32_t allowed[kVPT], touched[kVPT];
+struct TileWords {
+  uint32_t allowed[2], touched[2];  // touched: and allowed
 };
 
 template <int DT, bool VEC>
-__device__ __forceinline__ void load_bits(const TileCursor& c, const uint8_t* mask,
-                                          const uint8_t* touched, RawBits& r) {
+__device__ __forceinline__ TileWords load_words(const TileCursor& c, const uint8_t* mask,
+                                                const uint8_t* touched) {
   constexpr int EPU = Cfg<DT, VEC>::kEPU;
-  static_assert(kVPT == 8, "eight units a lane: one byte each of a 64-bit word");
+  constexpr int W = EPU / 4;  // words a lane
   const int lane = threadIdx.x & 31;
+  TileWords r;
+  r.allowed[1] = r.touched[1] = 0u;
 #pragma unroll
-  for (int k = 0; k < kVPT; ++k) {
-    const int32_t u = c.t0 + k * 32 + lane;
-    const bool in = c.valid && u < c.t_hi;
-    r.allowed[k] = !in ? 0u : mask ? (uint32_t)__ldcg(mask + (u * EPU >> 3)) : 0xFFu;
-    r.touched[k] = in && touched ? (uint32_t)__ldcg(touched + (u * EPU >> 3)) : 0u;
+  for (int i = 0; i < W; ++i) {
+    const int32_t w = c.t0 / (32 / EPU) + i * 32 + lane;
+    const bool in = c.valid && w < (c.t_hi + 32 / EPU - 1) / (32 / EPU);
+    r.allowed[i] = !in ? 0u
+                   : mask ? __ldcg(reinterpret_cast<const uint32_t*>(mask) + w)
+                          : 0xFFFFFFFFu;
+    r.touched[i] = in && touched ? __ldcg(reinterpret_cast<const uint32_t*>(touched) + w) : 0u;
+  }
+  return r;
+}
+
+// Elements left in a tile (masks aside, touched ones not counted).
+__device__ __forceinline__ int tile_left(const TileWords& w) {
+  return (int)__reduce_add_sync(0xFFFFFFFFu, __popc(w.allowed[0] & ~w.touched[0]) +
+                                                 __popc(w.allowed[1] & ~w.touched[1]));
+}
+
+// The bits of the lane's k-th unit (unit k * 32 + lane of the tile) in a tile's
+// words `w0` (words 0..31) and `w1` (32..63).
+template <int EPU>
+__device__ __forceinline__ uint32_t unit_of_words(uint32_t w0, uint32_t w1, int k, int lane) {
+  if constexpr (EPU == 8) {
+    const uint32_t w = __shfl_sync(0xFFFFFFFFu, k < 4 ? w0 : w1, (k * 8 + (lane >> 2)) & 31);
+    return (w >> ((lane & 3) * 8)) & 0xFFu;
+  } else {
+    const uint32_t w = __shfl_sync(0xFFFFFFFFu, w0, k * 4 + (lane >> 3));
+    return (w >> ((lane & 7) * 4)) & 0xFu;
   }
 }
 
-template <int DT, bool VEC>
-__device__ __forceinline__ TileBits pack_bits(const TileCursor& c, const RawBits& r) {
-  constexpr int EPU = Cfg<DT, VEC>::kEPU;
-  const int lane = threadIdx.x & 31;
-  TileBits b{0ull, 0ull};
-#pragma unroll
-  for (int k = 0; k < kVPT; ++k) {
-    uint32_t m = r.allowed[k], t = r.touched[k];
-    if constexpr (EPU == 4) {  // two units a byte
-      const int sh = ((c.t0 + k * 32 + lane) & 1) * 4;
-      m = (m >> sh) & 0xFu;
-      t = (t >> sh) & 0xFu;
-    }
-    b.allowed |= (uint64_t)m << (8 * k);
-    b.touched |= (uint64_t)(t & m) << (8 * k);
-  }
-  return b;
-}
-
-// issue_tile for constrained rows: units that the mask leaves nothing of are
-// not read, and a tile of such units alone is not even written to the stage.
+// issue_tile for constrained rows: units without an element left are not read.
 template <int DT, bool VEC>
 __device__ __forceinline__ void issue_tile_masked(const SampleParams& p, const TileCursor& c,
-                                                  uint64_t allowed, uint32_t stage,
+                                                  const TileWords& words, uint32_t stage,
                                                   uint64_t pol) {
   using C = Cfg<DT, VEC>;
-  if (__any_sync(0xFFFFFFFFu, allowed != 0ull)) {
-    const int lane = threadIdx.x & 31;
-    const char* row = p.logits + c.b * p.ld_bytes;
+  const int lane = threadIdx.x & 31;
+  const char* row = p.logits + c.b * p.ld_bytes;
+  const uint32_t w0 = words.allowed[0] & ~words.touched[0];
+  const uint32_t w1 = words.allowed[1] & ~words.touched[1];
 #pragma unroll
-    for (int k = 0; k < kVPT; ++k) {
-      const int32_t u = c.t0 + k * 32 + lane;
-      const uint32_t dst = stage + (uint32_t)(k * 32 + lane) * 16u;
-      if (((allowed >> (8 * k)) & 0xFFull) == 0ull) {  // masked, or past the tile
-        sts128(dst, empty_unit<DT, VEC>());
-      } else if (VEC && (u + 1) * C::kEPU <= p.V) {
-        cp_async16(dst, row + (size_t)u * 16, pol);
-      } else {
-        sts128(dst, load_unit_sync<DT, VEC>(row, u, p.V));
-      }
+  for (int k = 0; k < kVPT; ++k) {
+    const uint32_t m = unit_of_words<C::kEPU>(w0, w1, k, lane);
+    const int32_t u = c.t0 + k * 32 + lane;
+    const uint32_t dst = stage + (uint32_t)(k * 32 + lane) * 16u;
+    if (m == 0u || u >= c.t_hi) {
+      sts128(dst, empty_unit<DT, VEC>());
+    } else if (VEC && (u + 1) * C::kEPU <= p.V) {
+      cp_async16(dst, row + (size_t)u * 16, pol);
+    } else {
+      sts128(dst, load_unit_sync<DT, VEC>(row, u, p.V));
     }
   }
-  cp_async_commit();
 }
 
-// The constraints of a landed tile, in place (see gsample_constrain.cuh).
+// The masked and touched places of a landed tile become -inf.
 template <int DT, bool VEC>
-__device__ __forceinline__ void constrain_tile(uint32_t stage, int32_t t0, const TileBits& b,
-                                               const RowConstraints& rc, bool sampled, float& bs,
-                                               int32_t& bi) {
+__device__ __forceinline__ void clear_tile(uint32_t stage, const TileWords& words) {
   using C = Cfg<DT, VEC>;
   const int lane = threadIdx.x & 31;
   constexpr uint32_t kFull = (1u << C::kEPU) - 1u;
-  apply_touched<DT, C::kF32Bits, C::kEPU, 32>(stage + (uint32_t)lane * 16u, t0 + lane, b.touched,
-                                              rc, sampled, bs, bi);
+  const uint32_t w0 = words.allowed[0] & ~words.touched[0];
+  const uint32_t w1 = words.allowed[1] & ~words.touched[1];
+  if (__all_sync(0xFFFFFFFFu, w0 == 0xFFFFFFFFu && (C::kEPU == 4 || w1 == 0xFFFFFFFFu))) return;
 #pragma unroll
   for (int k = 0; k < kVPT; ++k) {
-    const uint32_t m = (uint32_t)(b.allowed >> (8 * k)) & 0xFFu;
-    if (m != kFull && m != 0u) {  // 0: the unit was never read and holds -inf
+    const uint32_t m = unit_of_words<C::kEPU>(w0, w1, k, lane);
+    if (m != kFull && m != 0u) {  // 0: the unit was not read and holds -inf
       const uint32_t a = stage + (uint32_t)(k * 32 + lane) * 16u;
       sts128(a, masked_unit<DT, C::kF32Bits>(lds128(a), m));
     }
   }
   __syncwarp();  // other lanes read the units
+}
+
+// The row of the listed elements.
+struct ListRow {
+  const char* row;
+  const uint32_t* history;  // nullptr: no state
+  const float* bias;
+  float rep, freq, pres;
+};
+
+// Scores the list, one element a lane at a time; every gather has landed.
+template <int DT>
+__device__ __noinline__ Best score_list(const uint32_t* list, int n, float T, float rT,
+                                        PhiloxRow ph, Prune pr, float bs, int32_t bi,
+                                        ListRow lr) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  const ReachTest rt = make_reach(pr, rT);
+  RowConstraints r;
+  r.rep = lr.rep;
+  r.freq = lr.freq;
+  r.pres = lr.pres;
+  for (int i = lane; i < n; i += 32) {
+    const int32_t v = (int32_t)list[i];
+    const uint32_t xw = list[kListCap + i];
+    float x;
+    if constexpr (DT == 0) {
+      x = __uint_as_float(xw);
+    } else {  // the half of the aligned word that holds the element
+      const bool high = ((uintptr_t)lr.row + 2u * (uint32_t)v) & 2u;
+      x = half_to_f32<DT>(high ? xw >> 16 : xw & 0xFFFFu);
+    }
+    if (lr.history)
+      x = penalised(x, list[2 * kListCap + i], __uint_as_float(list[3 * kListCap + i]), r);
+    if (!(T > 0.0f)) {
+      take_better(x, v, bs, bi);
+    } else if (x >= pr.thr_x) {  // not NaN
+      const uint32_t w = word_of(philox_row_1((uint32_t)v >> 2, ph), v & 3);
+      if (!pr.use_bound || may_reach(x, w, rt)) take_better(exact_score(x, w, T), v, bs, bi);
+    }
+  }
+  __syncwarp();  // before the list is refilled
+  return Best{bs, bi};
+}
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Requests entry s of the list: element v of the row.
+template <int DT>
+__device__ __forceinline__ void request_entry(uint32_t* list, int s, int32_t v,
+                                              const ListRow& lr, int32_t V) {
+  list[s] = (uint32_t)v;
+  uint32_t* xw = list + kListCap + s;
+  if constexpr (DT == 0) {
+    cp_async4(smem_addr(xw), lr.row + (size_t)v * 4);
+  } else {
+    const uintptr_t at = (uintptr_t)lr.row + 2u * (size_t)v;
+    const uintptr_t word = at & ~(uintptr_t)3;
+    // An aligned word that reaches past an end of the row is not read.
+    if (word >= (uintptr_t)lr.row && word + 4 <= (uintptr_t)lr.row + 2u * (size_t)V) {
+      cp_async4(smem_addr(xw), reinterpret_cast<const void*>(word));
+    } else {
+      *xw = (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(at)) * 0x10001u;
+    }
+  }
+  if (lr.history) {
+    cp_async4(smem_addr(list + 2 * kListCap + s), lr.history + v);
+    if (lr.bias)
+      cp_async4(smem_addr(list + 3 * kListCap + s), lr.bias + v);
+    else
+      list[3 * kListCap + s] = 0u;
+  }
 }
 
 // Greedy over a constrained tile: the running best may already hold a touched
@@ -821,12 +874,14 @@ __device__ __forceinline__ float score_of_hint(uint32_t h) {
 // lines: with ranges that split lines, both neighbours fetch the shared line,
 // and host reads measured a third slower. Device reads are unaffected.
 template <bool VEC>
-__device__ __forceinline__ int64_t split_point(const SampleParams& p, int64_t w) {
+__device__ __forceinline__ int64_t split_point(const SampleParams& p, int64_t w,
+                                               bool constrained = false) {
   const int64_t U = p.total_units, NW = p.warps;
   const int64_t base = U / NW, rem = U % NW;
   const int64_t u = w * base + (w < rem ? w : rem);
-  if (!VEC || u >= U) return u;
+  if ((!VEC && !constrained) || u >= U) return u;
   const int64_t NU = p.units_per_row, b = u / NU, l = u - b * NU;
+  if (constrained) return b * NU + (l & ~(int64_t)7);  // whole words of the row's bits
   const uint64_t row_unit = (uint64_t)(uintptr_t)(p.logits + b * p.ld_bytes) / 16u;
   const int64_t la = l - (int64_t)((row_unit + (uint64_t)l) & 7u);
   return b * NU + (la > 0 ? la : 0);
@@ -836,6 +891,11 @@ template <bool CON>
 using KernelParams = typename std::conditional<CON, ConSampleParams, SampleParams>::type;
 
 template <int DT, bool VEC, bool CON>
+__host__ __device__ constexpr int warp_bytes() {
+  return Cfg<DT, VEC>::kWarpBytes + (CON ? kConListBytes : 0);
+}
+
+template <int DT, bool VEC, bool CON>
 __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
     sample_kernel(const KernelParams<CON> p) {
   using C = Cfg<DT, VEC>;
@@ -843,42 +903,74 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
   pdl_wait_then_release();
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  unsigned char* wbase = smem + (size_t)warp * C::kWarpBytes;
+  unsigned char* wbase = smem + (size_t)warp * warp_bytes<DT, VEC, CON>();
   const uint32_t ring = smem_addr(wbase);
   const uint64_t pol = evict_first_policy();
 
   const int64_t NU = p.units_per_row, NW = p.warps;
   const int64_t gw = (int64_t)blockIdx.x * kWarps + warp;
   if (gw >= NW) return;
-  const int64_t u_begin = split_point<VEC>(p, gw), u_end = split_point<VEC>(p, gw + 1);
+  const int64_t u_begin = split_point<VEC>(p, gw, CON), u_end = split_point<VEC>(p, gw + 1, CON);
   if (u_begin >= u_end) return;  // no units (only with fewer than 8 units per warp)
 
   // Prologue: the first kStages - 1 tiles go in flight.
   TileCursor cur = segment_at(u_begin / NU, u_begin, u_end, NU, C::kTile);
   TileCursor ahead = cur;
-  // Constrained rows: the bits of the current tile and of the one in flight,
-  // the raw bytes of the one after (its units are requested by them), and the
-  // rows those belong to.
-  [[maybe_unused]] TileBits bits{0ull, 0ull}, bits_ahead{0ull, 0ull};
-  [[maybe_unused]] RawBits raw;
-  [[maybe_unused]] const uint8_t *mask_ahead = nullptr, *touched_ahead = nullptr;
-  [[maybe_unused]] ExactCtx<CON> ec;
-  if constexpr (CON) {
-    static_assert(kStages == 2, "one tile in flight: its bits are bits_ahead");
-    ec.row = p.logits + cur.b * p.ld_bytes;
-    ec.c = row_constraints(p.con, cur.b);
-    mask_ahead = ec.c.mask;
-    touched_ahead = ec.c.touched;
-    load_bits<DT, VEC>(ahead, mask_ahead, touched_ahead, raw);
-    bits_ahead = pack_bits<DT, VEC>(ahead, raw);
-    issue_tile_masked<DT, VEC>(p, ahead, bits_ahead.allowed, ring, pol);
-    ahead = next_tile<C::kTile>(ahead, u_end, NU);
-    if (ahead.valid && ahead.b != cur.b) {
-      const RowConstraints n = row_constraints(p.con, ahead.b);
-      mask_ahead = n.mask;
-      touched_ahead = n.touched;
+  // Constrained rows: the words of the current tile, of the one in flight and
+  // of the one after, and the bit rows that those of the last come from.
+  [[maybe_unused]] TileWords words, words_ahead, words_next;
+  [[maybe_unused]] bool dense = true, dense_ahead = true;
+  [[maybe_unused]] const uint8_t *mask_next = nullptr, *touched_next = nullptr;
+  [[maybe_unused]] ListRow lr;
+  [[maybe_unused]] uint32_t* list =
+      reinterpret_cast<uint32_t*>(wbase + C::kWarpBytes);
+  [[maybe_unused]] int listed = 0;
+  auto enter_row = [&](int64_t b) {
+    if constexpr (CON) {
+      const RowConstraints c = row_constraints(p.con, b);
+      lr.row = p.logits + b * p.ld_bytes;
+      lr.history = c.history;
+      lr.bias = c.bias;
+      lr.rep = c.rep;
+      lr.freq = c.freq;
+      lr.pres = c.pres;
     }
-    load_bits<DT, VEC>(ahead, mask_ahead, touched_ahead, raw);
+  };
+  auto next_words = [&](int64_t row_before) {
+    if constexpr (CON) {
+      if (ahead.valid && ahead.b != row_before) {
+        const RowConstraints c = row_constraints(p.con, ahead.b);
+        mask_next = c.mask;
+        touched_next = c.touched;
+      }
+      words_next = load_words<DT, VEC>(ahead, mask_next, touched_next);
+    }
+  };
+  // Requests the tile under `ahead`, whose words have arrived, then the words
+  // of the one after it.
+  auto advance = [&](uint32_t stage) {
+    if constexpr (CON) {
+      words_ahead = words_next;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int32_t in = p.V - (ahead.t0 * C::kEPU + i * 1024 + lane * 32);  // bits of the row
+        if (in < 32) words_ahead.allowed[i] &= in <= 0 ? 0u : (1u << in) - 1u;
+        words_ahead.touched[i] &= words_ahead.allowed[i];
+      }
+      dense_ahead = tile_left(words_ahead) > kFewLeft;
+      if (dense_ahead) issue_tile_masked<DT, VEC>(p, ahead, words_ahead, stage, pol);
+      cp_async_commit();
+      const int64_t row = ahead.b;
+      ahead = next_tile<C::kTile>(ahead, u_end, NU);
+      next_words(row);
+    }
+  };
+  if constexpr (CON) {
+    static_assert(kStages == 2, "one tile in flight: its words are words_ahead");
+    enter_row(cur.b);
+    next_words(-1);
+    advance(ring);
+    cp_async_commit();  // the place of the gathers' group, which the loop expects
   } else {
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) {
@@ -906,39 +998,37 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
   // tile that listed the last of them.
   unsigned char* rbase = wbase + kStages * C::kTileBytes;
   int rcnt = 0;
-  Prune pr_last{INFINITY, -INFINITY, false};
+  Prune pr_last{CON ? -INFINITY : INFINITY, -INFINITY, false};
+  auto flush_list = [&]() {
+    if constexpr (CON) {
+      const Best r = score_list<DT>(list, listed, rc.T, rc.rT, rc.ph, pr_last, bs, bi, lr);
+      bs = r.s;
+      bi = r.i;
+      listed = 0;
+    }
+  };
 
   while (true) {
     // The current tile has landed (this lane's copies, then everyone's).
-    cp_async_wait<kStages - 2>();
+    // Constrained rows: a group of gathers may still be on its way.
+    cp_async_wait<kStages - 2 + (CON ? 1 : 0)>();
     __syncwarp();
     const uint32_t stage = ring + slot * C::kTileBytes;
     // Refill the ring slot that the previous tile freed.
     int fill = slot + kStages - 1;
     if (fill >= kStages) fill -= kStages;
     if constexpr (CON) {
-      bits = bits_ahead;
-      bits_ahead = pack_bits<DT, VEC>(ahead, raw);
-      issue_tile_masked<DT, VEC>(p, ahead, bits_ahead.allowed, ring + fill * C::kTileBytes, pol);
-      const int64_t row = ahead.b;
-      ahead = next_tile<C::kTile>(ahead, u_end, NU);
-      if (ahead.valid && ahead.b != row) {
-        const RowConstraints n = row_constraints(p.con, ahead.b);
-        mask_ahead = n.mask;
-        touched_ahead = n.touched;
-      }
-      load_bits<DT, VEC>(ahead, mask_ahead, touched_ahead, raw);
+      words = words_ahead;
+      dense = dense_ahead;
+      advance(ring + fill * C::kTileBytes);
+      if (dense) clear_tile<DT, VEC>(stage, words);
     } else {
       issue_tile<DT, VEC>(p, ahead, ring + fill * C::kTileBytes, pol);
       ahead = next_tile<C::kTile>(ahead, u_end, NU);
     }
 
     const int32_t t0 = cur.t0, t_hi = cur.t_hi;
-    bool left = true;  // constrained rows: whether the tile may hold a candidate
-    if constexpr (CON) {
-      left = __any_sync(0xFFFFFFFFu, bits.allowed != 0ull);
-      if (left) constrain_tile<DT, VEC>(stage, t0, bits, ec.c, rc.T > 0.0f, bs, bi);
-    }
+    bool left = !CON || dense;  // whether the tile may hold a candidate
     if (rc.T > 0.0f) {
       seen = seg_first ? 0u : pending;
       // The first bound of the row's part: each lane's best of the first tile
@@ -949,8 +1039,8 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
         first = left && (seg_first || !known);
       }
       if (first) {
-        const bool found =
-            lane_candidate<DT, VEC>(stage, t0, t_hi, rc, bs, bi, bits.touched, ec);
+        [[maybe_unused]] const bool found =
+            lane_candidate<DT, VEC>(stage, t0, t_hi, rc, bs, bi);
         if constexpr (CON) left = __any_sync(0xFFFFFFFFu, found);
       }
       pending = __ldcg(&rc.ws->hint);
@@ -964,8 +1054,7 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
       pr_last = pr;
       if (left)
         sampled_tile<DT, VEC>(stage, (uint32_t)t0 * C::kGPU, rc, pr, rbase,
-                              reinterpret_cast<unsigned short*>(rbase + kRareBytes), rcnt, bs, bi,
-                              ec);
+                              reinterpret_cast<unsigned short*>(rbase + kRareBytes), rcnt, bs, bi);
     } else if (left) {
 #pragma unroll
       for (int k = 0; k < kVPT; ++k) {
@@ -977,6 +1066,34 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
           greedy_unit<DT, VEC>(r, u, bs, bi);
       }
     }
+    if constexpr (CON) {
+      // The elements listed before have landed (the tile in flight need not).
+      if (listed >= kListFlush) {
+        cp_async_wait<1>();
+        flush_list();
+      }
+      // This tile's listed elements.
+      uint32_t todo[2] = {dense ? words.touched[0] : words.allowed[0],
+                          dense ? words.touched[1] : words.allowed[1]};
+      const int32_t e0 = cur.t0 * C::kEPU + lane * 32;
+      while (__any_sync(0xFFFFFFFFu, (todo[0] | todo[1]) != 0u)) {
+        const bool has = (todo[0] | todo[1]) != 0u;
+        const unsigned m = __ballot_sync(0xFFFFFFFFu, has);
+        if (listed + __popc(m) > kListCap) {
+          cp_async_commit();
+          cp_async_wait<0>();
+          flush_list();
+        }
+        if (has) {
+          const int i = todo[0] != 0u ? 0 : 1;
+          const int32_t v = e0 + i * 1024 + __ffs((int)todo[i]) - 1;
+          todo[i] &= todo[i] - 1u;
+          request_entry<DT>(list, listed + __popc(m & ((1u << lane) - 1u)), v, lr, p.V);
+        }
+        listed += __popc(m);
+      }
+      cp_async_commit();
+    }
     __syncwarp();  // every lane is done with this stage before it is refilled
 
     if (lane == 0 && tk_pending) {
@@ -987,8 +1104,14 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
       // This warp's part of row b is done: merge its best, then add its units
       // to the row's ticket; the warp that brings the count to NU writes the
       // answer and clears the row's slot (checked one tile later).
+      if constexpr (CON) {
+        if (listed > 0) {
+          cp_async_wait<0>();
+          flush_list();
+        }
+      }
       if (rcnt > 0) {
-        flush_rare<DT, VEC>(rbase, rcnt, rc, pr_last, bs, bi, ec);
+        flush_rare<DT, VEC>(rbase, rcnt, rc, pr_last, bs, bi);
         rcnt = 0;
       }
       warp_argmax(bs, bi);
@@ -1004,8 +1127,8 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
       if (!cur.valid) break;
       rc = row_context_from(p, cur.b, next_params);
       if constexpr (CON) {
-        ec.row = p.logits + cur.b * p.ld_bytes;
-        ec.c = row_constraints(p.con, cur.b);
+        enter_row(cur.b);
+        pr_last = Prune{-INFINITY, -INFINITY, false};
       }
       next_params = load_row_params(p, cur.b + 1);
       bs = -INFINITY;
@@ -1038,13 +1161,13 @@ void* select_kernel(int dtype, bool vec, bool constrained) {
   }
 }
 
-cudaError_t launch_kernel(void* fn, const SampleParams& p, void* param, int dtype, bool vec,
+cudaError_t launch_kernel(void* fn, const SampleParams& p, void* param, size_t smem,
                           cudaStream_t stream) {
   void* args[] = {param};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = sample_smem_bytes(dtype, vec);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
@@ -1054,7 +1177,8 @@ cudaError_t launch_kernel(void* fn, const SampleParams& p, void* param, int dtyp
 
 }  // namespace
 
-size_t sample_smem_bytes(int dtype, bool vec) {
+size_t sample_smem_bytes(int dtype, bool vec, bool constrained) {
+  if (constrained) return sample_smem_bytes(dtype, vec, false) + (size_t)kWarps * kConListBytes;
   switch (dtype * 2 + (vec ? 1 : 0)) {
     case 0: return Cfg<0, false>::kSmem;
     case 1: return Cfg<0, true>::kSmem;
@@ -1070,7 +1194,7 @@ size_t sample_smem_bytes(int dtype, bool vec) {
 // then report how many CTAs of the variant fit on one SM.
 int sample_ctas_per_sm(int dtype, bool vec, bool constrained) {
   void* fn = select_kernel(dtype, vec, constrained);
-  const size_t smem = sample_smem_bytes(dtype, vec);
+  const size_t smem = sample_smem_bytes(dtype, vec, constrained);
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
       cudaSuccess)
     return 0;
@@ -1080,13 +1204,13 @@ int sample_ctas_per_sm(int dtype, bool vec, bool constrained) {
 }
 
 cudaError_t launch_sample(const SampleParams& p, int dtype, bool vec, cudaStream_t stream) {
-  return launch_kernel(select_kernel(dtype, vec, false), p, const_cast<SampleParams*>(&p), dtype,
-                       vec, stream);
+  return launch_kernel(select_kernel(dtype, vec, false), p, const_cast<SampleParams*>(&p),
+                       sample_smem_bytes(dtype, vec, false), stream);
 }
 
 cudaError_t launch_sample(const ConSampleParams& p, int dtype, bool vec, cudaStream_t stream) {
-  return launch_kernel(select_kernel(dtype, vec, true), p, const_cast<ConSampleParams*>(&p), dtype,
-                       vec, stream);
+  return launch_kernel(select_kernel(dtype, vec, true), p, const_cast<ConSampleParams*>(&p),
+                       sample_smem_bytes(dtype, vec, true), stream);
 }
 
 // ---------------------------------------------------------------------------
