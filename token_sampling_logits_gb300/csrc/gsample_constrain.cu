@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kConThreads) process_kernel(const ProcessParam
       }
 #pragma unroll
       for (int q = 0; q < M; ++q)
-        if (on[q]) store_one<ODT>(out, v[q], penalised(l[q], h[q], bias[q], r));
+        if (on[q]) store_one<ODT>(out, v[q], penalised(l[q], h[q], bias[q], r.pen));
     }
     // The partial units at the row's ends.
 #pragma unroll 1

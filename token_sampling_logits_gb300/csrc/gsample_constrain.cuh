@@ -38,14 +38,45 @@ struct ConstrainArgs {
   const int32_t* mask_row;
 };
 
-// One batch row's view of them; a null pointer means "none for this row".
+
+// The penalties of batch row b.
+struct RowPenalties {
+  float rep, freq, pres;
+};
+
+__device__ __forceinline__ RowPenalties row_penalties(const ConstrainArgs& c, int64_t b) {
+  RowPenalties r{1.0f, 0.0f, 0.0f};
+  if (c.repetition) {
+    const float v = __ldg(c.repetition + b);
+    if (v > 0.0f && v < INFINITY) r.rep = v;  // NaN, <= 0 and inf: no penalty
+  }
+  if (c.frequency) {
+    const float v = __ldg(c.frequency + b);
+    if (v == v) r.freq = v;
+  }
+  if (c.presence) {
+    const float v = __ldg(c.presence + b);
+    if (v == v) r.pres = v;
+  }
+  return r;
+}
+
+// One batch row's view of the constraints; a null pointer means "none for this
+// row".
 struct RowConstraints {
   const uint8_t* mask;
   const uint8_t* touched;
   const uint32_t* history;
   const float* bias;
-  float rep, freq, pres;
+  RowPenalties pen;
 };
+
+// The state row of batch row b, or -1.
+__device__ __forceinline__ int64_t state_row_of(const ConstrainArgs& c, int64_t b) {
+  if (!c.history) return -1;
+  const int64_t s = c.slot ? (int64_t)__ldg(c.slot + b) : b;
+  return s >= 0 && s < c.state_rows ? s : -1;
+}
 
 __device__ __forceinline__ RowConstraints row_constraints(const ConstrainArgs& c, int64_t b) {
   RowConstraints r;
@@ -53,39 +84,23 @@ __device__ __forceinline__ RowConstraints row_constraints(const ConstrainArgs& c
   r.touched = nullptr;
   r.history = nullptr;
   r.bias = nullptr;
-  r.rep = 1.0f;
-  r.freq = 0.0f;
-  r.pres = 0.0f;
   if (c.mask) {
     const int64_t m = c.mask_row ? (int64_t)__ldg(c.mask_row + b) : b;
     if (m >= 0 && m < c.mask_rows) r.mask = c.mask + m * c.mask_ld_bytes;
   }
-  if (c.history) {
-    const int64_t s = c.slot ? (int64_t)__ldg(c.slot + b) : b;
-    if (s >= 0 && s < c.state_rows) {
-      r.touched = c.touched + s * (c.state_ld / 8);
-      r.history = c.history + s * c.state_ld;
-      if (c.bias) r.bias = c.bias + s * c.state_ld;
-    }
-    if (c.repetition) {
-      const float v = __ldg(c.repetition + b);
-      if (v > 0.0f && v < INFINITY) r.rep = v;  // NaN, <= 0 and inf: no penalty
-    }
-    if (c.frequency) {
-      const float v = __ldg(c.frequency + b);
-      if (v == v) r.freq = v;
-    }
-    if (c.presence) {
-      const float v = __ldg(c.presence + b);
-      if (v == v) r.pres = v;
-    }
+  const int64_t s = state_row_of(c, b);
+  if (s >= 0) {
+    r.touched = c.touched + s * (c.state_ld / 8);
+    r.history = c.history + s * c.state_ld;
+    if (c.bias) r.bias = c.bias + s * c.state_ld;
   }
+  r.pen = row_penalties(c, b);
   return r;
 }
 
 // Logit x of a touched token with history word h and bias `bias`.
 __device__ __forceinline__ float penalised(float x, uint32_t h, float bias,
-                                           const RowConstraints& r) {
+                                           const RowPenalties& r) {
   if (x == -INFINITY) return x;
   float y = __fadd_rn(x, bias);
   if (h != 0u) y = y > 0.0f ? __fdiv_rn(y, r.rep) : __fmul_rn(y, r.rep);
@@ -169,9 +184,9 @@ __device__ __forceinline__ void apply_touched(uint32_t a0, int32_t u0, uint64_t 
     for (int q = 0; q < N; ++q) {
       if (!on[q]) continue;
       if constexpr (F32BITS) {
-        sts_f32(at[q], penalised(lds_f32(at[q]), h[q], b[q], r));
+        sts_f32(at[q], penalised(lds_f32(at[q]), h[q], b[q], r.pen));
       } else {
-        const float y = penalised(half_to_f32<DT>(lds_u16(at[q])), h[q], b[q], r);
+        const float y = penalised(half_to_f32<DT>(lds_u16(at[q])), h[q], b[q], r.pen);
         if (sampled) {
           sts_u16(at[q], bound_bits<DT>(y));
         } else {
@@ -206,7 +221,17 @@ template <int DT>
 __device__ __forceinline__ float exact_touched(const char* row, int32_t v,
                                                const RowConstraints& r) {
   const float x = half_to_f32<DT>(__ldg(reinterpret_cast<const unsigned short*>(row) + v));
-  return penalised(x, __ldcg(r.history + v), r.bias ? __ldcg(r.bias + v) : 0.0f, r);
+  return penalised(x, __ldcg(r.history + v), r.bias ? __ldcg(r.bias + v) : 0.0f, r.pen);
+}
+
+// The value of element v of a 16-bit row whose place holds `x`: a bound, if it
+// is touched.
+template <int DT>
+__device__ __forceinline__ float exact_value(int32_t v, float x, const char* row,
+                                             const RowConstraints& r) {
+  if (r.touched && (((uint32_t)__ldcg(r.touched + (v >> 3)) >> (v & 7)) & 1u))
+    return exact_touched<DT>(row, v, r);
+  return x;
 }
 
 // The values of group g (elements 4 g .. 4 g + 3) of a 16-bit row whose touched
@@ -233,7 +258,7 @@ __device__ __forceinline__ uint32_t unit_bits(const uint8_t* bits, int32_t e0) {
 // Logit x of element v, constrained: the element-by-element form.
 __device__ __forceinline__ float constrained_logit(float x, int32_t v, const RowConstraints& r) {
   if (r.touched && (__ldcg(r.touched + (v >> 3)) >> (v & 7) & 1u))
-    x = penalised(x, __ldcg(r.history + v), r.bias ? __ldcg(r.bias + v) : 0.0f, r);
+    x = penalised(x, __ldcg(r.history + v), r.bias ? __ldcg(r.bias + v) : 0.0f, r.pen);
   if (r.mask && !(__ldcg(r.mask + (v >> 3)) >> (v & 7) & 1u)) x = -INFINITY;
   return x;
 }

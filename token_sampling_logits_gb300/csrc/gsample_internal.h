@@ -125,7 +125,7 @@ inline int units_elems(int dtype, bool vec) { return vec ? (dtype == 0 ? 4 : 8) 
 
 // Occupancy-derived CTA slots per SM for the sampler kernel of (dtype, vec).
 int sample_ctas_per_sm(int dtype, bool vec, bool constrained);
-size_t sample_smem_bytes(int dtype, bool vec, bool constrained);
+size_t sample_smem_bytes(int dtype, bool vec);
 cudaError_t launch_sample(const SampleParams& p, int dtype, bool vec, cudaStream_t stream);
 cudaError_t launch_sample(const ConSampleParams& p, int dtype, bool vec, cudaStream_t stream);
 

@@ -656,31 +656,30 @@ __device__ __forceinline__ void issue_tile(const SampleParams& p, const TileCurs
 }
 
 // ---------------------------------------------------------------------------
-// Constrained rows. A tile's elements fall into three kinds by their mask and
-// touched bits: masked ones, which do not exist; touched ones, which wait in a
-// per-warp list with their logit, history word and bias until they are scored
-// one a lane; and the rest, which go through the tile as they are. Only the
-// last kind needs the stage: touched and masked places of it are set to -inf.
-// A tile with few elements left (a grammar that allows a few tokens) has all of
-// them listed and is not loaded at all.
-//
-// The list's three words an entry are gathered with cp.async, issued when the
-// tile has been swept and used after the next one, so no lane waits for them
-// but at the end of a row's part.
+// Constrained rows. By their mask and touched bits a tile's elements are masked
+// (they do not exist), touched, or plain. Plain ones go through the tile as
+// they are, with the places of the others set to -inf. Touched ones are scored
+// before the first tile (list_phase): the CTA lists those of its whole part of
+// the batch in shared memory and its threads share them out, so that the low
+// ids, where most of a request's tokens lie, keep no single warp. A tile with
+// few elements left (a grammar that allows a few tokens) has all of them listed
+// and is never loaded.
 //
 // Split points lie on multiples of 8 units of the row (32 or 64 elements), so a
 // tile's bits are whole words: lane l holds words l and, for 16-bit units (64
 // words a tile), l + 32.
 // ---------------------------------------------------------------------------
-constexpr int kListCap = 128;     // entries of a warp's list
-constexpr int kListFlush = 32;    // scored from this many on
-constexpr int kFewLeft = 64;      // a tile with at most this many elements left is listed whole
-constexpr int kConListBytes = kListCap * 16;  // element, logit word, history word, bias
+constexpr int kListCap = 4096;  // entries a CTA lists at a time; any tile fits
+constexpr int kFewLeft = 64;    // a tile with at most this many elements left is listed whole
+constexpr int kClearBits = 256; // up to this many cleared elements: one by one, not by units
+static_assert(kListCap * 12 <= kWarps * kStages * 32 * kVPT * 16,
+              "the list lies in the ring, before the ring is used");
 
 struct TileWords {
   uint32_t allowed[2], touched[2];  // touched: and allowed
 };
 
+// The words of a tile as loaded; row_words cuts them to the row.
 template <int DT, bool VEC>
 __device__ __forceinline__ TileWords load_words(const TileCursor& c, const uint8_t* mask,
                                                 const uint8_t* touched) {
@@ -701,10 +700,27 @@ __device__ __forceinline__ TileWords load_words(const TileCursor& c, const uint8
   return r;
 }
 
-// Elements left in a tile (masks aside, touched ones not counted).
-__device__ __forceinline__ int tile_left(const TileWords& w) {
-  return (int)__reduce_add_sync(0xFFFFFFFFu, __popc(w.allowed[0] & ~w.touched[0]) +
-                                                 __popc(w.allowed[1] & ~w.touched[1]));
+// Bits past the row's end mean nothing; masked elements are not touched.
+template <int EPU>
+__device__ __forceinline__ void row_words(TileWords& w, int32_t t0, int32_t V) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int32_t in = V - (t0 * EPU + i * 1024 + lane * 32);
+    if (in < 32) w.allowed[i] &= in <= 0 ? 0u : (1u << in) - 1u;
+    w.touched[i] &= w.allowed[i];
+  }
+}
+
+// What a tile's words say of it: elements allowed (low half), and touched
+// among them (high half).
+__device__ __forceinline__ uint32_t tile_counts(const TileWords& w) {
+  const uint32_t a = __popc(w.allowed[0]) + __popc(w.allowed[1]);
+  const uint32_t t = __popc(w.touched[0]) + __popc(w.touched[1]);
+  return __reduce_add_sync(0xFFFFFFFFu, a | t << 16);
+}
+__device__ __forceinline__ bool tile_dense(uint32_t counts) {
+  return (counts & 0xFFFFu) > (uint32_t)kFewLeft;
 }
 
 // The bits of the lane's k-th unit (unit k * 32 + lane of the tile) in a tile's
@@ -720,7 +736,8 @@ __device__ __forceinline__ uint32_t unit_of_words(uint32_t w0, uint32_t w1, int 
   }
 }
 
-// issue_tile for constrained rows: units without an element left are not read.
+// issue_tile for constrained rows: units that the mask leaves nothing of are
+// not read.
 template <int DT, bool VEC>
 __device__ __forceinline__ void issue_tile_masked(const SampleParams& p, const TileCursor& c,
                                                   const TileWords& words, uint32_t stage,
@@ -728,9 +745,24 @@ __device__ __forceinline__ void issue_tile_masked(const SampleParams& p, const T
   using C = Cfg<DT, VEC>;
   const int lane = threadIdx.x & 31;
   const char* row = p.logits + c.b * p.ld_bytes;
-  const uint32_t w0 = words.allowed[0] & ~words.touched[0];
-  const uint32_t w1 = words.allowed[1] & ~words.touched[1];
+  const uint32_t w0 = words.allowed[0], w1 = words.allowed[1];
+  if (VEC && c.t_hi - c.t0 == C::kTile && c.t_hi * C::kEPU <= p.V) {
+    // A full tile: without an empty unit (a zero byte, or nibble, of a word; a
+    // false alarm costs nothing), eight plain copies.
+    bool empty;
+    if constexpr (C::kEPU == 8)
+      empty = (__vcmpeq4(w0, 0u) | __vcmpeq4(w1, 0u)) != 0u;
+    else
+      empty = ((w0 - 0x11111111u) & ~w0 & 0x88888888u) != 0u;
+    if (!__any_sync(0xFFFFFFFFu, empty)) {
+      const char* src = row + (size_t)(c.t0 + lane) * 16;
+      const uint32_t dst = stage + (uint32_t)lane * 16u;
 #pragma unroll
+      for (int k = 0; k < kVPT; ++k) cp_async16(dst + k * 512u, src + k * 512, pol);
+      return;
+    }
+  }
+#pragma unroll 1
   for (int k = 0; k < kVPT; ++k) {
     const uint32_t m = unit_of_words<C::kEPU>(w0, w1, k, lane);
     const int32_t u = c.t0 + k * 32 + lane;
@@ -745,98 +777,211 @@ __device__ __forceinline__ void issue_tile_masked(const SampleParams& p, const T
   }
 }
 
-// The masked and touched places of a landed tile become -inf.
+// The places of a landed tile whose bits in `keep` (a lane's two words) are
+// clear become -inf; `cleared` is their number.
 template <int DT, bool VEC>
-__device__ __forceinline__ void clear_tile(uint32_t stage, const TileWords& words) {
+__device__ __forceinline__ void clear_tile(uint32_t stage, uint32_t keep0, uint32_t keep1,
+                                           int cleared) {
   using C = Cfg<DT, VEC>;
+  if (cleared == 0) return;
   const int lane = threadIdx.x & 31;
-  constexpr uint32_t kFull = (1u << C::kEPU) - 1u;
-  const uint32_t w0 = words.allowed[0] & ~words.touched[0];
-  const uint32_t w1 = words.allowed[1] & ~words.touched[1];
-  if (__all_sync(0xFFFFFFFFu, w0 == 0xFFFFFFFFu && (C::kEPU == 4 || w1 == 0xFFFFFFFFu))) return;
-#pragma unroll
-  for (int k = 0; k < kVPT; ++k) {
-    const uint32_t m = unit_of_words<C::kEPU>(w0, w1, k, lane);
-    if (m != kFull && m != 0u) {  // 0: the unit was not read and holds -inf
-      const uint32_t a = stage + (uint32_t)(k * 32 + lane) * 16u;
-      sts128(a, masked_unit<DT, C::kF32Bits>(lds128(a), m));
+  if (cleared <= kClearBits) {
+    uint32_t c0 = ~keep0, c1 = C::kEPU == 8 ? ~keep1 : 0u;
+    while ((c0 | c1) != 0u) {
+      const int e = c0 != 0u ? __ffs((int)c0) - 1 : 1024 + __ffs((int)c1) - 1;
+      if (c0 != 0u)
+        c0 &= c0 - 1u;
+      else
+        c1 &= c1 - 1u;
+      const uint32_t at = (uint32_t)(lane * 32 + e);
+      if constexpr (C::kF32Bits)
+        sts_f32(stage + at * 4u, -INFINITY);
+      else
+        sts_u16(stage + at * 2u, neg_inf_half<DT>());
     }
-  }
-  __syncwarp();  // other lanes read the units
-}
-
-// The row of the listed elements.
-struct ListRow {
-  const char* row;
-  const uint32_t* history;  // nullptr: no state
-  const float* bias;
-  float rep, freq, pres;
-};
-
-// Scores the list, one element a lane at a time; every gather has landed.
-template <int DT>
-__device__ __noinline__ Best score_list(const uint32_t* list, int n, float T, float rT,
-                                        PhiloxRow ph, Prune pr, float bs, int32_t bi,
-                                        ListRow lr) {
-  const int lane = threadIdx.x & 31;
-  __syncwarp();
-  const ReachTest rt = make_reach(pr, rT);
-  RowConstraints r;
-  r.rep = lr.rep;
-  r.freq = lr.freq;
-  r.pres = lr.pres;
-  for (int i = lane; i < n; i += 32) {
-    const int32_t v = (int32_t)list[i];
-    const uint32_t xw = list[kListCap + i];
-    float x;
-    if constexpr (DT == 0) {
-      x = __uint_as_float(xw);
-    } else {  // the half of the aligned word that holds the element
-      const bool high = ((uintptr_t)lr.row + 2u * (uint32_t)v) & 2u;
-      x = half_to_f32<DT>(high ? xw >> 16 : xw & 0xFFFFu);
-    }
-    if (lr.history)
-      x = penalised(x, list[2 * kListCap + i], __uint_as_float(list[3 * kListCap + i]), r);
-    if (!(T > 0.0f)) {
-      take_better(x, v, bs, bi);
-    } else if (x >= pr.thr_x) {  // not NaN
-      const uint32_t w = word_of(philox_row_1((uint32_t)v >> 2, ph), v & 3);
-      if (!pr.use_bound || may_reach(x, w, rt)) take_better(exact_score(x, w, T), v, bs, bi);
-    }
-  }
-  __syncwarp();  // before the list is refilled
-  return Best{bs, bi};
-}
-
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-
-// Requests entry s of the list: element v of the row.
-template <int DT>
-__device__ __forceinline__ void request_entry(uint32_t* list, int s, int32_t v,
-                                              const ListRow& lr, int32_t V) {
-  list[s] = (uint32_t)v;
-  uint32_t* xw = list + kListCap + s;
-  if constexpr (DT == 0) {
-    cp_async4(smem_addr(xw), lr.row + (size_t)v * 4);
   } else {
-    const uintptr_t at = (uintptr_t)lr.row + 2u * (size_t)v;
-    const uintptr_t word = at & ~(uintptr_t)3;
-    // An aligned word that reaches past an end of the row is not read.
-    if (word >= (uintptr_t)lr.row && word + 4 <= (uintptr_t)lr.row + 2u * (size_t)V) {
-      cp_async4(smem_addr(xw), reinterpret_cast<const void*>(word));
-    } else {
-      *xw = (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(at)) * 0x10001u;
+    constexpr uint32_t kFull = (1u << C::kEPU) - 1u;
+#pragma unroll 1
+    for (int k = 0; k < kVPT; ++k) {
+      const uint32_t m = unit_of_words<C::kEPU>(keep0, keep1, k, lane);
+      if (m != kFull) {
+        const uint32_t a = stage + (uint32_t)(k * 32 + lane) * 16u;
+        sts128(a, masked_unit<DT, C::kF32Bits>(lds128(a), m));
+      }
     }
   }
-  if (lr.history) {
-    cp_async4(smem_addr(list + 2 * kListCap + s), lr.history + v);
-    if (lr.bias)
-      cp_async4(smem_addr(list + 3 * kListCap + s), lr.bias + v);
-    else
-      list[3 * kListCap + s] = 0u;
+  __syncwarp();  // other lanes read the places
+}
+
+// One thread's best of a row, into the row's slot and its pruning hint.
+__device__ __forceinline__ void publish(const SampleParams& p, int64_t b, float bs, int32_t bi) {
+  if (bi == INT32_MAX || !(bs > -INFINITY)) return;
+  atomicMax(&p.ws[b].key, pack_key(bs, bi));
+  atomicMax(&p.ws[b].hint, ordered_bits(bs));
+}
+
+// Scores the listed elements of the CTA's part [u_begin, u_end) (of this warp)
+// of the batch, all of them exactly, and publishes the rows' bests. Every warp
+// of the CTA takes part.
+template <int DT, bool VEC>
+__device__ __forceinline__ void list_phase(const ConSampleParams& p, int64_t u_begin,
+                                           int64_t u_end, unsigned char* smem) {
+  using C = Cfg<DT, VEC>;
+  if (!p.con.history && !p.con.mask) return;  // nothing is ever listed
+  __shared__ int listed;
+  uint32_t* lv = reinterpret_cast<uint32_t*>(smem);           // element
+  int32_t* lb = reinterpret_cast<int32_t*>(lv + kListCap);    // row
+  float* ly = reinterpret_cast<float*>(lb + kListCap);        // constrained logit
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int64_t NU = p.units_per_row;
+  TileCursor c = segment_at(u_begin / NU, u_begin, u_end, NU, C::kTile);
+  int64_t row = -1;
+  const uint8_t *mask = nullptr, *touched = nullptr;
+  float bs = -INFINITY;
+  int32_t bi = INT32_MAX, bb = -1;
+  if (tid == 0) listed = 0;
+  __syncthreads();
+  for (;;) {
+    // List tiles until they are done or the list is full; the words of four
+    // tiles are on their way at a time.
+    bool full = false;
+    while (c.valid && !full) {
+      constexpr int N = 4;
+      TileCursor t[N];
+      TileWords w[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        if (c.valid && c.b != row) {
+          row = c.b;
+          const RowConstraints r = row_constraints(p.con, row);
+          mask = r.mask;
+          touched = r.touched;
+        }
+        t[j] = c;
+        w[j] = load_words<DT, VEC>(c, mask, touched);
+        c = mask || touched ? next_tile<C::kTile>(c, u_end, NU)
+            : c.valid       ? next_row(c.b, u_end, NU, C::kTile)  // nothing in this row
+                            : c;
+        if (!mask && !touched) t[j].valid = false;
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        if (!t[j].valid || full) continue;
+        row_words<C::kEPU>(w[j], t[j].t0, p.V);
+        const uint32_t counts = tile_counts(w[j]);
+        const bool dense = tile_dense(counts);
+        const int n = (int)(dense ? counts >> 16 : counts & 0xFFFFu);
+        if (n == 0) continue;
+        int base = 0;
+        if (lane == 0) {  // reserve n entries, or nothing
+          int seen = *(volatile int*)&listed;
+          while (seen + n <= kListCap) {
+            const int was = atomicCAS(&listed, seen, seen + n);
+            if (was == seen) break;
+            seen = was;
+          }
+          base = seen;
+        }
+        base = __shfl_sync(0xFFFFFFFFu, base, 0);
+        if (base + n > kListCap) {  // this tile comes again after the list is scored
+          full = true;
+          c = t[j];
+          continue;
+        }
+        uint32_t b0 = dense ? w[j].touched[0] : w[j].allowed[0];
+        uint32_t b1 = dense ? w[j].touched[1] : w[j].allowed[1];
+        const int mine = __popc(b0) + __popc(b1);
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+          if (lane >= o) incl += up;
+        }
+        int at = base + incl - mine;
+        const uint32_t e0 = (uint32_t)(t[j].t0 * C::kEPU + lane * 32);
+        while ((b0 | b1) != 0u) {
+          const bool low = b0 != 0u;
+          const uint32_t b = low ? b0 : b1;
+          lv[at] = e0 + (low ? 0u : 1024u) + (uint32_t)__ffs((int)b) - 1u;
+          lb[at] = (int32_t)t[j].b;
+          ++at;
+          if (low)
+            b0 &= b0 - 1u;
+          else
+            b1 &= b1 - 1u;
+        }
+      }
+    }
+    const bool more = __syncthreads_or(full) != 0;
+    const int n = listed;
+    // The constrained logits, four gathers a thread in flight.
+    for (int i0 = tid; i0 < n; i0 += 4 * kThreads) {
+      float x[4], bias[4];
+      uint32_t h[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = i0 + q * kThreads;
+        x[q] = -INFINITY;
+        h[q] = 0u;
+        bias[q] = 0.0f;
+        if (i < n) {
+          const int64_t b = lb[i];
+          const int32_t v = (int32_t)lv[i];
+          x[q] = load_elt<DT>(p.logits + b * p.ld_bytes, v);
+          const int64_t r = state_row_of(p.con, b);
+          if (r >= 0) {
+            h[q] = __ldcg(p.con.history + r * p.con.state_ld + v);
+            if (p.con.bias) bias[q] = __ldcg(p.con.bias + r * p.con.state_ld + v);
+          }
+        }
+      }
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        const int i = i0 + q * kThreads;
+        if (i >= n) break;
+        const float xq = q == 0 ? x[0] : q == 1 ? x[1] : q == 2 ? x[2] : x[3];
+        const uint32_t hq = q == 0 ? h[0] : q == 1 ? h[1] : q == 2 ? h[2] : h[3];
+        const float bq = q == 0 ? bias[0] : q == 1 ? bias[1] : q == 2 ? bias[2] : bias[3];
+        ly[i] = penalised(xq, hq, bq, row_penalties(p.con, lb[i]));  // read by this thread only
+      }
+    }
+#pragma unroll 1
+    for (int i = tid; i < n; i += kThreads) {
+      const int32_t b = lb[i], v = (int32_t)lv[i];
+      const float y = ly[i];
+      if (b != bb) {
+        if (bb >= 0) publish(p, bb, bs, bi);
+        bb = b;
+        bs = -INFINITY;
+        bi = INT32_MAX;
+      }
+      const float T = __ldg(p.temperature + b);
+      if (!(T > 0.0f)) {
+        take_better(y, v, bs, bi);
+      } else if (y > -INFINITY) {
+        const uint64_t sd = __ldg(p.seed + b), of = __ldg(p.offset + b);
+        const PhiloxRow ph = philox_row((uint32_t)b, (uint32_t)of, (uint32_t)(of >> 32),
+                                        (uint32_t)sd, (uint32_t)(sd >> 32));
+        const uint32_t w = word_of(philox_row_1((uint32_t)v >> 2, ph), v & 3);
+        take_better(exact_score(y, w, T), v, bs, bi);
+      }
+    }
+    __syncthreads();
+    if (!more) break;
+    if (tid == 0) listed = 0;
+    __syncthreads();
   }
+  int same = 0;
+  __match_all_sync(0xFFFFFFFFu, bb, &same);
+  if (same) {
+    warp_argmax(bs, bi);
+    if (lane == 0 && bb >= 0) publish(p, bb, bs, bi);
+  } else if (bb >= 0) {
+    publish(p, bb, bs, bi);
+  }
+  // The rows' slots hold these before any warp of the CTA takes a ticket.
+  __threadfence();
+  __syncthreads();
 }
 
 // Greedy over a constrained tile: the running best may already hold a touched
@@ -891,11 +1036,6 @@ template <bool CON>
 using KernelParams = typename std::conditional<CON, ConSampleParams, SampleParams>::type;
 
 template <int DT, bool VEC, bool CON>
-__host__ __device__ constexpr int warp_bytes() {
-  return Cfg<DT, VEC>::kWarpBytes + (CON ? kConListBytes : 0);
-}
-
-template <int DT, bool VEC, bool CON>
 __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
     sample_kernel(const KernelParams<CON> p) {
   using C = Cfg<DT, VEC>;
@@ -903,12 +1043,16 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
   pdl_wait_then_release();
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  unsigned char* wbase = smem + (size_t)warp * warp_bytes<DT, VEC, CON>();
+  unsigned char* wbase = smem + (size_t)warp * C::kWarpBytes;
   const uint32_t ring = smem_addr(wbase);
   const uint64_t pol = evict_first_policy();
 
   const int64_t NU = p.units_per_row, NW = p.warps;
   const int64_t gw = (int64_t)blockIdx.x * kWarps + warp;
+  if constexpr (CON) {
+    const int64_t w0 = gw < NW ? gw : NW, w1 = gw < NW ? gw + 1 : NW;
+    list_phase<DT, VEC>(p, split_point<VEC>(p, w0, true), split_point<VEC>(p, w1, true), smem);
+  }
   if (gw >= NW) return;
   const int64_t u_begin = split_point<VEC>(p, gw, CON), u_end = split_point<VEC>(p, gw + 1, CON);
   if (u_begin >= u_end) return;  // no units (only with fewer than 8 units per warp)
@@ -919,23 +1063,8 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
   // Constrained rows: the words of the current tile, of the one in flight and
   // of the one after, and the bit rows that those of the last come from.
   [[maybe_unused]] TileWords words, words_ahead, words_next;
-  [[maybe_unused]] bool dense = true, dense_ahead = true;
+  [[maybe_unused]] uint32_t counts = 0u, counts_ahead = 0u;
   [[maybe_unused]] const uint8_t *mask_next = nullptr, *touched_next = nullptr;
-  [[maybe_unused]] ListRow lr;
-  [[maybe_unused]] uint32_t* list =
-      reinterpret_cast<uint32_t*>(wbase + C::kWarpBytes);
-  [[maybe_unused]] int listed = 0;
-  auto enter_row = [&](int64_t b) {
-    if constexpr (CON) {
-      const RowConstraints c = row_constraints(p.con, b);
-      lr.row = p.logits + b * p.ld_bytes;
-      lr.history = c.history;
-      lr.bias = c.bias;
-      lr.rep = c.rep;
-      lr.freq = c.freq;
-      lr.pres = c.pres;
-    }
-  };
   auto next_words = [&](int64_t row_before) {
     if constexpr (CON) {
       if (ahead.valid && ahead.b != row_before) {
@@ -951,14 +1080,9 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
   auto advance = [&](uint32_t stage) {
     if constexpr (CON) {
       words_ahead = words_next;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int32_t in = p.V - (ahead.t0 * C::kEPU + i * 1024 + lane * 32);  // bits of the row
-        if (in < 32) words_ahead.allowed[i] &= in <= 0 ? 0u : (1u << in) - 1u;
-        words_ahead.touched[i] &= words_ahead.allowed[i];
-      }
-      dense_ahead = tile_left(words_ahead) > kFewLeft;
-      if (dense_ahead) issue_tile_masked<DT, VEC>(p, ahead, words_ahead, stage, pol);
+      row_words<C::kEPU>(words_ahead, ahead.t0, p.V);
+      counts_ahead = tile_counts(words_ahead);
+      if (tile_dense(counts_ahead)) issue_tile_masked<DT, VEC>(p, ahead, words_ahead, stage, pol);
       cp_async_commit();
       const int64_t row = ahead.b;
       ahead = next_tile<C::kTile>(ahead, u_end, NU);
@@ -967,10 +1091,8 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
   };
   if constexpr (CON) {
     static_assert(kStages == 2, "one tile in flight: its words are words_ahead");
-    enter_row(cur.b);
     next_words(-1);
     advance(ring);
-    cp_async_commit();  // the place of the gathers' group, which the loop expects
   } else {
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) {
@@ -998,20 +1120,10 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
   // tile that listed the last of them.
   unsigned char* rbase = wbase + kStages * C::kTileBytes;
   int rcnt = 0;
-  Prune pr_last{CON ? -INFINITY : INFINITY, -INFINITY, false};
-  auto flush_list = [&]() {
-    if constexpr (CON) {
-      const Best r = score_list<DT>(list, listed, rc.T, rc.rT, rc.ph, pr_last, bs, bi, lr);
-      bs = r.s;
-      bi = r.i;
-      listed = 0;
-    }
-  };
-
+  Prune pr_last{INFINITY, -INFINITY, false};
   while (true) {
     // The current tile has landed (this lane's copies, then everyone's).
-    // Constrained rows: a group of gathers may still be on its way.
-    cp_async_wait<kStages - 2 + (CON ? 1 : 0)>();
+    cp_async_wait<kStages - 2>();
     __syncwarp();
     const uint32_t stage = ring + slot * C::kTileBytes;
     // Refill the ring slot that the previous tile freed.
@@ -1019,16 +1131,20 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
     if (fill >= kStages) fill -= kStages;
     if constexpr (CON) {
       words = words_ahead;
-      dense = dense_ahead;
+      counts = counts_ahead;
       advance(ring + fill * C::kTileBytes);
-      if (dense) clear_tile<DT, VEC>(stage, words);
+      if (tile_dense(counts))
+        clear_tile<DT, VEC>(stage, words.allowed[0] & ~words.touched[0],
+                            words.allowed[1] & ~words.touched[1],
+                            (cur.t_hi - cur.t0) * C::kEPU - (int)(counts & 0xFFFFu) +
+                                (int)(counts >> 16));
     } else {
       issue_tile<DT, VEC>(p, ahead, ring + fill * C::kTileBytes, pol);
       ahead = next_tile<C::kTile>(ahead, u_end, NU);
     }
 
     const int32_t t0 = cur.t0, t_hi = cur.t_hi;
-    bool left = !CON || dense;  // whether the tile may hold a candidate
+    bool left = !CON || tile_dense(counts);  // whether the tile may hold a candidate
     if (rc.T > 0.0f) {
       seen = seg_first ? 0u : pending;
       // The first bound of the row's part: each lane's best of the first tile
@@ -1066,34 +1182,6 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
           greedy_unit<DT, VEC>(r, u, bs, bi);
       }
     }
-    if constexpr (CON) {
-      // The elements listed before have landed (the tile in flight need not).
-      if (listed >= kListFlush) {
-        cp_async_wait<1>();
-        flush_list();
-      }
-      // This tile's listed elements.
-      uint32_t todo[2] = {dense ? words.touched[0] : words.allowed[0],
-                          dense ? words.touched[1] : words.allowed[1]};
-      const int32_t e0 = cur.t0 * C::kEPU + lane * 32;
-      while (__any_sync(0xFFFFFFFFu, (todo[0] | todo[1]) != 0u)) {
-        const bool has = (todo[0] | todo[1]) != 0u;
-        const unsigned m = __ballot_sync(0xFFFFFFFFu, has);
-        if (listed + __popc(m) > kListCap) {
-          cp_async_commit();
-          cp_async_wait<0>();
-          flush_list();
-        }
-        if (has) {
-          const int i = todo[0] != 0u ? 0 : 1;
-          const int32_t v = e0 + i * 1024 + __ffs((int)todo[i]) - 1;
-          todo[i] &= todo[i] - 1u;
-          request_entry<DT>(list, listed + __popc(m & ((1u << lane) - 1u)), v, lr, p.V);
-        }
-        listed += __popc(m);
-      }
-      cp_async_commit();
-    }
     __syncwarp();  // every lane is done with this stage before it is refilled
 
     if (lane == 0 && tk_pending) {
@@ -1104,12 +1192,6 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
       // This warp's part of row b is done: merge its best, then add its units
       // to the row's ticket; the warp that brings the count to NU writes the
       // answer and clears the row's slot (checked one tile later).
-      if constexpr (CON) {
-        if (listed > 0) {
-          cp_async_wait<0>();
-          flush_list();
-        }
-      }
       if (rcnt > 0) {
         flush_rare<DT, VEC>(rbase, rcnt, rc, pr_last, bs, bi);
         rcnt = 0;
@@ -1126,10 +1208,6 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
       cur = next_tile<C::kTile>(cur, u_end, NU);
       if (!cur.valid) break;
       rc = row_context_from(p, cur.b, next_params);
-      if constexpr (CON) {
-        enter_row(cur.b);
-        pr_last = Prune{-INFINITY, -INFINITY, false};
-      }
       next_params = load_row_params(p, cur.b + 1);
       bs = -INFINITY;
       bi = INT32_MAX;
@@ -1177,8 +1255,7 @@ cudaError_t launch_kernel(void* fn, const SampleParams& p, void* param, size_t s
 
 }  // namespace
 
-size_t sample_smem_bytes(int dtype, bool vec, bool constrained) {
-  if (constrained) return sample_smem_bytes(dtype, vec, false) + (size_t)kWarps * kConListBytes;
+size_t sample_smem_bytes(int dtype, bool vec) {
   switch (dtype * 2 + (vec ? 1 : 0)) {
     case 0: return Cfg<0, false>::kSmem;
     case 1: return Cfg<0, true>::kSmem;
@@ -1194,7 +1271,7 @@ size_t sample_smem_bytes(int dtype, bool vec, bool constrained) {
 // then report how many CTAs of the variant fit on one SM.
 int sample_ctas_per_sm(int dtype, bool vec, bool constrained) {
   void* fn = select_kernel(dtype, vec, constrained);
-  const size_t smem = sample_smem_bytes(dtype, vec, constrained);
+  const size_t smem = sample_smem_bytes(dtype, vec);
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
       cudaSuccess)
     return 0;
@@ -1205,12 +1282,12 @@ int sample_ctas_per_sm(int dtype, bool vec, bool constrained) {
 
 cudaError_t launch_sample(const SampleParams& p, int dtype, bool vec, cudaStream_t stream) {
   return launch_kernel(select_kernel(dtype, vec, false), p, const_cast<SampleParams*>(&p),
-                       sample_smem_bytes(dtype, vec, false), stream);
+                       sample_smem_bytes(dtype, vec), stream);
 }
 
 cudaError_t launch_sample(const ConSampleParams& p, int dtype, bool vec, cudaStream_t stream) {
   return launch_kernel(select_kernel(dtype, vec, true), p, const_cast<ConSampleParams*>(&p),
-                       sample_smem_bytes(dtype, vec, true), stream);
+                       sample_smem_bytes(dtype, vec), stream);
 }
 
 // ---------------------------------------------------------------------------
