@@ -656,30 +656,47 @@ __device__ __forceinline__ void issue_tile(const SampleParams& p, const TileCurs
 }
 
 // ---------------------------------------------------------------------------
-// Constrained rows. By their mask and touched bits a tile's elements are masked
-// (they do not exist), touched, or plain. Plain ones go through the tile as
-// they are, with the places of the others set to -inf. Touched ones are scored
-// before the first tile (list_phase): the CTA lists those of its whole part of
-// the batch in shared memory and its threads share them out, so that the low
-// ids, where most of a request's tokens lie, keep no single warp. A tile with
-// few elements left (a grammar that allows a few tokens) has all of them listed
-// and is never loaded.
+// Constrained rows. Two kernels share a row's elements by its mask and touched
+// bits, word by word (32 elements):
+//   - list_kernel scores the touched elements that the mask allows, and every
+//     allowed element of a word in which the mask leaves at most kFewInWord (a
+//     grammar that allows a few tokens), one a thread, and publishes each row's
+//     best in its workspace slot;
+//   - sample_kernel then sweeps the others as it does for unconstrained rows:
+//     the remaining places of its tiles are -inf, units without an element for
+//     it are not read, and a tile without one is passed over.
+// Scoring the touched elements where the sweep meets them was measured slower
+// (B = 256, V = 151936 bf16, some 1600 touched tokens a row: 112 us with a list
+// a warp, 86 us with a list a CTA): the sweep runs 16 warps an SM, too few to
+// hide the gathers, and the low ids, where most tokens of a request lie, keep
+// one warp of a row long after the others.
 //
 // Split points lie on multiples of 8 units of the row (32 or 64 elements), so a
 // tile's bits are whole words: lane l holds words l and, for 16-bit units (64
 // words a tile), l + 32.
 // ---------------------------------------------------------------------------
-constexpr int kListCap = 4096;  // entries a CTA lists at a time; any tile fits
-constexpr int kFewLeft = 64;    // a tile with at most this many elements left is listed whole
-constexpr int kClearBits = 256; // up to this many cleared elements: one by one, not by units
-static_assert(kListCap * 12 <= kWarps * kStages * 32 * kVPT * 16,
-              "the list lies in the ring, before the ring is used");
+constexpr int kFewInWord = 8;
+constexpr int kClearBits = 256;  // up to this many cleared elements: one by one, not by units
 
+// The words `mask` and `touched` of a row's elements [e0, e0 + 32), cut to the
+// row: the elements of the sweep, and those of the list.
+struct WordSplit {
+  uint32_t sweep, list;
+};
+__device__ __forceinline__ WordSplit split_word(uint32_t mask, uint32_t touched, int32_t e0,
+                                                int32_t V) {
+  const uint32_t listed = __popc(mask) <= kFewInWord ? 0xFFFFFFFFu : touched;
+  const int32_t in = V - e0;  // bits past the row's end mean nothing
+  if (in < 32) mask &= in <= 0 ? 0u : (1u << in) - 1u;
+  return WordSplit{mask & ~listed, mask & listed};
+}
+
+// A tile's mask and touched words as loaded (mask words of a row without one:
+// all set; past the tile: none).
 struct TileWords {
-  uint32_t allowed[2], touched[2];  // touched: and allowed
+  uint32_t mask[2], touched[2];
 };
 
-// The words of a tile as loaded; row_words cuts them to the row.
 template <int DT, bool VEC>
 __device__ __forceinline__ TileWords load_words(const TileCursor& c, const uint8_t* mask,
                                                 const uint8_t* touched) {
@@ -687,40 +704,17 @@ __device__ __forceinline__ TileWords load_words(const TileCursor& c, const uint8
   constexpr int W = EPU / 4;  // words a lane
   const int lane = threadIdx.x & 31;
   TileWords r;
-  r.allowed[1] = r.touched[1] = 0u;
+  r.mask[1] = r.touched[1] = 0u;
 #pragma unroll
   for (int i = 0; i < W; ++i) {
     const int32_t w = c.t0 / (32 / EPU) + i * 32 + lane;
     const bool in = c.valid && w < (c.t_hi + 32 / EPU - 1) / (32 / EPU);
-    r.allowed[i] = !in ? 0u
-                   : mask ? __ldcg(reinterpret_cast<const uint32_t*>(mask) + w)
-                          : 0xFFFFFFFFu;
+    r.mask[i] = !in    ? 0u
+                : mask ? __ldcg(reinterpret_cast<const uint32_t*>(mask) + w)
+                       : 0xFFFFFFFFu;
     r.touched[i] = in && touched ? __ldcg(reinterpret_cast<const uint32_t*>(touched) + w) : 0u;
   }
   return r;
-}
-
-// Bits past the row's end mean nothing; masked elements are not touched.
-template <int EPU>
-__device__ __forceinline__ void row_words(TileWords& w, int32_t t0, int32_t V) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int32_t in = V - (t0 * EPU + i * 1024 + lane * 32);
-    if (in < 32) w.allowed[i] &= in <= 0 ? 0u : (1u << in) - 1u;
-    w.touched[i] &= w.allowed[i];
-  }
-}
-
-// What a tile's words say of it: elements allowed (low half), and touched
-// among them (high half).
-__device__ __forceinline__ uint32_t tile_counts(const TileWords& w) {
-  const uint32_t a = __popc(w.allowed[0]) + __popc(w.allowed[1]);
-  const uint32_t t = __popc(w.touched[0]) + __popc(w.touched[1]);
-  return __reduce_add_sync(0xFFFFFFFFu, a | t << 16);
-}
-__device__ __forceinline__ bool tile_dense(uint32_t counts) {
-  return (counts & 0xFFFFu) > (uint32_t)kFewLeft;
 }
 
 // The bits of the lane's k-th unit (unit k * 32 + lane of the tile) in a tile's
@@ -736,16 +730,15 @@ __device__ __forceinline__ uint32_t unit_of_words(uint32_t w0, uint32_t w1, int 
   }
 }
 
-// issue_tile for constrained rows: units that the mask leaves nothing of are
-// not read.
+// issue_tile for constrained rows: units without an element of the sweep (the
+// lane's words w0, w1) are not read.
 template <int DT, bool VEC>
 __device__ __forceinline__ void issue_tile_masked(const SampleParams& p, const TileCursor& c,
-                                                  const TileWords& words, uint32_t stage,
+                                                  uint32_t w0, uint32_t w1, uint32_t stage,
                                                   uint64_t pol) {
   using C = Cfg<DT, VEC>;
   const int lane = threadIdx.x & 31;
   const char* row = p.logits + c.b * p.ld_bytes;
-  const uint32_t w0 = words.allowed[0], w1 = words.allowed[1];
   if (VEC && c.t_hi - c.t0 == C::kTile && c.t_hi * C::kEPU <= p.V) {
     // A full tile: without an empty unit (a zero byte, or nibble, of a word; a
     // false alarm costs nothing), eight plain copies.
@@ -813,175 +806,109 @@ __device__ __forceinline__ void clear_tile(uint32_t stage, uint32_t keep0, uint3
   __syncwarp();  // other lanes read the places
 }
 
-// One thread's best of a row, into the row's slot and its pruning hint.
-__device__ __forceinline__ void publish(const SampleParams& p, int64_t b, float bs, int32_t bi) {
-  if (bi == INT32_MAX || !(bs > -INFINITY)) return;
-  atomicMax(&p.ws[b].key, pack_key(bs, bi));
-  atomicMax(&p.ws[b].hint, ordered_bits(bs));
-}
+// The list kernel: one CTA takes a run of words of one row, lists their listed
+// elements in shared memory in order, and shares them out among its threads.
+constexpr int kListThreads = 256;
+constexpr int kListWords = 4;    // words a thread
+constexpr int kListCap = 2048;   // entries listed at a time
 
-// Scores the listed elements of the CTA's part [u_begin, u_end) (of this warp)
-// of the batch, all of them exactly, and publishes the rows' bests. Every warp
-// of the CTA takes part.
-template <int DT, bool VEC>
-__device__ __forceinline__ void list_phase(const ConSampleParams& p, int64_t u_begin,
-                                           int64_t u_end, unsigned char* smem) {
-  using C = Cfg<DT, VEC>;
-  if (!p.con.history && !p.con.mask) return;  // nothing is ever listed
-  __shared__ int listed;
-  uint32_t* lv = reinterpret_cast<uint32_t*>(smem);           // element
-  int32_t* lb = reinterpret_cast<int32_t*>(lv + kListCap);    // row
-  float* ly = reinterpret_cast<float*>(lb + kListCap);        // constrained logit
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int64_t NU = p.units_per_row;
-  TileCursor c = segment_at(u_begin / NU, u_begin, u_end, NU, C::kTile);
-  int64_t row = -1;
-  const uint8_t *mask = nullptr, *touched = nullptr;
-  float bs = -INFINITY;
-  int32_t bi = INT32_MAX, bb = -1;
-  if (tid == 0) listed = 0;
-  __syncthreads();
-  for (;;) {
-    // List tiles until they are done or the list is full; the words of four
-    // tiles are on their way at a time.
-    bool full = false;
-    while (c.valid && !full) {
-      constexpr int N = 4;
-      TileCursor t[N];
-      TileWords w[N];
+template <int DT>
+__global__ void __launch_bounds__(kListThreads) list_kernel(const ConSampleParams p,
+                                                            int32_t chunks, int32_t chunk_words) {
+  __shared__ uint32_t list[kListCap];
+  __shared__ int warp_sum[kListThreads / 32];
+  __shared__ unsigned long long warp_best[kListThreads / 32];
+  pdl_wait_then_release();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int64_t c = blockIdx.x; c < p.B * chunks; c += gridDim.x) {
+    const int64_t b = c / chunks;
+    const int32_t w_lo = (int32_t)(c - b * chunks) * chunk_words;
+    const int32_t w_hi = min(w_lo + chunk_words, (p.V + 31) / 32);
+    const RowConstraints r = row_constraints(p.con, b);
+    if (!r.mask && !r.touched) continue;  // the same for the whole CTA
+    const float T = __ldg(p.temperature + b);
+    const uint64_t sd = __ldg(p.seed + b), of = __ldg(p.offset + b);
+    uint32_t m[kListWords], t[kListWords];
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if (c.valid && c.b != row) {
-          row = c.b;
-          const RowConstraints r = row_constraints(p.con, row);
-          mask = r.mask;
-          touched = r.touched;
-        }
-        t[j] = c;
-        w[j] = load_words<DT, VEC>(c, mask, touched);
-        c = mask || touched ? next_tile<C::kTile>(c, u_end, NU)
-            : c.valid       ? next_row(c.b, u_end, NU, C::kTile)  // nothing in this row
-                            : c;
-        if (!mask && !touched) t[j].valid = false;
-      }
+    for (int k = 0; k < kListWords; ++k) {
+      const int32_t w = w_lo + k * kListThreads + tid;
+      const bool in = w < w_hi;
+      m[k] = !in      ? 0u
+             : r.mask ? __ldcg(reinterpret_cast<const uint32_t*>(r.mask) + w)
+                      : 0xFFFFFFFFu;
+      t[k] = in && r.touched ? __ldcg(reinterpret_cast<const uint32_t*>(r.touched) + w) : 0u;
+    }
+    int mine = 0;
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if (!t[j].valid || full) continue;
-        row_words<C::kEPU>(w[j], t[j].t0, p.V);
-        const uint32_t counts = tile_counts(w[j]);
-        const bool dense = tile_dense(counts);
-        const int n = (int)(dense ? counts >> 16 : counts & 0xFFFFu);
-        if (n == 0) continue;
-        int base = 0;
-        if (lane == 0) {  // reserve n entries, or nothing
-          int seen = *(volatile int*)&listed;
-          while (seen + n <= kListCap) {
-            const int was = atomicCAS(&listed, seen, seen + n);
-            if (was == seen) break;
-            seen = was;
-          }
-          base = seen;
-        }
-        base = __shfl_sync(0xFFFFFFFFu, base, 0);
-        if (base + n > kListCap) {  // this tile comes again after the list is scored
-          full = true;
-          c = t[j];
-          continue;
-        }
-        uint32_t b0 = dense ? w[j].touched[0] : w[j].allowed[0];
-        uint32_t b1 = dense ? w[j].touched[1] : w[j].allowed[1];
-        const int mine = __popc(b0) + __popc(b1);
-        int incl = mine;
+    for (int k = 0; k < kListWords; ++k) {
+      t[k] = split_word(m[k], t[k], (w_lo + k * kListThreads + tid) * 32, p.V).list;
+      mine += __popc(t[k]);
+    }
+    int incl = mine;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-          if (lane >= o) incl += up;
-        }
-        int at = base + incl - mine;
-        const uint32_t e0 = (uint32_t)(t[j].t0 * C::kEPU + lane * 32);
-        while ((b0 | b1) != 0u) {
-          const bool low = b0 != 0u;
-          const uint32_t b = low ? b0 : b1;
-          lv[at] = e0 + (low ? 0u : 1024u) + (uint32_t)__ffs((int)b) - 1u;
-          lb[at] = (int32_t)t[j].b;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int at0 = incl - mine, total = 0;
+#pragma unroll
+    for (int i = 0; i < kListThreads / 32; ++i) {
+      const int n = warp_sum[i];
+      if (i < warp) at0 += n;
+      total += n;
+    }
+    const PhiloxRow ph = philox_row((uint32_t)b, (uint32_t)of, (uint32_t)(of >> 32), (uint32_t)sd,
+                                    (uint32_t)(sd >> 32));
+    const char* row = p.logits + b * p.ld_bytes;
+    float bs = -INFINITY;
+    int32_t bi = INT32_MAX;
+    for (int base = 0; base < total; base += kListCap) {
+      int at = at0 - base;
+#pragma unroll
+      for (int k = 0; k < kListWords; ++k) {
+        uint32_t bits = t[k];
+        const uint32_t e0 = (uint32_t)(w_lo + k * kListThreads + tid) * 32u;
+        while (bits != 0u) {
+          if (at >= 0 && at < kListCap) list[at] = e0 + (uint32_t)__ffs((int)bits) - 1u;
+          bits &= bits - 1u;
           ++at;
-          if (low)
-            b0 &= b0 - 1u;
-          else
-            b1 &= b1 - 1u;
         }
       }
-    }
-    const bool more = __syncthreads_or(full) != 0;
-    const int n = listed;
-    // The constrained logits, four gathers a thread in flight.
-    for (int i0 = tid; i0 < n; i0 += 4 * kThreads) {
-      float x[4], bias[4];
-      uint32_t h[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int i = i0 + q * kThreads;
-        x[q] = -INFINITY;
-        h[q] = 0u;
-        bias[q] = 0.0f;
-        if (i < n) {
-          const int64_t b = lb[i];
-          const int32_t v = (int32_t)lv[i];
-          x[q] = load_elt<DT>(p.logits + b * p.ld_bytes, v);
-          const int64_t r = state_row_of(p.con, b);
-          if (r >= 0) {
-            h[q] = __ldcg(p.con.history + r * p.con.state_ld + v);
-            if (p.con.bias) bias[q] = __ldcg(p.con.bias + r * p.con.state_ld + v);
-          }
+      __syncthreads();
+      const int n = min(kListCap, total - base);
+#pragma unroll 2
+      for (int i = tid; i < n; i += kListThreads) {
+        const int32_t v = (int32_t)list[i];
+        const float x = load_elt<DT>(row, v);
+        const uint32_t h = r.history ? __ldcg(r.history + v) : 0u;
+        const float y = penalised(x, h, r.bias ? __ldcg(r.bias + v) : 0.0f, r.pen);
+        if (!(T > 0.0f)) {
+          take_better(y, v, bs, bi);
+        } else if (y > -INFINITY) {  // not NaN
+          const uint32_t w = word_of(philox_row_1((uint32_t)v >> 2, ph), v & 3);
+          take_better(exact_score(y, w, T), v, bs, bi);
         }
       }
-#pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
-        const int i = i0 + q * kThreads;
-        if (i >= n) break;
-        const float xq = q == 0 ? x[0] : q == 1 ? x[1] : q == 2 ? x[2] : x[3];
-        const uint32_t hq = q == 0 ? h[0] : q == 1 ? h[1] : q == 2 ? h[2] : h[3];
-        const float bq = q == 0 ? bias[0] : q == 1 ? bias[1] : q == 2 ? bias[2] : bias[3];
-        ly[i] = penalised(xq, hq, bq, row_penalties(p.con, lb[i]));  // read by this thread only
-      }
+      __syncthreads();
     }
-#pragma unroll 1
-    for (int i = tid; i < n; i += kThreads) {
-      const int32_t b = lb[i], v = (int32_t)lv[i];
-      const float y = ly[i];
-      if (b != bb) {
-        if (bb >= 0) publish(p, bb, bs, bi);
-        bb = b;
-        bs = -INFINITY;
-        bi = INT32_MAX;
-      }
-      const float T = __ldg(p.temperature + b);
-      if (!(T > 0.0f)) {
-        take_better(y, v, bs, bi);
-      } else if (y > -INFINITY) {
-        const uint64_t sd = __ldg(p.seed + b), of = __ldg(p.offset + b);
-        const PhiloxRow ph = philox_row((uint32_t)b, (uint32_t)of, (uint32_t)(of >> 32),
-                                        (uint32_t)sd, (uint32_t)(sd >> 32));
-        const uint32_t w = word_of(philox_row_1((uint32_t)v >> 2, ph), v & 3);
-        take_better(exact_score(y, w, T), v, bs, bi);
-      }
+    if (total == 0) {
+      __syncthreads();  // warp_sum is rewritten by the next round
+      continue;
     }
-    __syncthreads();
-    if (!more) break;
-    if (tid == 0) listed = 0;
-    __syncthreads();
-  }
-  int same = 0;
-  __match_all_sync(0xFFFFFFFFu, bb, &same);
-  if (same) {
     warp_argmax(bs, bi);
-    if (lane == 0 && bb >= 0) publish(p, bb, bs, bi);
-  } else if (bb >= 0) {
-    publish(p, bb, bs, bi);
+    if (lane == 0) warp_best[warp] = bi != INT32_MAX && bs > -INFINITY ? pack_key(bs, bi) : 0ull;
+    __syncthreads();
+    if (warp == 0) {
+      const unsigned long long k =
+          warp_max_u64(lane < kListThreads / 32 ? warp_best[lane] : 0ull);
+      if (lane == 0 && k != 0ull) {
+        atomicMax(&p.ws[b].key, k);
+        atomicMax(&p.ws[b].hint, (uint32_t)(k >> 32));
+      }
+    }
   }
-  // The rows' slots hold these before any warp of the CTA takes a ticket.
-  __threadfence();
-  __syncthreads();
 }
 
 // Greedy over a constrained tile: the running best may already hold a touched
@@ -1049,10 +976,6 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
 
   const int64_t NU = p.units_per_row, NW = p.warps;
   const int64_t gw = (int64_t)blockIdx.x * kWarps + warp;
-  if constexpr (CON) {
-    const int64_t w0 = gw < NW ? gw : NW, w1 = gw < NW ? gw + 1 : NW;
-    list_phase<DT, VEC>(p, split_point<VEC>(p, w0, true), split_point<VEC>(p, w1, true), smem);
-  }
   if (gw >= NW) return;
   const int64_t u_begin = split_point<VEC>(p, gw, CON), u_end = split_point<VEC>(p, gw + 1, CON);
   if (u_begin >= u_end) return;  // no units (only with fewer than 8 units per warp)
@@ -1060,10 +983,10 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
   // Prologue: the first kStages - 1 tiles go in flight.
   TileCursor cur = segment_at(u_begin / NU, u_begin, u_end, NU, C::kTile);
   TileCursor ahead = cur;
-  // Constrained rows: the words of the current tile, of the one in flight and
-  // of the one after, and the bit rows that those of the last come from.
-  [[maybe_unused]] TileWords words, words_ahead, words_next;
-  [[maybe_unused]] uint32_t counts = 0u, counts_ahead = 0u;
+  // Constrained rows: the sweep's words of the current tile and of the one in
+  // flight, the raw words of the one after, and the bit rows those come from.
+  [[maybe_unused]] uint32_t words[2] = {0u, 0u}, words_ahead[2] = {0u, 0u};
+  [[maybe_unused]] TileWords words_next;
   [[maybe_unused]] const uint8_t *mask_next = nullptr, *touched_next = nullptr;
   auto next_words = [&](int64_t row_before) {
     if constexpr (CON) {
@@ -1079,10 +1002,13 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
   // of the one after it.
   auto advance = [&](uint32_t stage) {
     if constexpr (CON) {
-      words_ahead = words_next;
-      row_words<C::kEPU>(words_ahead, ahead.t0, p.V);
-      counts_ahead = tile_counts(words_ahead);
-      if (tile_dense(counts_ahead)) issue_tile_masked<DT, VEC>(p, ahead, words_ahead, stage, pol);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        words_ahead[i] = split_word(words_next.mask[i], words_next.touched[i],
+                                    ahead.t0 * C::kEPU + i * 1024 + lane * 32, p.V)
+                             .sweep;
+      if (__any_sync(0xFFFFFFFFu, (words_ahead[0] | words_ahead[1]) != 0u))
+        issue_tile_masked<DT, VEC>(p, ahead, words_ahead[0], words_ahead[1], stage, pol);
       cp_async_commit();
       const int64_t row = ahead.b;
       ahead = next_tile<C::kTile>(ahead, u_end, NU);
@@ -1129,22 +1055,22 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
     // Refill the ring slot that the previous tile freed.
     int fill = slot + kStages - 1;
     if (fill >= kStages) fill -= kStages;
+    bool left = true;  // whether the tile may hold a candidate
     if constexpr (CON) {
-      words = words_ahead;
-      counts = counts_ahead;
+      words[0] = words_ahead[0];
+      words[1] = words_ahead[1];
       advance(ring + fill * C::kTileBytes);
-      if (tile_dense(counts))
-        clear_tile<DT, VEC>(stage, words.allowed[0] & ~words.touched[0],
-                            words.allowed[1] & ~words.touched[1],
-                            (cur.t_hi - cur.t0) * C::kEPU - (int)(counts & 0xFFFFu) +
-                                (int)(counts >> 16));
+      const int swept = (int)__reduce_add_sync(0xFFFFFFFFu, __popc(words[0]) + __popc(words[1]));
+      left = swept > 0;
+      if (left)
+        clear_tile<DT, VEC>(stage, words[0], words[1],
+                            (cur.t_hi - cur.t0) * C::kEPU - swept);
     } else {
       issue_tile<DT, VEC>(p, ahead, ring + fill * C::kTileBytes, pol);
       ahead = next_tile<C::kTile>(ahead, u_end, NU);
     }
 
     const int32_t t0 = cur.t0, t_hi = cur.t_hi;
-    bool left = !CON || tile_dense(counts);  // whether the tile may hold a candidate
     if (rc.T > 0.0f) {
       seen = seg_first ? 0u : pending;
       // The first bound of the row's part: each lane's best of the first tile
@@ -1286,6 +1212,25 @@ cudaError_t launch_sample(const SampleParams& p, int dtype, bool vec, cudaStream
 }
 
 cudaError_t launch_sample(const ConSampleParams& p, int dtype, bool vec, cudaStream_t stream) {
+  if (p.con.history || p.con.mask) {  // else nothing is ever listed
+    const int32_t words = (p.V + 31) / 32, most = kListThreads * kListWords;
+    int32_t chunks = (words + most - 1) / most;
+    int32_t chunk_words = (words + chunks - 1) / chunks;
+    const int64_t blocks = p.B * chunks;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks < INT32_MAX ? blocks : INT32_MAX));
+    cfg.blockDim = dim3(kListThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void* args[] = {const_cast<ConSampleParams*>(&p), &chunks, &chunk_words};
+    void* fn = dtype == 0   ? reinterpret_cast<void*>(&list_kernel<0>)
+               : dtype == 1 ? reinterpret_cast<void*>(&list_kernel<1>)
+                            : reinterpret_cast<void*>(&list_kernel<2>);
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
+    if (e != cudaSuccess) return e;
+  }
   return launch_kernel(select_kernel(dtype, vec, true), p, const_cast<ConSampleParams*>(&p),
                        sample_smem_bytes(dtype, vec), stream);
 }
