@@ -257,6 +257,39 @@ void plan_sample(const DeviceInfo& d, const void* logits, gsample_dtype dtype, i
   *vec_out = vec;
 }
 
+#ifndef GSAMPLE_MIN_CHUNKS
+#define GSAMPLE_MIN_CHUNKS 2
+#endif
+
+// The chunks of a constrained launch, multiples of 8 units dealt to the warps
+// in turn. With k chunks a warp, rows cut into floor(k * warps / B) of them end
+// together; of k = 2 .. 12 the one whose warps have least to do is taken, a
+// chunk's fixed costs (row context, merge) counting as kChunkUnits units. Two
+// or more a warp, because rows differ in work: a warp that meets a row with
+// nothing left has another.
+void plan_chunks(gsample::ConSampleParams* p) {
+  constexpr int64_t kChunkUnits = 64;
+  const int64_t nu = p->units_per_row, warps = (int64_t)p->ctas * gsample::kWarps;
+  int64_t best = -1, units = 8;
+  for (int64_t k = GSAMPLE_MIN_CHUNKS; k <= 12; ++k) {
+    const int64_t per_row = k * warps / p->B;
+    if (per_row < 1) continue;
+    int64_t u = (nu + per_row - 1) / per_row;
+    u = (u + 7) / 8 * 8;
+    const int64_t rounds = (p->B * ((nu + u - 1) / u) + warps - 1) / warps;
+    const int64_t cost = rounds * (u + kChunkUnits);
+    if (best < 0 || cost < best) {
+      best = cost;
+      units = u;
+    }
+  }
+  if (best < 0) units = (nu + 7) / 8 * 8;  // more rows than 12 a warp: a row a chunk
+  p->chunk_units = (int32_t)units;
+  p->chunks_per_row = (int32_t)((nu + units - 1) / units);
+  p->total_chunks = (uint32_t)(p->B * p->chunks_per_row);
+  p->warps = warps < (int64_t)p->total_chunks ? warps : (int64_t)p->total_chunks;
+}
+
 // Batches of at most this many rows take the cluster-per-row kernel; a CTA of
 // it gets at least this many units.
 constexpr int64_t kClusterMaxRows = 64;
@@ -328,6 +361,7 @@ gsample_status run_sample(const void* logits, gsample_dtype dtype, int64_t B, in
   cudaError_t err;
   if (con) {
     p.con = *con;
+    plan_chunks(&p);
     err = gsample::launch_sample(p, (int)dtype, vec, stream);
   } else {
     err = gsample::launch_sample(static_cast<const SampleParams&>(p), (int)dtype, vec, stream);

@@ -40,9 +40,13 @@ struct SampleParams {
   WsRow* ws;
 };
 
-// The same launch, drawing from constrained logits.
+// The same launch, drawing from constrained logits: each row is cut into
+// chunks of chunk_units units, dealt to the warps in turn.
 struct ConSampleParams : SampleParams {
   ConstrainArgs con;
+  int32_t chunk_units;
+  int32_t chunks_per_row;
+  uint32_t total_chunks;
 };
 
 // One row's curve; the same layout as the public gsample_hlg_params.

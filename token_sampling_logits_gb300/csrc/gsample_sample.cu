@@ -671,9 +671,12 @@ __device__ __forceinline__ void issue_tile(const SampleParams& p, const TileCurs
 // hide the gathers, and the low ids, where most tokens of a request lie, keep
 // one warp of a row long after the others.
 //
-// Split points lie on multiples of 8 units of the row (32 or 64 elements), so a
-// tile's bits are whole words: lane l holds words l and, for 16-bit units (64
-// words a tile), l + 32.
+// Rows differ in work here (a row whose grammar allows a few tokens has none),
+// so the warps take chunks of rows in turn rather than one contiguous range
+// each: chunk c, of chunk_units units, goes to warp c modulo the number of
+// warps. A chunk starts on a multiple of 8 units of its row (32 or 64
+// elements), so a tile's bits are whole words: lane l holds words l and, for
+// 16-bit units (64 words a tile), l + 32.
 // ---------------------------------------------------------------------------
 constexpr int kFewInWord = 8;
 constexpr int kClearBits = 256;  // up to this many cleared elements: one by one, not by units
@@ -728,6 +731,35 @@ __device__ __forceinline__ uint32_t unit_of_words(uint32_t w0, uint32_t w1, int 
     const uint32_t w = __shfl_sync(0xFFFFFFFFu, w0, k * 4 + (lane >> 3));
     return (w >> ((lane & 7) * 4)) & 0xFu;
   }
+}
+
+// The first tile of chunk c.
+__device__ __forceinline__ TileCursor chunk_at(const ConSampleParams& p, uint32_t c, int tile) {
+  TileCursor t;
+  const uint32_t b = c / (uint32_t)p.chunks_per_row;
+  t.b = b;
+  t.valid = c < p.total_chunks;
+  t.seg_lo = (int32_t)(c - b * (uint32_t)p.chunks_per_row) * p.chunk_units;
+  t.seg_hi = min(t.seg_lo + p.chunk_units, p.units_per_row);
+  t.t0 = t.seg_lo;
+  t.t_hi = min(t.t0 + tile, t.seg_hi);
+  return t;
+}
+
+// The tile after t in the warp's chunks; c is t's chunk, and then its
+// successor's.
+template <int TILE>
+__device__ __forceinline__ TileCursor next_chunk_tile(const ConSampleParams& p,
+                                                      const TileCursor& t, uint32_t& c) {
+  if (!t.valid) return t;
+  if (t.t_hi < t.seg_hi) {
+    TileCursor n = t;
+    n.t0 = t.t_hi;
+    n.t_hi = min(n.t0 + TILE, t.seg_hi);
+    return n;
+  }
+  c += (uint32_t)p.warps;
+  return chunk_at(p, c, TILE);
 }
 
 // issue_tile for constrained rows: units without an element of the sweep (the
@@ -806,33 +838,47 @@ __device__ __forceinline__ void clear_tile(uint32_t stage, uint32_t keep0, uint3
   __syncwarp();  // other lanes read the places
 }
 
-// The list kernel: one CTA takes a run of words of one row, lists their listed
-// elements in shared memory in order, and shares them out among its threads.
-constexpr int kListThreads = 256;
-constexpr int kListWords = 4;    // words a thread
-constexpr int kListCap = 2048;   // entries listed at a time
+// The list kernel. Every warp works alone: it takes kListWords words a lane of
+// one row, lists their listed elements in shared memory and scores them one a
+// lane. Its words come in small groups spread over the row, because the low ids
+// hold most of a request's tokens: of 1600 touched tokens some 700 lie in the
+// first 64 words, and one warp with all of them would work long after the
+// others.
+#ifndef GSAMPLE_LIST_WORDS
+#define GSAMPLE_LIST_WORDS 8
+#endif
+#ifndef GSAMPLE_LIST_CTAS
+#define GSAMPLE_LIST_CTAS 8
+#endif
+#ifndef GSAMPLE_LIST_GROUP
+#define GSAMPLE_LIST_GROUP 4
+#endif
+constexpr int kListThreads = 128;
+constexpr int kListWords = GSAMPLE_LIST_WORDS;  // words a lane
+constexpr int kListCap = 256;                   // entries a warp lists at a time
 
 template <int DT>
-__global__ void __launch_bounds__(kListThreads) list_kernel(const ConSampleParams p,
-                                                            int32_t chunks, int32_t chunk_words) {
-  __shared__ uint32_t list[kListCap];
-  __shared__ int warp_sum[kListThreads / 32];
-  __shared__ unsigned long long warp_best[kListThreads / 32];
+__global__ void __launch_bounds__(kListThreads, GSAMPLE_LIST_CTAS)
+    list_kernel(const ConSampleParams p, int32_t warps_per_row) {
+  __shared__ uint32_t lists[kListThreads / 32][kListCap];
   pdl_wait_then_release();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int64_t c = blockIdx.x; c < p.B * chunks; c += gridDim.x) {
-    const int64_t b = c / chunks;
-    const int32_t w_lo = (int32_t)(c - b * chunks) * chunk_words;
-    const int32_t w_hi = min(w_lo + chunk_words, (p.V + 31) / 32);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t q = (int32_t)blockIdx.x * (kListThreads / 32) + warp;
+  if (q >= warps_per_row) return;
+  uint32_t* list = lists[warp];
+  const int32_t words = (p.V + 31) / 32;
+  // The lane's k-th word: of the warp's 32 / G groups a step, warps_per_row apart.
+  constexpr int G = GSAMPLE_LIST_GROUP;
+  const int32_t w0 = (q + (lane / G) * warps_per_row) * G + lane % G;
+  const int32_t step = warps_per_row * 32;
+  for (int64_t b = blockIdx.y; b < p.B; b += gridDim.y) {
     const RowConstraints r = row_constraints(p.con, b);
-    if (!r.mask && !r.touched) continue;  // the same for the whole CTA
-    const float T = __ldg(p.temperature + b);
-    const uint64_t sd = __ldg(p.seed + b), of = __ldg(p.offset + b);
+    if (!r.mask && !r.touched) continue;
     uint32_t m[kListWords], t[kListWords];
 #pragma unroll
     for (int k = 0; k < kListWords; ++k) {
-      const int32_t w = w_lo + k * kListThreads + tid;
-      const bool in = w < w_hi;
+      const int32_t w = w0 + k * step;
+      const bool in = w < words;
       m[k] = !in      ? 0u
              : r.mask ? __ldcg(reinterpret_cast<const uint32_t*>(r.mask) + w)
                       : 0xFFFFFFFFu;
@@ -841,7 +887,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const ConSampleParam
     int mine = 0;
 #pragma unroll
     for (int k = 0; k < kListWords; ++k) {
-      t[k] = split_word(m[k], t[k], (w_lo + k * kListThreads + tid) * 32, p.V).list;
+      t[k] = split_word(m[k], t[k], (w0 + k * step) * 32, p.V).list;
       mine += __popc(t[k]);
     }
     int incl = mine;
@@ -850,63 +896,54 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const ConSampleParam
       const int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
       if (lane >= o) incl += up;
     }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    int at0 = incl - mine, total = 0;
-#pragma unroll
-    for (int i = 0; i < kListThreads / 32; ++i) {
-      const int n = warp_sum[i];
-      if (i < warp) at0 += n;
-      total += n;
-    }
-    const PhiloxRow ph = philox_row((uint32_t)b, (uint32_t)of, (uint32_t)(of >> 32), (uint32_t)sd,
-                                    (uint32_t)(sd >> 32));
+    const int total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+    if (total == 0) continue;
     const char* row = p.logits + b * p.ld_bytes;
+    const float T = __ldg(p.temperature + b);
+    const uint64_t sd = __ldg(p.seed + b), of = __ldg(p.offset + b);
     float bs = -INFINITY;
     int32_t bi = INT32_MAX;
     for (int base = 0; base < total; base += kListCap) {
-      int at = at0 - base;
+      int at = incl - mine - base;
 #pragma unroll
       for (int k = 0; k < kListWords; ++k) {
-        uint32_t bits = t[k];
-        const uint32_t e0 = (uint32_t)(w_lo + k * kListThreads + tid) * 32u;
-        while (bits != 0u) {
+        const uint32_t e0 = (uint32_t)(w0 + k * step) * 32u;
+        for (uint32_t bits = t[k]; bits != 0u; bits &= bits - 1u, ++at)
           if (at >= 0 && at < kListCap) list[at] = e0 + (uint32_t)__ffs((int)bits) - 1u;
-          bits &= bits - 1u;
-          ++at;
-        }
       }
-      __syncthreads();
+      __syncwarp();
       const int n = min(kListCap, total - base);
-#pragma unroll 2
-      for (int i = tid; i < n; i += kListThreads) {
-        const int32_t v = (int32_t)list[i];
-        const float x = load_elt<DT>(row, v);
-        const uint32_t h = r.history ? __ldcg(r.history + v) : 0u;
-        const float y = penalised(x, h, r.bias ? __ldcg(r.bias + v) : 0.0f, r.pen);
-        if (!(T > 0.0f)) {
-          take_better(y, v, bs, bi);
-        } else if (y > -INFINITY) {  // not NaN
-          const uint32_t w = word_of(philox_row_1((uint32_t)v >> 2, ph), v & 3);
-          take_better(exact_score(y, w, T), v, bs, bi);
-        }
+      const PhiloxRow ph = philox_row((uint32_t)b, (uint32_t)of, (uint32_t)(of >> 32),
+                                      (uint32_t)sd, (uint32_t)(sd >> 32));
+      // The next element's gathers are on their way while one is scored.
+      int32_t v_next = 0;
+      float x_next = 0.0f, bias_next = 0.0f;
+      uint32_t h_next = 0u;
+      auto gather = [&](int i) {
+        if (i >= n) return;
+        v_next = (int32_t)list[i];
+        x_next = load_elt<DT>(row, v_next);
+        if (r.history) h_next = __ldcg(r.history + v_next);
+        if (r.bias) bias_next = __ldcg(r.bias + v_next);
+      };
+      gather(lane);
+#pragma unroll 1
+      for (int i = lane; i < n; i += 32) {
+        const int32_t v = v_next;
+        const float x = x_next, bias = bias_next;
+        const uint32_t h = h_next;
+        gather(i + 32);
+        const uint32_t w = word_of(philox_row_1((uint32_t)v >> 2, ph), v & 3);
+        const float y = penalised(x, h, bias, r.pen);
+        if (y > -INFINITY)  // not NaN
+          take_better(T > 0.0f ? exact_score(y, w, T) : y, v, bs, bi);
       }
-      __syncthreads();
-    }
-    if (total == 0) {
-      __syncthreads();  // warp_sum is rewritten by the next round
-      continue;
+      __syncwarp();
     }
     warp_argmax(bs, bi);
-    if (lane == 0) warp_best[warp] = bi != INT32_MAX && bs > -INFINITY ? pack_key(bs, bi) : 0ull;
-    __syncthreads();
-    if (warp == 0) {
-      const unsigned long long k =
-          warp_max_u64(lane < kListThreads / 32 ? warp_best[lane] : 0ull);
-      if (lane == 0 && k != 0ull) {
-        atomicMax(&p.ws[b].key, k);
-        atomicMax(&p.ws[b].hint, (uint32_t)(k >> 32));
-      }
+    if (lane == 0 && bi != INT32_MAX && bs > -INFINITY) {
+      atomicMax(&p.ws[b].key, pack_key(bs, bi));
+      atomicMax(&p.ws[b].hint, ordered_bits(bs));
     }
   }
 }
@@ -946,14 +983,12 @@ __device__ __forceinline__ float score_of_hint(uint32_t h) {
 // lines: with ranges that split lines, both neighbours fetch the shared line,
 // and host reads measured a third slower. Device reads are unaffected.
 template <bool VEC>
-__device__ __forceinline__ int64_t split_point(const SampleParams& p, int64_t w,
-                                               bool constrained = false) {
+__device__ __forceinline__ int64_t split_point(const SampleParams& p, int64_t w) {
   const int64_t U = p.total_units, NW = p.warps;
   const int64_t base = U / NW, rem = U % NW;
   const int64_t u = w * base + (w < rem ? w : rem);
-  if ((!VEC && !constrained) || u >= U) return u;
+  if (!VEC || u >= U) return u;
   const int64_t NU = p.units_per_row, b = u / NU, l = u - b * NU;
-  if (constrained) return b * NU + (l & ~(int64_t)7);  // whole words of the row's bits
   const uint64_t row_unit = (uint64_t)(uintptr_t)(p.logits + b * p.ld_bytes) / 16u;
   const int64_t la = l - (int64_t)((row_unit + (uint64_t)l) & 7u);
   return b * NU + (la > 0 ? la : 0);
@@ -977,11 +1012,19 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
   const int64_t NU = p.units_per_row, NW = p.warps;
   const int64_t gw = (int64_t)blockIdx.x * kWarps + warp;
   if (gw >= NW) return;
-  const int64_t u_begin = split_point<VEC>(p, gw, CON), u_end = split_point<VEC>(p, gw + 1, CON);
-  if (u_begin >= u_end) return;  // no units (only with fewer than 8 units per warp)
+  TileCursor cur;
+  [[maybe_unused]] int64_t u_end = 0;
+  [[maybe_unused]] uint32_t chunk = (uint32_t)gw, chunk_ahead = (uint32_t)gw;
+  if constexpr (CON) {
+    cur = chunk_at(p, chunk, C::kTile);
+  } else {
+    const int64_t u_begin = split_point<VEC>(p, gw);
+    u_end = split_point<VEC>(p, gw + 1);
+    if (u_begin >= u_end) return;  // no units (only with fewer than 8 units per warp)
+    cur = segment_at(u_begin / NU, u_begin, u_end, NU, C::kTile);
+  }
 
   // Prologue: the first kStages - 1 tiles go in flight.
-  TileCursor cur = segment_at(u_begin / NU, u_begin, u_end, NU, C::kTile);
   TileCursor ahead = cur;
   // Constrained rows: the sweep's words of the current tile and of the one in
   // flight, the raw words of the one after, and the bit rows those come from.
@@ -1011,7 +1054,7 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
         issue_tile_masked<DT, VEC>(p, ahead, words_ahead[0], words_ahead[1], stage, pol);
       cp_async_commit();
       const int64_t row = ahead.b;
-      ahead = next_tile<C::kTile>(ahead, u_end, NU);
+      ahead = next_chunk_tile<C::kTile>(p, ahead, chunk_ahead);
       next_words(row);
     }
   };
@@ -1028,8 +1071,24 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
   }
 
   RowCtx rc = row_context(p, cur.b);
-  // The next row's parameters, loaded a whole segment before they are needed.
-  RowParams next_params = load_row_params(p, cur.b + 1);
+  // The next row's parameters, loaded a whole segment before they are needed
+  // (constrained rows: the next chunk's, and its row's hint, a valid if stale
+  // bound).
+  RowParams next_params;
+  [[maybe_unused]] uint32_t hint_known = 0u, hint_next = 0u;
+  auto load_next = [&]() {
+    if constexpr (CON) {
+      const int64_t b = (chunk + (uint32_t)NW) / (uint32_t)p.chunks_per_row;
+      next_params = load_row_params(p, b);
+      hint_next = b < p.B ? __ldcg(&p.ws[b].hint) : 0u;
+    }
+  };
+  if constexpr (CON) {
+    hint_known = __ldcg(&rc.ws->hint);
+    load_next();
+  } else {
+    next_params = load_row_params(p, cur.b + 1);
+  }
   bool seg_first = true;
   float bs = -INFINITY;
   int32_t bi = INT32_MAX;
@@ -1072,13 +1131,14 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
 
     const int32_t t0 = cur.t0, t_hi = cur.t_hi;
     if (rc.T > 0.0f) {
-      seen = seg_first ? 0u : pending;
+      seen = !seg_first ? pending : CON ? hint_known : 0u;
       // The first bound of the row's part: each lane's best of the first tile
-      // (for constrained rows, of the first tile that holds any candidate).
+      // (for constrained rows, of the first tile that holds any candidate, and
+      // only where the row has no hint yet).
       bool first = seg_first;
       if constexpr (CON) {
         const bool known = __any_sync(0xFFFFFFFFu, bi != INT32_MAX || seen != 0u);
-        first = left && (seg_first || !known);
+        first = left && !known;
       }
       if (first) {
         [[maybe_unused]] const bool found =
@@ -1131,15 +1191,26 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
         tk_row = cur.b;
         tk_pending = true;
       }
-      cur = next_tile<C::kTile>(cur, u_end, NU);
+      if constexpr (CON)
+        cur = next_chunk_tile<C::kTile>(p, cur, chunk);
+      else
+        cur = next_tile<C::kTile>(cur, u_end, NU);
       if (!cur.valid) break;
       rc = row_context_from(p, cur.b, next_params);
-      next_params = load_row_params(p, cur.b + 1);
+      if constexpr (CON) {
+        hint_known = hint_next;
+        load_next();
+      } else {
+        next_params = load_row_params(p, cur.b + 1);
+      }
       bs = -INFINITY;
       bi = INT32_MAX;
       seg_first = true;
     } else {
-      cur = next_tile<C::kTile>(cur, u_end, NU);
+      if constexpr (CON)
+        cur = next_chunk_tile<C::kTile>(p, cur, chunk);
+      else
+        cur = next_tile<C::kTile>(cur, u_end, NU);
       seg_first = false;
     }
     slot = slot + 1 == kStages ? 0 : slot + 1;
@@ -1213,18 +1284,17 @@ cudaError_t launch_sample(const SampleParams& p, int dtype, bool vec, cudaStream
 
 cudaError_t launch_sample(const ConSampleParams& p, int dtype, bool vec, cudaStream_t stream) {
   if (p.con.history || p.con.mask) {  // else nothing is ever listed
-    const int32_t words = (p.V + 31) / 32, most = kListThreads * kListWords;
-    int32_t chunks = (words + most - 1) / most;
-    int32_t chunk_words = (words + chunks - 1) / chunks;
-    const int64_t blocks = p.B * chunks;
+    const int32_t words = (p.V + 31) / 32, per_warp = 32 * kListWords;
+    int32_t warps_per_row = (words + per_warp - 1) / per_warp;
+    const unsigned ctas = (unsigned)((warps_per_row + kListThreads / 32 - 1) / (kListThreads / 32));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(blocks < INT32_MAX ? blocks : INT32_MAX));
+    cfg.gridDim = dim3(ctas, (unsigned)(p.B < 65535 ? p.B : 65535));
     cfg.blockDim = dim3(kListThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    void* args[] = {const_cast<ConSampleParams*>(&p), &chunks, &chunk_words};
+    void* args[] = {const_cast<ConSampleParams*>(&p), &warps_per_row};
     void* fn = dtype == 0   ? reinterpret_cast<void*>(&list_kernel<0>)
                : dtype == 1 ? reinterpret_cast<void*>(&list_kernel<1>)
                             : reinterpret_cast<void*>(&list_kernel<2>);
