@@ -1133,12 +1133,13 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
     if (rc.T > 0.0f) {
       seen = !seg_first ? pending : CON ? hint_known : 0u;
       // The first bound of the row's part: each lane's best of the first tile
-      // (for constrained rows, of the first tile that holds any candidate, and
-      // only where the row has no hint yet).
+      // (for constrained rows, also of the first tile that holds any candidate;
+      // the list kernel's hint alone is a weak bound, the best of a hundredth
+      // of the row).
       bool first = seg_first;
       if constexpr (CON) {
         const bool known = __any_sync(0xFFFFFFFFu, bi != INT32_MAX || seen != 0u);
-        first = left && !known;
+        first = left && (seg_first || !known);
       }
       if (first) {
         [[maybe_unused]] const bool found =
