@@ -42,7 +42,7 @@ def test_bad_states_are_refused_by_every_call(kw):
     assert L.gsample_history_append(ref(s), None, 0, FAKE, 0, FAKE, 0, None) == BAD
     assert L.gsample_bias_set(ref(s), None, 0, FAKE, FAKE, 0, FAKE, None) == BAD
     c = gs._ConstraintsC()
-    c.state = ctypes.pointer(s)
+    c.state, c.keep = ctypes.addressof(s), s
     c.slot = FAKE
     V = s.vocab if 0 < s.vocab < (1 << 31) - 128 else 100
     assert L.gsample_process_logits(FAKE, gs.F32, 2, V, V, ctypes.byref(c), FAKE + (1 << 30),
@@ -100,7 +100,7 @@ def test_kind_slots_and_missing_biases():
 def constraints(s=None, **kw):
     c = gs._ConstraintsC()
     if s is not None:
-        c.state = ctypes.pointer(s)
+        c.state, c.keep = ctypes.addressof(s), s
     for k, v in kw.items():
         setattr(c, k, v)
     return c

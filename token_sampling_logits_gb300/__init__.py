@@ -13,7 +13,6 @@ All calls are asynchronous on ``torch.cuda.current_stream()``.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -53,7 +52,8 @@ class _StateC(ctypes.Structure):
 
 
 class _ConstraintsC(ctypes.Structure):
-    _fields_ = [("state", ctypes.POINTER(_StateC)), ("slot", _vp), ("repetition", _vp),
+    # state: the address of a _StateC that outlives the call
+    _fields_ = [("state", _vp), ("slot", _vp), ("repetition", _vp),
                 ("frequency", _vp), ("presence", _vp), ("mask", _vp), ("mask_rows", _i64),
                 ("mask_ld", _i64), ("mask_row", _vp)]
 
@@ -92,6 +92,8 @@ def lib() -> ctypes.CDLL:
     """Load libgsample.so (building it first if its sources are newer).
     Raises if the library cannot be built or loaded: there is no fallback."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -162,18 +164,26 @@ def _check(status: int, what: str) -> None:
 # --------------------------------------------------------------------------
 # torch marshalling
 # --------------------------------------------------------------------------
-def _torch():
-    import torch
+_torch_mod = None
+_DTYPES = {}
 
-    return torch
+
+def _torch():
+    global _torch_mod
+    if _torch_mod is None:
+        import torch
+
+        _DTYPES.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
+        _torch_mod = torch
+    return _torch_mod
 
 
 def _dtype_code(t) -> int:
-    torch = _torch()
-    m = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
-    if t.dtype not in m:
+    _torch()
+    code = _DTYPES.get(t.dtype)
+    if code is None:
         raise TypeError("logits must be float32, bfloat16 or float16, got %s" % t.dtype)
-    return m[t.dtype]
+    return code
 
 
 def _stream_ptr(device) -> int:
@@ -186,18 +196,19 @@ def _logits_args(logits):
         raise ValueError("logits must be a CUDA tensor")
     if logits.dim() != 2:
         raise ValueError("logits must be 2-D [B, V]")
-    if logits.stride(1) != 1:
+    ld, inner = logits.stride()
+    if inner != 1:
         raise ValueError("logits rows must be contiguous (stride(1) == 1)")
     B, V = logits.shape
-    ld = logits.stride(0) if B > 1 else V
-    return _dtype_code(logits), B, V, ld
+    return _dtype_code(logits), B, V, ld if B > 1 else V
 
 
 def _row_tensor(x, B, dtype, device, name):
     torch = _torch()
-    if not torch.is_tensor(x):
+    if not isinstance(x, torch.Tensor):
         x = torch.full((B,), x, dtype=dtype, device=device)
-    if x.dtype != dtype or x.device != device or x.shape != (B,) or not x.is_contiguous():
+    if x.dtype != dtype or x.device != device or x.dim() != 1 or x.numel() != B or \
+            not x.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape [%d] on %s" %
                          (name, dtype, B, device))
     return x
@@ -460,6 +471,7 @@ class LogitState:
         self.rows, self.ld, self.device = rows, ld, dev
         self._c = _StateC(history.data_ptr(), None if bias is None else bias.data_ptr(),
                           touched.data_ptr(), rows, self.vocab, ld)
+        self._at = ctypes.addressof(self._c)
 
 
 def new_logit_state(rows: int, vocab: int, device=None, bias: bool = True) -> LogitState:
@@ -472,44 +484,52 @@ def new_logit_state(rows: int, vocab: int, device=None, bias: bool = True) -> Lo
                       torch.zeros((rows, ld // 32), dtype=torch.int32, device=dev), vocab)
 
 
-def _on(device):
-    """The tensors' device as the current one (the library launches there)."""
+def _launch(device, what, fn, *args):
+    """fn(*args, the device's current stream) with the device as the current
+    one (the library launches there)."""
     torch = _torch()
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+    index = device.index
+    if torch.cuda.current_device() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != OK:
+        raise GSampleError(status, what)
 
 
 def _vector(x, n, dtype, device, name):
-    if x is not None and (x.dtype != dtype or x.device != device or x.dim() != 1 or
-                          (n is not None and x.shape[0] != n) or not x.is_contiguous()):
+    """The address of a contiguous 1-D tensor of n (None: any number of)
+    entries; None for None."""
+    if x is None:
+        return None
+    if x.dtype != dtype or x.device != device or x.dim() != 1 or \
+            (n is not None and x.numel() != n) or not x.is_contiguous():
         raise ValueError("%s must be a contiguous 1-D %s tensor%s on %s" %
                          (name, dtype, "" if n is None else " of %d entries" % n, device))
-    return x
+    return x.data_ptr()
 
 
 def _lists(state, slots, tokens, offsets):
+    """n requests: (slot, n, tokens, total, offsets) as the library takes them."""
     torch = _torch()
-    _vector(tokens, None, torch.int64, state.device, "tokens")
-    _vector(offsets, None, torch.int64, state.device, "offsets")
-    if offsets is not None and offsets.shape[0] < 1:
-        raise ValueError("offsets has one entry more than there are requests")
-    n = tokens.shape[0] if offsets is None else offsets.shape[0] - 1
-    _vector(slots, n, torch.int32, state.device, "slots")
-    return n
+    dev = state.device
+    tokens_at = _vector(tokens, None, torch.int64, dev, "tokens")
+    offsets_at = _vector(offsets, None, torch.int64, dev, "offsets")
+    total = tokens.numel()
+    n = total
+    if offsets is not None:
+        n = offsets.numel() - 1
+        if n < 0:
+            raise ValueError("offsets has one entry more than there are requests")
+    return _vector(slots, n, torch.int32, dev, "slots"), n, tokens_at, total, offsets_at
 
 
 def state_reset(state: LogitState, slots=None) -> None:
     """Clears the state rows in `slots` (int32 device tensor), or all of them."""
-    _vector(slots, None, _torch().int32, state.device, "slots")
-    n = state.rows if slots is None else slots.shape[0]
-    with _on(state.device):
-        _check(lib().gsample_state_reset(ctypes.byref(state._c), _ptr(slots), n,
-                                         _stream_ptr(state.device)), "gsample_state_reset")
+    at = _vector(slots, None, _torch().int32, state.device, "slots")
+    _launch(state.device, "gsample_state_reset", lib().gsample_state_reset, state._at, at,
+            state.rows if slots is None else slots.numel())
 
 
 def history_append(state: LogitState, tokens, slots=None, offsets=None,
@@ -518,64 +538,66 @@ def history_append(state: LogitState, tokens, slots=None, offsets=None,
     i owns tokens[offsets[i]:offsets[i + 1]], or tokens[i] alone without
     offsets (the indices a sampler just drew). slots[i] (int32) is its state
     row; without slots, row i. Ids outside the vocabulary are ignored."""
-    n = _lists(state, slots, tokens, offsets)
-    with _on(state.device):
-        _check(lib().gsample_history_append(ctypes.byref(state._c), _ptr(slots), n, _ptr(tokens),
-                                            tokens.shape[0], _ptr(offsets), 0 if prompt else 1,
-                                            _stream_ptr(state.device)), "gsample_history_append")
+    _launch(state.device, "gsample_history_append", lib().gsample_history_append, state._at,
+            *_lists(state, slots, tokens, offsets), 0 if prompt else 1)
 
 
 def bias_set(state: LogitState, tokens, values, slots=None, offsets=None) -> None:
     """Sets the biases of the listed tokens (lists as in history_append,
     values float32). Other entries keep theirs."""
-    torch = _torch()
     if state.bias is None:
         raise ValueError("the state was made without biases")
-    n = _lists(state, slots, tokens, offsets)
-    _vector(values, tokens.shape[0], torch.float32, state.device, "values")
-    with _on(state.device):
-        _check(lib().gsample_bias_set(ctypes.byref(state._c), _ptr(slots), n, _ptr(tokens),
-                                      _ptr(values), tokens.shape[0], _ptr(offsets),
-                                      _stream_ptr(state.device)), "gsample_bias_set")
+    slot, n, tokens_at, total, offsets_at = _lists(state, slots, tokens, offsets)
+    values_at = _vector(values, total, _torch().float32, state.device, "values")
+    _launch(state.device, "gsample_bias_set", lib().gsample_bias_set, state._at, slot, n,
+            tokens_at, values_at, total, offsets_at)
 
 
 def _constraints(B, V, dev, state, slots, repetition, frequency, presence, mask, mask_rows):
-    """The C struct, and the tensors it points into (to be kept until the call)."""
+    """The C struct, and the tensors made here that it points into (to be kept
+    until the call)."""
     torch = _torch()
-    c = _ConstraintsC()
     keep = []
+    state_at = slot = rep = freq = pres = None
     if state is not None:
         if state.device != dev or state.vocab != V:
             raise ValueError("the state must be on the logits' device and of their vocabulary")
         if slots is None and state.rows < B:
             raise ValueError("without slots the state needs a row for every batch row")
-        c.state = ctypes.pointer(state._c)
-        c.slot = _ptr(_vector(slots, B, torch.int32, dev, "slots"))
-        for name, x in (("repetition", repetition), ("frequency", frequency),
-                        ("presence", presence)):
-            if x is not None:
-                x = _row_tensor(x, B, torch.float32, dev, name)
-                keep.append(x)
-                setattr(c, name, x.data_ptr())
+        state_at = state._at
+        slot = _vector(slots, B, torch.int32, dev, "slots")
+
+        def row(x, name):
+            if x is None:
+                return None
+            x = _row_tensor(x, B, torch.float32, dev, name)
+            keep.append(x)
+            return x.data_ptr()
+
+        rep, freq, pres = row(repetition, "repetition"), row(frequency, "frequency"), \
+            row(presence, "presence")
     elif slots is not None or repetition is not None or frequency is not None or \
             presence is not None:
         raise ValueError("slots and penalties need a state")
+    mask_at = mask_row = None
+    masks = mask_ld = 0
     if mask is not None:
-        if mask.dtype != torch.int32 or mask.device != dev or mask.dim() != 2 or \
-                (mask.shape[1] > 1 and mask.stride(1) != 1) or mask.shape[1] < (V + 31) // 32:
-            raise ValueError("mask must be an int32 tensor [masks, >= ceil(V / 32)] with "
-                             "contiguous rows on the logits' device")
-        if mask_rows is None and mask.shape[0] < B:
+        if mask.dtype != torch.int32 or mask.device != dev or mask.dim() != 2:
+            raise ValueError("mask must be a 2-D int32 tensor on the logits' device")
+        masks, words = mask.shape
+        mask_ld, inner = mask.stride()
+        if masks <= 1:
+            mask_ld = words
+        if words < (V + 31) // 32 or (words > 1 and inner != 1) or mask_ld < words:
+            raise ValueError("mask must have >= ceil(V / 32) words a row, in contiguous rows that "
+                             "do not overlap")
+        if mask_rows is None and masks < B:
             raise ValueError("without mask_rows there must be a mask for every batch row")
-        if mask.shape[0] > 1 and mask.stride(0) < mask.shape[1]:
-            raise ValueError("mask rows must not overlap")
-        c.mask = mask.data_ptr()
-        c.mask_rows = mask.shape[0]
-        c.mask_ld = mask.stride(0) if mask.shape[0] > 1 else mask.shape[1]
-        c.mask_row = _ptr(_vector(mask_rows, B, torch.int32, dev, "mask_rows"))
+        mask_at = mask.data_ptr()
+        mask_row = _vector(mask_rows, B, torch.int32, dev, "mask_rows")
     elif mask_rows is not None:
         raise ValueError("mask_rows needs a mask")
-    return c, keep
+    return _ConstraintsC(state_at, slot, rep, freq, pres, mask_at, masks, mask_ld, mask_row), keep
 
 
 def process_logits(logits, state: LogitState | None = None, slots=None, repetition=None,
@@ -605,10 +627,8 @@ def process_logits(logits, state: LogitState | None = None, slots=None, repetiti
         raise ValueError("out must be of the logits' type or float32")
     c, keep = _constraints(B, V, dev, state, slots, repetition, frequency, presence, mask,
                            mask_rows)
-    with _on(dev):
-        _check(lib().gsample_process_logits(logits.data_ptr(), dt, B, V, ld, ctypes.byref(c),
-                                            out.data_ptr(), odt, out_ld, _stream_ptr(dev)),
-               "gsample_process_logits")
+    _launch(dev, "gsample_process_logits", lib().gsample_process_logits, logits.data_ptr(), dt, B,
+            V, ld, ctypes.byref(c), out.data_ptr(), odt, out_ld)
     return out
 
 
@@ -627,11 +647,9 @@ def constrained_gumbel_argmax(logits, temperature, seed, offset, state: LogitSta
     O = _row_tensor(offset, B, torch.int64, dev, "offset")
     c, keep = _constraints(B, V, dev, state, slots, repetition, frequency, presence, mask,
                            mask_rows)
-    with _on(dev):
-        _check(lib().gsample_constrained_gumbel_argmax(
+    _launch(dev, "gsample_constrained_gumbel_argmax", lib().gsample_constrained_gumbel_argmax,
             logits.data_ptr(), dt, B, V, ld, T.data_ptr(), S.data_ptr(), O.data_ptr(),
-            ctypes.byref(c), out.data_ptr(), ws.data_ptr(), _stream_ptr(dev)),
-            "gsample_constrained_gumbel_argmax")
+            ctypes.byref(c), out.data_ptr(), ws.data_ptr())
     return out
 
 
