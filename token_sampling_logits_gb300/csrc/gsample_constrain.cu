@@ -147,16 +147,28 @@ __device__ __forceinline__ void store_one(char* row, int32_t i, float x) {
 // partial and go element by element. The logits of a full unit are one 128-bit
 // load where they are aligned too; otherwise the two aligned 16-byte pieces
 // that hold them, shifted together (both inside the row: units for which they
-// are not count as partial).
+// are not count as partial). ALIGNED: both matrices' rows all start on 16-byte
+// boundaries.
 //
-// Order of work in a thread: the mask and touched bits of its units, the units
-// that the mask leaves anything of (the others are never read), the masked
-// units' stores, and then the touched elements, four at a time, each written
-// over its place in the unit (the same thread wrote that, so the order holds).
+// A warp works alone, on kBatch runs of 32 units at a time that lie
+// warps_per_row runs apart: the low ids, which hold most of a request's
+// tokens, are shared by many warps. First the mask and touched bits, then the
+// units that the mask leaves anything of (the others are never read), then
+// their stores; then the touched elements, listed in shared memory, are
+// fetched again with their state words and written over their places, one a
+// lane.
+//
 // In place, a unit is read and written only where the mask takes some but not
 // all of it, written only where it takes all, and touched elements are the only
 // traffic elsewhere.
-constexpr int kUnits = 4;  // units a thread
+#ifndef GSAMPLE_PROCESS_CTAS
+#define GSAMPLE_PROCESS_CTAS 4
+#endif
+#ifndef GSAMPLE_PROCESS_RUNS
+#define GSAMPLE_PROCESS_RUNS 8
+#endif
+constexpr int kBatch = 4;
+constexpr int kTouchedCap = 256;  // elements a warp lists at a time
 
 __device__ __forceinline__ uint4 ld_unit(const char* p, uint64_t pol) {
   uint4 v;
@@ -191,112 +203,156 @@ __device__ __forceinline__ uint32_t bits_at(const uint8_t* bits, int32_t e0) {
   return (v >> sh) & ((1u << N) - 1u);
 }
 
-template <int DT, int ODT, bool INPLACE>
-__global__ void __launch_bounds__(kConThreads) process_kernel(const ProcessParams p) {
+template <int DT, int ODT, bool INPLACE, bool ALIGNED>
+__global__ void __launch_bounds__(kConThreads, GSAMPLE_PROCESS_CTAS)
+    process_kernel(const ProcessParams p) {
   constexpr int N = DT == 0 ? 4 : 8;
   constexpr int ISZ = DT == 0 ? 4 : 2, OSZ = ODT == 0 ? 4 : 2;
   constexpr uint32_t kFull = (1u << N) - 1u;
+  __shared__ uint32_t lists[kConThreads / 32][kTouchedCap];
   pdl_wait_then_release();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t Q = p.warps_per_row;
+  const int32_t q = (int32_t)blockIdx.x * (kConThreads / 32) + warp;
+  if (q >= Q) return;
+  uint32_t* list = lists[warp];
   const uint64_t pol = evict_first_policy();
   const int32_t V = (int32_t)p.V;
-  for (int64_t c = blockIdx.x; c < p.B * p.chunks_per_row; c += gridDim.x) {
-    const int64_t b = c / p.chunks_per_row;
-    const int32_t j0 = (int32_t)(c - b * p.chunks_per_row) * (kConThreads * kUnits) + threadIdx.x;
-    const RowConstraints r = row_constraints(p.con, b);
+  for (int64_t b = blockIdx.y; b < p.B; b += gridDim.y) {
+    const RowBits r = row_bits(p.con, b);
     const char* in = p.logits + b * p.ld_bytes;
     char* out = p.out + b * p.out_ld_bytes;
     // Elements by which unit 0 starts before the row, and the misalignment of
     // the logits of every unit.
-    const int32_t s = (int32_t)((uintptr_t)out & 15u) / OSZ;
-    const int a = (int)(((uintptr_t)in - (uintptr_t)(s * ISZ)) & 15u);
+    const int32_t s = ALIGNED ? 0 : (int32_t)((uintptr_t)out & 15u) / OSZ;
+    const int a = ALIGNED ? 0 : (int)(((uintptr_t)in - (uintptr_t)(s * ISZ)) & 15u);
     // Full units start in [lo, hi]: all N elements lie in the row, and every
     // byte that is loaded for them (a multiple of ISZ before and after).
     const int32_t lo = a / ISZ, hi = V - (a == 0 ? N : (32 - a) / ISZ);
-
-    int32_t e0[kUnits];
-    uint32_t allowed[kUnits], touched[kUnits];
-    bool full[kUnits];
-#pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      // Past the row's last unit: V, which is neither full nor partial.
-      e0[k] = j0 + k * kConThreads < p.units_per_row ? (j0 + k * kConThreads) * N - s : V;
-      full[k] = e0[k] >= lo && e0[k] <= hi;
-      allowed[k] = full[k] ? (r.mask ? bits_at<N>(r.mask, e0[k]) : kFull) : 0u;
-      touched[k] = full[k] && r.touched ? bits_at<N>(r.touched, e0[k]) : 0u;
-    }
-    uint4 x[kUnits];
-#pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      const char* q = in + (int64_t)e0[k] * ISZ;
-      if (allowed[k] != 0u && (!INPLACE || allowed[k] != kFull))
-        x[k] = a == 0 ? ld_unit(q, pol) : ld_unit_shifted(q, a, pol);
-    }
-    uint32_t todo = 0u;  // N bits a unit
-#pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      if (!full[k]) continue;
-      todo |= (touched[k] & allowed[k]) << (N * k);
-      if (INPLACE && allowed[k] == kFull) continue;
-      const uint4 y = masked_unit<DT, DT == 0>(x[k], allowed[k]);
-      uint4* dst = reinterpret_cast<uint4*>(out + (int64_t)e0[k] * OSZ);
-      if constexpr (DT != 0 && ODT == 0) {
-        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f[2 * i] = half_to_f32<DT>(w[i] & 0xFFFFu);
-          f[2 * i + 1] = half_to_f32<DT>(w[i] >> 16);
-        }
-        dst[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                            __float_as_uint(f[3]));
-        dst[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
-                            __float_as_uint(f[7]));
-      } else {
-        dst[0] = y;
-      }
-    }
-    static_assert(N * kUnits <= 32, "a thread's touched bits fit in one word");
-    while (todo != 0u) {
-      constexpr int M = 4;
-      int32_t v[M];
-      uint32_t h[M];
-      float bias[M], l[M];
-      bool on[M];
-#pragma unroll
-      for (int q = 0; q < M; ++q) {
-        on[q] = todo != 0u;
-        const int j = on[q] ? __ffs((int)todo) - 1 : 0;
-        todo &= todo - 1u;  // 0 stays 0
-        v[q] = (j0 + (j / N) * kConThreads) * N - s + j % N;
-        h[q] = on[q] ? __ldcg(r.history + v[q]) : 0u;
-        bias[q] = on[q] && r.bias ? __ldcg(r.bias + v[q]) : 0.0f;
-        l[q] = on[q] ? load_one<DT>(in, v[q]) : 0.0f;
-      }
-#pragma unroll
-      for (int q = 0; q < M; ++q)
-        if (on[q]) store_one<ODT>(out, v[q], penalised(l[q], h[q], bias[q], r.pen));
-    }
-    // The partial units at the row's ends.
 #pragma unroll 1
-    for (int k = 0; k < kUnits; ++k) {
-      if (j0 + k * kConThreads >= p.units_per_row) break;
-      const int32_t e = (j0 + k * kConThreads) * N - s;
-      if (e >= lo && e <= hi) continue;
-      for (int32_t v = e < 0 ? 0 : e; v < e + N && v < V; ++v) {
-        const float l = load_one<DT>(in, v);
-        const float y = constrained_logit(l, v, r);
-        if (!INPLACE || __float_as_uint(l) != __float_as_uint(y)) store_one<ODT>(out, v, y);
+    for (int32_t run = q; run < p.runs_per_row; run += kBatch * Q) {
+      int32_t e0[kBatch];
+      uint32_t allowed[kBatch], touched[kBatch];
+      bool full[kBatch], partial = false;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int32_t u = (run + k * Q) * 32 + lane;
+        const bool in_row = run + k * Q < p.runs_per_row && u < p.units_per_row;
+        e0[k] = in_row ? u * N - s : V;  // V: neither full nor partial
+        full[k] = in_row && e0[k] >= lo && e0[k] <= hi;
+        partial |= in_row && !full[k];
+        allowed[k] = 0u;
+        touched[k] = 0u;
+        if (full[k]) {
+          if constexpr (ALIGNED) {
+            allowed[k] = r.mask ? unit_bits<N>(r.mask, e0[k]) : kFull;
+            if (r.touched) touched[k] = unit_bits<N>(r.touched, e0[k]);
+          } else {
+            allowed[k] = r.mask ? bits_at<N>(r.mask, e0[k]) : kFull;
+            if (r.touched) touched[k] = bits_at<N>(r.touched, e0[k]);
+          }
+        }
       }
+      uint4 x[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const char* at = in + (int64_t)e0[k] * ISZ;
+        if (allowed[k] != 0u && (!INPLACE || allowed[k] != kFull))
+          x[k] = a == 0 ? ld_unit(at, pol) : ld_unit_shifted(at, a, pol);
+      }
+      uint32_t todo = 0u;  // the lane's touched elements, N bits a unit
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (!full[k]) continue;
+        todo |= (touched[k] & allowed[k]) << (N * k);
+        if (INPLACE && allowed[k] == kFull) continue;
+        const uint4 y = allowed[k] == kFull ? x[k] : masked_unit<DT, DT == 0>(x[k], allowed[k]);
+        uint4* dst = reinterpret_cast<uint4*>(out + (int64_t)e0[k] * OSZ);
+        if constexpr (DT != 0 && ODT == 0) {
+          const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f[2 * i] = half_to_f32<DT>(w[i] & 0xFFFFu);
+            f[2 * i + 1] = half_to_f32<DT>(w[i] >> 16);
+          }
+          dst[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                              __float_as_uint(f[3]));
+          dst[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
+                              __float_as_uint(f[7]));
+        } else {
+          dst[0] = y;
+        }
+      }
+      static_assert(N * kBatch <= 32, "a lane's touched bits fit in one word");
+      if (__any_sync(0xFFFFFFFFu, todo != 0u)) {
+        int incl = __popc(todo);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+          if (lane >= o) incl += up;
+        }
+        const int total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+        const int first = incl - __popc(todo);
+#pragma unroll 1
+        for (int base = 0; base < total; base += kTouchedCap) {
+          int at = first - base;
+          for (uint32_t bits = todo; bits != 0u; bits &= bits - 1u, ++at) {
+            const int j = __ffs((int)bits) - 1;
+            if (at >= 0 && at < kTouchedCap)
+              list[at] = (uint32_t)(((run + j / N * Q) * 32 + lane) * N - s + j % N);
+          }
+          __syncwarp();  // also orders the units' stores before these elements'
+          const int n = min(kTouchedCap, total - base);
+          // The next element's gathers are on their way while one is written.
+          int32_t v_next = 0;
+          float l_next = 0.0f, bias_next = 0.0f;
+          uint32_t h_next = 0u;
+          auto gather = [&](int i) {
+            if (i >= n) return;
+            v_next = (int32_t)list[i];
+            l_next = load_one<DT>(in, v_next);
+            h_next = __ldcg(p.con.history + r.state + v_next);
+            if (p.con.bias) bias_next = __ldcg(p.con.bias + r.state + v_next);
+          };
+          gather(lane);
+          const RowPenalties pen = row_penalties(p.con, b);
+#pragma unroll 1
+          for (int i = lane; i < n; i += 32) {
+            const int32_t v = v_next;
+            const float l = l_next, bias = bias_next;
+            const uint32_t h = h_next;
+            gather(i + 32);
+            store_one<ODT>(out, v, penalised(l, h, bias, pen));
+          }
+          __syncwarp();
+        }
+      }
+      if (partial) {  // the units at the row's ends
+#pragma unroll 1
+        for (int k = 0; k < kBatch; ++k) {
+          const int32_t u = (run + k * Q) * 32 + lane;
+          if (run + k * Q >= p.runs_per_row || u >= p.units_per_row) break;
+          const int32_t e = u * N - s;
+          if (e >= lo && e <= hi) continue;
+          for (int32_t v = e < 0 ? 0 : e; v < e + N && v < V; ++v) {
+            const float l = load_one<DT>(in, v);
+            const float y = constrained_logit(l, v, row_constraints(p.con, b));
+            if (!INPLACE || __float_as_uint(l) != __float_as_uint(y)) store_one<ODT>(out, v, y);
+          }
+        }
+      }
+      __syncwarp();
     }
   }
 }
 
 // Launch with programmatic stream serialization, as every kernel here.
 template <typename... Params, typename... Args>
-cudaError_t launch(void (*fn)(Params...), int64_t blocks, int threads, cudaStream_t stream,
+cudaError_t launch(void (*fn)(Params...), dim3 grid, int threads, cudaStream_t stream,
                    Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
@@ -305,23 +361,23 @@ cudaError_t launch(void (*fn)(Params...), int64_t blocks, int threads, cudaStrea
   return cudaLaunchKernelEx(&cfg, fn, static_cast<Params>(args)...);
 }
 
-int64_t blocks_for(int64_t items, int64_t per_block, int64_t most) {
+dim3 blocks_for(int64_t items, int64_t per_block, int64_t most) {
   const int64_t n = (items + per_block - 1) / per_block;
-  return n < 1 ? 1 : n > most ? most : n;
+  return dim3((unsigned)(n < 1 ? 1 : n > most ? most : n));
 }
 
 }  // namespace
 
 cudaError_t launch_state_reset(const StateArgs& s, const int32_t* slot, int64_t n, int sms,
                                cudaStream_t stream) {
-  const int64_t blocks = blocks_for(n * (s.ld / 32), kConThreads, (int64_t)sms * 8);
+  const dim3 blocks = blocks_for(n * (s.ld / 32), kConThreads, (int64_t)sms * 8);
   return launch(state_reset_kernel, blocks, kConThreads, stream, s, slot, n);
 }
 
 cudaError_t launch_history_append(const StateArgs& s, const int32_t* slot, int64_t n,
                                   const int64_t* tokens, int64_t total, const int64_t* offsets,
                                   bool prompt, int sms, cudaStream_t stream) {
-  const int64_t blocks = blocks_for(total, kConThreads, (int64_t)sms * 8);
+  const dim3 blocks = blocks_for(total, kConThreads, (int64_t)sms * 8);
   return launch(history_append_kernel, blocks, kConThreads, stream, s, slot, n, tokens, total,
                 offsets, prompt);
 }
@@ -329,25 +385,44 @@ cudaError_t launch_history_append(const StateArgs& s, const int32_t* slot, int64
 cudaError_t launch_bias_set(const StateArgs& s, const int32_t* slot, int64_t n,
                             const int64_t* tokens, const float* values, int64_t total,
                             const int64_t* offsets, cudaStream_t stream) {
-  return launch(bias_set_kernel, n, 32, stream, s, slot, tokens, values, total, offsets);
+  return launch(bias_set_kernel, dim3((unsigned)n), 32, stream, s, slot, tokens, values, total, offsets);
 }
 
-cudaError_t launch_process(ProcessParams p, int dtype, int out_dtype, cudaStream_t stream) {
-  // One unit more than the elements need: the first may start before the row.
+cudaError_t launch_process(ProcessParams p, int dtype, int out_dtype, int sms,
+                           cudaStream_t stream) {
+  // One unit more than the elements need where the first may start before the
+  // row. A warp takes up to GSAMPLE_PROCESS_RUNS runs of a row, fewer while
+  // there are not enough warps to fill the device.
   const int64_t n = dtype == 0 ? 4 : 8;
-  const int64_t units = (p.V + n - 1) / n + 1;
+  const bool aligned = (((uintptr_t)p.logits | (uintptr_t)p.out | (uintptr_t)p.ld_bytes |
+                         (uintptr_t)p.out_ld_bytes) & 15u) == 0;
+  const int64_t units = (p.V + n - 1) / n + (aligned ? 0 : 1);
+  const int64_t runs = (units + 31) / 32;
+  int64_t per_warp = GSAMPLE_PROCESS_RUNS;
+  const int64_t slots = (int64_t)sms * GSAMPLE_PROCESS_CTAS * (kConThreads / 32);
+  while (per_warp > 1 && p.B * ((runs + per_warp - 1) / per_warp) < slots) per_warp /= 2;
   p.units_per_row = (int32_t)units;
-  p.chunks_per_row = (units + kConThreads * kUnits - 1) / (kConThreads * kUnits);
-  const int64_t blocks = blocks_for(p.B * p.chunks_per_row, 1, INT32_MAX);
-  switch (dtype * 4 + (out_dtype == 0 ? 0 : 2) + (p.inplace ? 1 : 0)) {
-    case 0: return launch(process_kernel<0, 0, false>, blocks, kConThreads, stream, p);
-    case 1: return launch(process_kernel<0, 0, true>, blocks, kConThreads, stream, p);
-    case 4: return launch(process_kernel<1, 0, false>, blocks, kConThreads, stream, p);
-    case 6: return launch(process_kernel<1, 1, false>, blocks, kConThreads, stream, p);
-    case 7: return launch(process_kernel<1, 1, true>, blocks, kConThreads, stream, p);
-    case 8: return launch(process_kernel<2, 0, false>, blocks, kConThreads, stream, p);
-    case 10: return launch(process_kernel<2, 2, false>, blocks, kConThreads, stream, p);
-    default: return launch(process_kernel<2, 2, true>, blocks, kConThreads, stream, p);
+  p.runs_per_row = (int32_t)runs;
+  p.warps_per_row = (int32_t)((runs + per_warp - 1) / per_warp);
+  const int64_t bx = (p.warps_per_row + kConThreads / 32 - 1) / (kConThreads / 32);
+  const dim3 grid((unsigned)bx, (unsigned)(p.B < 65535 ? p.B : 65535));
+  switch (dtype * 8 + (out_dtype == 0 ? 0 : 4) + (p.inplace ? 2 : 0) + (aligned ? 1 : 0)) {
+    case 0: return launch(process_kernel<0, 0, false, false>, grid, kConThreads, stream, p);
+    case 1: return launch(process_kernel<0, 0, false, true>, grid, kConThreads, stream, p);
+    case 2: return launch(process_kernel<0, 0, true, false>, grid, kConThreads, stream, p);
+    case 3: return launch(process_kernel<0, 0, true, true>, grid, kConThreads, stream, p);
+    case 8: return launch(process_kernel<1, 0, false, false>, grid, kConThreads, stream, p);
+    case 9: return launch(process_kernel<1, 0, false, true>, grid, kConThreads, stream, p);
+    case 12: return launch(process_kernel<1, 1, false, false>, grid, kConThreads, stream, p);
+    case 13: return launch(process_kernel<1, 1, false, true>, grid, kConThreads, stream, p);
+    case 14: return launch(process_kernel<1, 1, true, false>, grid, kConThreads, stream, p);
+    case 15: return launch(process_kernel<1, 1, true, true>, grid, kConThreads, stream, p);
+    case 16: return launch(process_kernel<2, 0, false, false>, grid, kConThreads, stream, p);
+    case 17: return launch(process_kernel<2, 0, false, true>, grid, kConThreads, stream, p);
+    case 20: return launch(process_kernel<2, 2, false, false>, grid, kConThreads, stream, p);
+    case 21: return launch(process_kernel<2, 2, false, true>, grid, kConThreads, stream, p);
+    case 22: return launch(process_kernel<2, 2, true, false>, grid, kConThreads, stream, p);
+    default: return launch(process_kernel<2, 2, true, true>, grid, kConThreads, stream, p);
   }
 }
 

@@ -98,6 +98,27 @@ __device__ __forceinline__ RowConstraints row_constraints(const ConstrainArgs& c
   return r;
 }
 
+// A row's bits alone, and where its state row starts (elements; -1: none).
+struct RowBits {
+  const uint8_t* mask;
+  const uint8_t* touched;
+  int64_t state;
+};
+
+__device__ __forceinline__ RowBits row_bits(const ConstrainArgs& c, int64_t b) {
+  RowBits r{nullptr, nullptr, -1};
+  if (c.mask) {
+    const int64_t m = c.mask_row ? (int64_t)__ldg(c.mask_row + b) : b;
+    if (m >= 0 && m < c.mask_rows) r.mask = c.mask + m * c.mask_ld_bytes;
+  }
+  const int64_t s = state_row_of(c, b);
+  if (s >= 0) {
+    r.state = s * c.state_ld;
+    r.touched = c.touched + r.state / 8;
+  }
+  return r;
+}
+
 // Logit x of a touched token with history word h and bias `bias`.
 __device__ __forceinline__ float penalised(float x, uint32_t h, float bias,
                                            const RowPenalties& r) {

@@ -185,7 +185,8 @@ gsample_status gsample_process_logits(const void* logits, gsample_dtype dtype, i
   int sms = 0;
   st = gsample::current_device_sms(&sms);
   if (st != GSAMPLE_OK) return st;
-  return launched(gsample::launch_process(p, (int)dtype, (int)out_dtype, (cudaStream_t)stream));
+  return launched(
+      gsample::launch_process(p, (int)dtype, (int)out_dtype, sms, (cudaStream_t)stream));
 }
 
 gsample_status gsample_constrained_gumbel_argmax(const void* logits, gsample_dtype dtype,

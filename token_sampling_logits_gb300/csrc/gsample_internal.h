@@ -187,9 +187,8 @@ struct ProcessParams {
   char* out;
   int64_t ld_bytes, out_ld_bytes;
   int64_t B, V;
-  int64_t chunks_per_row;  // set by the launch, as units_per_row
-  int32_t units_per_row;
   bool inplace;
+  int32_t units_per_row, runs_per_row, warps_per_row;  // set by the launch
   ConstrainArgs con;
 };
 
@@ -201,7 +200,8 @@ cudaError_t launch_history_append(const StateArgs& s, const int32_t* slot, int64
 cudaError_t launch_bias_set(const StateArgs& s, const int32_t* slot, int64_t n,
                             const int64_t* tokens, const float* values, int64_t total,
                             const int64_t* offsets, cudaStream_t stream);
-cudaError_t launch_process(ProcessParams p, int dtype, int out_dtype, cudaStream_t stream);
+cudaError_t launch_process(ProcessParams p, int dtype, int out_dtype, int sms,
+                           cudaStream_t stream);
 
 // The host-side checks of the logits arguments and of the current device,
 // shared with gsample_api.cu. current_device_sms returns the status of the
