@@ -140,27 +140,226 @@ __device__ __forceinline__ void store_one(char* row, int32_t i, float x) {
   }
 }
 
-// The row kernel. Row b of the result is cut into units of N elements (N = 8
+// Two kernels. process_wide_kernel takes rows that all start on 32-byte
+// boundaries, process_kernel any others.
+//
+// process_wide_kernel: a lane takes 32 elements at a time, one word of mask and
+// of touched bits, so that what goes by element is a vector instruction or
+// nothing: 256-bit loads and stores (a lane's 32 bytes are one sector, so the
+// 64-byte stride between lanes costs no traffic). Words that the mask leaves
+// nothing of are never read. A warp works alone; its words come in groups of
+// kWordGroup spread over the row, because the low ids hold most of a request's
+// tokens. Touched elements are listed in shared memory and written over their
+// places, one a lane, from the logit and the state words fetched for them
+// while the words are on their way.
+//
+// In place, a word is read and written only where the mask takes some but not
+// all of it, written only where it takes all, and touched elements are the only
+// traffic elsewhere.
+constexpr int kWideThreads = 128;
+constexpr int kWideCtas = 8;     // an SM, 64 registers a thread (80 for binary32 logits)
+constexpr int kWideWords = 2;    // words a lane, one after the other
+constexpr int kWordGroup = 4;
+constexpr int kTouchedCap = 256;  // elements a warp lists at a time
+
+struct Oct {
+  uint32_t w[8];
+};
+
+__device__ __forceinline__ Oct ld_oct(const char* p) {
+  Oct v;
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]),
+                 "=r"(v.w[5]), "=r"(v.w[6]), "=r"(v.w[7])
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void st_oct(char* p, const Oct& v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v.w[0]),
+               "r"(v.w[1]), "r"(v.w[2]), "r"(v.w[3]), "r"(v.w[4]), "r"(v.w[5]), "r"(v.w[6]),
+               "r"(v.w[7])
+               : "memory");
+}
+
+// 32 bytes of a row with the elements whose bit in `allowed` is clear set to -inf.
+template <int DT>
+__device__ __forceinline__ void mask_oct(Oct& v, uint32_t allowed) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (DT == 0) {
+      if (!((allowed >> i) & 1u)) v.w[i] = 0xFF800000u;
+    } else {
+      constexpr uint32_t ninf = (DT == 1 ? 0xFF80u : 0xFC00u) * 0x10001u;
+      const uint32_t two = (allowed >> (2 * i)) & 3u;  // the two bits, widened to halves
+      const uint32_t keep = ((two | two << 15) & 0x10001u) * 0xFFFFu;
+      v.w[i] = (v.w[i] & keep) | (ninf & ~keep);
+    }
+  }
+}
+
+// A listed element on its way: what penalised() needs of it.
+struct Gathered {
+  int32_t v;
+  float l, bias;
+  uint32_t h;
+};
+
+template <int DT>
+__device__ __forceinline__ Gathered gather_element(const ProcessParams& p, int64_t state,
+                                                   const char* in, int32_t v) {
+  Gathered g;
+  g.v = v;
+  g.l = load_one<DT>(in, v);
+  g.h = __ldcg(p.con.history + state + v);
+  g.bias = p.con.bias ? __ldcg(p.con.bias + state + v) : 0.0f;
+  return g;
+}
+
+// Writes n listed elements over their places; the next one's gathers are on
+// their way while one is written. `g`: the lane's first, gathered already.
+template <int DT, int ODT>
+__device__ __forceinline__ void write_listed(const ProcessParams& p, int64_t b, int64_t state,
+                                             const char* in, char* out, const uint32_t* list,
+                                             int n, Gathered g) {
+  const int lane = threadIdx.x & 31;
+  const RowPenalties pen = row_penalties(p.con, b);
+#pragma unroll 1
+  for (int i = lane; i < n; i += 32) {
+    const Gathered now = g;
+    if (i + 32 < n) g = gather_element<DT>(p, state, in, (int32_t)list[i + 32]);
+    store_one<ODT>(out, now.v, penalised(now.l, now.h, now.bias, pen));
+  }
+  __syncwarp();  // before the list is refilled
+}
+
+// Where a lane's `mine` elements go in the warp's list, and how many there are
+// in all.
+struct ListPlace {
+  int first, total;
+};
+
+__device__ __forceinline__ ListPlace list_place(int mine) {
+  if (!__any_sync(0xFFFFFFFFu, mine != 0)) return ListPlace{0, 0};
+  const int lane = threadIdx.x & 31;
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += up;
+  }
+  return ListPlace{incl - mine, __shfl_sync(0xFFFFFFFFu, incl, 31)};
+}
+
+template <int DT, int ODT, bool INPLACE>
+__global__ void __launch_bounds__(kWideThreads, DT == 0 ? 6 : kWideCtas)
+    process_wide_kernel(const ProcessParams p) {
+  constexpr int ISZ = DT == 0 ? 4 : 2, OSZ = ODT == 0 ? 4 : 2;
+  constexpr int NI = ISZ;            // 32-byte pieces of a word's logits
+  constexpr int EPO = 32 / ISZ;      // elements a piece
+  __shared__ uint32_t lists[kWideThreads / 32][kTouchedCap];
+  pdl_wait_then_release();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t Q = p.warps_per_row;
+  const int32_t q = (int32_t)blockIdx.x * (kWideThreads / 32) + warp;
+  if (q >= Q) return;
+  uint32_t* list = lists[warp];
+  const int32_t V = (int32_t)p.V, words = (V + 31) / 32;
+  // The lane's k-th word is w0 + k * step: of the warp's 32 / G groups, Q apart.
+  constexpr int G = kWordGroup;
+  const int32_t w0 = (q + (lane / G) * Q) * G + lane % G, step = 32 * Q;
+  for (int64_t b = blockIdx.y; b < p.B; b += gridDim.y) {
+    const RowBits r = row_bits(p.con, b);
+    const char* in = p.logits + b * p.ld_bytes;
+    char* out = p.out + b * p.out_ld_bytes;
+#pragma unroll 1
+    for (int32_t k = 0; k < p.items_per_lane; ++k) {
+      const int32_t w = w0 + k * step;
+      const bool whole = w < V / 32;  // the row's last word may be cut off
+      uint32_t m = 0u, t = 0u;
+      if (w < words) {
+        m = r.mask ? __ldcg(reinterpret_cast<const uint32_t*>(r.mask) + w) : 0xFFFFFFFFu;
+        if (r.touched) t = __ldcg(reinterpret_cast<const uint32_t*>(r.touched) + w);
+      }
+      Oct x[NI];
+      if (whole && m != 0u && (!INPLACE || m != 0xFFFFFFFFu)) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) x[i] = ld_oct(in + (int64_t)w * (32 * ISZ) + i * 32);
+      }
+      // The touched elements, listed, and the first of them on its way, while
+      // the word above is.
+      const uint32_t todo = whole ? t & m : 0u;
+      const ListPlace place = list_place(__popc(todo));
+      auto list_round = [&](int base) {  // the elements from the base-th on, as many as it holds
+        int at = place.first - base;
+        for (uint32_t bits = todo; bits != 0u; bits &= bits - 1u, ++at)
+          if (at >= 0 && at < kTouchedCap)
+            list[at] = (uint32_t)w * 32u + (uint32_t)__ffs((int)bits) - 1u;
+        __syncwarp();
+      };
+      Gathered g;
+      if (place.total != 0) {
+        list_round(0);
+        if (lane < place.total) g = gather_element<DT>(p, r.state, in, (int32_t)list[lane]);
+      }
+      if (whole && !(INPLACE && m == 0xFFFFFFFFu)) {
+        char* dst = out + (int64_t)w * (32 * OSZ);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          if (m != 0xFFFFFFFFu) mask_oct<DT>(x[i], m >> (i * EPO));
+          if constexpr (DT != 0 && ODT == 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              Oct y;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t v = x[i].w[h * 4 + j];
+                y.w[2 * j] = __float_as_uint(half_to_f32<DT>(v & 0xFFFFu));
+                y.w[2 * j + 1] = __float_as_uint(half_to_f32<DT>(v >> 16));
+              }
+              st_oct(dst + i * 64 + h * 32, y);
+            }
+          } else {
+            st_oct(dst + i * 32, x[i]);
+          }
+        }
+      }
+      if (place.total != 0) {
+        __syncwarp();  // orders the words' stores before these elements'
+        write_listed<DT, ODT>(p, b, r.state, in, out, list, min(kTouchedCap, place.total), g);
+#pragma unroll 1
+        for (int base = kTouchedCap; base < place.total; base += kTouchedCap) {
+          list_round(base);  // more rounds only where the words are full of touched elements
+          const int n = min(kTouchedCap, place.total - base);
+          if (lane < n) g = gather_element<DT>(p, r.state, in, (int32_t)list[lane]);
+          write_listed<DT, ODT>(p, b, r.state, in, out, list, n, g);
+        }
+      }
+      if (!whole && w < words) {
+        const RowConstraints rc = row_constraints(p.con, b);
+#pragma unroll 1
+        for (int32_t v = w * 32; v < V; ++v) {
+          const float l = load_one<DT>(in, v);
+          const float y = constrained_logit(l, v, rc);
+          if (!INPLACE || __float_as_uint(l) != __float_as_uint(y)) store_one<ODT>(out, v, y);
+        }
+      }
+    }
+  }
+}
+
+// process_kernel: row b of the result is cut into units of N elements (N = 8
 // for 16-bit logits, 4 for binary32: 16 bytes of the logits) that start on
 // 16-byte boundaries of the RESULT, so that every full unit is stored with
 // 128-bit stores wherever the two rows start; the first and last unit may be
 // partial and go element by element. The logits of a full unit are one 128-bit
 // load where they are aligned too; otherwise the two aligned 16-byte pieces
 // that hold them, shifted together (both inside the row: units for which they
-// are not count as partial). ALIGNED: both matrices' rows all start on 16-byte
-// boundaries.
+// are not count as partial).
 //
-// A warp works alone, on kBatch runs of 32 units at a time that lie
-// warps_per_row runs apart: the low ids, which hold most of a request's
-// tokens, are shared by many warps. First the mask and touched bits, then the
-// units that the mask leaves anything of (the others are never read), then
-// their stores; then the touched elements, listed in shared memory, are
-// fetched again with their state words and written over their places, one a
-// lane.
-//
-// In place, a unit is read and written only where the mask takes some but not
-// all of it, written only where it takes all, and touched elements are the only
-// traffic elsewhere.
+// A warp works alone, as in the wide kernel, on kBatch units a lane at a time:
+// groups of kUnitGroup units spread over the row.
 #ifndef GSAMPLE_PROCESS_CTAS
 #define GSAMPLE_PROCESS_CTAS 4
 #endif
@@ -168,7 +367,7 @@ __device__ __forceinline__ void store_one(char* row, int32_t i, float x) {
 #define GSAMPLE_PROCESS_RUNS 8
 #endif
 constexpr int kBatch = 4;
-constexpr int kTouchedCap = 256;  // elements a warp lists at a time
+constexpr int kUnitGroup = 8;
 
 __device__ __forceinline__ uint4 ld_unit(const char* p, uint64_t pol) {
   uint4 v;
@@ -203,7 +402,7 @@ __device__ __forceinline__ uint32_t bits_at(const uint8_t* bits, int32_t e0) {
   return (v >> sh) & ((1u << N) - 1u);
 }
 
-template <int DT, int ODT, bool INPLACE, bool ALIGNED>
+template <int DT, int ODT, bool INPLACE>
 __global__ void __launch_bounds__(kConThreads, GSAMPLE_PROCESS_CTAS)
     process_kernel(const ProcessParams p) {
   constexpr int N = DT == 0 ? 4 : 8;
@@ -218,39 +417,37 @@ __global__ void __launch_bounds__(kConThreads, GSAMPLE_PROCESS_CTAS)
   uint32_t* list = lists[warp];
   const uint64_t pol = evict_first_policy();
   const int32_t V = (int32_t)p.V;
+  // The lane's k-th unit is u0 + k * step.
+  constexpr int G = kUnitGroup;
+  const int32_t u0 = (q + (lane / G) * Q) * G + lane % G, step = 32 * Q;
   for (int64_t b = blockIdx.y; b < p.B; b += gridDim.y) {
     const RowBits r = row_bits(p.con, b);
     const char* in = p.logits + b * p.ld_bytes;
     char* out = p.out + b * p.out_ld_bytes;
     // Elements by which unit 0 starts before the row, and the misalignment of
     // the logits of every unit.
-    const int32_t s = ALIGNED ? 0 : (int32_t)((uintptr_t)out & 15u) / OSZ;
-    const int a = ALIGNED ? 0 : (int)(((uintptr_t)in - (uintptr_t)(s * ISZ)) & 15u);
+    const int32_t s = (int32_t)((uintptr_t)out & 15u) / OSZ;
+    const int a = (int)(((uintptr_t)in - (uintptr_t)(s * ISZ)) & 15u);
     // Full units start in [lo, hi]: all N elements lie in the row, and every
     // byte that is loaded for them (a multiple of ISZ before and after).
     const int32_t lo = a / ISZ, hi = V - (a == 0 ? N : (32 - a) / ISZ);
 #pragma unroll 1
-    for (int32_t run = q; run < p.runs_per_row; run += kBatch * Q) {
+    for (int32_t k0 = 0; k0 < p.items_per_lane; k0 += kBatch) {
       int32_t e0[kBatch];
       uint32_t allowed[kBatch], touched[kBatch];
       bool full[kBatch], partial = false;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int32_t u = (run + k * Q) * 32 + lane;
-        const bool in_row = run + k * Q < p.runs_per_row && u < p.units_per_row;
+        const int32_t u = u0 + (k0 + k) * step;
+        const bool in_row = k0 + k < p.items_per_lane && u < p.units_per_row;
         e0[k] = in_row ? u * N - s : V;  // V: neither full nor partial
         full[k] = in_row && e0[k] >= lo && e0[k] <= hi;
         partial |= in_row && !full[k];
         allowed[k] = 0u;
         touched[k] = 0u;
         if (full[k]) {
-          if constexpr (ALIGNED) {
-            allowed[k] = r.mask ? unit_bits<N>(r.mask, e0[k]) : kFull;
-            if (r.touched) touched[k] = unit_bits<N>(r.touched, e0[k]);
-          } else {
-            allowed[k] = r.mask ? bits_at<N>(r.mask, e0[k]) : kFull;
-            if (r.touched) touched[k] = bits_at<N>(r.touched, e0[k]);
-          }
+          allowed[k] = r.mask ? bits_at<N>(r.mask, e0[k]) : kFull;
+          if (r.touched) touched[k] = bits_at<N>(r.touched, e0[k]);
         }
       }
       uint4 x[kBatch];
@@ -260,12 +457,28 @@ __global__ void __launch_bounds__(kConThreads, GSAMPLE_PROCESS_CTAS)
         if (allowed[k] != 0u && (!INPLACE || allowed[k] != kFull))
           x[k] = a == 0 ? ld_unit(at, pol) : ld_unit_shifted(at, a, pol);
       }
+      static_assert(N * kBatch <= 32, "a lane's touched bits fit in one word");
       uint32_t todo = 0u;  // the lane's touched elements, N bits a unit
 #pragma unroll
+      for (int k = 0; k < kBatch; ++k) todo |= (touched[k] & allowed[k]) << (N * k);
+      const ListPlace place = list_place(__popc(todo));
+      auto list_round = [&](int base) {
+        int at = place.first - base;
+        for (uint32_t bits = todo; bits != 0u; bits &= bits - 1u, ++at) {
+          const int j = __ffs((int)bits) - 1;
+          if (at >= 0 && at < kTouchedCap)
+            list[at] = (uint32_t)((u0 + (k0 + j / N) * step) * N - s + j % N);
+        }
+        __syncwarp();
+      };
+      Gathered g;
+      if (place.total != 0) {
+        list_round(0);
+        if (lane < place.total) g = gather_element<DT>(p, r.state, in, (int32_t)list[lane]);
+      }
+#pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        if (!full[k]) continue;
-        todo |= (touched[k] & allowed[k]) << (N * k);
-        if (INPLACE && allowed[k] == kFull) continue;
+        if (!full[k] || (INPLACE && allowed[k] == kFull)) continue;
         const uint4 y = allowed[k] == kFull ? x[k] : masked_unit<DT, DT == 0>(x[k], allowed[k]);
         uint4* dst = reinterpret_cast<uint4*>(out + (int64_t)e0[k] * OSZ);
         if constexpr (DT != 0 && ODT == 0) {
@@ -284,55 +497,22 @@ __global__ void __launch_bounds__(kConThreads, GSAMPLE_PROCESS_CTAS)
           dst[0] = y;
         }
       }
-      static_assert(N * kBatch <= 32, "a lane's touched bits fit in one word");
-      if (__any_sync(0xFFFFFFFFu, todo != 0u)) {
-        int incl = __popc(todo);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-          if (lane >= o) incl += up;
-        }
-        const int total = __shfl_sync(0xFFFFFFFFu, incl, 31);
-        const int first = incl - __popc(todo);
+      if (place.total != 0) {
+        __syncwarp();  // orders the units' stores before these elements'
+        write_listed<DT, ODT>(p, b, r.state, in, out, list, min(kTouchedCap, place.total), g);
 #pragma unroll 1
-        for (int base = 0; base < total; base += kTouchedCap) {
-          int at = first - base;
-          for (uint32_t bits = todo; bits != 0u; bits &= bits - 1u, ++at) {
-            const int j = __ffs((int)bits) - 1;
-            if (at >= 0 && at < kTouchedCap)
-              list[at] = (uint32_t)(((run + j / N * Q) * 32 + lane) * N - s + j % N);
-          }
-          __syncwarp();  // also orders the units' stores before these elements'
-          const int n = min(kTouchedCap, total - base);
-          // The next element's gathers are on their way while one is written.
-          int32_t v_next = 0;
-          float l_next = 0.0f, bias_next = 0.0f;
-          uint32_t h_next = 0u;
-          auto gather = [&](int i) {
-            if (i >= n) return;
-            v_next = (int32_t)list[i];
-            l_next = load_one<DT>(in, v_next);
-            h_next = __ldcg(p.con.history + r.state + v_next);
-            if (p.con.bias) bias_next = __ldcg(p.con.bias + r.state + v_next);
-          };
-          gather(lane);
-          const RowPenalties pen = row_penalties(p.con, b);
-#pragma unroll 1
-          for (int i = lane; i < n; i += 32) {
-            const int32_t v = v_next;
-            const float l = l_next, bias = bias_next;
-            const uint32_t h = h_next;
-            gather(i + 32);
-            store_one<ODT>(out, v, penalised(l, h, bias, pen));
-          }
-          __syncwarp();
+        for (int base = kTouchedCap; base < place.total; base += kTouchedCap) {
+          list_round(base);
+          const int n = min(kTouchedCap, place.total - base);
+          if (lane < n) g = gather_element<DT>(p, r.state, in, (int32_t)list[lane]);
+          write_listed<DT, ODT>(p, b, r.state, in, out, list, n, g);
         }
       }
       if (partial) {  // the units at the row's ends
 #pragma unroll 1
         for (int k = 0; k < kBatch; ++k) {
-          const int32_t u = (run + k * Q) * 32 + lane;
-          if (run + k * Q >= p.runs_per_row || u >= p.units_per_row) break;
+          const int32_t u = u0 + (k0 + k) * step;
+          if (k0 + k >= p.items_per_lane || u >= p.units_per_row) break;
           const int32_t e = u * N - s;
           if (e >= lo && e <= hi) continue;
           for (int32_t v = e < 0 ? 0 : e; v < e + N && v < V; ++v) {
@@ -390,39 +570,46 @@ cudaError_t launch_bias_set(const StateArgs& s, const int32_t* slot, int64_t n,
 
 cudaError_t launch_process(ProcessParams p, int dtype, int out_dtype, int sms,
                            cudaStream_t stream) {
-  // One unit more than the elements need where the first may start before the
-  // row. A warp takes up to GSAMPLE_PROCESS_RUNS runs of a row, fewer while
-  // there are not enough warps to fill the device.
-  const int64_t n = dtype == 0 ? 4 : 8;
-  const bool aligned = (((uintptr_t)p.logits | (uintptr_t)p.out | (uintptr_t)p.ld_bytes |
-                         (uintptr_t)p.out_ld_bytes) & 15u) == 0;
-  const int64_t units = (p.V + n - 1) / n + (aligned ? 0 : 1);
-  const int64_t runs = (units + 31) / 32;
-  int64_t per_warp = GSAMPLE_PROCESS_RUNS;
-  const int64_t slots = (int64_t)sms * GSAMPLE_PROCESS_CTAS * (kConThreads / 32);
-  while (per_warp > 1 && p.B * ((runs + per_warp - 1) / per_warp) < slots) per_warp /= 2;
-  p.units_per_row = (int32_t)units;
-  p.runs_per_row = (int32_t)runs;
-  p.warps_per_row = (int32_t)((runs + per_warp - 1) / per_warp);
-  const int64_t bx = (p.warps_per_row + kConThreads / 32 - 1) / (kConThreads / 32);
+  // A warp takes up to kWideWords words, or GSAMPLE_PROCESS_RUNS units, a lane
+  // of a row; fewer while there are not enough warps to fill the device.
+  const bool wide = (((uintptr_t)p.logits | (uintptr_t)p.out | (uintptr_t)p.ld_bytes |
+                      (uintptr_t)p.out_ld_bytes) & 31u) == 0;
+  int64_t items, per_warp, slots;
+  if (wide) {
+    items = ((p.V + 31) / 32 + 31) / 32;
+    per_warp = kWideWords;
+    slots = (int64_t)sms * kWideCtas * (kWideThreads / 32);
+  } else {
+    const int64_t n = dtype == 0 ? 4 : 8;
+    const int64_t units = (p.V + n - 1) / n + 1;  // the first may start before the row
+    items = (units + 31) / 32;
+    per_warp = GSAMPLE_PROCESS_RUNS;
+    slots = (int64_t)sms * GSAMPLE_PROCESS_CTAS * (kConThreads / 32);
+    p.units_per_row = (int32_t)units;
+  }
+  while (per_warp > 1 && p.B * ((items + per_warp - 1) / per_warp) < slots) per_warp /= 2;
+  p.warps_per_row = (int32_t)((items + per_warp - 1) / per_warp);
+  p.items_per_lane = (int32_t)((items + p.warps_per_row - 1) / p.warps_per_row);
+  const int threads = wide ? kWideThreads : kConThreads;
+  const int64_t bx = (p.warps_per_row + threads / 32 - 1) / (threads / 32);
   const dim3 grid((unsigned)bx, (unsigned)(p.B < 65535 ? p.B : 65535));
-  switch (dtype * 8 + (out_dtype == 0 ? 0 : 4) + (p.inplace ? 2 : 0) + (aligned ? 1 : 0)) {
-    case 0: return launch(process_kernel<0, 0, false, false>, grid, kConThreads, stream, p);
-    case 1: return launch(process_kernel<0, 0, false, true>, grid, kConThreads, stream, p);
-    case 2: return launch(process_kernel<0, 0, true, false>, grid, kConThreads, stream, p);
-    case 3: return launch(process_kernel<0, 0, true, true>, grid, kConThreads, stream, p);
-    case 8: return launch(process_kernel<1, 0, false, false>, grid, kConThreads, stream, p);
-    case 9: return launch(process_kernel<1, 0, false, true>, grid, kConThreads, stream, p);
-    case 12: return launch(process_kernel<1, 1, false, false>, grid, kConThreads, stream, p);
-    case 13: return launch(process_kernel<1, 1, false, true>, grid, kConThreads, stream, p);
-    case 14: return launch(process_kernel<1, 1, true, false>, grid, kConThreads, stream, p);
-    case 15: return launch(process_kernel<1, 1, true, true>, grid, kConThreads, stream, p);
-    case 16: return launch(process_kernel<2, 0, false, false>, grid, kConThreads, stream, p);
-    case 17: return launch(process_kernel<2, 0, false, true>, grid, kConThreads, stream, p);
-    case 20: return launch(process_kernel<2, 2, false, false>, grid, kConThreads, stream, p);
-    case 21: return launch(process_kernel<2, 2, false, true>, grid, kConThreads, stream, p);
-    case 22: return launch(process_kernel<2, 2, true, false>, grid, kConThreads, stream, p);
-    default: return launch(process_kernel<2, 2, true, true>, grid, kConThreads, stream, p);
+  switch (dtype * 8 + (out_dtype == 0 ? 0 : 4) + (p.inplace ? 2 : 0) + (wide ? 1 : 0)) {
+    case 0: return launch(process_kernel<0, 0, false>, grid, threads, stream, p);
+    case 1: return launch(process_wide_kernel<0, 0, false>, grid, threads, stream, p);
+    case 2: return launch(process_kernel<0, 0, true>, grid, threads, stream, p);
+    case 3: return launch(process_wide_kernel<0, 0, true>, grid, threads, stream, p);
+    case 8: return launch(process_kernel<1, 0, false>, grid, threads, stream, p);
+    case 9: return launch(process_wide_kernel<1, 0, false>, grid, threads, stream, p);
+    case 12: return launch(process_kernel<1, 1, false>, grid, threads, stream, p);
+    case 13: return launch(process_wide_kernel<1, 1, false>, grid, threads, stream, p);
+    case 14: return launch(process_kernel<1, 1, true>, grid, threads, stream, p);
+    case 15: return launch(process_wide_kernel<1, 1, true>, grid, threads, stream, p);
+    case 16: return launch(process_kernel<2, 0, false>, grid, threads, stream, p);
+    case 17: return launch(process_wide_kernel<2, 0, false>, grid, threads, stream, p);
+    case 20: return launch(process_kernel<2, 2, false>, grid, threads, stream, p);
+    case 21: return launch(process_wide_kernel<2, 2, false>, grid, threads, stream, p);
+    case 22: return launch(process_kernel<2, 2, true>, grid, threads, stream, p);
+    default: return launch(process_wide_kernel<2, 2, true>, grid, threads, stream, p);
   }
 }
 

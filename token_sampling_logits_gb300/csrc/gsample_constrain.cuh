@@ -229,8 +229,9 @@ __device__ __forceinline__ uint4 masked_unit(uint4 r, uint32_t allowed) {
       if (!((allowed >> i) & 1u)) w[i] = 0xFF800000u;
     } else {
       constexpr uint32_t ninf = DT == 1 ? 0xFF80u : 0xFC00u;
-      const uint32_t keep = ((allowed >> (2 * i)) & 1u ? 0xFFFFu : 0u) |
-                            ((allowed >> (2 * i)) & 2u ? 0xFFFF0000u : 0u);
+      // the two bits, 16 apart, widened to halves
+      const uint32_t two = (allowed >> (2 * i)) & 3u;
+      const uint32_t keep = ((two | two << 15) & 0x10001u) * 0xFFFFu;
       w[i] = (w[i] & keep) | ((ninf * 0x10001u) & ~keep);
     }
   }

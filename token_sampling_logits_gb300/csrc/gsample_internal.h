@@ -188,7 +188,7 @@ struct ProcessParams {
   int64_t ld_bytes, out_ld_bytes;
   int64_t B, V;
   bool inplace;
-  int32_t units_per_row, runs_per_row, warps_per_row;  // set by the launch
+  int32_t units_per_row, warps_per_row, items_per_lane;  // set by the launch
   ConstrainArgs con;
 };
 
