@@ -67,22 +67,108 @@ __device__ __forceinline__ int64_t owner(const int64_t* offsets, int64_t n, int6
   return lo;
 }
 
-// One thread per token. Integer atomics commute, so the state does not depend
-// on their order.
+// The history word and the touched bit of one token, `times` times. Integer
+// atomics commute, so the state does not depend on their order.
+__device__ __forceinline__ void count_token(const StateArgs& s, int64_t at, uint32_t times,
+                                            bool prompt) {
+  const uint32_t before =
+      prompt ? atomicOr(s.history + at, 0x80000000u) : atomicAdd(s.history + at, times);
+  if (before == 0u) atomicOr(s.touched + (at >> 5), 1u << (at & 31));  // ld is a multiple of 32
+}
+
+// Where token j's history word is (an index into the whole history), or -1.
+__device__ __forceinline__ int64_t token_place(const StateArgs& s, const int32_t* slot, int64_t n,
+                                               const int64_t* tokens, const int64_t* offsets,
+                                               int64_t j) {
+  const int64_t t = __ldg(tokens + j);
+  const int64_t i = owner(offsets, n, j);
+  if (i < 0 || t < 0 || t >= s.vocab) return -1;
+  const int64_t r = state_row(s, slot, i);
+  return r < 0 ? -1 : r * s.ld + t;
+}
+
+// One thread per token.
 __global__ void __launch_bounds__(kConThreads)
     history_append_kernel(const StateArgs s, const int32_t* slot, int64_t n, const int64_t* tokens,
                           int64_t total, const int64_t* offsets, bool prompt) {
   pdl_wait_then_release();
   for (int64_t j = blockIdx.x * (int64_t)kConThreads + threadIdx.x; j < total;
        j += (int64_t)gridDim.x * kConThreads) {
-    const int64_t t = __ldg(tokens + j);
-    const int64_t i = owner(offsets, n, j);
-    if (i < 0 || t < 0 || t >= s.vocab) continue;
-    const int64_t r = state_row(s, slot, i);
-    if (r < 0) continue;
-    uint32_t* h = s.history + r * s.ld + t;
-    const uint32_t before = prompt ? atomicOr(h, 0x80000000u) : atomicAdd(h, 1u);
-    if (before == 0u) atomicOr(s.touched + r * (s.ld / 32) + (t >> 5), 1u << (t & 31));
+    const int64_t at = token_place(s, slot, n, tokens, offsets, j);
+    if (at >= 0) count_token(s, at, 1u, prompt);
+  }
+}
+
+// Long lists of one request: text repeats its frequent tokens (one in twenty
+// is the most frequent one), and atomics on one word of memory run one after
+// the other, 2.7 ns each. A CTA first counts its kAppendTokens tokens in a
+// table in shared memory, where a token takes the first of kAppendProbes places
+// that is free or its own (the few that find none go to memory directly), then
+// adds each place's count once. Measured for one request of 131072 tokens:
+// 11 us, against 21 us one atomic a token; of 32768 5.6 against 6.5, of 16384
+// 5.3 against 3.9, so a call of at least kAppendLong tokens a request takes it.
+constexpr int kAppendTokens = 1024;
+constexpr int kAppendSlots = 2048;
+constexpr int kAppendProbes = 4;
+constexpr int64_t kAppendLong = 32768;
+
+__global__ void __launch_bounds__(kConThreads)
+    history_append_long_kernel(const StateArgs s, const int32_t* slot, int64_t n,
+                               const int64_t* tokens, int64_t total, const int64_t* offsets,
+                               bool prompt) {
+  __shared__ unsigned long long key[kAppendSlots];
+  __shared__ uint32_t count[kAppendSlots];
+  constexpr unsigned long long kEmpty = ~0ull;
+  for (int i = threadIdx.x; i < kAppendSlots; i += kConThreads) {
+    key[i] = kEmpty;
+    count[i] = 0u;
+  }
+  pdl_wait_then_release();
+  __syncthreads();
+  for (int64_t j0 = blockIdx.x * (int64_t)kAppendTokens; j0 < total;
+       j0 += (int64_t)gridDim.x * kAppendTokens) {
+    constexpr int N = kAppendTokens / kConThreads, M = kAppendSlots / kConThreads;
+    int64_t at[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int64_t j = j0 + k * kConThreads + threadIdx.x;
+      at[k] = j < total ? token_place(s, slot, n, tokens, offsets, j) : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      if (at[k] < 0) continue;
+      const unsigned long long mine = (unsigned long long)at[k];
+      uint32_t h = ((uint32_t)at[k] * 2654435761u) >> 21;  // Fibonacci hashing, 11 bits
+      int tries = 0;
+      for (; tries < kAppendProbes; ++tries, h = (h + 1) % kAppendSlots) {
+        const unsigned long long was = atomicCAS(&key[h], kEmpty, mine);
+        if (was == kEmpty || was == mine) break;
+      }
+      if (tries < kAppendProbes)
+        atomicAdd(&count[h], 1u);
+      else
+        count_token(s, at[k], 1u, prompt);
+    }
+    __syncthreads();
+    // All of a thread's additions are on their way before the first is looked at.
+    unsigned long long k8[M];
+    uint32_t before[M];
+#pragma unroll
+    for (int k = 0; k < M; ++k) {
+      const int i = k * kConThreads + threadIdx.x;
+      k8[k] = key[i];
+      before[k] = 1u;
+      if (k8[k] != kEmpty) {
+        before[k] = prompt ? atomicOr(s.history + k8[k], 0x80000000u)
+                           : atomicAdd(s.history + k8[k], count[i]);
+        key[i] = kEmpty;
+        count[i] = 0u;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < M; ++k)
+      if (before[k] == 0u) atomicOr(s.touched + (k8[k] >> 5), 1u << (k8[k] & 31));
+    __syncthreads();
   }
 }
 
@@ -101,21 +187,30 @@ __global__ void __launch_bounds__(32)
   int64_t hi = offsets ? __ldg(offsets + i + 1) : i + 1;
   lo = lo < 0 ? 0 : lo;
   hi = hi > total ? total : hi;
-  for (int64_t j0 = lo; j0 < hi; j0 += 32) {
-    const int64_t j = j0 + lane;
-    int64_t t = -1;
-    float v = 0.0f;
-    if (j < hi) {
-      t = __ldg(tokens + j);
-      v = __ldg(values + j);
-      if (t < 0 || t >= s.vocab) t = -1;
+  constexpr int N = 4;  // steps whose entries are on their way together
+  for (int64_t j0 = lo; j0 < hi; j0 += 32 * N) {
+    int64_t t[N];
+    float v[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int64_t j = j0 + k * 32 + lane;
+      t[k] = -1;
+      v[k] = 0.0f;
+      if (j < hi) {
+        t[k] = __ldg(tokens + j);
+        v[k] = __ldg(values + j);
+        if (t[k] < 0 || t[k] >= s.vocab) t[k] = -1;
+      }
     }
-    const unsigned same = __match_any_sync(0xFFFFFFFFu, (unsigned long long)t);
-    if (t >= 0 && lane == 31 - __clz(same)) {
-      s.bias[r * s.ld + t] = v;
-      atomicOr(s.touched + r * (s.ld / 32) + (t >> 5), 1u << (t & 31));
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, (unsigned long long)t[k]);
+      if (t[k] >= 0 && lane == 31 - __clz(same)) {
+        s.bias[r * s.ld + t[k]] = v[k];
+        atomicOr(s.touched + r * (s.ld / 32) + (t[k] >> 5), 1u << (t[k] & 31));
+      }
+      __syncwarp();
     }
-    __syncwarp();
   }
 }
 
@@ -557,6 +652,11 @@ cudaError_t launch_state_reset(const StateArgs& s, const int32_t* slot, int64_t 
 cudaError_t launch_history_append(const StateArgs& s, const int32_t* slot, int64_t n,
                                   const int64_t* tokens, int64_t total, const int64_t* offsets,
                                   bool prompt, int sms, cudaStream_t stream) {
+  if (total / n >= kAppendLong) {
+    const dim3 blocks = blocks_for(total, kAppendTokens, (int64_t)sms * 8);
+    return launch(history_append_long_kernel, blocks, kConThreads, stream, s, slot, n, tokens,
+                  total, offsets, prompt);
+  }
   const dim3 blocks = blocks_for(total, kConThreads, (int64_t)sms * 8);
   return launch(history_append_kernel, blocks, kConThreads, stream, s, slot, n, tokens, total,
                 offsets, prompt);

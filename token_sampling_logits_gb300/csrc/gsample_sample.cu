@@ -811,19 +811,19 @@ __device__ __forceinline__ void clear_tile(uint32_t stage, uint32_t keep0, uint3
   if (cleared == 0) return;
   const int lane = threadIdx.x & 31;
   if (cleared <= kClearBits) {
-    uint32_t c0 = ~keep0, c1 = C::kEPU == 8 ? ~keep1 : 0u;
-    while ((c0 | c1) != 0u) {
-      const int e = c0 != 0u ? __ffs((int)c0) - 1 : 1024 + __ffs((int)c1) - 1;
-      if (c0 != 0u)
-        c0 &= c0 - 1u;
-      else
-        c1 &= c1 - 1u;
-      const uint32_t at = (uint32_t)(lane * 32 + e);
-      if constexpr (C::kF32Bits)
-        sts_f32(stage + at * 4u, -INFINITY);
-      else
-        sts_u16(stage + at * 2u, neg_inf_half<DT>());
-    }
+    constexpr uint32_t kSize = C::kF32Bits ? 4u : 2u;
+    auto clear_word = [&](uint32_t c, uint32_t at) {
+      while (c != 0u) {  // from the highest bit down
+        const int e = 31 - __clz((int)c);
+        c ^= 1u << e;
+        if constexpr (C::kF32Bits)
+          sts_f32(at + (uint32_t)e * kSize, -INFINITY);
+        else
+          sts_u16(at + (uint32_t)e * kSize, neg_inf_half<DT>());
+      }
+    };
+    clear_word(~keep0, stage + (uint32_t)lane * 32u * kSize);
+    if constexpr (C::kEPU == 8) clear_word(~keep1, stage + (uint32_t)(1024 + lane * 32) * kSize);
   } else {
     constexpr uint32_t kFull = (1u << C::kEPU) - 1u;
 #pragma unroll 1
