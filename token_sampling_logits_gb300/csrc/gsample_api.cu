@@ -337,6 +337,8 @@ gsample_status run_sample(const void* logits, gsample_dtype dtype, int64_t B, in
       q.out_idx = out_idx;
       cudaError_t e;
       if (con) {
+        const int64_t g = gsample::rc_con_group(), groups = (nu + g - 1) / g;
+        q.units_per_cta = (int32_t)((groups + cluster - 1) / cluster * g);
         q.con = *con;
         e = gsample::launch_sample_cluster(q, (int)dtype, vec, stream);
       } else {

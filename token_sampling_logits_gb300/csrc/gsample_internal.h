@@ -153,7 +153,9 @@ size_t rc_smem_limit();
 cudaError_t launch_sample_cluster(const RowClusterParams& p, int dtype, bool vec,
                                   cudaStream_t stream);
 // The same drawing from constrained logits: the slice limit leaves room for
-// the slice's mask and touched bits.
+// the slice's mask and touched bits, and units_per_cta is a multiple of
+// rc_con_group().
+int rc_con_group();
 void* rc_con_kernel(int dtype, bool vec, bool resident, int* threads);
 size_t rc_con_slice_limit();
 cudaError_t launch_sample_cluster(const ConRowClusterParams& p, int dtype, bool vec,

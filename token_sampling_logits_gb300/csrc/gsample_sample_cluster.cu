@@ -77,11 +77,17 @@ __device__ __noinline__ RcBest rc_score_constrained(uint32_t g, float x0, float 
   return RcBest{bs, bi};
 }
 
-// Bytes of one bit row's words that cover a slice of `units` units, wherever
-// it starts.
+// A constrained row is dealt to its CTAs in blocks of kConGroup units in turn,
+// not in contiguous slices: the low ids hold most of a request's tokens, and the
+// CTA with all of them would keep the cluster waiting. units_per_cta is a
+// multiple of kConGroup there, so that a CTA's bits are whole words.
+constexpr int kConGroup = 32;
+static_assert(kRcThreads % kConGroup == 0, "a thread's units are a fixed stride apart");
+
+// Bytes of one bit row of `units` units.
 template <int DT, bool VEC>
 __host__ __device__ constexpr size_t slice_bit_bytes(int32_t units) {
-  return ((size_t)units * (VEC && DT != 0 ? 8 : 4) / 32 + 2) * 4;
+  return (size_t)units * (VEC && DT != 0 ? 8 : 4) / 8;
 }
 
 template <bool CON>
@@ -126,11 +132,19 @@ __global__ void __launch_bounds__(kRcThreads, 1)
   const uint64_t sd = p.seed ? __ldg(p.seed + b) : 0ull;
   const uint64_t of = p.offset ? __ldg(p.offset + b) : 0ull;
 
-  auto unit_at = [&](int32_t u) -> uint4 {
-    if constexpr (RESIDENT)
-      return lds128(slice + (uint32_t)(u - u_lo) * 16u);
+  // The CTA's i-th unit (0 <= i < n_units), read at slice + 16 * i.
+  const int32_t n_units = CON ? p.units_per_cta : u_hi - u_lo;
+  auto unit_of = [&](int32_t i) -> int32_t {
+    if constexpr (CON)
+      return (i / kConGroup * p.cluster + rank) * kConGroup + i % kConGroup;
     else
-      return load_unit<DT, VEC>(row, u, p.V, pol);
+      return u_lo + i;
+  };
+  auto unit_at = [&](int32_t i) -> uint4 {
+    if constexpr (RESIDENT)
+      return lds128(slice + (uint32_t)i * 16u);
+    else
+      return load_unit<DT, VEC>(row, u_lo + i, p.V, pol);
   };
 
   // The thread's largest logit, lowest index on ties: the greedy answer, and
@@ -140,8 +154,8 @@ __global__ void __launch_bounds__(kRcThreads, 1)
   // that equals it. On the resident path the thread's units are requested in
   // GSAMPLE_RC_CHUNKS groups and each is reduced as it lands.
   float cand_x = -INFINITY;
-  int32_t cand_u = -1;
-  auto unit_max_of = [&](int32_t u, const uint4& r) {
+  int32_t cand_u = -1;  // the CTA's cand_u-th unit
+  auto unit_max_of = [&](int32_t i, const uint4& r) {
     float m;
     if constexpr (C::kF32Bits) {
       m = fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
@@ -152,86 +166,92 @@ __global__ void __launch_bounds__(kRcThreads, 1)
     }
     if (m > cand_x) {
       cand_x = m;
-      cand_u = u;
+      cand_u = i;
     }
   };
   float bs = -INFINITY;
   int32_t bi = INT32_MAX;
   [[maybe_unused]] RowConstraints con;
-  [[maybe_unused]] const unsigned char* slice_touched = nullptr;  // byte of unit u at byte_of(u)
-  [[maybe_unused]] const int32_t w_lo = (int32_t)((int64_t)u_lo * C::kEPU >> 5);
-  [[maybe_unused]] auto byte_of = [&](int32_t u) { return (u * C::kEPU >> 3) - w_lo * 4; };
+  [[maybe_unused]] const unsigned char* touched_bytes = nullptr;
+  // The bits of the CTA's i-th unit in one of its bit rows.
+  [[maybe_unused]] auto bits_of = [&](const unsigned char* bits, int32_t i) -> uint32_t {
+    return C::kEPU == 8 ? bits[i] : (bits[i >> 1] >> ((i & 1) * 4)) & 0xFu;
+  };
   if constexpr (CON) {
-    // The slice and the words of its mask and touched bits are requested side
+    // The units and the words of their mask and touched bits are requested side
     // by side; the words are shared by the CTA's threads.
-    for (int32_t u = u_lo + tid; u < u_hi; u += kRcThreads) {
-      const uint32_t dst = slice + (uint32_t)(u - u_lo) * 16u;
+    for (int32_t i = tid; i < n_units; i += kRcThreads) {
+      const int32_t u = unit_of(i);
+      const uint32_t dst = slice + (uint32_t)i * 16u;
       if (VEC && (u + 1) * C::kEPU <= p.V)
         cp_async16(dst, row + (size_t)u * 16, pol);
       else
-        sts128(dst, load_unit<DT, VEC>(row, u, p.V, pol));
+        sts128(dst, load_unit<DT, VEC>(row, u, p.V, pol));  // -inf past the row
     }
     cp_async_commit();
     con = row_constraints(p.con, b);
     unsigned char* mask_bytes = smem + (size_t)p.units_per_cta * 16;
-    unsigned char* touched_bytes = mask_bytes + slice_bit_bytes<DT, VEC>(p.units_per_cta);
-    slice_touched = touched_bytes;
-    if (u_lo < u_hi) {
-      const int64_t e_hi = (int64_t)u_hi * C::kEPU;
-      const int32_t words = (int32_t)(((e_hi < p.V ? e_hi : p.V) + 31) >> 5) - w_lo;
+    touched_bytes = mask_bytes + slice_bit_bytes<DT, VEC>(p.units_per_cta);
+    {
+      constexpr int W = kConGroup * C::kEPU / 32;  // words a block
+      const int32_t words = n_units / kConGroup * W, row_words = (p.V + 31) / 32;
       const uint32_t* mw = reinterpret_cast<const uint32_t*>(con.mask);
       const uint32_t* tw = reinterpret_cast<const uint32_t*>(con.touched);
 #pragma unroll 4
-      for (int32_t w = tid; w < words; w += kRcThreads) {
-        const uint32_t m = mw ? __ldcg(mw + w_lo + w) : 0xFFFFFFFFu;
-        const uint32_t t = tw ? __ldcg(tw + w_lo + w) : 0u;
-        reinterpret_cast<uint32_t*>(mask_bytes)[w] = m;
-        reinterpret_cast<uint32_t*>(touched_bytes)[w] = t & m;
+      for (int32_t i = tid; i < words; i += kRcThreads) {
+        const int32_t w = (i / W * p.cluster + rank) * W + i % W;
+        const bool in = w < row_words;
+        const uint32_t m = !in ? 0u : mw ? __ldcg(mw + w) : 0xFFFFFFFFu;
+        const uint32_t t = in && tw ? __ldcg(tw + w) : 0u;
+        reinterpret_cast<uint32_t*>(mask_bytes)[i] = m;
+        reinterpret_cast<uint32_t*>(smem + (size_t)p.units_per_cta * 16 +
+                                    slice_bit_bytes<DT, VEC>(p.units_per_cta))[i] = t & m;
       }
     }
     cp_async_wait<0>();
     __syncthreads();
     // Each thread constrains its own units, eight at a time, and takes their
     // maxima.
-    for (int32_t u0 = u_lo + tid; u0 < u_hi; u0 += 8 * kRcThreads) {
+    for (int32_t i0 = tid; i0 < n_units; i0 += 8 * kRcThreads) {
       constexpr uint32_t kFull = (1u << C::kEPU) - 1u;
       uint64_t allowed = 0ull, touched = 0ull;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int32_t u = u0 + k * kRcThreads;
-        if (u >= u_hi) break;
-        const int sh = C::kEPU == 4 ? (u & 1) * 4 : 0;
-        allowed |= (uint64_t)((mask_bytes[byte_of(u)] >> sh) & kFull) << (8 * k);
-        touched |= (uint64_t)((touched_bytes[byte_of(u)] >> sh) & kFull) << (8 * k);
+        const int32_t i = i0 + k * kRcThreads;
+        if (i >= n_units) break;
+        allowed |= (uint64_t)bits_of(mask_bytes, i) << (8 * k);
+        touched |= (uint64_t)bits_of(touched_bytes, i) << (8 * k);
       }
-      const uint32_t a0 = slice + (uint32_t)(u0 - u_lo) * 16u;
-      apply_touched<DT, C::kF32Bits, C::kEPU, kRcThreads>(a0, u0, touched, con, sampled, bs, bi);
+      const uint32_t a0 = slice + (uint32_t)i0 * 16u;
+      apply_touched<DT, C::kF32Bits, C::kEPU, kRcThreads>(a0, unit_of(i0), kRcThreads * p.cluster,
+                                                          touched, con, sampled, bs, bi);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int32_t u = u0 + k * kRcThreads;
-        if (u >= u_hi) break;
-        const uint32_t a = a0 + (uint32_t)(k * kRcThreads) * 16u;
+        const int32_t i = i0 + k * kRcThreads;
+        if (i >= n_units) break;
+        const uint32_t a = slice + (uint32_t)i * 16u;
         const uint32_t m = (uint32_t)(allowed >> (8 * k)) & 0xFFu;
         uint4 r = lds128(a);
         if (m != kFull) {
           r = masked_unit<DT, C::kF32Bits>(r, m);
           sts128(a, r);
         }
-        unit_max_of(u, r);
+        unit_max_of(i, r);
       }
     }
   } else if constexpr (RESIDENT) {
-    load_slice_then<DT, VEC, kRcThreads, GSAMPLE_RC_CHUNKS>(row, u_lo, u_hi, p.V, slice, pol,
-                                                           unit_max_of);
+    load_slice_then<DT, VEC, kRcThreads, GSAMPLE_RC_CHUNKS>(
+        row, u_lo, u_hi, p.V, slice, pol,
+        [&](int32_t u, const uint4& r) { unit_max_of(u - u_lo, r); });
   } else {
-    for (int32_t u = u_lo + tid; u < u_hi; u += kRcThreads) unit_max_of(u, unit_at(u));
+    for (int32_t i = tid; i < n_units; i += kRcThreads) unit_max_of(i, unit_at(i));
   }
   int32_t cand_i = INT32_MAX;
   if (cand_u >= 0) {
     const uint4 r = unit_at(cand_u);
 #pragma unroll
     for (int e = C::kEPU - 1; e >= 0; --e)
-      if (elt<DT, VEC>(r, e) == cand_x) cand_i = cand_u * C::kEPU + e;
+      if (elt<DT, VEC>(r, e) == cand_x) cand_i = unit_of(cand_u) * C::kEPU + e;
   }
 
   // Constrained slices without any candidate are not swept.
@@ -250,7 +270,7 @@ __global__ void __launch_bounds__(kRcThreads, 1)
     if (cand_i != INT32_MAX && cand_x > -INFINITY) {
       const uint4 blk = philox_row_1((uint32_t)cand_i >> 2, ph);
       if constexpr (CON && !C::kF32Bits) {
-        if ((slice_touched[byte_of(cand_u)] >> (cand_i - cand_u * C::kEPU)) & 1)
+        if ((bits_of(touched_bytes, cand_u) >> (cand_i % C::kEPU)) & 1u)
           cand_x = exact_touched<DT>(row, cand_i, con);
       }
       take_better(exact_score(cand_x, word_of(blk, cand_i & 3), T), cand_i, bs, bi);
@@ -263,7 +283,7 @@ __global__ void __launch_bounds__(kRcThreads, 1)
     // of 16-bit), one Philox block each, the word bound, then the rare exact
     // scores.
     constexpr int kUPB = 4 / C::kGPU;
-    const int32_t n_iter = (u_hi - u_lo + kRcThreads - 1) / kRcThreads;
+    const int32_t n_iter = (n_units + kRcThreads - 1) / kRcThreads;
     for (int32_t it = 0; it < n_iter; it += kUPB) {
       uint4 r[kUPB];
       float xm[4];
@@ -271,9 +291,9 @@ __global__ void __launch_bounds__(kRcThreads, 1)
       bool ok[4];
 #pragma unroll
       for (int j = 0; j < kUPB; ++j) {
-        const int32_t u = u_lo + tid + (it + j) * kRcThreads;
-        const bool valid = u < u_hi;
-        r[j] = valid ? unit_at(u) : make_uint4(0, 0, 0, 0);
+        const int32_t i = tid + (it + j) * kRcThreads, u = unit_of(i);
+        const bool valid = i < n_units;
+        r[j] = valid ? unit_at(i) : make_uint4(0, 0, 0, 0);
         if constexpr (C::kF32Bits) {
           xm[j] = fmaxf(fmaxf(__uint_as_float(r[j].x), __uint_as_float(r[j].y)),
                         fmaxf(__uint_as_float(r[j].z), __uint_as_float(r[j].w)));
@@ -389,7 +409,7 @@ void* select_rc(int dtype, bool vec, bool resident) {
 constexpr size_t kRcSmemLimit = 200 * 1024;
 // Slices of constrained rows: with two rows of bits (an eighth of the slice at
 // most) they stay within kRcSmemLimit.
-constexpr size_t kRcConSliceLimit = 176 * 1024;
+constexpr size_t kRcConSliceLimit = 160 * 1024;
 
 }  // namespace
 
@@ -406,6 +426,8 @@ void* rc_con_kernel(int dtype, bool vec, bool, int* threads) {
   *threads = kRcThreads;
   return select_rc_constrained(dtype, vec);
 }
+
+int rc_con_group() { return kConGroup; }
 
 int rc_max_cluster(int dtype, bool vec, bool constrained) {
   for (int res = constrained ? 1 : 0; res < 2; ++res) {
