@@ -257,25 +257,24 @@ void plan_sample(const DeviceInfo& d, const void* logits, gsample_dtype dtype, i
   *vec_out = vec;
 }
 
-#ifndef GSAMPLE_MIN_CHUNKS
-#define GSAMPLE_MIN_CHUNKS 2
-#endif
-
 // The chunks of a constrained launch, multiples of 8 units dealt to the warps
 // in turn. With k chunks a warp, rows cut into floor(k * warps / B) of them end
-// together; of k = 2 .. 12 the one whose warps have least to do is taken, a
-// chunk's fixed costs (row context, merge) counting as kChunkUnits units. Two
-// or more a warp, because rows differ in work: a warp that meets a row with
-// nothing left has another.
+// together; of k = 1 .. 12 the one whose warps have least to do is taken, a
+// chunk's fixed costs (row context, first bound, merge) counting as kChunkUnits
+// units. Measured at V = 151936 bf16, B = 256 and 512: one or two chunks a warp
+// 69 and 130 us, at least two 70 and 135, about four 83 and 160.
+// A chunk is at least a tile (256 units): with 56 units a chunk, 65 rows of
+// 32000 took 61 us instead of 22.
 void plan_chunks(gsample::ConSampleParams* p) {
-  constexpr int64_t kChunkUnits = 64;
+  constexpr int64_t kChunkUnits = 512, kMinUnits = 256;
   const int64_t nu = p->units_per_row, warps = (int64_t)p->ctas * gsample::kWarps;
   int64_t best = -1, units = 8;
-  for (int64_t k = GSAMPLE_MIN_CHUNKS; k <= 12; ++k) {
+  for (int64_t k = 1; k <= 12; ++k) {
     const int64_t per_row = k * warps / p->B;
     if (per_row < 1) continue;
     int64_t u = (nu + per_row - 1) / per_row;
     u = (u + 7) / 8 * 8;
+    if (u < kMinUnits) u = kMinUnits;
     const int64_t rounds = (p->B * ((nu + u - 1) / u) + warps - 1) / warps;
     const int64_t cost = rounds * (u + kChunkUnits);
     if (best < 0 || cost < best) {
@@ -316,10 +315,20 @@ gsample_status run_sample(const void* logits, gsample_dtype dtype, int64_t B, in
     const int max_cluster = con ? d->con_cluster[at] : d->rc_cluster[at];
     const size_t limit = con ? gsample::rc_con_slice_limit() : gsample::rc_smem_limit();
     int cluster = cluster_override;
-    if (cluster == 0 && B <= kClusterMaxRows) {
-      cluster = pick_cluster(con ? gsample::rc_con_kernel : gsample::rc_kernel, (int)dtype, vec, B,
-                             nu, max_cluster, kClusterUnitsPerCta, limit);
-      if ((nu + cluster - 1) / cluster * 16 > (int64_t)limit) cluster = 0;
+    if (cluster == 0 && (B <= kClusterMaxRows || (con && B <= d->sms))) {
+      const auto kernel = con ? gsample::rc_con_kernel : gsample::rc_kernel;
+      cluster = pick_cluster(kernel, (int)dtype, vec, B, nu, max_cluster, kClusterUnitsPerCta,
+                             limit);
+      const size_t slice = (size_t)((nu + cluster - 1) / cluster) * 16;
+      if (slice > limit) cluster = 0;
+      // Constrained rows take it past kClusterMaxRows while the clusters run in
+      // one wave: measured at V = 32000 bf16, B = 128, 18 us against 22; at V =
+      // 151936, B = 65, 25 against 34.
+      if (cluster > 0 && B > kClusterMaxRows) {
+        int threads = 0;
+        void* fn = kernel((int)dtype, vec, true, &threads);
+        if (B > active_clusters(fn, threads, cluster, slice + slice / 8)) cluster = 0;
+      }
     }
     if (cluster > 0) {
       if (cluster > 16 || cluster > max_cluster) return GSAMPLE_ERR_INVALID_ARG;
@@ -364,7 +373,7 @@ gsample_status run_sample(const void* logits, gsample_dtype dtype, int64_t B, in
   if (con) {
     p.con = *con;
     plan_chunks(&p);
-    err = gsample::launch_sample(p, (int)dtype, vec, stream);
+    err = gsample::launch_sample(p, (int)dtype, vec, d->sms, stream);
   } else {
     err = gsample::launch_sample(static_cast<const SampleParams&>(p), (int)dtype, vec, stream);
   }

@@ -131,7 +131,8 @@ inline int units_elems(int dtype, bool vec) { return vec ? (dtype == 0 ? 4 : 8) 
 int sample_ctas_per_sm(int dtype, bool vec, bool constrained);
 size_t sample_smem_bytes(int dtype, bool vec);
 cudaError_t launch_sample(const SampleParams& p, int dtype, bool vec, cudaStream_t stream);
-cudaError_t launch_sample(const ConSampleParams& p, int dtype, bool vec, cudaStream_t stream);
+cudaError_t launch_sample(const ConSampleParams& p, int dtype, bool vec, int sms,
+                          cudaStream_t stream);
 
 // HLG: the largest cluster size the device can co-schedule for this kernel and
 // the shared memory a CTA needs to hold `units_per_cta` units.

@@ -838,15 +838,12 @@ __device__ __forceinline__ void clear_tile(uint32_t stage, uint32_t keep0, uint3
   __syncwarp();  // other lanes read the places
 }
 
-// The list kernel. Every warp works alone: it takes kListWords words a lane of
-// one row, lists their listed elements in shared memory and scores them one a
+// The list kernel. Every warp works alone: it takes kListWords words a lane (8,
+// or fewer while there are not warps enough to fill the device) of one row, lists their listed elements in shared memory and scores them one a
 // lane. Its words come in small groups spread over the row, because the low ids
 // hold most of a request's tokens: of 1600 touched tokens some 700 lie in the
 // first 64 words, and one warp with all of them would work long after the
 // others.
-#ifndef GSAMPLE_LIST_WORDS
-#define GSAMPLE_LIST_WORDS 8
-#endif
 #ifndef GSAMPLE_LIST_CTAS
 #define GSAMPLE_LIST_CTAS 8
 #endif
@@ -854,10 +851,9 @@ __device__ __forceinline__ void clear_tile(uint32_t stage, uint32_t keep0, uint3
 #define GSAMPLE_LIST_GROUP 4
 #endif
 constexpr int kListThreads = 128;
-constexpr int kListWords = GSAMPLE_LIST_WORDS;  // words a lane
 constexpr int kListCap = 256;                   // entries a warp lists at a time
 
-template <int DT>
+template <int DT, int kListWords>
 __global__ void __launch_bounds__(kListThreads, GSAMPLE_LIST_CTAS)
     list_kernel(const ConSampleParams p, int32_t warps_per_row) {
   __shared__ uint32_t lists[kListThreads / 32][kListCap];
@@ -1237,6 +1233,16 @@ void* select_kernel(int dtype, bool vec, bool constrained) {
   }
 }
 
+template <int DT>
+void* list_kernel_ptr(int lane_words) {
+  switch (lane_words) {
+    case 1: return reinterpret_cast<void*>(&list_kernel<DT, 1>);
+    case 2: return reinterpret_cast<void*>(&list_kernel<DT, 2>);
+    case 4: return reinterpret_cast<void*>(&list_kernel<DT, 4>);
+    default: return reinterpret_cast<void*>(&list_kernel<DT, 8>);
+  }
+}
+
 cudaError_t launch_kernel(void* fn, const SampleParams& p, void* param, size_t smem,
                           cudaStream_t stream) {
   void* args[] = {param};
@@ -1283,10 +1289,18 @@ cudaError_t launch_sample(const SampleParams& p, int dtype, bool vec, cudaStream
                        sample_smem_bytes(dtype, vec), stream);
 }
 
-cudaError_t launch_sample(const ConSampleParams& p, int dtype, bool vec, cudaStream_t stream) {
+cudaError_t launch_sample(const ConSampleParams& p, int dtype, bool vec, int sms,
+                          cudaStream_t stream) {
   if (p.con.history || p.con.mask) {  // else nothing is ever listed
-    const int32_t words = (p.V + 31) / 32, per_warp = 32 * kListWords;
-    int32_t warps_per_row = (words + per_warp - 1) / per_warp;
+    const int32_t words = (p.V + 31) / 32;
+    // Halved until there is a warp for every place on the device: at V = 32000,
+    // B = 128 the launch took 27 us with 8 words a lane throughout, 7 so.
+    const int64_t places = (int64_t)sms * GSAMPLE_LIST_CTAS * (kListThreads / 32);
+    int lane_words = 8;
+    while (lane_words > 1 &&
+           p.B * ((words + 32 * lane_words - 1) / (32 * lane_words)) < places)
+      lane_words /= 2;
+    int32_t warps_per_row = (words + 32 * lane_words - 1) / (32 * lane_words);
     const unsigned ctas = (unsigned)((warps_per_row + kListThreads / 32 - 1) / (kListThreads / 32));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas, (unsigned)(p.B < 65535 ? p.B : 65535));
@@ -1296,9 +1310,9 @@ cudaError_t launch_sample(const ConSampleParams& p, int dtype, bool vec, cudaStr
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     void* args[] = {const_cast<ConSampleParams*>(&p), &warps_per_row};
-    void* fn = dtype == 0   ? reinterpret_cast<void*>(&list_kernel<0>)
-               : dtype == 1 ? reinterpret_cast<void*>(&list_kernel<1>)
-                            : reinterpret_cast<void*>(&list_kernel<2>);
+    void* fn = dtype == 0   ? list_kernel_ptr<0>(lane_words)
+               : dtype == 1 ? list_kernel_ptr<1>(lane_words)
+                            : list_kernel_ptr<2>(lane_words);
     const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
     if (e != cudaSuccess) return e;
   }
