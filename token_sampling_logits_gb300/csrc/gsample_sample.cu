@@ -863,6 +863,7 @@ __global__ void __launch_bounds__(kListThreads, GSAMPLE_LIST_CTAS)
   if (q >= warps_per_row) return;
   uint32_t* list = lists[warp];
   const int32_t words = (p.V + 31) / 32;
+  const uint32_t tail = 0xFFFFFFFFu >> ((32 - (p.V & 31)) & 31);
   // The lane's k-th word: of the warp's 32 / G groups a step, warps_per_row apart.
   constexpr int G = GSAMPLE_LIST_GROUP;
   const int32_t w0 = (q + (lane / G) * warps_per_row) * G + lane % G;
@@ -883,7 +884,9 @@ __global__ void __launch_bounds__(kListThreads, GSAMPLE_LIST_CTAS)
     int mine = 0;
 #pragma unroll
     for (int k = 0; k < kListWords; ++k) {
-      t[k] = split_word(m[k], t[k], (w0 + k * step) * 32, p.V).list;
+      // split_word(...).list, with the cut at the row's end made ready
+      const uint32_t listed = __popc(m[k]) <= kFewInWord ? 0xFFFFFFFFu : t[k];
+      t[k] = m[k] & listed & (w0 + k * step == words - 1 ? tail : 0xFFFFFFFFu);
       mine += __popc(t[k]);
     }
     int incl = mine;
@@ -901,11 +904,23 @@ __global__ void __launch_bounds__(kListThreads, GSAMPLE_LIST_CTAS)
     int32_t bi = INT32_MAX;
     for (int base = 0; base < total; base += kListCap) {
       int at = incl - mine - base;
+      if (total <= kListCap) {
 #pragma unroll
-      for (int k = 0; k < kListWords; ++k) {
-        const uint32_t e0 = (uint32_t)(w0 + k * step) * 32u;
-        for (uint32_t bits = t[k]; bits != 0u; bits &= bits - 1u, ++at)
-          if (at >= 0 && at < kListCap) list[at] = e0 + (uint32_t)__ffs((int)bits) - 1u;
+        for (int k = 0; k < kListWords; ++k) {
+          const uint32_t e0 = (uint32_t)(w0 + k * step) * 32u;
+          for (uint32_t bits = t[k]; bits != 0u; bits &= bits - 1u)
+            list[at++] = e0 + (uint32_t)__ffs((int)bits) - 1u;
+        }
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < kListWords; ++k) {
+          uint32_t bits = t[0];
+#pragma unroll
+          for (int i = 1; i < kListWords; ++i) bits = k == i ? t[i] : bits;
+          const uint32_t e0 = (uint32_t)(w0 + k * step) * 32u;
+          for (; bits != 0u; bits &= bits - 1u, ++at)
+            if (at >= 0 && at < kListCap) list[at] = e0 + (uint32_t)__ffs((int)bits) - 1u;
+        }
       }
       __syncwarp();
       const int n = min(kListCap, total - base);
