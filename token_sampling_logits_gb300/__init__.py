@@ -242,7 +242,7 @@ def _prepare(logits, out, workspace, need_ws: bool = True):
         return dt, B, V, ld, out, None
     if workspace is None:
         workspace = new_workspace(B, dev)
-    elif workspace.device != dev or workspace.numel() * workspace.element_size() < workspace_bytes(B):
+    elif workspace.device != dev or workspace.nbytes < workspace_bytes(B):
         raise ValueError("workspace too small or on another device")
     return dt, B, V, ld, out, workspace
 
@@ -484,11 +484,10 @@ def new_logit_state(rows: int, vocab: int, device=None, bias: bool = True) -> Lo
                       torch.zeros((rows, ld // 32), dtype=torch.int32, device=dev), vocab)
 
 
-def _launch(device, what, fn, *args):
-    """fn(*args, the device's current stream) with the device as the current
-    one (the library launches there)."""
+def _launch(index, what, fn, *args):
+    """fn(*args, the current stream of device `index`) with that device as the
+    current one (the library launches there)."""
     torch = _torch()
-    index = device.index
     if torch.cuda.current_device() == index:
         status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
@@ -498,37 +497,48 @@ def _launch(device, what, fn, *args):
         raise GSampleError(status, what)
 
 
-def _vector(x, n, dtype, device, name):
+def _vector(x, n, dtype, index, name):
     """The address of a contiguous 1-D tensor of n (None: any number of)
-    entries; None for None."""
+    entries on device `index`; None for None."""
     if x is None:
         return None
-    if x.dtype != dtype or x.device != device or x.dim() != 1 or \
+    if x.dtype != dtype or x.get_device() != index or x.dim() != 1 or \
             (n is not None and x.numel() != n) or not x.is_contiguous():
-        raise ValueError("%s must be a contiguous 1-D %s tensor%s on %s" %
-                         (name, dtype, "" if n is None else " of %d entries" % n, device))
+        raise ValueError("%s must be a contiguous 1-D %s tensor%s on cuda:%d" %
+                         (name, dtype, "" if n is None else " of %d entries" % n, index))
     return x.data_ptr()
+
+
+def _row_at(x, B, dtype, index, name, keep):
+    """The address of a per-row array given as a tensor of B entries or as a
+    scalar; a tensor made here goes into `keep`."""
+    torch = _torch()
+    if not isinstance(x, torch.Tensor):
+        x = torch.full((B,), x, dtype=dtype, device="cuda:%d" % index)
+        keep.append(x)
+    return _vector(x, B, dtype, index, name)
 
 
 def _lists(state, slots, tokens, offsets):
     """n requests: (slot, n, tokens, total, offsets) as the library takes them."""
     torch = _torch()
-    dev = state.device
-    tokens_at = _vector(tokens, None, torch.int64, dev, "tokens")
-    offsets_at = _vector(offsets, None, torch.int64, dev, "offsets")
+    index = state.device.index
+    tokens_at = _vector(tokens, None, torch.int64, index, "tokens")
+    offsets_at = _vector(offsets, None, torch.int64, index, "offsets")
     total = tokens.numel()
     n = total
     if offsets is not None:
         n = offsets.numel() - 1
         if n < 0:
             raise ValueError("offsets has one entry more than there are requests")
-    return _vector(slots, n, torch.int32, dev, "slots"), n, tokens_at, total, offsets_at
+    return _vector(slots, n, torch.int32, index, "slots"), n, tokens_at, total, offsets_at
 
 
 def state_reset(state: LogitState, slots=None) -> None:
     """Clears the state rows in `slots` (int32 device tensor), or all of them."""
-    at = _vector(slots, None, _torch().int32, state.device, "slots")
-    _launch(state.device, "gsample_state_reset", lib().gsample_state_reset, state._at, at,
+    index = state.device.index
+    at = _vector(slots, None, _torch().int32, index, "slots")
+    _launch(index, "gsample_state_reset", lib().gsample_state_reset, state._at, at,
             state.rows if slots is None else slots.numel())
 
 
@@ -538,7 +548,7 @@ def history_append(state: LogitState, tokens, slots=None, offsets=None,
     i owns tokens[offsets[i]:offsets[i + 1]], or tokens[i] alone without
     offsets (the indices a sampler just drew). slots[i] (int32) is its state
     row; without slots, row i. Ids outside the vocabulary are ignored."""
-    _launch(state.device, "gsample_history_append", lib().gsample_history_append, state._at,
+    _launch(state.device.index, "gsample_history_append", lib().gsample_history_append, state._at,
             *_lists(state, slots, tokens, offsets), 0 if prompt else 1)
 
 
@@ -548,41 +558,38 @@ def bias_set(state: LogitState, tokens, values, slots=None, offsets=None) -> Non
     if state.bias is None:
         raise ValueError("the state was made without biases")
     slot, n, tokens_at, total, offsets_at = _lists(state, slots, tokens, offsets)
-    values_at = _vector(values, total, _torch().float32, state.device, "values")
-    _launch(state.device, "gsample_bias_set", lib().gsample_bias_set, state._at, slot, n,
-            tokens_at, values_at, total, offsets_at)
+    index = state.device.index
+    values_at = _vector(values, total, _torch().float32, index, "values")
+    _launch(index, "gsample_bias_set", lib().gsample_bias_set, state._at, slot, n, tokens_at,
+            values_at, total, offsets_at)
 
 
-def _constraints(B, V, dev, state, slots, repetition, frequency, presence, mask, mask_rows):
-    """The C struct, and the tensors made here that it points into (to be kept
-    until the call)."""
+def _constraints(B, V, index, state, slots, repetition, frequency, presence, mask, mask_rows,
+                 keep):
+    """The C struct; tensors made here that it points into go into `keep`."""
     torch = _torch()
-    keep = []
     state_at = slot = rep = freq = pres = None
     if state is not None:
-        if state.device != dev or state.vocab != V:
+        if state.device.index != index or state.vocab != V:
             raise ValueError("the state must be on the logits' device and of their vocabulary")
         if slots is None and state.rows < B:
             raise ValueError("without slots the state needs a row for every batch row")
         state_at = state._at
-        slot = _vector(slots, B, torch.int32, dev, "slots")
-
-        def row(x, name):
-            if x is None:
-                return None
-            x = _row_tensor(x, B, torch.float32, dev, name)
-            keep.append(x)
-            return x.data_ptr()
-
-        rep, freq, pres = row(repetition, "repetition"), row(frequency, "frequency"), \
-            row(presence, "presence")
+        slot = _vector(slots, B, torch.int32, index, "slots")
+        f32 = torch.float32
+        if repetition is not None:
+            rep = _row_at(repetition, B, f32, index, "repetition", keep)
+        if frequency is not None:
+            freq = _row_at(frequency, B, f32, index, "frequency", keep)
+        if presence is not None:
+            pres = _row_at(presence, B, f32, index, "presence", keep)
     elif slots is not None or repetition is not None or frequency is not None or \
             presence is not None:
         raise ValueError("slots and penalties need a state")
     mask_at = mask_row = None
     masks = mask_ld = 0
     if mask is not None:
-        if mask.dtype != torch.int32 or mask.device != dev or mask.dim() != 2:
+        if mask.dtype != torch.int32 or mask.get_device() != index or mask.dim() != 2:
             raise ValueError("mask must be a 2-D int32 tensor on the logits' device")
         masks, words = mask.shape
         mask_ld, inner = mask.stride()
@@ -594,10 +601,10 @@ def _constraints(B, V, dev, state, slots, repetition, frequency, presence, mask,
         if mask_rows is None and masks < B:
             raise ValueError("without mask_rows there must be a mask for every batch row")
         mask_at = mask.data_ptr()
-        mask_row = _vector(mask_rows, B, torch.int32, dev, "mask_rows")
+        mask_row = _vector(mask_rows, B, torch.int32, index, "mask_rows")
     elif mask_rows is not None:
         raise ValueError("mask_rows needs a mask")
-    return _ConstraintsC(state_at, slot, rep, freq, pres, mask_at, masks, mask_ld, mask_row), keep
+    return _ConstraintsC(state_at, slot, rep, freq, pres, mask_at, masks, mask_ld, mask_row)
 
 
 def process_logits(logits, state: LogitState | None = None, slots=None, repetition=None,
@@ -625,10 +632,11 @@ def process_logits(logits, state: LogitState | None = None, slots=None, repetiti
     odt, _, _, out_ld = _logits_args(out)
     if odt not in (F32, dt):
         raise ValueError("out must be of the logits' type or float32")
-    c, keep = _constraints(B, V, dev, state, slots, repetition, frequency, presence, mask,
-                           mask_rows)
-    _launch(dev, "gsample_process_logits", lib().gsample_process_logits, logits.data_ptr(), dt, B,
-            V, ld, ctypes.byref(c), out.data_ptr(), odt, out_ld)
+    index, keep = dev.index, []
+    c = _constraints(B, V, index, state, slots, repetition, frequency, presence, mask, mask_rows,
+                     keep)
+    _launch(index, "gsample_process_logits", lib().gsample_process_logits, logits.data_ptr(), dt,
+            B, V, ld, ctypes.byref(c), out.data_ptr(), odt, out_ld)
     return out
 
 
@@ -641,15 +649,15 @@ def constrained_gumbel_argmax(logits, temperature, seed, offset, state: LogitSta
     row whose constraints leave nothing."""
     torch = _torch()
     dt, B, V, ld, out, ws = _prepare(logits, out, workspace)
-    dev = logits.device
-    T = _row_tensor(temperature, B, torch.float32, dev, "temperature")
-    S = _row_tensor(seed, B, torch.int64, dev, "seed")
-    O = _row_tensor(offset, B, torch.int64, dev, "offset")
-    c, keep = _constraints(B, V, dev, state, slots, repetition, frequency, presence, mask,
-                           mask_rows)
-    _launch(dev, "gsample_constrained_gumbel_argmax", lib().gsample_constrained_gumbel_argmax,
-            logits.data_ptr(), dt, B, V, ld, T.data_ptr(), S.data_ptr(), O.data_ptr(),
-            ctypes.byref(c), out.data_ptr(), ws.data_ptr())
+    index, keep = logits.get_device(), []
+    T = _row_at(temperature, B, torch.float32, index, "temperature", keep)
+    S = _row_at(seed, B, torch.int64, index, "seed", keep)
+    O = _row_at(offset, B, torch.int64, index, "offset", keep)
+    c = _constraints(B, V, index, state, slots, repetition, frequency, presence, mask, mask_rows,
+                     keep)
+    _launch(index, "gsample_constrained_gumbel_argmax", lib().gsample_constrained_gumbel_argmax,
+            logits.data_ptr(), dt, B, V, ld, T, S, O, ctypes.byref(c), out.data_ptr(),
+            ws.data_ptr())
     return out
 
 

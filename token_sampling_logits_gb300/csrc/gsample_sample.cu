@@ -844,17 +844,13 @@ __device__ __forceinline__ void clear_tile(uint32_t stage, uint32_t keep0, uint3
 // hold most of a request's tokens: of 1600 touched tokens some 700 lie in the
 // first 64 words, and one warp with all of them would work long after the
 // others.
-#ifndef GSAMPLE_LIST_CTAS
-#define GSAMPLE_LIST_CTAS 8
-#endif
-#ifndef GSAMPLE_LIST_GROUP
-#define GSAMPLE_LIST_GROUP 4
-#endif
 constexpr int kListThreads = 128;
+constexpr int kListCtas = 8;   // an SM: 64 registers a thread (6 and 10: 2 % and 7 % slower)
+constexpr int kListGroup = 4;  // words a group (2 and 8: 1 % and 8 % slower)
 constexpr int kListCap = 256;                   // entries a warp lists at a time
 
 template <int DT, int kListWords>
-__global__ void __launch_bounds__(kListThreads, GSAMPLE_LIST_CTAS)
+__global__ void __launch_bounds__(kListThreads, kListCtas)
     list_kernel(const ConSampleParams p, int32_t warps_per_row) {
   __shared__ uint32_t lists[kListThreads / 32][kListCap];
   pdl_wait_then_release();
@@ -865,7 +861,7 @@ __global__ void __launch_bounds__(kListThreads, GSAMPLE_LIST_CTAS)
   const int32_t words = (p.V + 31) / 32;
   const uint32_t tail = 0xFFFFFFFFu >> ((32 - (p.V & 31)) & 31);
   // The lane's k-th word: of the warp's 32 / G groups a step, warps_per_row apart.
-  constexpr int G = GSAMPLE_LIST_GROUP;
+  constexpr int G = kListGroup;
   const int32_t w0 = (q + (lane / G) * warps_per_row) * G + lane % G;
   const int32_t step = warps_per_row * 32;
   for (int64_t b = blockIdx.y; b < p.B; b += gridDim.y) {
@@ -1310,7 +1306,7 @@ cudaError_t launch_sample(const ConSampleParams& p, int dtype, bool vec, int sms
     const int32_t words = (p.V + 31) / 32;
     // Halved until there is a warp for every place on the device: at V = 32000,
     // B = 128 the launch took 27 us with 8 words a lane throughout, 7 so.
-    const int64_t places = (int64_t)sms * GSAMPLE_LIST_CTAS * (kListThreads / 32);
+    const int64_t places = (int64_t)sms * kListCtas * (kListThreads / 32);
     int lane_words = 8;
     while (lane_words > 1 &&
            p.B * ((words + 32 * lane_words - 1) / (32 * lane_words)) < places)
