@@ -1017,7 +1017,10 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
   const uint64_t pol = evict_first_policy();
 
   const int64_t NU = p.units_per_row, NW = p.warps;
-  const int64_t gw = (int64_t)blockIdx.x * kWarps + warp;
+  // Constrained rows differ in work: the warps of a CTA take chunks of different
+  // rows, so that every SM has its share of the rows with little left.
+  const int64_t gw = CON ? (int64_t)warp * gridDim.x + blockIdx.x
+                         : (int64_t)blockIdx.x * kWarps + warp;
   if (gw >= NW) return;
   TileCursor cur;
   [[maybe_unused]] int64_t u_end = 0;
