@@ -269,6 +269,39 @@ def test_process_in_place(V, dtype):
         assert torch.equal(base[edge], before[edge])
 
 
+@pytest.mark.parametrize("V", [1, 40, 257, 5000, 33000])
+@pytest.mark.parametrize("dtype", [W.F32, W.BF16, W.F16])
+def test_process_rows_on_odd_multiples_of_16_bytes(V, dtype):
+    """Logits, results or both start 16 bytes past a 32-byte boundary."""
+    size = 4 if dtype == W.F32 else 2
+    for code in {dtype, W.F32}:
+        osize = 4 if code == W.F32 else 2
+        for x16, y16 in ((True, False), (False, True), (True, True)):
+            p = Problem(17, 15, V, dtype, pitch=(-V) % 64, shift=16 // size if x16 else 0)
+            ld = -(-V // 16) * 16
+            buf = torch.full((15 * ld + 64,), 5.0, dtype=TYPES[code], device="cuda")
+            out = torch.as_strided(buf, (15, V), (ld, 1), 16 // osize if y16 else 0)
+            assert p.logits.data_ptr() % 32 == (16 if x16 else 0)
+            assert out.data_ptr() % 32 == (16 if y16 else 0)
+            gs.process_logits(p.logits, out=out, **p.kw)
+            cu.check_values(out_values(out), *p.want(), code, "%s %s" % (x16, y16))
+            rest = torch.ones_like(buf, dtype=torch.bool)
+            torch.as_strided(rest, (15, V), (ld, 1), 16 // osize if y16 else 0).fill_(False)
+            assert bool((buf[rest] == 5.0).all())
+    p = Problem(18, 15, V, dtype, pitch=(-V) % 64, shift=16 // size)
+    want = p.want()
+    gs.process_logits(p.logits, out=p.logits, **p.kw)
+    cu.check_values(out_values(p.logits), *want, dtype, "in place")
+
+
+def test_process_allocates_rows_on_32_byte_boundaries():
+    for V, dtype in ((33, torch.float32), (33, torch.float16), (64, torch.bfloat16)):
+        y = gs.process_logits(torch.zeros(3, V, dtype=dtype, device="cuda"))
+        assert y.shape == (3, V) and y.stride(1) == 1
+        assert y.data_ptr() % 32 == 0 and y.stride(0) * y.element_size() % 32 == 0
+        assert y.is_contiguous() == (V == 64)
+
+
 def test_process_results_elsewhere_keep_their_surroundings():
     p = Problem(8, 12, 777, W.BF16)
     for ld, shift in ((777, 0), (784, 0), (800, 3), (1600, 777)):

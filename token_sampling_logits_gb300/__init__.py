@@ -621,12 +621,16 @@ def process_logits(logits, state: LogitState | None = None, slots=None, repetiti
                 row's mask, -1 for none (default: row b uses mask b).
     out         a [B, V] tensor with contiguous rows, in the logits' type or
                 float32; out=logits works in place. Default: a new tensor of
-                out_dtype (the logits' type, or torch.float32)."""
+                out_dtype (the logits' type, or torch.float32) whose rows start
+                on 32-byte boundaries, as the samplers read them fastest:
+                stride(0) is V rounded up."""
     torch = _torch()
     dt, B, V, ld = _logits_args(logits)
     dev = logits.device
     if out is None:
-        out = torch.empty((B, V), dtype=out_dtype or logits.dtype, device=dev)
+        dtype = out_dtype or logits.dtype
+        pitch = -(-V * dtype.itemsize // 32) * 32 // dtype.itemsize
+        out = torch.empty_strided((B, V), (pitch, 1), dtype=dtype, device=dev)
     elif out.device != dev or out.shape != (B, V) or (out_dtype or out.dtype) != out.dtype:
         raise ValueError("out must be a [B, V] tensor on the logits' device, of out_dtype")
     odt, _, _, out_ld = _logits_args(out)

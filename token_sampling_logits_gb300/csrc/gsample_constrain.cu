@@ -235,13 +235,14 @@ __device__ __forceinline__ void store_one(char* row, int32_t i, float x) {
   }
 }
 
-// Two kernels. process_wide_kernel takes rows that all start on 32-byte
+// Two kernels. process_wide_kernel takes rows that all start on 16-byte
 // boundaries, process_kernel any others.
 //
 // process_wide_kernel: a lane takes 32 elements at a time, one word of mask and
 // of touched bits, so that what goes by element is a vector instruction or
 // nothing: 256-bit loads and stores (a lane's 32 bytes are one sector, so the
-// 64-byte stride between lanes costs no traffic). Words that the mask leaves
+// 64-byte stride between lanes costs no traffic), or pairs of 128-bit ones where
+// rows start on odd multiples of 16 bytes. Words that the mask leaves
 // nothing of are never read. A warp works alone; its words come in groups of
 // kWordGroup spread over the row, because the low ids hold most of a request's
 // tokens. Touched elements are listed in shared memory and written over their
@@ -261,21 +262,41 @@ struct Oct {
   uint32_t w[8];
 };
 
-__device__ __forceinline__ Oct ld_oct(const char* p) {
+// `whole`: p is a multiple of 32; else of 16, and two 128-bit accesses do.
+__device__ __forceinline__ Oct ld_oct(const char* p, bool whole) {
   Oct v;
-  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]),
-                 "=r"(v.w[5]), "=r"(v.w[6]), "=r"(v.w[7])
-               : "l"(p)
-               : "memory");
+  if (whole) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]),
+                   "=r"(v.w[5]), "=r"(v.w[6]), "=r"(v.w[7])
+                 : "l"(p)
+                 : "memory");
+  } else {
+    asm volatile(
+        "ld.global.v4.b32 {%0, %1, %2, %3}, [%8];\n\t"
+        "ld.global.v4.b32 {%4, %5, %6, %7}, [%8 + 16];"
+        : "=&r"(v.w[0]), "=&r"(v.w[1]), "=&r"(v.w[2]), "=&r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]),
+          "=r"(v.w[6]), "=r"(v.w[7])
+        : "l"(p)
+        : "memory");
+  }
   return v;
 }
 
-__device__ __forceinline__ void st_oct(char* p, const Oct& v) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v.w[0]),
-               "r"(v.w[1]), "r"(v.w[2]), "r"(v.w[3]), "r"(v.w[4]), "r"(v.w[5]), "r"(v.w[6]),
-               "r"(v.w[7])
-               : "memory");
+__device__ __forceinline__ void st_oct(char* p, const Oct& v, bool whole) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v.w[0]),
+                 "r"(v.w[1]), "r"(v.w[2]), "r"(v.w[3]), "r"(v.w[4]), "r"(v.w[5]), "r"(v.w[6]),
+                 "r"(v.w[7])
+                 : "memory");
+  } else {
+    asm volatile(
+        "st.global.v4.b32 [%0], {%1, %2, %3, %4};\n\t"
+        "st.global.v4.b32 [%0 + 16], {%5, %6, %7, %8};" ::"l"(p),
+        "r"(v.w[0]), "r"(v.w[1]), "r"(v.w[2]), "r"(v.w[3]), "r"(v.w[4]), "r"(v.w[5]), "r"(v.w[6]),
+        "r"(v.w[7])
+        : "memory");
+  }
 }
 
 // 32 bytes of a row with the elements whose bit in `allowed` is clear set to -inf.
@@ -380,7 +401,7 @@ __global__ void __launch_bounds__(kWideThreads, DT == 0 ? 6 : kWideCtas)
       Oct x[NI];
       if (whole && m != 0u && (!INPLACE || m != 0xFFFFFFFFu)) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) x[i] = ld_oct(in + (int64_t)w * (32 * ISZ) + i * 32);
+        for (int i = 0; i < NI; ++i) x[i] = ld_oct(in + (int64_t)w * (32 * ISZ) + i * 32, p.in_by_32);
       }
       // The touched elements, listed, and the first of them on its way, while
       // the word above is.
@@ -413,10 +434,10 @@ __global__ void __launch_bounds__(kWideThreads, DT == 0 ? 6 : kWideCtas)
                 y.w[2 * j] = __float_as_uint(half_to_f32<DT>(v & 0xFFFFu));
                 y.w[2 * j + 1] = __float_as_uint(half_to_f32<DT>(v >> 16));
               }
-              st_oct(dst + i * 64 + h * 32, y);
+              st_oct(dst + i * 64 + h * 32, y, p.out_by_32);
             }
           } else {
-            st_oct(dst + i * 32, x[i]);
+            st_oct(dst + i * 32, x[i], p.out_by_32);
           }
         }
       }
@@ -672,8 +693,11 @@ cudaError_t launch_process(ProcessParams p, int dtype, int out_dtype, int sms,
                            cudaStream_t stream) {
   // A warp takes up to kWideWords words, or GSAMPLE_PROCESS_RUNS units, a lane
   // of a row; fewer while there are not enough warps to fill the device.
-  const bool wide = (((uintptr_t)p.logits | (uintptr_t)p.out | (uintptr_t)p.ld_bytes |
-                      (uintptr_t)p.out_ld_bytes) & 31u) == 0;
+  const uintptr_t in_at = (uintptr_t)p.logits | (uintptr_t)p.ld_bytes;
+  const uintptr_t out_at = (uintptr_t)p.out | (uintptr_t)p.out_ld_bytes;
+  const bool wide = ((in_at | out_at) & 15u) == 0;
+  p.in_by_32 = (in_at & 31u) == 0;
+  p.out_by_32 = (out_at & 31u) == 0;
   int64_t items, per_warp, slots;
   if (wide) {
     items = ((p.V + 31) / 32 + 31) / 32;

@@ -191,7 +191,9 @@ struct ProcessParams {
   int64_t ld_bytes, out_ld_bytes;
   int64_t B, V;
   bool inplace;
-  int32_t units_per_row, warps_per_row, items_per_lane;  // set by the launch
+  // Set by the launch:
+  bool in_by_32, out_by_32;  // rows all start on 32-byte boundaries
+  int32_t units_per_row, warps_per_row, items_per_lane;
   ConstrainArgs con;
 };
 
