@@ -58,6 +58,34 @@ def test_append_ragged_lists(vocab, lengths):
     same_state(state, s)
 
 
+@pytest.mark.parametrize("lengths", [[40000], [140000], [0, 70000, 1, 64000]])
+def test_append_long_lists(lengths):
+    """Long lists of one request are counted in tables first: few frequent
+    tokens, many rare ones, and ids that are none."""
+    rng = np.random.default_rng(len(lengths))
+    V = 50021
+    s = cu.random_state(rng, 5, V)
+    state = upload(s)
+    offsets = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int64)
+    n = int(offsets[-1])
+    tokens = np.minimum((float(V) ** rng.random(n)).astype(np.int64) - 1, V - 1)
+    tokens[rng.random(n) < 0.01] = -1
+    tokens[rng.random(n) < 0.01] = V
+    slots = rng.permutation(5)[:len(lengths)].astype(np.int32)
+    for prompt in (False, True):
+        gs.history_append(state, dev(tokens), slots=dev(slots), offsets=dev(offsets),
+                          prompt=prompt)
+        for i, r in enumerate(slots):
+            mine = tokens[offsets[i]:offsets[i + 1]]
+            mine = mine[(mine >= 0) & (mine < V)]
+            if prompt:
+                s.history[r, mine] |= np.uint32(0x80000000)
+            else:
+                np.add.at(s.history[r], mine, np.uint32(1))
+            s.touched[r, mine] = True
+    same_state(state, s)
+
+
 def test_append_one_token_a_row():
     rng = np.random.default_rng(1)
     s = cu.random_state(rng, 70, 333)
@@ -349,6 +377,30 @@ def test_bits_of_the_written_logits_are_the_formulas_in_binary32():
     assert np.array_equal(got, cu.binary32(*p.parts()), equal_nan=True)
 
 
+@pytest.mark.parametrize("dtype", [W.F32, W.BF16, W.F16])
+@pytest.mark.parametrize("B", [3, 170])
+def test_every_element_touched(dtype, B):
+    """More touched elements than any list holds at a time: written, in place
+    and drawn, on aligned and unaligned rows."""
+    V = 5003
+    for pitch, shift in (((-V) % 64, 0), (3, 1)):
+        p = Problem(19, B, V, dtype, special=False, pitch=pitch, shift=shift)
+        rng = np.random.default_rng(19)
+        h = rng.integers(0, 4, p.host.history.shape).astype(np.uint32)
+        h |= rng.integers(0, 2, h.shape).astype(np.uint32) << np.uint32(31)
+        p.host.history[:], p.host.touched[:] = h, True
+        p.host.history[:, V:] = 0
+        p.host.bias[:, :V] = rng.uniform(-3, 3, (p.host.rows, V))
+        p.kw["state"] = upload(p.host)
+        got, want, _ = draw_both(p, rng)
+        assert np.array_equal(got, want)
+        code = dtype
+        cu.check_values(out_values(gs.process_logits(p.logits, **p.kw)), *p.want(), code)
+        want = p.want()
+        gs.process_logits(p.logits, out=p.logits, **p.kw)
+        cu.check_values(out_values(p.logits), *want, code)
+
+
 # ---- the draw ---------------------------------------------------------------------
 def keys(rng, B, greedy=0.25):
     T = rng.uniform(0.3, 2.0, B).astype(np.float32)
@@ -376,7 +428,7 @@ def draw_both(p, rng, **over):
 def test_draw_equals_the_sampler_on_the_written_logits(V, dtype):
     rng = np.random.default_rng([V, dtype])
     for B, pitch, shift in ((1, 0, 0), (15, (-V) % 64, 0), (15, 3, 1), (70, (-V) % 64, 0),
-                            (70, 3, 1)):
+                            (170, (-V) % 64, 0), (170, 3, 1)):
         for special in (False, True):
             p = Problem(10, B, V, dtype, special=special, pitch=pitch, shift=shift)
             got, want, _ = draw_both(p, rng)
@@ -387,7 +439,7 @@ def test_draw_equals_the_sampler_on_the_written_logits(V, dtype):
 @pytest.mark.parametrize("state,mask", [(True, False), (False, True), (False, False)])
 def test_draw_with_parts_absent(state, mask):
     rng = np.random.default_rng(11)
-    for B in (3, 100):
+    for B in (3, 100, 200):
         for dtype in (W.F32, W.BF16):
             p = Problem(11, B, 5000, dtype, special=False, state=state, mask=mask)
             got, want, _ = draw_both(p, rng)
@@ -404,7 +456,8 @@ def tally(t, got, y, T, ref, gap, where):
 
 
 @pytest.mark.parametrize("B,V,dtype", [(4, 32768, W.F32), (33, 20000, W.BF16),
-                                       (300, 9001, W.F16), (130, 40000, W.BF16)])
+                                       (300, 9001, W.F16), (130, 40000, W.BF16),
+                                       (160, 40000, W.BF16)])
 def test_draw_against_the_oracle(B, V, dtype):
     rng = np.random.default_rng([12, B])
     p = Problem(12, B, V, dtype, special=False, tokens=2000)
@@ -416,7 +469,7 @@ def test_draw_against_the_oracle(B, V, dtype):
     register("7 constrained draw", t, assert_bound=False)
 
 
-@pytest.mark.parametrize("B", [2, 80])
+@pytest.mark.parametrize("B", [2, 80, 200])
 @pytest.mark.parametrize("dtype", [W.F32, W.BF16, W.F16])
 def test_draw_rows_with_nothing_or_one_token_left(B, dtype):
     V = 6000
@@ -446,7 +499,7 @@ def test_draw_rows_with_nothing_or_one_token_left(B, dtype):
         assert np.array_equal(got, w)
 
 
-@pytest.mark.parametrize("B", [3, 90])
+@pytest.mark.parametrize("B", [3, 90, 180])
 @pytest.mark.parametrize("dtype", [W.BF16, W.F16, W.F32])
 def test_draw_bans_and_forces_by_bias(B, dtype):
     V = 9000
@@ -476,7 +529,7 @@ def test_draw_bans_and_forces_by_bias(B, dtype):
 @pytest.mark.parametrize("T", [1e-30, 1e-21, 1e-3, 50.0, 1e21, np.inf])
 def test_draw_at_extreme_temperatures(T):
     rng = np.random.default_rng(15)
-    for B in (4, 80):
+    for B in (4, 80, 160):
         for dtype in (W.F32, W.BF16):
             p = Problem(15, B, 3000, dtype, special=False, tokens=300)
             got, want, _ = draw_both(p, rng, T=np.full(B, T, np.float32))
@@ -486,8 +539,8 @@ def test_draw_at_extreme_temperatures(T):
 def test_draw_ties_go_to_the_lowest_index():
     """Equal constrained logits, some of them penalised down to the value of
     others, greedily: the lowest index."""
-    V = 4000
-    for B in (2, 70):
+    V = 8000
+    for B in (2, 70, 170):
         for dtype in (W.F32, W.BF16, W.F16):
             x = np.zeros((B, V), np.float32)
             s = cu.HostState(B, V)
@@ -599,7 +652,7 @@ def test_constrained_logits_feed_the_other_samplers():
     assert np.array_equal(gs.argmax(y).cpu().numpy(), oracle.argmax(host)[0])
 
 
-@pytest.mark.parametrize("B", [6, 100])
+@pytest.mark.parametrize("B", [6, 100, 200])
 def test_captured_and_replayed_on_another_stream(B):
     """A decode step (draw, append) captured once and replayed, as the eager
     steps on another copy of the state."""
@@ -640,8 +693,8 @@ def test_captured_and_replayed_on_another_stream(B):
 
 
 def test_two_streams_share_a_state_that_neither_writes():
-    p = Problem(23, 80, 20000, W.BF16, special=False)
-    T, seed, offset = keys(np.random.default_rng(23), 80)
+    p = Problem(23, 180, 20000, W.BF16, special=False)
+    T, seed, offset = keys(np.random.default_rng(23), 180)
     args = dev(T), gs.seeds_as_tensor(seed, "cuda"), gs.seeds_as_tensor(offset, "cuda")
     want = gs.constrained_gumbel_argmax(p.logits, *args, **p.kw)
     y = gs.process_logits(p.logits, **p.kw)
@@ -649,7 +702,7 @@ def test_two_streams_share_a_state_that_neither_writes():
     streams, got = [torch.cuda.Stream() for _ in range(2)], []
     for st in streams:
         with torch.cuda.stream(st):
-            ws = gs.new_workspace(80)
+            ws = gs.new_workspace(180)
             for _ in range(5):
                 got.append((gs.constrained_gumbel_argmax(p.logits, *args, workspace=ws, **p.kw),
                             gs.process_logits(p.logits, **p.kw)))

@@ -202,8 +202,12 @@ gsample_status gsample_constrained_gumbel_argmax(const void* logits, gsample_dty
   ConstrainArgs con;
   st = check_constraints(constraints, B, V, &con);
   if (st != GSAMPLE_OK) return st;
-  return gsample::sample_constrained(logits, dtype, B, V, ld, temperature, seed, offset, con,
-                                     out_idx, workspace, (cudaStream_t)stream);
+  try {  // launch plans are kept in a map, which may fail to grow
+    return gsample::sample_constrained(logits, dtype, B, V, ld, temperature, seed, offset, con,
+                                       out_idx, workspace, (cudaStream_t)stream);
+  } catch (...) {
+    return GSAMPLE_ERR_CUDA;
+  }
 }
 
 }  // extern "C"
