@@ -582,6 +582,21 @@ __device__ __forceinline__ bool lane_candidate(uint32_t stage, int32_t t0, int32
   return true;
 }
 
+// The same out of line: constrained rows take it once a chunk, and their tile
+// loop is long enough without it.
+struct Candidate {
+  float s;
+  int32_t i;
+  bool found;
+};
+template <int DT, bool VEC>
+__device__ __noinline__ Candidate lane_candidate_cold(uint32_t stage, int32_t t0, int32_t t_hi,
+                                                      RowCtx rc, float bs, int32_t bi) {
+  Candidate c{bs, bi, false};
+  c.found = lane_candidate<DT, VEC>(stage, t0, t_hi, rc, c.s, c.i);
+  return c;
+}
+
 // Warp-uniform cursor over this warp's tiles: row b, row-local units
 // [t0, t_hi), and the warp's part of row b, [seg_lo, seg_hi).
 struct TileCursor {
@@ -1044,7 +1059,7 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
   auto next_words = [&](int64_t row_before) {
     if constexpr (CON) {
       if (ahead.valid && ahead.b != row_before) {
-        const RowConstraints c = row_constraints(p.con, ahead.b);
+        const RowBits c = row_bits(p.con, ahead.b);
         mask_next = c.mask;
         touched_next = c.touched;
       }
@@ -1152,9 +1167,14 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
         first = left && (seg_first || !known);
       }
       if (first) {
-        [[maybe_unused]] const bool found =
-            lane_candidate<DT, VEC>(stage, t0, t_hi, rc, bs, bi);
-        if constexpr (CON) left = __any_sync(0xFFFFFFFFu, found);
+        if constexpr (CON) {
+          const Candidate c = lane_candidate_cold<DT, VEC>(stage, t0, t_hi, rc, bs, bi);
+          bs = c.s;
+          bi = c.i;
+          left = __any_sync(0xFFFFFFFFu, c.found);
+        } else {
+          lane_candidate<DT, VEC>(stage, t0, t_hi, rc, bs, bi);
+        }
       }
       pending = __ldcg(&rc.ws->hint);
       // The best exact score this warp knows; publish it (fire-and-forget) if
