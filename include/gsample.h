@@ -296,6 +296,7 @@ gsample_status gsample_gumbel_argmax_host(const void* logits, gsample_dtype dtyp
  *   rows >= 1; vocab = V of the logits; ld a multiple of 32, >= vocab
  *   (gsample_logit_state_ld). history and bias are 16-byte aligned, touched
  *   4-byte aligned.
+ * A token may be counted up to 2^31 - 1 times.
  * The layout is public: rows may be copied (a forked request), saved and
  * restored by plain copies of the three arrays. Calls that write a state must
  * be ordered (by stream or event) with every call that uses it. */
@@ -383,8 +384,10 @@ gsample_status gsample_process_logits(const void* logits, gsample_dtype dtype, i
 /* gsample_gumbel_argmax on the constrained logits, which are not written
  * anywhere and not rounded below binary32: the indices are those of
  * gsample_process_logits with GSAMPLE_F32 followed by gsample_gumbel_argmax.
- * A row whose mask leaves nothing gets -1. Everything else (greedy rows,
- * workspace, validation, asynchrony) as gsample_gumbel_argmax. */
+ * A row whose mask leaves nothing gets -1; a constrained logit that is NaN
+ * (a NaN bias, +inf less +inf) is never drawn. One or two launches. Everything
+ * else (greedy rows, workspace, validation, asynchrony) as
+ * gsample_gumbel_argmax. */
 gsample_status gsample_constrained_gumbel_argmax(const void* logits, gsample_dtype dtype,
                                                  int64_t B, int64_t V, int64_t ld,
                                                  const float* temperature, const uint64_t* seed,

@@ -682,9 +682,10 @@ __device__ __forceinline__ void issue_tile(const SampleParams& p, const TileCurs
 //     it are not read, and a tile without one is passed over.
 // Scoring the touched elements where the sweep meets them was measured slower
 // (B = 256, V = 151936 bf16, some 1600 touched tokens a row: 112 us with a list
-// a warp, 86 us with a list a CTA): the sweep runs 16 warps an SM, too few to
-// hide the gathers, and the low ids, where most tokens of a request lie, keep
-// one warp of a row long after the others.
+// a warp, 86 us with a list a CTA, 68 us so): the sweep runs 16 warps an SM, too
+// few to hide the gathers, and the low ids, where most tokens of a request lie,
+// keep one warp of a row long after the others. The sweep itself takes 48 us
+// with nothing constrained (45 the unconstrained kernel), 56 with masks.
 //
 // Rows differ in work here (a row whose grammar allows a few tokens has none),
 // so the warps take chunks of rows in turn rather than one contiguous range
@@ -854,11 +855,14 @@ __device__ __forceinline__ void clear_tile(uint32_t stage, uint32_t keep0, uint3
 }
 
 // The list kernel. Every warp works alone: it takes kListWords words a lane (8,
-// or fewer while there are not warps enough to fill the device) of one row, lists their listed elements in shared memory and scores them one a
-// lane. Its words come in small groups spread over the row, because the low ids
-// hold most of a request's tokens: of 1600 touched tokens some 700 lie in the
-// first 64 words, and one warp with all of them would work long after the
-// others.
+// or fewer while there are not warps enough to fill the device) of one row,
+// lists their listed elements in shared memory and scores them one a lane. Its
+// words come in small groups spread over the row, because the low ids hold most
+// of a request's tokens: of 1600 touched tokens some 700 lie in the first 64
+// words, and one warp with all of them would work long after the others. Some
+// 13 us at B = 256, V = 151936 with 1600 touched tokens a row: 61 MB of DRAM
+// reads (a sector for each logit, history word and bias) at a third of the copy
+// rate, bound by the latency of the gathers and the exact scores.
 constexpr int kListThreads = 128;
 constexpr int kListCtas = 8;   // an SM: 64 registers a thread (6 and 10: 2 % and 7 % slower)
 constexpr int kListGroup = 4;  // words a group (2 and 8: 1 % and 8 % slower)
