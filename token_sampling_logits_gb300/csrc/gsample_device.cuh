@@ -277,7 +277,11 @@ __device__ __forceinline__ Prune make_prune(float L, float T) {
     p.lm = -INFINITY;
     p.use_bound = false;
   } else if (!(L > -INFINITY) || !(T >= 1e-20f && T <= 1e20f)) {
-    p.thr_x = -INFINITY;  // nothing known yet, or an extreme temperature: no pruning
+    // Nothing known yet, or an extreme temperature: only -inf, which is never a
+    // candidate, is skipped. Rows that are masked in places (a grammar's -inf)
+    // would otherwise take every masked group through the exact pass until
+    // their first candidate: 94 us for 64 such rows of 151936.
+    p.thr_x = -3.402823466e38f;
     p.lm = -INFINITY;
     p.use_bound = false;
   } else {
