@@ -291,8 +291,8 @@ gsample_status gsample_gumbel_argmax_host(const void* logits, gsample_dtype dtyp
  *            output alone.
  *   bias     float [rows, ld], or NULL: no biases.
  *   touched  uint32 [rows, ld / 32]: bit v & 31 of word v >> 5 is set where
- *            history or bias may be nonzero. Entries without it are not read
- *            and hold zeros. The calls below keep it so.
+ *            history or bias may be nonzero; entries without it hold zeros. The
+ *            calls below keep it so.
  *   rows >= 1; vocab = V of the logits; ld a multiple of 32, >= vocab
  *   (gsample_logit_state_ld). history and bias are 16-byte aligned, touched
  *   4-byte aligned.
