@@ -682,10 +682,10 @@ __device__ __forceinline__ void issue_tile(const SampleParams& p, const TileCurs
 //     it are not read, and a tile without one is passed over.
 // Scoring the touched elements where the sweep meets them was measured slower
 // (B = 256, V = 151936 bf16, some 1600 touched tokens a row: 112 us with a list
-// a warp, 86 us with a list a CTA, 68 us so): the sweep runs 16 warps an SM, too
+// a warp, 86 us with a list a CTA, 66 us so): the sweep runs 16 warps an SM, too
 // few to hide the gathers, and the low ids, where most tokens of a request lie,
 // keep one warp of a row long after the others. The sweep itself takes 48 us
-// with nothing constrained (45 the unconstrained kernel), 56 with masks.
+// with nothing constrained (45 the unconstrained kernel), 55 with masks.
 //
 // Rows differ in work here (a row whose grammar allows a few tokens has none),
 // so the warps take chunks of rows in turn rather than one contiguous range
@@ -818,14 +818,18 @@ __device__ __forceinline__ void issue_tile_masked(const SampleParams& p, const T
   }
 }
 
-// The places of a landed tile whose bits in `keep` (a lane's two words) are
-// clear become -inf; `cleared` is their number.
+// The places of a landed tile of `elements` whose bits in `keep` (a lane's two
+// words) are clear become -inf; `kept` counts the set ones. Places past the
+// tile hold -inf already.
 template <int DT, bool VEC>
 __device__ __forceinline__ void clear_tile(uint32_t stage, uint32_t keep0, uint32_t keep1,
-                                           int cleared) {
+                                           int elements, int kept) {
   using C = Cfg<DT, VEC>;
+  const int cleared = elements - kept;
   if (cleared == 0) return;
   const int lane = threadIdx.x & 31;
+  if (lane * 32 >= elements) keep0 = 0xFFFFFFFFu;
+  if (1024 + lane * 32 >= elements) keep1 = 0xFFFFFFFFu;
   if (cleared <= kClearBits) {
     constexpr uint32_t kSize = C::kF32Bits ? 4u : 2u;
     auto clear_word = [&](uint32_t c, uint32_t at) {
@@ -866,7 +870,7 @@ __device__ __forceinline__ void clear_tile(uint32_t stage, uint32_t keep0, uint3
 constexpr int kListThreads = 128;
 constexpr int kListCtas = 8;   // an SM: 64 registers a thread (6 and 10: 2 % and 7 % slower)
 constexpr int kListGroup = 4;  // words a group (2 and 8: 1 % and 8 % slower)
-constexpr int kListCap = 256;                   // entries a warp lists at a time
+constexpr int kListCap = 256;  // entries a warp lists at a time
 
 template <int DT, int kListWords>
 __global__ void __launch_bounds__(kListThreads, kListCtas)
@@ -1135,6 +1139,7 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
   unsigned char* rbase = wbase + kStages * C::kTileBytes;
   int rcnt = 0;
   Prune pr_last{INFINITY, -INFINITY, false};
+
   while (true) {
     // The current tile has landed (this lane's copies, then everyone's).
     cp_async_wait<kStages - 2>();
@@ -1151,8 +1156,7 @@ __global__ void __launch_bounds__(kThreads, GSAMPLE_MIN_CTAS_PER_SM)
       const int swept = (int)__reduce_add_sync(0xFFFFFFFFu, __popc(words[0]) + __popc(words[1]));
       left = swept > 0;
       if (left)
-        clear_tile<DT, VEC>(stage, words[0], words[1],
-                            (cur.t_hi - cur.t0) * C::kEPU - swept);
+        clear_tile<DT, VEC>(stage, words[0], words[1], (cur.t_hi - cur.t0) * C::kEPU, swept);
     } else {
       issue_tile<DT, VEC>(p, ahead, ring + fill * C::kTileBytes, pol);
       ahead = next_tile<C::kTile>(ahead, u_end, NU);
