@@ -762,6 +762,62 @@ def test_python_refusals():
             call()
 
 
+@pytest.mark.parametrize("B", [5, 90, 170])
+def test_wider_states_and_masks(B):
+    """State rows and mask rows with room to spare, mask words that start
+    anywhere, and mask bits past the vocabulary set."""
+    for V, dtype in ((77, W.F32), (1000, W.BF16), (6001, W.F16)):
+        p = Problem(27, B, V, dtype, special=False)
+        rng = np.random.default_rng([27, B])
+        got, want, keys_ = draw_both(p, rng)
+        written = gs.process_logits(p.logits, **p.kw)
+        wide = cu.HostState(p.host.rows, V, ld=p.host.ld + 96)
+        for a, b in ((wide.history, p.host.history), (wide.bias, p.host.bias),
+                     (wide.touched, p.host.touched)):
+            a[:, :V] = b[:, :V]
+        words = cu.pack_bits(p.bits)
+        n, w = words.shape
+        if V % 32:
+            words[:, -1] |= np.uint32((0xFFFFFFFF << (V % 32)) & 0xFFFFFFFF)
+        buf = np.full(n * (w + 3) + 5, 0xFFFFFFFF, np.uint32)
+        view = torch.as_strided(dev(buf), (n, w), (w + 3, 1), 1)
+        view.copy_(dev(words))
+        kw = dict(p.kw, state=upload(wide), mask=view)
+        T, seed, offset = keys_
+        again = gs.constrained_gumbel_argmax(p.logits, dev(T), gs.seeds_as_tensor(seed, "cuda"),
+                                             gs.seeds_as_tensor(offset, "cuda"), **kw)
+        assert np.array_equal(got, want) and np.array_equal(again.cpu().numpy(), want)
+        assert torch.equal(gs.process_logits(p.logits, **kw), written)
+
+
+def test_more_rows_than_a_grid_dimension():
+    B, V = 70000, 37
+    rng = np.random.default_rng(28)
+    x = logits_for(rng, B, V, W.BF16, special=False)
+    s = cu.HostState(B, V)
+    t = rng.integers(0, V, (B, 2))
+    rows = np.arange(B)
+    s.history[rows, t[:, 0]] |= np.uint32(0x80000000)
+    np.add.at(s.history, (rows, t[:, 1]), np.uint32(1))
+    s.touched[rows, t[:, 0]] = s.touched[rows, t[:, 1]] = True
+    state = gs.new_logit_state(B, V)
+    gs.history_append(state, dev(t[:, 0]), prompt=True)
+    gs.history_append(state, dev(t[:, 1]))
+    same_state(state, s)
+    bits = rng.random((B, V)) < 0.5
+    kw = dict(state=state, repetition=1.5, frequency=0.5, mask=dev(cu.pack_bits(bits)))
+    lg = to_device(W.encode(x, W.BF16), W.BF16)
+    y = gs.process_logits(lg, out_dtype=torch.float32, **kw)
+    one = np.ones(B)
+    want = cu.constrained(x, s.history[:, :V], s.bias[:, :V], 1.5 * one, 0.5 * one, 0 * one, bits)
+    cu.check_values(out_values(y), *want, W.F32)
+    T = dev(np.where(rows % 3 == 0, 0, 1).astype(np.float32))
+    a = gs.constrained_gumbel_argmax(lg, T, 3, 4, **kw)
+    assert torch.equal(a, gs.gumbel_argmax(y, T, 3, 4))
+    gs.state_reset(state)
+    assert not bool(state.touched.any()) and not bool(state.history.any())
+
+
 def test_empty_batches():
     x = torch.zeros(0, 50, device="cuda")
     assert gs.process_logits(x).shape == (0, 50)
