@@ -120,6 +120,7 @@ CON = [
     (lambda: constraints(mask=FAKE + 2, mask_rows=4, mask_ld=4), BAD),
     (lambda: constraints(mask=FAKE, mask_rows=4, mask_ld=4, mask_row=FAKE + 2), BAD),
     (lambda: constraints(mask=FAKE, mask_rows=1 << 40, mask_ld=1 << 40, mask_row=FAKE), BAD),
+    (lambda: constraints(mask=FAKE, mask_rows=0, mask_ld=(1 << 63) - 1, mask_row=FAKE), BAD),
 ]
 
 

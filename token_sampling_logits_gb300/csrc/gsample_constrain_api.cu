@@ -60,7 +60,7 @@ gsample_status check_constraints(const gsample_constraints* c, int64_t B, int64_
   if (c->mask) {
     if (misaligned(c->mask, 4) || misaligned(c->mask_row, 4) || c->mask_rows < 0 ||
         c->mask_ld < (V + 31) / 32 || (!c->mask_row && c->mask_rows < B) ||
-        (c->mask_rows > 0 && c->mask_ld > INT64_MAX / 4 / c->mask_rows))
+        c->mask_ld > INT64_MAX / 4 / (c->mask_rows > 0 ? c->mask_rows : 1))
       return GSAMPLE_ERR_INVALID_ARG;
     out->mask = reinterpret_cast<const uint8_t*>(c->mask);
     out->mask_rows = c->mask_rows;
