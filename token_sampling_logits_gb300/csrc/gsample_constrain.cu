@@ -82,7 +82,7 @@ __device__ __forceinline__ void count_token(const StateArgs& s, int64_t at, uint
 __device__ __forceinline__ int64_t token_place(const StateArgs& s, const int32_t* slot, int64_t n,
                                                const int64_t* tokens, const int64_t* offsets,
                                                int64_t j) {
-  const int64_t t = __ldg(tokens + j);
+  const int64_t t = __ldcg(tokens + j);  // written by the draw just before, often
   const int64_t i = owner(offsets, n, j);
   if (i < 0 || t < 0 || t >= s.vocab) return -1;
   const int64_t r = state_row(s, slot, i);
@@ -221,8 +221,8 @@ __global__ void __launch_bounds__(32)
 // ---------------------------------------------------------------------------
 template <int DT>
 __device__ __forceinline__ float load_one(const char* row, int32_t i) {
-  if constexpr (DT == 0) return reinterpret_cast<const float*>(row)[i];
-  const uint32_t h = reinterpret_cast<const unsigned short*>(row)[i];
+  if constexpr (DT == 0) return __ldcg(reinterpret_cast<const float*>(row) + i);
+  const uint32_t h = __ldcg(reinterpret_cast<const unsigned short*>(row) + i);
   return half_to_f32<DT>(h);
 }
 

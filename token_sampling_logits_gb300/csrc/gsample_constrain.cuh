@@ -8,8 +8,9 @@
 // Every operation is rounded once to binary32 (no contraction into an fma), so
 // the written logits and the samplers' in-register ones are the same bits.
 //
-// State and mask words are read once a launch, through L2 only (ld.cg): a state
-// row is often rewritten by the kernel just before on the stream.
+// State and mask words, and single logits, are read once a launch and through L2
+// only (ld.cg): the kernel just before on the stream, which this one's start may
+// overlap, often writes them.
 #pragma once
 
 #include <cstdint>
@@ -243,7 +244,7 @@ __device__ __forceinline__ uint4 masked_unit(uint4 r, uint32_t allowed) {
 template <int DT>
 __device__ __forceinline__ float exact_touched(const char* row, int32_t v,
                                                const RowConstraints& r) {
-  const float x = half_to_f32<DT>(__ldg(reinterpret_cast<const unsigned short*>(row) + v));
+  const float x = half_to_f32<DT>(__ldcg(reinterpret_cast<const unsigned short*>(row) + v));
   return penalised(x, __ldcg(r.history + v), r.bias ? __ldcg(r.bias + v) : 0.0f, r.pen);
 }
 
