@@ -220,13 +220,6 @@ __global__ void __launch_bounds__(32)
 // Constrained logits
 // ---------------------------------------------------------------------------
 template <int DT>
-__device__ __forceinline__ float load_one(const char* row, int32_t i) {
-  if constexpr (DT == 0) return __ldcg(reinterpret_cast<const float*>(row) + i);
-  const uint32_t h = __ldcg(reinterpret_cast<const unsigned short*>(row) + i);
-  return half_to_f32<DT>(h);
-}
-
-template <int DT>
 __device__ __forceinline__ void store_one(char* row, int32_t i, float x) {
   if constexpr (DT == 0) {
     reinterpret_cast<float*>(row)[i] = x;
@@ -336,7 +329,7 @@ __device__ __forceinline__ Gathered gather_element(const ProcessParams& p, int64
                                                    const char* in, int32_t v) {
   Gathered g;
   g.v = v;
-  g.l = load_one<DT>(in, v);
+  g.l = logit_at<DT>(in, v);
   g.h = __ldcg(p.con.history + state + v);
   g.bias = p.con.bias ? __ldcg(p.con.bias + state + v) : 0.0f;
   return g;
@@ -465,7 +458,7 @@ __global__ void __launch_bounds__(kWideThreads, DT == 0 ? 6 : kWideCtas)
         const RowConstraints rc = row_constraints(p.con, b);
 #pragma unroll 1
         for (int32_t v = w * 32; v < V; ++v) {
-          const float l = load_one<DT>(in, v);
+          const float l = logit_at<DT>(in, v);
           const float y = constrained_logit(l, v, rc);
           if (!INPLACE || __float_as_uint(l) != __float_as_uint(y)) store_one<ODT>(out, v, y);
         }
@@ -637,7 +630,7 @@ __global__ void __launch_bounds__(kConThreads, kProcessCtas)
           const int32_t e = u * N - s;
           if (e >= lo && e <= hi) continue;
           for (int32_t v = e < 0 ? 0 : e; v < e + N && v < V; ++v) {
-            const float l = load_one<DT>(in, v);
+            const float l = logit_at<DT>(in, v);
             const float y = constrained_logit(l, v, row_constraints(p.con, b));
             if (!INPLACE || __float_as_uint(l) != __float_as_uint(y)) store_one<ODT>(out, v, y);
           }

@@ -120,6 +120,16 @@ __device__ __forceinline__ RowBits row_bits(const ConstrainArgs& c, int64_t b) {
   return r;
 }
 
+// One logit of a row.
+template <int DT>
+__device__ __forceinline__ float logit_at(const char* row, int32_t v) {
+  if constexpr (DT == 0) {
+    return __ldcg(reinterpret_cast<const float*>(row) + v);
+  } else {
+    return half_to_f32<DT>(__ldcg(reinterpret_cast<const unsigned short*>(row) + v));
+  }
+}
+
 // Logit x of a touched token with history word h and bias `bias`.
 __device__ __forceinline__ float penalised(float x, uint32_t h, float bias,
                                            const RowPenalties& r) {
@@ -244,8 +254,8 @@ __device__ __forceinline__ uint4 masked_unit(uint4 r, uint32_t allowed) {
 template <int DT>
 __device__ __forceinline__ float exact_touched(const char* row, int32_t v,
                                                const RowConstraints& r) {
-  const float x = half_to_f32<DT>(__ldcg(reinterpret_cast<const unsigned short*>(row) + v));
-  return penalised(x, __ldcg(r.history + v), r.bias ? __ldcg(r.bias + v) : 0.0f, r.pen);
+  return penalised(logit_at<DT>(row, v), __ldcg(r.history + v),
+                   r.bias ? __ldcg(r.bias + v) : 0.0f, r.pen);
 }
 
 // The value of element v of a 16-bit row whose place holds `x`: a bound, if it

@@ -952,7 +952,7 @@ __global__ void __launch_bounds__(kListThreads, kListCtas)
       auto gather = [&](int i) {
         if (i >= n) return;
         v_next = (int32_t)list[i];
-        x_next = load_elt<DT>(row, v_next);
+        x_next = logit_at<DT>(row, v_next);
         if (r.history) h_next = __ldcg(r.history + v_next);
         if (r.bias) bias_next = __ldcg(r.bias + v_next);
       };
