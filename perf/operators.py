@@ -166,11 +166,10 @@ def _mask(g, rows, vocab, kind):
     words = (vocab + 31) // 32
     most = max(2, min(300, vocab // 8))
     free = _uniform(g, rows, words * 32) < 0.97
+    few = torch.zeros(rows, words * 32, dtype=torch.bool, device="cuda")
     size = (torch.exp(_uniform(g, rows) * math.log(most + 1)) - 0.5).long()
     ids = (_uniform(g, rows, most) * vocab).long()
-    # an id may come twice: sums of whole numbers do not depend on their order
-    few = torch.zeros(rows, words * 32, dtype=torch.int32, device="cuda")
-    few = few.scatter_add_(1, ids, (torch.arange(most, device="cuda")[None, :] < size[:, None]).int()) > 0
+    few.scatter_(1, ids, torch.arange(most, device="cuda")[None, :] < size[:, None])
     place = torch.arange(rows, device="cuda") % 4
     bits = torch.where((place == 3)[:, None], few, free) if kind == "mixed" else few
     which = torch.arange(rows, device="cuda", dtype=torch.int32)
