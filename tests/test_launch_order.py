@@ -1,0 +1,110 @@
+"""Stream order between the library's own kernels, which all are launched with
+programmatic stream serialization: each may start while the one before it
+drains. The rules that order rests on are read from the sources (no GPU), and
+the chains that depend on them are run."""
+import glob
+import os
+import re
+
+import numpy as np
+import pytest
+
+import token_sampling_logits_gb300 as gs
+from token_sampling_logits_gb300 import build
+
+gpu = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+# ---- the sources ----------------------------------------------------------------
+def _without_comments(text):
+    return re.sub(r"//[^\n]*|/\*.*?\*/", " ", text, flags=re.S)
+
+
+def kernels():
+    """(name, body) of every kernel but the diagnostic ones, which are launched
+    without the attribute."""
+    found = {}
+    for path in sorted(glob.glob(os.path.join(build.CSRC, "*.cu"))):
+        text = _without_comments(open(path).read())
+        for m in re.finditer(r"__global__\s+void\s+(?:__launch_bounds__\([^)]*\)\s*)?(\w+)\(", text):
+            start = text.index("{", m.end())
+            depth, i = 1, start + 1
+            while depth:
+                depth += {"{": 1, "}": -1}.get(text[i], 0)
+                i += 1
+            found[m.group(1)] = text[start:i]
+    return {k: v for k, v in found.items() if not k.startswith(("debug_", "probe_"))}
+
+
+WAIT = re.compile(r"pdl_wait\w*\(\)|griddepcontrol\.wait")
+
+
+def test_the_kernels_are_found():
+    assert {"sample_kernel", "list_kernel", "sample_cluster_kernel", "hlg_kernel",
+            "categorical_kernel", "filter_cluster_kernel", "process_kernel",
+            "process_wide_kernel", "history_append_kernel", "history_append_long_kernel",
+            "bias_set_kernel", "state_reset_kernel"} <= set(kernels())
+
+
+@pytest.mark.parametrize("name", sorted(kernels()))
+def test_every_kernel_waits_before_it_may_exit(name):
+    """A kernel whose blocks all exit without having waited ends before its
+    predecessor does, and its successor's wait covers it alone."""
+    body = kernels()[name]
+    wait, leave = WAIT.search(body), re.search(r"\breturn\b", body)
+    assert wait, name
+    assert leave is None or wait.start() < leave.start(), name
+
+
+# ---- chains on the GPU --------------------------------------------------------------
+def captured(fn):
+    """fn recorded once: its launches follow one another without the host's pauses."""
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            fn()
+    torch.cuda.current_stream().wait_stream(side)
+    return g
+
+
+@gpu
+@pytest.mark.parametrize("B,V,dtype", [(1, 32768, torch.float32), (8, 262144, torch.float32),
+                                       (8, 151936, torch.bfloat16), (200, 20000, torch.bfloat16)])
+def test_append_after_a_filter_with_nothing_to_filter(B, V, dtype):
+    """Greedy rows, and rows without a filter, leave the filter kernel at once;
+    the tokens appended next are still those that the sampler before it wrote."""
+    n = 12
+    g = torch.Generator("cuda").manual_seed(B)
+    x = [(torch.randn(B, V, generator=g, device="cuda") * 3).to(dtype) for _ in range(n)]
+    T = torch.zeros(B, device="cuda")
+    T[1::2] = 0.9
+    seed = torch.arange(B, device="cuda")
+    offset = torch.zeros(B, dtype=torch.int64, device="cuda")
+    k = torch.where(T > 0, 0, 5).to(torch.int32)  # 0: no filter
+    ws = gs.new_workspace(B)
+    want = [gs.gumbel_argmax(y, T, seed, offset).cpu().numpy() for y in x]
+    out = torch.full((n, B), -1, dtype=torch.int64, device="cuda")
+    state = gs.new_logit_state(B, V, bias=False)
+    warm = gs.new_logit_state(B, V, bias=False)
+    gs.filtered_gumbel_argmax(x[0], T, seed, offset, top_k=k, out=out[0], workspace=ws)
+    gs.history_append(warm, out[0])
+
+    def steps():
+        for i in range(n):
+            gs.filtered_gumbel_argmax(x[i], T, seed, offset, top_k=k, out=out[i], workspace=ws)
+            gs.history_append(state, out[i])
+
+    graph = captured(steps)
+    for _ in range(10):
+        out.fill_(-1)
+        gs.state_reset(state)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(out.cpu().numpy(), np.stack(want))
+        counts = np.zeros((B, V), np.int32)
+        for w in want:
+            np.add.at(counts, (np.arange(B), w), 1)
+        assert np.array_equal(state.history[:, :V].cpu().numpy(), counts)

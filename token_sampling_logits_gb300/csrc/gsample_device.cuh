@@ -34,9 +34,12 @@ static_assert(sizeof(WsRow) == 16, "workspace row is 16 bytes");
 // programmatic stream serialization, so its CTAs may be scheduled while the
 // previous kernel of the stream drains. Each kernel first waits for that
 // kernel to complete and its memory to be visible (griddepcontrol.wait),
-// before touching global memory, then lets the next kernel of the stream be
-// scheduled early in turn. A kernel that follows on the same stream with the
-// same launch attribute must likewise wait before reading the indices.
+// before touching global memory that it may have written, then lets the next
+// kernel of the stream be scheduled early in turn. Every thread waits before it
+// exits, too: a grid that ended without its wait would end before its
+// predecessor, and its successor's wait covers it alone. A kernel that follows
+// on the same stream with the same launch attribute must likewise wait before
+// reading the indices.
 __device__ __forceinline__ void pdl_wait_then_release() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -272,7 +272,12 @@ __global__ void __launch_bounds__(kFiltThreads, 4) filter_cluster_kernel(const F
   // Every CTA of a cluster reads the same row, filter and proposal, so the
   // early exits below are taken by the whole cluster or by none of it.
   const RowFilter f = row_filter(fp, b);
-  if (!(f.T > 0.0f) || !(f.k_on || f.p_on)) return;  // greedy or unfiltered: the proposal stands
+  if (!(f.T > 0.0f) || !(f.k_on || f.p_on)) {  // greedy or unfiltered: the proposal stands
+    // Not before the kernel that writes it is done: a kernel that follows waits
+    // for this one alone.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const char* row = fp.logits + b * fp.ld_bytes;
   const uint64_t sd = __ldg(fp.seed + b), of = __ldg(fp.offset + b);
   if (threadIdx.x == 0) s_ln = 0u;
