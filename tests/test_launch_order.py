@@ -57,6 +57,13 @@ def test_every_kernel_waits_before_it_may_exit(name):
     assert leave is None or wait.start() < leave.start(), name
 
 
+@pytest.mark.parametrize("name", ["process_kernel", "process_wide_kernel"])
+def test_kernels_that_write_logits_do_not_release_early(name):
+    """The samplers read logits through non-coherent loads, which may not read
+    what is written during their kernel's life."""
+    assert not re.search(r"release|launch_dependents", kernels()[name])
+
+
 # ---- chains on the GPU --------------------------------------------------------------
 def captured(fn):
     """fn recorded once: its launches follow one another without the host's pauses."""
@@ -108,3 +115,52 @@ def test_append_after_a_filter_with_nothing_to_filter(B, V, dtype):
         for w in want:
             np.add.at(counts, (np.arange(B), w), 1)
         assert np.array_equal(state.history[:, :V].cpu().numpy(), counts)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("B,V", [(1, 50257), (9, 33000), (90, 20001), (180, 9001)])
+def test_draws_from_logits_processed_in_place(B, V, dtype):
+    """Refill, constrain in place, draw, over and over without a pause: every
+    sampler sees the logits that were just written, wherever rows start."""
+    n = 6
+    rng = np.random.default_rng([B, V])
+    for pitch, shift in ((3, 1), ((-V) % 64, 0)):
+        g = torch.Generator("cuda").manual_seed(V)
+        src = [(torch.randn(B, V, generator=g, device="cuda") * 3).to(dtype) for _ in range(n)]
+        words = (V + 31) // 32
+        masks = [torch.from_numpy(rng.integers(-2**31, 2**31, (B, words)).astype(np.int32)).cuda()
+                 for _ in range(n)]
+        state = gs.new_logit_state(B, V)
+        gs.bias_set(state, torch.arange(B, device="cuda") * 5 % V,
+                    torch.full((B,), 9.0, device="cuda"))
+        buf = torch.zeros(B * (V + pitch) + shift + 8, dtype=dtype, device="cuda")
+        x = buf[shift:shift + B * (V + pitch)].view(B, V + pitch)[:, :V]
+        T = torch.full((B,), 0.8, device="cuda")
+        T[::3] = 0.0
+        seed = torch.arange(B, device="cuda")
+        zero = torch.zeros(B, dtype=torch.int64, device="cuda")
+        three = torch.full((B,), 3, dtype=torch.int32, device="cuda")
+        ws = gs.new_workspace(B)
+        calls = [lambda o: gs.gumbel_argmax(x, T, seed, zero, out=o, workspace=ws),
+                 lambda o: gs.constrained_gumbel_argmax(x, T, seed, zero, out=o, workspace=ws),
+                 lambda o: gs.argmax(x, out=o, workspace=ws),
+                 lambda o: gs.filtered_gumbel_argmax(x, T, seed, zero, top_k=three, out=o,
+                                                     workspace=ws),
+                 lambda o: gs.categorical(x, T, seed, zero, out=o)]
+        for call in calls:
+            want = []
+            for s, m in zip(src, masks):
+                x.copy_(s)
+                gs.process_logits(x, state=state, mask=m, out=x)
+                torch.cuda.synchronize()
+                want.append(torch.full((B,), -5, dtype=torch.int64, device="cuda"))
+                call(want[-1])
+                torch.cuda.synchronize()
+            for _ in range(3):
+                got = torch.full((n, B), -5, dtype=torch.int64, device="cuda")
+                for i in range(n):
+                    x.copy_(src[i])
+                    gs.process_logits(x, state=state, mask=masks[i], out=x)
+                    call(got[i])
+                assert torch.equal(got, torch.stack(want))

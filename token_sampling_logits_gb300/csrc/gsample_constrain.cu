@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kWideThreads, DT == 0 ? 6 : kWideCtas)
   constexpr int NI = ISZ;            // 32-byte pieces of a word's logits
   constexpr int EPO = 32 / ISZ;      // elements a piece
   __shared__ uint32_t lists[kWideThreads / 32][kTouchedCap];
-  pdl_wait_then_release();
+  pdl_wait();  // no release: this kernel writes logits
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t Q = p.warps_per_row;
   const int32_t q = (int32_t)blockIdx.x * (kWideThreads / 32) + warp;
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kConThreads, kProcessCtas)
   constexpr int ISZ = DT == 0 ? 4 : 2, OSZ = ODT == 0 ? 4 : 2;
   constexpr uint32_t kFull = (1u << N) - 1u;
   __shared__ uint32_t lists[kConThreads / 32][kTouchedCap];
-  pdl_wait_then_release();
+  pdl_wait();  // no release: this kernel writes logits
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t Q = p.warps_per_row;
   const int32_t q = (int32_t)blockIdx.x * (kConThreads / 32) + warp;

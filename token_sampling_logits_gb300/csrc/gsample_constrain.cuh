@@ -8,9 +8,11 @@
 // Every operation is rounded once to binary32 (no contraction into an fma), so
 // the written logits and the samplers' in-register ones are the same bits.
 //
-// State and mask words, and single logits, are read once a launch and through L2
-// only (ld.cg): the kernel just before on the stream, which this one's start may
-// overlap, often writes them.
+// State and mask words, and single logits, are read through L2 only (ld.cg): the
+// kernel just before on the stream, which this one's start may overlap, often
+// writes state words. (Whole rows of logits are read by non-coherent loads; no
+// kernel that writes logits lets its successor start early.) The exact pass of
+// the small-batch kernel reads the words of the elements it scores again.
 #pragma once
 
 #include <cstdint>

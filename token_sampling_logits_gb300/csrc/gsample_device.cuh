@@ -40,8 +40,15 @@ static_assert(sizeof(WsRow) == 16, "workspace row is 16 bytes");
 // predecessor, and its successor's wait covers it alone. A kernel that follows
 // on the same stream with the same launch attribute must likewise wait before
 // reading the indices.
+//
+// Logits are read by non-coherent loads, which may not read what is written
+// during their own kernel's life. So a kernel that writes logits waits and does
+// not release: its successor starts when its CTAs have ended. What else a kernel
+// reads of its predecessor's results goes past L1 (ld.cg).
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ void pdl_wait_then_release() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_wait();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 

@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kFiltThreads, 4) filter_cluster_kernel(const F
   if (!(f.T > 0.0f) || !(f.k_on || f.p_on)) {  // greedy or unfiltered: the proposal stands
     // Not before the kernel that writes it is done: a kernel that follows waits
     // for this one alone.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    pdl_wait();
     return;
   }
   const char* row = fp.logits + b * fp.ld_bytes;
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kFiltThreads, 4) filter_cluster_kernel(const F
     }
     cp_async_commit();
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_wait();
   const int64_t w = fp.out_idx[b];
   const float xw = w >= 0 ? elt_at<DT>(row, w) : -INFINITY;
   if constexpr (RESIDENT) cp_async_wait<0>();

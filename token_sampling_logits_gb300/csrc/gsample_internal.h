@@ -12,7 +12,7 @@
 
 namespace gsample {
 
-// The launch attribute that pairs with pdl_wait_then_release() in every kernel.
+// The launch attribute that pairs with the pdl_wait of every kernel.
 inline cudaLaunchAttribute pdl_attribute() {
   cudaLaunchAttribute a;
   a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
