@@ -64,6 +64,18 @@ def test_kernels_that_write_logits_do_not_release_early(name):
     assert not re.search(r"release|launch_dependents", kernels()[name])
 
 
+@pytest.mark.parametrize("name", ["bias_set_kernel", "history_append_kernel",
+                                  "history_append_long_kernel"])
+def test_lists_are_read_past_l1(name):
+    """A list may be what a sampler, or a kernel that writes logits, just wrote."""
+    text = _without_comments(open(os.path.join(build.CSRC, "gsample_constrain.cu")).read())
+    body = kernels()[name]
+    body += text[text.index("token_place("):text.index("history_append_kernel(")] \
+        if "token_place(" in body else ""
+    assert re.search(r"__ldcg\(tokens", body)
+    assert not re.search(r"__ldg\((tokens|values)", body)
+
+
 # ---- chains on the GPU --------------------------------------------------------------
 def captured(fn):
     """fn recorded once: its launches follow one another without the host's pauses."""
@@ -164,3 +176,37 @@ def test_draws_from_logits_processed_in_place(B, V, dtype):
                     gs.process_logits(x, state=state, mask=masks[i], out=x)
                     call(got[i])
                 assert torch.equal(got, torch.stack(want))
+
+
+@gpu
+def test_biases_of_the_tokens_and_values_just_written():
+    """Lists that the kernel before wrote: the tokens a sampler drew, and
+    constrained logits as values."""
+    B, V, n = 40, 5000, 8
+    g = torch.Generator("cuda").manual_seed(1)
+    x = [torch.randn(B, V, generator=g, device="cuda") for _ in range(n)]
+    ids = torch.arange(B, device="cuda")
+    place, ends = ids.float(), torch.tensor([0, B], device="cuda")
+    rows = torch.zeros(B, dtype=torch.int32, device="cuda")
+    state = gs.new_logit_state(1, V)
+    idx = torch.zeros(B, dtype=torch.int64, device="cuda")
+    vals = torch.zeros(1, B, device="cuda")
+    ws = gs.new_workspace(B)
+    seen = []
+    for y in x:
+        gs.argmax(y, out=idx, workspace=ws)
+        gs.bias_set(state, idx, place, offsets=ends)
+        seen.append(state.bias[0].clone())
+        gs.state_reset(state, slots=rows[:1])
+        gs.process_logits(y[:1, :B], out=vals)
+        gs.bias_set(state, ids, vals[0], offsets=ends)
+        seen.append(state.bias[0].clone())
+        gs.state_reset(state, slots=rows[:1])
+    for i, y in enumerate(x):
+        want = np.zeros(state.ld, np.float32)
+        for j, t in enumerate(y.argmax(1).tolist()):  # the later value stays
+            want[t] = j
+        assert np.array_equal(seen[2 * i].cpu().numpy(), want)
+        want[:] = 0
+        want[:B] = y[0, :B].cpu().numpy()
+        assert np.array_equal(seen[2 * i + 1].cpu().numpy(), want)

@@ -199,8 +199,8 @@ __global__ void __launch_bounds__(32)
       t[k] = -1;
       v[k] = 0.0f;
       if (j < hi) {
-        t[k] = __ldg(tokens + j);
-        v[k] = __ldg(values + j);
+        t[k] = __ldcg(tokens + j);  // both may be what the kernel before wrote
+        v[k] = __ldcg(values + j);
         if (t[k] < 0 || t[k] >= s.vocab) t[k] = -1;
       }
     }
