@@ -298,7 +298,9 @@ __device__ __forceinline__ Prune make_prune(float L, float T) {
     const float margin = 1e-3f * (1.0f + fabsf(L));
     p.thr_x = (L - kGumbelMax - margin) * T;
     p.lm = L - margin - 0.01f;
-    p.use_bound = true;
+    // From 2^128 / log2(e) on, the bound's exponent (make_reach) is past binary32
+    // and would reject better scores too: there the logit alone decides.
+    p.use_bound = L < 1e38f;
   }
   return p;
 }
