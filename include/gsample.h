@@ -22,7 +22,8 @@
  *   - out_idx: device int64[B], written with the sampled index of each row, or
  *     -1 for a row with no candidate (every logit -inf or NaN).
  *   - NaN logits are never drawn; a +inf logit scores +inf (so the lowest +inf
- *     index of a row wins); scores are formed in binary32.
+ *     index of a row wins); scores are formed in binary32, where a finite logit
+ *     whose quotient by T overflows scores +inf as well.
  *   - temperature / seed / offset: device arrays of B entries. A row whose
  *     temperature is <= 0 or NaN is sampled greedily (plain argmax of the raw
  *     logits, lowest index on ties), as the issue's Task 3 keeps greedy on argmax.

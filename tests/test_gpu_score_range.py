@@ -63,6 +63,42 @@ def check(x, dtype, T, **kw):
             assert bad.size == 0, (name, pitch, len(bad), bad[:5], got[bad[:5]], want[bad[:5]])
 
 
+@pytest.mark.parametrize("T", [1.2e-38, 2.0 ** -149, 1e-42])
+@pytest.mark.parametrize("dtype", [W.F32, W.BF16, W.F16])
+@pytest.mark.parametrize("B,V", SHAPES)
+def test_quotients_that_overflow_tie(B, V, dtype, T):
+    rng = np.random.default_rng([B, V, dtype])
+    x = W.roundtrip((rng.standard_normal((B, V)) * 4).astype(np.float32), dtype)
+    x[rng.random((B, V)) < 0.3] = -np.inf
+    x[0, :] = -1.0  # one row with a single infinite score
+    x[0, V // 2] = 6.0
+    check(x, dtype, T)
+
+
+@pytest.mark.parametrize("T", [0.7, 1.0 - 2.0 ** -24, 1e-3, 1e-19])
+@pytest.mark.parametrize("dtype", [W.F32, W.BF16])
+@pytest.mark.parametrize("B,V", SHAPES)
+def test_large_logits_that_overflow_tie(B, V, dtype, T):
+    """A few logits of the last octave before the quotient overflows and the
+    first after it."""
+    rng = np.random.default_rng([B, V, dtype, 1])
+    x = (rng.standard_normal((B, V)) * 4).astype(np.float32)
+    edge, most = 3.4028234e38 * T, 3.4028234e38 if dtype == W.F32 else 3.3895e38
+    some = rng.random((B, V)) < 0.01
+    x[some] = np.minimum(edge * rng.uniform(0.5, 2.0, some.sum()), most)
+    x[:, 1000 % V] = min(edge * 0.99999, most)
+    check(W.roundtrip(x, dtype), dtype, T)
+
+
+@pytest.mark.parametrize("dtype", [W.F32, W.BF16, W.F16])
+def test_infinite_logits_and_overflowing_ones_tie(dtype):
+    rng = np.random.default_rng(5)
+    x = W.roundtrip(rng.standard_normal((100, 6000)).astype(np.float32), dtype)
+    x[np.arange(100), rng.integers(0, 6000, 100)] = np.inf
+    x[np.arange(50), rng.integers(0, 6000, 50)] = 30.0
+    check(x, dtype, 2.0 ** -126)
+
+
 @pytest.mark.parametrize("T", [1.0, 3.0, 0.25])
 @pytest.mark.parametrize("dtype", [W.F32, W.BF16])
 @pytest.mark.parametrize("B,V", SHAPES)

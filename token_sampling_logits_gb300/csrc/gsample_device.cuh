@@ -282,11 +282,7 @@ __device__ __forceinline__ bool may_reach(float x, uint32_t w, const ReachTest& 
 
 __device__ __forceinline__ Prune make_prune(float L, float T) {
   Prune p;
-  if (L == INFINITY) {  // only +inf logits can still win
-    p.thr_x = INFINITY;
-    p.lm = -INFINITY;
-    p.use_bound = false;
-  } else if (!(L > -INFINITY) || !(T >= 1e-20f && T <= 1e20f)) {
+  if (!(L > -INFINITY) || !(T >= 1e-20f && T <= 1e20f)) {
     // Nothing known yet, or an extreme temperature: only -inf, which is never a
     // candidate, is skipped. Rows that are masked in places (a grammar's -inf)
     // would otherwise take every masked group through the exact pass until
@@ -295,6 +291,10 @@ __device__ __forceinline__ Prune make_prune(float L, float T) {
     p.lm = -INFINITY;
     p.use_bound = false;
   } else {
+    // A known +inf counts as the largest finite score: an element that scores
+    // +inf too can still win, at a lower index, and where T < 1 that may be a
+    // finite logit whose quotient overflows.
+    L = fminf(L, 3.402823466e38f);
     const float margin = 1e-3f * (1.0f + fabsf(L));
     p.thr_x = (L - kGumbelMax - margin) * T;
     p.lm = L - margin - 0.01f;
