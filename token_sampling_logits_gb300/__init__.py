@@ -14,6 +14,7 @@ All calls are asynchronous on ``torch.cuda.current_stream()``.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import threading
 from dataclasses import dataclass
@@ -448,7 +449,9 @@ class LogitState:
     touched  int32 [rows, ld // 32]: bit v set where history or bias may be
              nonzero.
     ld is `vocab` rounded up to a multiple of 32 (or more). Rows may be copied
-    with plain tensor copies (all three tensors): to fork a request, say."""
+    with plain tensor copies (all three tensors): to fork a request, say. The
+    calls use the memory that these tensors had here: the attributes cannot be
+    assigned."""
 
     def __init__(self, history, bias, touched, vocab: int):
         torch = _torch()
@@ -467,11 +470,19 @@ class LogitState:
                 touched.shape != (rows, ld // 32) or not touched.is_contiguous():
             raise ValueError("touched must be a contiguous int32 tensor [rows, ld // 32] on "
                              "history's device")
-        self.history, self.bias, self.touched, self.vocab = history, bias, touched, int(vocab)
-        self.rows, self.ld, self.device = rows, ld, dev
+        self._history, self._bias, self._touched, self._vocab = history, bias, touched, int(vocab)
+        self._rows, self._ld, self._device = rows, ld, dev
         self._c = _StateC(history.data_ptr(), None if bias is None else bias.data_ptr(),
-                          touched.data_ptr(), rows, self.vocab, ld)
+                          touched.data_ptr(), rows, int(vocab), ld)
         self._at = ctypes.addressof(self._c)
+
+    history = property(operator.attrgetter("_history"))
+    bias = property(operator.attrgetter("_bias"))
+    touched = property(operator.attrgetter("_touched"))
+    vocab = property(operator.attrgetter("_vocab"))
+    rows = property(operator.attrgetter("_rows"))
+    ld = property(operator.attrgetter("_ld"))
+    device = property(operator.attrgetter("_device"))
 
 
 def new_logit_state(rows: int, vocab: int, device=None, bias: bool = True) -> LogitState:
