@@ -1333,7 +1333,8 @@ cudaError_t launch_sample(const SampleParams& p, int dtype, bool vec, cudaStream
 
 cudaError_t launch_sample(const ConSampleParams& p, int dtype, bool vec, int sms,
                           cudaStream_t stream) {
-  if (p.con.history || p.con.mask) {  // else nothing is ever listed
+  const bool listed = p.con.history || p.con.mask;  // else nothing ever is
+  if (listed) {
     const int32_t words = (p.V + 31) / 32;
     // Halved until there is a warp for every place on the device: at V = 32000,
     // B = 128 the launch took 27 us with 8 words a lane throughout, 7 so.
@@ -1358,8 +1359,15 @@ cudaError_t launch_sample(const ConSampleParams& p, int dtype, bool vec, int sms
     const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
     if (e != cudaSuccess) return e;
   }
-  return launch_kernel(select_kernel(dtype, vec, true), p, const_cast<ConSampleParams*>(&p),
-                       sample_smem_bytes(dtype, vec), stream);
+  const cudaError_t e = launch_kernel(select_kernel(dtype, vec, true), p,
+                                      const_cast<ConSampleParams*>(&p),
+                                      sample_smem_bytes(dtype, vec), stream);
+  if (e != cudaSuccess && listed) {
+    // What the list kernel publishes would otherwise reach the next call.
+    cudaGetLastError();
+    cudaMemsetAsync(p.ws, 0, (size_t)p.B * sizeof(WsRow), stream);
+  }
+  return e;
 }
 
 // ---------------------------------------------------------------------------
