@@ -373,9 +373,12 @@ gsample_status gsample_bias_set(const gsample_logit_state* state, const int32_t*
 
 /* Writes the constrained logits of every row: out[b, v], rounded once to
  * out_dtype, which is GSAMPLE_F32 or the logits' type; out_ld elements from
- * row to row. In place (out == logits, same type and ld) it writes only the
- * elements that change. Any other overlap of a row of out with a row of the
- * logits returns GSAMPLE_ERR_INVALID_ARG. constraints == NULL converts. */
+ * row to row. In place (out == logits, same type and ld) the elements that
+ * change are written, and with them, unchanged, others near them: all of a run of
+ * 32 elements, or of 16 bytes, of which the mask takes a part, and every element
+ * whose touched bit is set. So nothing else may write the rows meanwhile. Any
+ * other overlap of a row of out with a row of the logits returns
+ * GSAMPLE_ERR_INVALID_ARG. constraints == NULL converts. */
 gsample_status gsample_process_logits(const void* logits, gsample_dtype dtype, int64_t B,
                                       int64_t V, int64_t ld,
                                       const gsample_constraints* constraints, void* out,
