@@ -681,15 +681,19 @@ __device__ __forceinline__ void issue_tile(const SampleParams& p, const TileCurs
 //     the remaining places of its tiles are -inf, units without an element for
 //     it are not read, and a tile without one is passed over.
 // Scoring the touched elements where the sweep meets them was measured slower
-// (B = 256, V = 151936 bf16, some 1600 touched tokens a row: 112 us with a list
-// a warp, 86 us with a list a CTA, 66 us so): the sweep runs 16 warps an SM, too
-// few to hide the gathers, and the low ids, where most tokens of a request lie,
-// keep one warp of a row long after the others. The sweep itself takes 48 us
-// with nothing constrained (45 the unconstrained kernel), 55 with masks.
+// (B = 256, V = 151936 bf16, some 1600 touched tokens a row, one input drawn
+// from over and over: 112 us with a list a warp, 86 us with a list a CTA, 67 us
+// so; 70 us so with inputs in turn): the sweep runs 16 warps an SM, too few to
+// hide the gathers, and the low ids, where most tokens of a request lie, keep
+// one warp of a row long after the others. With inputs in turn, the sweep alone
+// takes 48 us with nothing constrained (44 the unconstrained kernel); with masks
+// alone the two kernels take 55 us, with penalties and biases alone 75.
 //
 // Rows differ in work here (a row whose grammar allows a few tokens has none),
 // so the warps take chunks of rows in turn rather than one contiguous range
-// each: chunk c, of chunk_units units, goes to warp c modulo the number of
+// each, dealt before the launch: warps of nearly empty rows still idle, and such
+// a row's chunks are still walked tile by tile (20 us for 256 rows with a few
+// tokens left). Chunk c, of chunk_units units, goes to warp c modulo the number of
 // warps. A chunk starts on a multiple of 8 units of its row (32 or 64
 // elements), so a tile's bits are whole words: lane l holds words l and, for
 // 16-bit units (64 words a tile), l + 32.
