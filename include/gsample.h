@@ -402,6 +402,156 @@ gsample_status gsample_constrained_gumbel_argmax(const void* logits, gsample_dty
                                                  int64_t* out_idx, void* workspace,
                                                  gsample_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Draws from given random numbers: the sampler of the issue's categorical path
+ * ("Softmax-free GPU sampling", Background: temperature, top-k, top-p, min-p,
+ * then a categorical draw) for callers that bring their own random numbers,
+ * and the verification of speculative drafts by the same filter.
+ * ------------------------------------------------------------------------- */
+
+/* One draw a row from softmax(logits / T) restricted to the row's filter set K
+ * by the inverse CDF in index order: out_idx[b] is the smallest i in K with
+ *     sum of e_j over j <= i in K  >  u_b * (sum of e_j over K),
+ * e_j = exp((x_j - M) / T), M the largest logit. K is the first r candidates
+ * (logits that are neither NaN nor -inf) in the order (logit descending, index
+ * ascending), r the smallest of
+ *   - top_k[b], when top_k[b] >= 1 (else no limit),
+ *   - the smallest prefix whose softmax mass reaches top_p[b] * (row mass),
+ *     when top_p[b] < 1 (top_p[b] <= 0 keeps the first candidate only; >= 1 or
+ *     NaN: no limit),
+ *   - the elements with e_j >= min_p[b], when min_p[b] > 0 (above 1 counts as
+ *     1; <= 0 or NaN: no limit),
+ * and holds at least the first candidate.
+ *   - uniform: device array of B floats in [0, 1) (below, or NaN: 0; 1 and
+ *     above: the largest below 1). top_k, top_p, min_p: device arrays of B
+ *     entries; any may be NULL (that filter off).
+ *   - out_logprob: device float[B] or NULL: log(e_i / sum over K) of the drawn
+ *     token, natural, rounded once; 0 for greedy rows, -inf for a row without
+ *     candidates (out_idx -1).
+ *   - T <= 0 or NaN: greedy. +inf logits: the lowest such index. T = +inf: all
+ *     candidates weigh the same. Temperatures below 2^-126 count as that.
+ *   - Weights are fixed-point numbers with 44 fraction bits (fewer past V =
+ *     2^18), each within about 2^-39 of itself; their sums are exact and the
+ *     result does not depend on the launch. So an index differs from the exact
+ *     one only where u or a filter's border lies within about 1e-11 of the mass
+ *     from a boundary. An element whose weight is below 2^-45 is never drawn.
+ *   - Layout, alignment, errors and asynchrony as gsample_gumbel_argmax; B up
+ *     to (2^31 - 1) / 16. No workspace. */
+gsample_status gsample_filtered_categorical(const void* logits, gsample_dtype dtype, int64_t B,
+                                            int64_t V, int64_t ld, const float* temperature,
+                                            const float* uniform, const int32_t* top_k,
+                                            const float* top_p, const float* min_p,
+                                            int64_t* out_idx, float* out_logprob,
+                                            gsample_stream_t stream);
+
+/* Bytes of workspace gsample_verify_drafts needs for R rows (32 a row; need not
+ * be cleared). */
+size_t gsample_verify_workspace_bytes(int64_t R);
+
+/* Verification of the draft tokens of n requests against the target model's
+ * logits, so that the tokens that come out are distributed as the target's own
+ * draws. Request i owns rows offsets[i] .. offsets[i + 1] of the logits (device
+ * int64, offsets[0..n] not decreasing, clipped to [0, R]): row r holds the
+ * target's logits after the tokens up to draft[r - 1], draft[r] (device
+ * int64[R]) is the token proposed next, and the request's last row has no draft
+ * (its entry is ignored). p_r is softmax(logits / T) over the row's filter set,
+ * normalised, as gsample_filtered_categorical has it, with the settings of
+ * request i (temperature, top_k, top_p, min_p: device arrays of n entries).
+ *   - draft_probs: device float rows (draft_probs_ld >= V elements from row to
+ *     row), row r the distribution q_r that draft[r] was drawn from; NaN and
+ *     negative entries count as 0, in the residual those above 1 as 1. The rows
+ *     of last rows are not read. NULL: drafts without probabilities (looked up,
+ *     or greedy), q_r(t) = 1 for the draft alone.
+ *   - In order, draft[r] is accepted when uniform[r] * q_r(t) < p_r(t) (so a
+ *     token outside [0, V) or outside the filter set is not). At the first
+ *     that is not, the next token is drawn from max(p_r - q_r, 0), normalised
+ *     (from p_r where that is zero everywhere); when all are, from p of the last
+ *     row. uniform: device float[R]; uniform_draw: device float[n], the number
+ *     of the request's one draw, which is the inverse CDF in index order.
+ *   - out_tokens: device int64[R]. The rows of a request get its accepted
+ *     drafts, then the drawn token, then -1 (also in place of a draw from a row
+ *     without candidates): lists that gsample_history_append takes with the
+ *     same offsets. Rows outside every request are left as they were.
+ *   - out_count: device int32[n], the tokens a request got (0 for a request
+ *     without rows).
+ *   - workspace: device buffer of gsample_verify_workspace_bytes(R) bytes,
+ *     16-byte aligned, with any contents; launches in flight at the same time
+ *     must not share one. Two launches.
+ * Temperatures <= 0, special values, precision, layout, validation and
+ * asynchrony as gsample_filtered_categorical; R and n up to (2^31 - 1) / 16. */
+gsample_status gsample_verify_drafts(const void* logits, gsample_dtype dtype, int64_t R, int64_t V,
+                                     int64_t ld, int64_t n, const int64_t* offsets,
+                                     const int64_t* draft, const float* draft_probs,
+                                     int64_t draft_probs_ld, const float* temperature,
+                                     const int32_t* top_k, const float* top_p, const float* min_p,
+                                     const float* uniform, const float* uniform_draw,
+                                     int64_t* out_tokens, int32_t* out_count, void* workspace,
+                                     gsample_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Pages of a paged cache: the block tables and slot maps that the model's next
+ * step needs, built where the number of accepted tokens is known.
+ * ------------------------------------------------------------------------- */
+
+/* Which physical pages hold the tokens of each request slot (the caller owns
+ * the arrays; this struct is host memory, read during the call).
+ *   table       int32 [rows, ld]: entry c of a slot is the page of its tokens
+ *               c * page_size .. (c + 1) * page_size, -1 past its last page.
+ *   length      int32 [rows]: tokens of each slot.
+ *   free_list   int32 [pages]: a stack of free page ids; free_count int32[1]:
+ *               how many it holds (the top is free_list[free_count - 1]).
+ *   rows from 1 to 65536; ld * page_size, the longest slot, below 2^31.
+ * To begin: table -1, length 0, free_list a permutation of the page ids and
+ * free_count = pages. Page ids are the caller's: the library only moves them.
+ * Calls that write a state must be ordered with every call that uses it. */
+typedef struct {
+  int32_t* table;
+  int32_t* length;
+  int32_t* free_list;
+  int32_t* free_count;
+  int64_t rows;
+  int64_t ld;
+  int64_t pages;
+  int32_t page_size;
+} gsample_page_state;
+
+/* Appends room for tokens to n slots and builds what a model step over those
+ * tokens needs. Request i appends the tokens offsets[i] .. offsets[i + 1]
+ * (device int64, offsets[0..n] not decreasing, clipped to [0, total]), or one
+ * token when offsets is NULL (total == n), to the slot slot[i] (device int32;
+ * NULL: slot i). New pages come off the stack in order of i, lowest token first.
+ *   - A request is refused, its slot left as it was, when its slot is outside
+ *     [0, rows) or named by more than one request of the call, when it would
+ *     pass ld * page_size tokens, or when it needs pages and those that it and
+ *     the requests before it need (refused for want of pages or not) are more
+ *     than the stack holds. A request that needs no new page is never refused
+ *     for want of pages.
+ *   - out_start: device int32[n], the length before (the position of the first
+ *     new token), -1 for a refused request.
+ *   - out_slot_map: device int64[total]: page * page_size + place in the page
+ *     of each new token, -1 for those of a refused request; entries outside
+ *     every request are left as they were.
+ *   - out_length: device int32[n] or NULL: the length after, 0 where refused.
+ *   - out_table: device int32 rows (table_ld >= table_cols entries from row to
+ *     row) or NULL: the first table_cols entries of each request's table after
+ *     the call, -1 past its last page and where refused. */
+gsample_status gsample_pages_extend(const gsample_page_state* state, const int32_t* slot,
+                                    int64_t n, const int64_t* offsets, int64_t total,
+                                    int32_t* out_start, int64_t* out_slot_map, int32_t* out_length,
+                                    int32_t* out_table, int64_t table_cols, int64_t table_ld,
+                                    gsample_stream_t stream);
+
+/* Shortens n slots to start[i] + keep[i] tokens (device int32; NULL counts as
+ * 0, so both NULL release the slots), at least 0, and puts the pages past that
+ * back on the stack, where an extension of the same requests takes them from in
+ * the same order. A slot that is no longer, one outside [0, rows), one named
+ * more than once in the call and one with a negative start (a request that
+ * gsample_pages_extend refused) are left as they were. After a verification:
+ * start from gsample_pages_extend, keep = out_count of gsample_verify_drafts. */
+gsample_status gsample_pages_trim(const gsample_page_state* state, const int32_t* slot, int64_t n,
+                                  const int32_t* start, const int32_t* keep,
+                                  gsample_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

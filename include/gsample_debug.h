@@ -112,6 +112,14 @@ gsample_status gsample_debug_philox_alu_mix(int32_t warps_per_sm, uint32_t iters
  * GSAMPLE_ERR_UNSUPPORTED. Synchronous (reads a device counter). */
 gsample_status gsample_debug_blocks_computed(uint64_t* count, int32_t reset);
 
+/* The fixed-point softmax weights of gsample_filtered_categorical and
+ * gsample_verify_drafts: out[j], in units of 2^-44, is the weight of x[j] in a
+ * row whose largest logit is M at temperature T, exp((x[j] - M) / T) times a
+ * factor within 0.2% of 1 that all j share. x, out: device arrays of n entries
+ * (x[j] <= M, -inf or NaN); T > 0 and M finite, else GSAMPLE_ERR_INVALID_ARG. */
+gsample_status gsample_debug_weights(const float* x, int64_t n, float M, float T, uint64_t* out,
+                                     gsample_stream_t stream);
+
 /* The HLG kernel's exact candidate score ("HLG sampling", "The transfer
  * function"): out[j] = tone(x[j] + shift) / T + g(words[j]) in binary32, the
  * tone curve of `hlg` (pivot fields unused), the shift standing for the row's

@@ -27,6 +27,8 @@ __all__ = [
     "gumbel_argmax", "hlg_gumbel_argmax", "hlg_gumbel_argmax_rows", "hlg_rows_tensor",
     "categorical", "filtered_gumbel_argmax", "status_string", "LogitState", "new_logit_state",
     "state_reset", "history_append", "bias_set", "process_logits", "constrained_gumbel_argmax",
+    "filtered_categorical", "verify_workspace_bytes", "new_verify_workspace", "verify_drafts",
+    "PageState", "new_page_state", "pages_extend", "pages_trim",
 ]
 
 F32, BF16, F16 = 0, 1, 2
@@ -57,6 +59,11 @@ class _ConstraintsC(ctypes.Structure):
     _fields_ = [("state", _vp), ("slot", _vp), ("repetition", _vp),
                 ("frequency", _vp), ("presence", _vp), ("mask", _vp), ("mask_rows", _i64),
                 ("mask_ld", _i64), ("mask_row", _vp)]
+
+
+class _PagesC(ctypes.Structure):
+    _fields_ = [("table", _vp), ("length", _vp), ("free_list", _vp), ("free_count", _vp),
+                ("rows", _i64), ("ld", _i64), ("pages", _i64), ("page_size", _i32)]
 
 
 @dataclass(frozen=True)
@@ -142,6 +149,16 @@ def lib() -> ctypes.CDLL:
                                               _vp]),
             "gsample_constrained_gumbel_argmax": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp,
                                                          _vp, _vp, _vp, _vp, _vp]),
+            "gsample_filtered_categorical": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp,
+                                                    _vp, _vp, _vp, _vp, _vp]),
+            "gsample_verify_workspace_bytes": (ctypes.c_size_t, [_i64]),
+            "gsample_verify_drafts": (_int, [_vp, _int, _i64, _i64, _i64, _i64, _vp, _vp, _vp,
+                                             _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                             _vp]),
+            "gsample_debug_weights": (_int, [_vp, _i64, ctypes.c_float, ctypes.c_float, _vp, _vp]),
+            "gsample_pages_extend": (_int, [_vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64,
+                                            _i64, _vp]),
+            "gsample_pages_trim": (_int, [_vp, _vp, _i64, _vp, _vp, _vp]),
             "gsample_debug_filtered_ex": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp,
                                                  _vp, _vp, _vp, _i32, _vp]),
         }
@@ -676,6 +693,209 @@ def constrained_gumbel_argmax(logits, temperature, seed, offset, state: LogitSta
     return out
 
 
+# --------------------------------------------------------------------------
+# Draws from given random numbers
+# --------------------------------------------------------------------------
+def filtered_categorical(logits, temperature, uniform, top_k=None, top_p=None, min_p=None,
+                         out=None, logprob=None):
+    """One draw per row from softmax(logits / T) over the row's top-k / top-p /
+    min-p set by the caller's random numbers (gsample_filtered_categorical): the
+    inverse CDF in index order. uniform (float32 in [0, 1)), temperature
+    (float32), top_k (int32), top_p and min_p (float32) are per-row tensors or
+    scalars; None switches a filter off. Returns the indices (int64 [B], -1 for
+    a row without candidates), or (indices, log-probabilities) with logprob=True
+    or a float32 [B] tensor to write them to."""
+    torch = _torch()
+    dt, B, V, ld, out, _ = _prepare(logits, out, None, need_ws=False)
+    index, keep, f32 = logits.get_device(), [], torch.float32
+    T = _row_at(temperature, B, f32, index, "temperature", keep)
+    U = _row_at(uniform, B, f32, index, "uniform", keep)
+    K = None if top_k is None else _row_at(top_k, B, torch.int32, index, "top_k", keep)
+    P = None if top_p is None else _row_at(top_p, B, f32, index, "top_p", keep)
+    m = None if min_p is None else _row_at(min_p, B, f32, index, "min_p", keep)
+    if logprob is True:
+        logprob = torch.empty(B, dtype=f32, device=logits.device)
+    elif logprob is False:
+        logprob = None
+    _launch(index, "gsample_filtered_categorical", lib().gsample_filtered_categorical,
+            logits.data_ptr(), dt, B, V, ld, T, U, K, P, m, out.data_ptr(),
+            _vector(logprob, B, f32, index, "logprob"))
+    return out if logprob is None else (out, logprob)
+
+
+def verify_workspace_bytes(rows: int) -> int:
+    return int(lib().gsample_verify_workspace_bytes(rows))
+
+
+def new_verify_workspace(rows: int, device=None):
+    """A workspace of verify_drafts for up to `rows` rows of logits."""
+    torch = _torch()
+    return torch.empty(max(16, verify_workspace_bytes(rows)), dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+def verify_drafts(logits, draft, offsets, temperature, uniform, uniform_draw, probs=None,
+                  top_k=None, top_p=None, min_p=None, out=None, count=None, workspace=None):
+    """Verifies speculative drafts (gsample_verify_drafts). Request i owns rows
+    offsets[i]:offsets[i + 1] of the target's logits [R, V]; draft[r] (int64
+    [R]) is the token proposed after row r, and a request's last row has none.
+
+    uniform       float32 [R]: draft r is accepted when uniform[r] * q(t) < p(t).
+    uniform_draw  float32 [n]: the number of each request's one draw.
+    probs         float32 [R, V], the distributions that the drafts were drawn
+                  from (contiguous rows); None: drafts without probabilities.
+    temperature, top_k, top_p, min_p   per request, as filtered_categorical's.
+    Returns (tokens, count): tokens int64 [R] holds, in each request's rows, the
+    accepted drafts, the drawn token and then -1 (history_append takes it with
+    the same offsets), and is not written elsewhere; count int32 [n] the number
+    of tokens."""
+    torch = _torch()
+    dt, R, V, ld = _logits_args(logits)
+    dev, index, keep, f32 = logits.device, logits.get_device(), [], torch.float32
+    offsets_at = _vector(offsets, None, torch.int64, index, "offsets")
+    if offsets is None or offsets.numel() < 1:
+        raise ValueError("offsets has one entry more than there are requests")
+    n = offsets.numel() - 1
+    draft_at = _vector(draft, R, torch.int64, index, "draft")
+    T = _row_at(temperature, n, f32, index, "temperature", keep)
+    U = _row_at(uniform, R, f32, index, "uniform", keep)
+    D = _row_at(uniform_draw, n, f32, index, "uniform_draw", keep)
+    K = None if top_k is None else _row_at(top_k, n, torch.int32, index, "top_k", keep)
+    P = None if top_p is None else _row_at(top_p, n, f32, index, "top_p", keep)
+    m = None if min_p is None else _row_at(min_p, n, f32, index, "min_p", keep)
+    probs_at, probs_ld = None, 0
+    if probs is not None:
+        if probs.dtype != f32 or probs.device != dev or probs.shape != (R, V) or \
+                (V > 1 and probs.stride(1) != 1) or (R > 1 and probs.stride(0) < V):
+            raise ValueError("probs must be a float32 [R, V] tensor with contiguous rows on the "
+                             "logits' device")
+        probs_at, probs_ld = probs.data_ptr(), probs.stride(0) if R > 1 else V
+    if out is None:
+        out = torch.empty(R, dtype=torch.int64, device=dev)
+    out_at = _vector(out, R, torch.int64, index, "out")
+    if count is None:
+        count = torch.empty(n, dtype=torch.int32, device=dev)
+    count_at = _vector(count, n, torch.int32, index, "count")
+    if workspace is None:
+        workspace = new_verify_workspace(R, dev)
+    elif workspace.device != dev or not workspace.is_contiguous() or \
+            workspace.nbytes < verify_workspace_bytes(R):
+        raise ValueError("workspace too small or on another device")
+    _launch(index, "gsample_verify_drafts", lib().gsample_verify_drafts, logits.data_ptr(), dt, R,
+            V, ld, n, offsets_at, draft_at, probs_at, probs_ld, T, K, P, m, U, D, out_at,
+            count_at, workspace.data_ptr())
+    return out, count
+
+
+# --------------------------------------------------------------------------
+# Pages of a paged cache
+# --------------------------------------------------------------------------
+class PageState:
+    """Which physical pages hold the tokens of each request slot
+    (gsample_page_state): a view of caller-owned int32 tensors on one device.
+
+    table       [slots, columns]: page of each run of page_size tokens, -1 past
+                a slot's last page.
+    length      [slots]: tokens of each slot.
+    free        [pages]: a stack of free page ids.
+    free_count  [1]: how many it holds.
+    The calls use the memory that these tensors had here: the attributes cannot
+    be assigned."""
+
+    def __init__(self, table, length, free, free_count, page_size: int):
+        torch = _torch()
+        if not table.is_cuda or table.dim() != 2 or table.dtype != torch.int32 or \
+                not table.is_contiguous() or table.numel() == 0:
+            raise ValueError("table must be a contiguous int32 CUDA tensor [slots, columns]")
+        rows, ld = table.shape
+        index = table.get_device()
+        _vector(length, rows, torch.int32, index, "length")
+        _vector(free, None, torch.int32, index, "free")
+        _vector(free_count, 1, torch.int32, index, "free_count")
+        if free.numel() < 1 or page_size < 1 or ld * page_size >= 1 << 31:
+            raise ValueError("there must be pages of at least one token, and slots of fewer than "
+                             "2^31 tokens")
+        self._table, self._length, self._free, self._free_count = table, length, free, free_count
+        self._page_size, self._device = int(page_size), table.device
+        self._c = _PagesC(table.data_ptr(), length.data_ptr(), free.data_ptr(),
+                          free_count.data_ptr(), rows, ld, free.numel(), int(page_size))
+        self._at = ctypes.addressof(self._c)
+
+    table = property(operator.attrgetter("_table"))
+    length = property(operator.attrgetter("_length"))
+    free = property(operator.attrgetter("_free"))
+    free_count = property(operator.attrgetter("_free_count"))
+    page_size = property(operator.attrgetter("_page_size"))
+    device = property(operator.attrgetter("_device"))
+
+
+def new_page_state(slots: int, pages: int, page_size: int, columns: int, device=None) -> PageState:
+    """A state with `slots` empty slots of at most `columns` pages each and all
+    of `pages` pages free (page 0 is handed out first)."""
+    torch = _torch()
+    i32, dev = torch.int32, device or "cuda"
+    return PageState(torch.full((slots, columns), -1, dtype=i32, device=dev),
+                     torch.zeros(slots, dtype=i32, device=dev),
+                     torch.arange(pages - 1, -1, -1, dtype=i32, device=dev),
+                     torch.full((1,), pages, dtype=i32, device=dev), page_size)
+
+
+def pages_extend(state: PageState, total: int, slots=None, offsets=None, slot_map=None,
+                 start=None, lengths=None, table=None):
+    """Appends room for `total` tokens to request slots and builds what the
+    model's step over them needs (gsample_pages_extend): request i appends
+    offsets[i + 1] - offsets[i] tokens (int64 offsets; None: one each) to slot
+    slots[i] (int32; None: slot i). Returns (start, slot_map): start int32 [n],
+    the slots' lengths before (-1: refused), and slot_map int64 [total], which
+    is not written outside the requests. lengths
+    (int32 [n]) and table (int32 [n, columns], contiguous rows), when given, get
+    the lengths after and the requests' block tables."""
+    torch = _torch()
+    index, dev, i32 = state.device.index, state.device, torch.int32
+    total = int(total)
+    offsets_at = _vector(offsets, None, torch.int64, index, "offsets")
+    n = total if offsets is None else offsets.numel() - 1
+    if n < 0 or total < 0:
+        raise ValueError("offsets has one entry more than there are requests")
+    slots_at = _vector(slots, n, i32, index, "slots")
+    if slot_map is None:
+        slot_map = torch.empty(total, dtype=torch.int64, device=dev)
+    map_at = _vector(slot_map, total, torch.int64, index, "slot_map")
+    if start is None:
+        start = torch.empty(n, dtype=i32, device=dev)
+    start_at = _vector(start, n, i32, index, "start")
+    lengths_at = _vector(lengths, n, i32, index, "lengths")
+    table_at, cols, table_ld = None, 0, 0
+    if table is not None:
+        if table.dtype != i32 or table.get_device() != index or table.dim() != 2 or \
+                table.shape[0] != n or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise ValueError("table must be an int32 [n, columns] tensor with contiguous rows on "
+                             "the state's device")
+        cols = table.shape[1]
+        table_ld = table.stride(0) if n > 1 else cols
+        if table_ld < cols:
+            raise ValueError("the rows of table must not overlap")
+        table_at = table.data_ptr()
+    _launch(index, "gsample_pages_extend", lib().gsample_pages_extend, state._at, slots_at, n,
+            offsets_at, total, start_at, map_at, lengths_at, table_at, cols, table_ld)
+    return start, slot_map
+
+
+def pages_trim(state: PageState, slots=None, start=None, keep=None) -> None:
+    """Shortens slots to start[i] + keep[i] tokens and frees the pages past that
+    (gsample_pages_trim; int32 tensors, None counts as 0: the slots are
+    released). slots: int32 (None: the first ones, or all when start and keep
+    are None too). A slot is left alone where start is negative."""
+    torch = _torch()
+    index = state.device.index
+    given = [x for x in (slots, start, keep) if x is not None]
+    n = given[0].numel() if given else state.table.shape[0]
+    _launch(index, "gsample_pages_trim", lib().gsample_pages_trim, state._at,
+            _vector(slots, n, torch.int32, index, "slots"), n,
+            _vector(start, n, torch.int32, index, "start"),
+            _vector(keep, n, torch.int32, index, "keep"))
+
+
 def seeds_as_tensor(seeds, device):
     """uint64 seeds (numpy or ints) as an int64 tensor holding the same bits."""
     import numpy as np
@@ -705,6 +925,16 @@ def debug_gumbel(words, with_bound: bool = True):
                                       bnd.data_ptr() if bnd is not None else None,
                                       _stream_ptr(words.device)), "gsample_debug_gumbel")
     return g, bnd
+
+
+def debug_weights(x, M: float, T: float):
+    """The fixed-point softmax weights (units of 2^-44, int64) of float32 logits
+    in a row whose largest logit is M."""
+    torch = _torch()
+    out = torch.empty(x.shape, dtype=torch.int64, device=x.device)
+    _check(lib().gsample_debug_weights(x.data_ptr(), x.numel(), M, T, out.data_ptr(),
+                                       _stream_ptr(x.device)), "gsample_debug_weights")
+    return out
 
 
 def planned_ctas(dtype: int, B: int, V: int, ld: int | None = None, ptr: int = 0) -> int:

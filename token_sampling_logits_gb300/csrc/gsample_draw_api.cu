@@ -1,0 +1,197 @@
+// Host side of the draw from given random numbers and of the verification of
+// drafts (include/gsample.h, "Draws from given random numbers"): argument
+// checks, launch planning and status mapping. Nothing here touches device data
+// or synchronises.
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+
+#include "gsample.h"
+#include "gsample_debug.h"
+#include "gsample_internal.h"
+#include "gsample_weights.cuh"
+
+namespace {
+
+using gsample::DrawParams;
+
+constexpr int kMaxDevices = 64;
+constexpr int64_t kUnitsPerCta = 512;  // a CTA of a small batch gets at least this many
+
+int64_t elt_bytes(gsample_dtype dt) { return dt == GSAMPLE_F32 ? 4 : 2; }
+
+bool misaligned(const void* p, uintptr_t a) { return (uintptr_t)p % a != 0; }
+
+gsample_status launched(cudaError_t e) {
+  if (e == cudaSuccess) return GSAMPLE_OK;
+  cudaGetLastError();
+  return GSAMPLE_ERR_CUDA;
+}
+
+// The largest cluster of the kernels of (dtype, vec) on the current device.
+gsample_status max_cluster(int dtype, bool vec, int* out) {
+  static std::mutex mu;
+  static int known[kMaxDevices][6];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return GSAMPLE_ERR_CUDA;
+  }
+  std::lock_guard<std::mutex> lock(mu);
+  int& c = known[dev][dtype * 2 + (vec ? 1 : 0)];
+  if (c == 0) c = gsample::draw_max_cluster(dtype, vec);
+  if (c <= 0) {
+    c = 0;
+    cudaGetLastError();
+    return GSAMPLE_ERR_CUDA;
+  }
+  *out = c;
+  return GSAMPLE_OK;
+}
+
+void fill_rows(const void* logits, gsample_dtype dtype, int64_t B, int64_t V, int64_t ld,
+               bool vec, DrawParams* p) {
+  std::memset(p, 0, sizeof *p);
+  p->logits = static_cast<const char*>(logits);
+  p->ld_bytes = ld * elt_bytes(dtype);
+  p->B = B;
+  p->V = (int32_t)V;
+  const int epu = gsample::units_elems((int)dtype, vec);
+  p->units_per_row = (int32_t)((V + epu - 1) / epu);
+  // A row's V weights of little more than 2^F at most stay below 2^63.
+  int lg = 0;
+  while ((int64_t(1) << lg) < V) ++lg;
+  p->fraction_bits = lg <= 18 ? 44 : 62 - lg;
+}
+
+void set_cluster(int cluster, DrawParams* p) {
+  p->cluster = cluster;
+  p->units_per_cta = (p->units_per_row + cluster - 1) / cluster;
+}
+
+}  // namespace
+
+extern "C" {
+
+gsample_status gsample_filtered_categorical(const void* logits, gsample_dtype dtype, int64_t B,
+                                            int64_t V, int64_t ld, const float* temperature,
+                                            const float* uniform, const int32_t* top_k,
+                                            const float* top_p, const float* min_p,
+                                            int64_t* out_idx, float* out_logprob,
+                                            gsample_stream_t stream) {
+  gsample_status st = gsample::check_logits(logits, dtype, B, V, ld);
+  if (st != GSAMPLE_OK) return st;
+  if (B > 0 && (!temperature || !uniform || !out_idx)) return GSAMPLE_ERR_INVALID_ARG;
+  if (misaligned(temperature, 4) || misaligned(uniform, 4) || misaligned(top_k, 4) ||
+      misaligned(top_p, 4) || misaligned(min_p, 4) || misaligned(out_idx, 8) ||
+      misaligned(out_logprob, 4) || B > INT32_MAX / 16)
+    return GSAMPLE_ERR_INVALID_ARG;
+  if (B == 0) return GSAMPLE_OK;
+  int sms = 0, most = 0;
+  st = gsample::current_device_sms(&sms);
+  if (st != GSAMPLE_OK) return st;
+  const bool vec = gsample::wide_rows(logits, dtype, ld);
+  st = max_cluster((int)dtype, vec, &most);
+  if (st != GSAMPLE_OK) return st;
+  DrawParams p;
+  fill_rows(logits, dtype, B, V, ld, vec, &p);
+  p.temperature = temperature;
+  p.uniform = uniform;
+  p.top_k = top_k;
+  p.top_p = top_p;
+  p.min_p = min_p;
+  p.out_idx = out_idx;
+  p.out_logprob = out_logprob;
+  try {
+    set_cluster(gsample::plan_row_cluster(gsample::draw_kernel, (int)dtype, vec, B,
+                                          p.units_per_row, most, kUnitsPerCta,
+                                          gsample::draw_smem_limit()),
+                &p);
+  } catch (...) {
+    return GSAMPLE_ERR_CUDA;
+  }
+  return launched(gsample::launch_draw(p, (int)dtype, vec, (cudaStream_t)stream));
+}
+
+size_t gsample_verify_workspace_bytes(int64_t R) {
+  return R > 0 ? (size_t)R * sizeof(gsample::RowSet) : 0;
+}
+
+gsample_status gsample_verify_drafts(const void* logits, gsample_dtype dtype, int64_t R, int64_t V,
+                                     int64_t ld, int64_t n, const int64_t* offsets,
+                                     const int64_t* draft, const float* draft_probs,
+                                     int64_t draft_probs_ld, const float* temperature,
+                                     const int32_t* top_k, const float* top_p, const float* min_p,
+                                     const float* uniform, const float* uniform_draw,
+                                     int64_t* out_tokens, int32_t* out_count, void* workspace,
+                                     gsample_stream_t stream) {
+  gsample_status st = gsample::check_logits(logits, dtype, R, V, ld);
+  if (st != GSAMPLE_OK) return st;
+  if (n < 0 || n > INT32_MAX / 16 || R > INT32_MAX / 16) return GSAMPLE_ERR_INVALID_ARG;
+  if (n > 0 && (!offsets || !temperature || !uniform_draw || !out_count))
+    return GSAMPLE_ERR_INVALID_ARG;
+  if (R > 0 && n > 0 && (!draft || !uniform || !out_tokens)) return GSAMPLE_ERR_INVALID_ARG;
+  if (draft_probs && (draft_probs_ld < V || draft_probs_ld > INT64_MAX / 4 / (R > 0 ? R : 1)))
+    return GSAMPLE_ERR_INVALID_ARG;
+  if (misaligned(offsets, 8) || misaligned(draft, 8) || misaligned(draft_probs, 4) ||
+      misaligned(temperature, 4) || misaligned(top_k, 4) || misaligned(top_p, 4) ||
+      misaligned(min_p, 4) || misaligned(uniform, 4) || misaligned(uniform_draw, 4) ||
+      misaligned(out_tokens, 8) || misaligned(out_count, 4))
+    return GSAMPLE_ERR_INVALID_ARG;
+  if (R > 0 && n > 0 && (!workspace || misaligned(workspace, 16))) return GSAMPLE_ERR_WORKSPACE;
+  if (n == 0) return GSAMPLE_OK;
+  int sms = 0, most = 0;
+  st = gsample::current_device_sms(&sms);
+  if (st != GSAMPLE_OK) return st;
+  const bool vec = R > 0 && gsample::wide_rows(logits, dtype, ld);
+  st = max_cluster((int)dtype, vec, &most);
+  if (st != GSAMPLE_OK) return st;
+  DrawParams p;
+  fill_rows(logits, dtype, R, V, ld, vec, &p);
+  p.n = (int32_t)n;
+  p.temperature = temperature;
+  p.top_k = top_k;
+  p.top_p = top_p;
+  p.min_p = min_p;
+  p.uniform = uniform;
+  p.uniform_draw = uniform_draw;
+  p.offsets = offsets;
+  p.draft = draft;
+  p.probs = draft_probs;
+  p.probs_ld = draft_probs_ld;
+  p.out_idx = out_tokens;
+  p.out_count = out_count;
+  p.sets = static_cast<gsample::RowSet*>(workspace);
+  try {
+    if (R > 0) {
+      set_cluster(gsample::plan_row_cluster(gsample::verify_kernel, (int)dtype, vec, R,
+                                            p.units_per_row, most, kUnitsPerCta,
+                                            gsample::draw_smem_limit()),
+                  &p);
+      st = launched(gsample::launch_draw(p, (int)dtype, vec, (cudaStream_t)stream));
+      if (st != GSAMPLE_OK) return st;
+    }
+    set_cluster(gsample::plan_row_cluster(gsample::verify_draw_kernel_fn, (int)dtype, vec, n,
+                                          p.units_per_row, most, kUnitsPerCta, 0),
+                &p);
+  } catch (...) {
+    return GSAMPLE_ERR_CUDA;
+  }
+  return launched(gsample::launch_verify_draw(p, (int)dtype, vec, (cudaStream_t)stream));
+}
+
+gsample_status gsample_debug_weights(const float* x, int64_t n, float M, float T, uint64_t* out,
+                                     gsample_stream_t stream) {
+  if (n < 0 || !(T > 0.0f) || !std::isfinite(M) || (n > 0 && (!x || !out)) || misaligned(x, 4) ||
+      misaligned(out, 8))
+    return GSAMPLE_ERR_INVALID_ARG;
+  if (n == 0) return GSAMPLE_OK;
+  int sms = 0;
+  const gsample_status st = gsample::current_device_sms(&sms);
+  if (st != GSAMPLE_OK) return st;
+  return launched(gsample::launch_debug_weights(x, n, M, T, out, (cudaStream_t)stream));
+}
+
+}  // extern "C"

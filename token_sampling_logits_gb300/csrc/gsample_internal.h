@@ -124,6 +124,47 @@ int filter_max_cluster(int dtype, bool vec);
 size_t filter_smem_limit();
 cudaError_t launch_filter(const FilterParams& p, int dtype, bool vec, cudaStream_t stream);
 
+// The draw from a row's top-k / top-p / min-p set with the caller's random
+// number, and the verification of drafts (sets != nullptr): settings per row,
+// or per request there.
+struct RowSet;
+struct DrawParams {
+  const char* logits;
+  int64_t ld_bytes;
+  int64_t B;
+  int32_t V;
+  int32_t units_per_row;
+  int32_t cluster;
+  int32_t units_per_cta;
+  int32_t fraction_bits;  // F: weights are in units of 2^-F, a row's sum below 2^63
+  int32_t n;              // requests
+  const float* temperature;
+  const int32_t* top_k;  // nullptr: no top-k
+  const float* top_p;    // nullptr: no top-p
+  const float* min_p;    // nullptr: no min-p
+  const float* uniform;
+  int64_t* out_idx;
+  float* out_logprob;  // nullptr: not wanted
+  // verification
+  const float* uniform_draw;
+  const int64_t* offsets;
+  const int64_t* draft;
+  const float* probs;  // nullptr: drafts without probabilities
+  int64_t probs_ld;
+  RowSet* sets;
+  int32_t* out_count;
+};
+void* draw_kernel(int dtype, bool vec, bool resident, int* threads);
+void* verify_kernel(int dtype, bool vec, bool resident, int* threads);
+void* verify_draw_kernel_fn(int dtype, bool vec, bool resident, int* threads);
+size_t draw_smem_limit();
+int draw_max_cluster(int dtype, bool vec);
+cudaError_t launch_draw(const DrawParams& p, int dtype, bool vec, cudaStream_t stream);
+cudaError_t launch_verify_draw(const DrawParams& p, int dtype, bool vec, cudaStream_t stream);
+
+cudaError_t launch_debug_weights(const float* x, int64_t n, float M, float T, uint64_t* out,
+                                 cudaStream_t stream);
+
 // Elements per unit for a dtype code (0 f32, 1 bf16, 2 f16) and load path.
 inline int units_elems(int dtype, bool vec) { return vec ? (dtype == 0 ? 4 : 8) : 4; }
 
@@ -214,12 +255,48 @@ cudaError_t launch_process(ProcessParams p, int dtype, int out_dtype, int sms,
 gsample_status check_logits(const void* logits, gsample_dtype dtype, int64_t B, int64_t V,
                             int64_t ld);
 gsample_status current_device_sms(int* sms);
+// For a kernel with one cluster per row: the cluster size for B rows of nu
+// units (may throw: the occupancies are kept in a map), and the load path.
+int plan_row_cluster(void* (*kernel)(int, bool, bool, int*), int dtype, bool vec, int64_t B,
+                     int64_t nu, int max_cluster, int64_t min_units, size_t smem_limit);
+bool wide_rows(const void* logits, gsample_dtype dtype, int64_t ld);
 // The sampler of gsample_gumbel_argmax (its checks, plan and launch), drawing
 // from constrained logits.
 gsample_status sample_constrained(const void* logits, gsample_dtype dtype, int64_t B, int64_t V,
                                   int64_t ld, const float* temperature, const uint64_t* seed,
                                   const uint64_t* offset, const ConstrainArgs& con,
                                   int64_t* out_idx, void* workspace, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// Pages of a paged cache (gsample_pages.cu)
+// ---------------------------------------------------------------------------
+struct PageArgs {
+  int32_t* table;
+  int32_t* length;
+  int32_t* free_list;
+  int32_t* free_count;
+  int64_t rows, ld, pages;
+  int32_t page_size;
+};
+struct ExtendArgs {
+  const int32_t* slot;
+  const int64_t* offsets;
+  int64_t n, total;
+  int32_t* out_start;
+  int64_t* out_slot_map;
+  int32_t* out_length;
+  int32_t* out_table;
+  int64_t table_cols, table_ld;
+  int32_t map_ctas;  // set by the launch
+};
+struct TrimArgs {
+  const int32_t* slot;
+  int64_t n;
+  const int32_t* start;
+  const int32_t* keep;
+};
+cudaError_t launch_pages_extend(const PageArgs& s, ExtendArgs a, int sms, cudaStream_t stream);
+cudaError_t launch_pages_trim(const PageArgs& s, const TrimArgs& a, cudaStream_t stream);
 
 cudaError_t launch_debug_philox(uint64_t seed, uint32_t row, uint64_t offset, int64_t group0,
                                 int64_t n, uint32_t* out, cudaStream_t stream);
