@@ -608,9 +608,8 @@ gsample_status current_device_sms(int* sms) {
   return st;
 }
 
-int plan_row_cluster(void* (*kernel)(int, bool, bool, int*), int dtype, bool vec, int64_t B,
-                     int64_t nu, int max_cluster, int64_t min_units, size_t smem_limit) {
-  return pick_cluster(kernel, dtype, vec, B, nu, max_cluster, min_units, smem_limit);
+int clusters_at_once(void* fn, int threads, int cluster, size_t smem) {
+  return active_clusters(fn, threads, cluster, smem);
 }
 
 bool wide_rows(const void* logits, gsample_dtype dtype, int64_t ld) {

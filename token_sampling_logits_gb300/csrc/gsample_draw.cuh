@@ -1,0 +1,1289 @@
+// The draw from a row's top-k / top-p / min-p set with the caller's random
+// number, and the verification of speculative drafts by the same sets.
+//
+// The set K of a row is a prefix of its candidates (logits that are neither
+// NaN nor -inf) in the order (logit descending, index ascending): it ends at
+// the first of top_k elements, of the shortest prefix whose softmax mass
+// reaches top_p, and of the elements of at least min_p times the largest
+// probability. The draw is the inverse CDF over K in index order.
+//
+// Layout: one thread-block cluster per row, each CTA holding its slice of the
+// row in shared memory, each warp a run of it, so that ranks, warps, lanes and
+// units follow the index order. After the row maximum a row takes the first of
+// these ways that settles it:
+//   - one element only (greedy, +inf, nothing): the lowest index of the maximum;
+//   - short sets: one sweep lists the elements within 16 powers of two of the
+//     maximum (a few dozen to a few hundred of a language model's row), in
+//     index order, and sums the rest's weights in binary32 (top_p only, with a
+//     bound on its error); rank 0 gathers the lists, finds K's end with exact
+//     weights and draws. Not settled when a list runs over, K reaches past it or
+//     the bound leaves K's end open.
+//   - long sets: a histogram of the logits in 4096 equal steps brackets K's
+//     end; one sweep forms the exact weights of all, sums those above the
+//     bracket and lists those in it; rank 0 finds K's end; the draw is by the
+//     warps' sums.
+//   - the rest (very many equal logits at K's end): a radix select over
+//     order-preserving keys with counts and exact masses, eight bits a level.
+// Without a filter (or with min_p alone) the sweep of exact weights is all.
+// All sums but the bounded one are integers (gsample_weights.cuh), so the
+// result does not depend on the way taken, the order of any atomic or the
+// split of the row. The only waits are hardware barriers.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include <climits>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+
+#include "gsample_internal.h"
+#include "gsample_slice.cuh"
+#include "gsample_weights.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace gsample {
+namespace {
+
+using namespace slice;
+
+constexpr int kDrawThreads = 512;
+constexpr int kDrawWarps = kDrawThreads / 32;
+constexpr int kDrawMaxCluster = 16;
+constexpr int kMaxSegments = kDrawMaxCluster * kDrawWarps;
+constexpr int kWarpList = 64;                 // entries of a warp's list
+constexpr int kCtaList = kWarpList * kDrawWarps;
+constexpr int kRowList = 1280;                // entries of a row's list, at rank 0
+constexpr int kListBins = 512;
+constexpr int kLastBin = 384;                 // entries of a list's bin that are ranked
+constexpr int kBins = 4096;                   // steps of the histogram
+
+using u64 = unsigned long long;
+
+template <int DT>
+__device__ __forceinline__ float logit_at(const char* row, int64_t i) {
+  if constexpr (DT == 0) {
+    return __ldg(reinterpret_cast<const float*>(row) + i);
+  } else {
+    return half_to_f32<DT>(__ldg(reinterpret_cast<const unsigned short*>(row) + i));
+  }
+}
+
+// Order-preserving keys in the bits that the logit's dtype can set.
+template <int DT>
+struct KeyBits {
+  static constexpr int kZB = DT == 1 ? 16 : (DT == 2 ? 13 : 0);
+};
+
+template <int DT>
+__device__ __forceinline__ uint32_t key_of_short(uint32_t s) {
+  constexpr int ZB = KeyBits<DT>::kZB;
+  if constexpr (ZB == 0) {
+    return s;
+  } else {
+    const uint32_t k = s << ZB;
+    return (k & 0x80000000u) ? k : (k | ((1u << ZB) - 1u));
+  }
+}
+
+__device__ __forceinline__ float logit_of_key(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key);
+}
+
+struct Ranked {  // an element of the bin that K ends in
+  u64 w;
+  uint32_t key, idx;
+};
+
+struct DrawShared {
+  float2 table[kExp2Entries];
+  u64 sums[2][kMaxSegments];      // the warps' sums of the whole cluster (two buffers)
+  float wmax[kMaxSegments];       // their maxima; then, at rank 0, offsets of their lists
+  unsigned count[kMaxSegments];   // at rank 0: the lengths of their lists
+  union {
+    unsigned hist[kBins];
+    struct {
+      uint2 list[kRowList];  // logit bits and index
+      union {
+        struct {
+          u64 mass[kListBins];
+          unsigned count[kListBins];
+        } bin;
+        Ranked last[kLastBin];
+      };
+    } row;
+    struct {
+      u64 mass[2][256];  // a level of the radix select (two buffers)
+      unsigned count[2][256];
+    } digit;
+  };
+  uint2 own[kCtaList];  // this CTA's lists
+  u64 scan_m[kDrawWarps];
+  float scan_f[kDrawWarps];
+  unsigned scan_c[kDrawWarps];
+  int sel[4];
+  unsigned above_c, all_c;
+  u64 above_m, all_m;
+  double floor_step;     // T ln(min_p)
+  int32_t found;         // written by the CTA that finds an index
+  int32_t request;
+  unsigned own_n;
+  // K's end, written by rank 0
+  int32_t settled;
+  uint32_t key;
+  int32_t last;
+  u64 sum;
+};
+
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_barrier() {
+  cluster_arrive();
+  cluster_wait();
+}
+
+// The address of this CTA's shared variable in CTA `rank` of the cluster.
+template <typename T>
+__device__ __forceinline__ T* peer(T* p, int rank) {
+  return cg::this_cluster().map_shared_rank(p, rank);
+}
+
+// One row's work within its cluster: the slice of this CTA and how to read it.
+template <int DT, bool VEC, bool RESIDENT>
+struct RowCtx {
+  using C = HCfg<DT, VEC>;
+  static constexpr int EPU = C::kEPU;
+  static constexpr int kFlush = 256 / EPU;  // units between joins of a WeightSum
+  const char* row;
+  int32_t V, u_lo, u_hi;
+  uint32_t slice;
+  int rank, nrank, warp, lane;
+  int32_t w_lo, w_hi;  // units of this warp
+
+  __device__ __forceinline__ void place(const DrawParams& p, int64_t b, void* smem) {
+    row = p.logits + b * p.ld_bytes;
+    V = p.V;
+    u_lo = min(p.units_per_row, rank * p.units_per_cta);
+    u_hi = min(p.units_per_row, u_lo + p.units_per_cta);
+    slice = smem_addr(smem);
+    const int32_t n = u_hi - u_lo, per = (n + kDrawWarps - 1) / kDrawWarps;
+    w_lo = u_lo + min(n, warp * per);
+    w_hi = u_lo + min(n, (warp + 1) * per);
+  }
+
+  // The warp that holds element i of this CTA's slice.
+  __device__ __forceinline__ int warp_of(int32_t i) const {
+    const int32_t per = (u_hi - u_lo + kDrawWarps - 1) / kDrawWarps;
+    return (i / EPU - u_lo) / per;
+  }
+
+  __device__ __forceinline__ uint4 unit(int32_t u) const {
+    if constexpr (RESIDENT) {
+      return lds128(slice + (uint32_t)(u - u_lo) * 16u);
+    } else {
+      if constexpr (VEC) {
+        if ((u + 1) * EPU <= V) return __ldg(reinterpret_cast<const uint4*>(row) + u);
+      }
+      return load_unit<DT, VEC>(row, u, V, 0ull);
+    }
+  }
+
+  static __device__ __forceinline__ float element(const uint4& r, int e) {
+    return elt<DT, VEC>(r, e);
+  }
+
+  // The largest element of a unit (NaN only where all are).
+  static __device__ __forceinline__ float largest(const uint4& r) {
+    if constexpr (C::kF32Bits) {
+      return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
+                   fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+    } else {
+      uint32_t m;
+      if constexpr (DT == 1)
+        asm("{.reg .b32 a, b;\n max.bf16x2 a, %1, %2;\n max.bf16x2 b, %3, %4;\n max.bf16x2 %0, a, b;}"
+            : "=r"(m) : "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w));
+      else
+        asm("{.reg .b32 a, b;\n max.f16x2 a, %1, %2;\n max.f16x2 b, %3, %4;\n max.f16x2 %0, a, b;}"
+            : "=r"(m) : "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w));
+      return fmaxf(half_to_f32<DT>(m & 0xFFFFu), half_to_f32<DT>(m >> 16));
+    }
+  }
+
+  // f(x, i) on every element of this thread's units, in index order.
+  template <typename F>
+  __device__ __forceinline__ void each(F&& f) const {
+    for (int32_t u = w_lo + lane; u < w_hi; u += 32) {
+      const uint4 r = unit(u);
+#pragma unroll
+      for (int e = 0; e < EPU; ++e) f(element(r, e), u * EPU + e);
+    }
+  }
+
+  // f(x0, x1, i) on every pair of neighbours; g() after every kFlush units.
+  template <typename F, typename G>
+  __device__ __forceinline__ void each_pair(F&& f, G&& g) const {
+    int n = 0;
+    for (int32_t u = w_lo + lane; u < w_hi; u += 32) {
+      const uint4 r = unit(u);
+#pragma unroll
+      for (int e = 0; e < EPU; e += 2) f(element(r, e), element(r, e + 1), u * EPU + e);
+      if (++n == kFlush) {
+        g(kFlush * EPU);
+        n = 0;
+      }
+    }
+    g(n * EPU);
+  }
+};
+
+__device__ __forceinline__ u64 warp_sum(u64 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// The row's sum of v and what of it lies in the warps before this one; `own`
+// is this warp's. `buf` alternates between calls: a warp may still read one
+// call's sums while another writes the next one's.
+struct Sum {
+  u64 before, own, all;
+};
+template <typename Row>
+__device__ __forceinline__ Sum cluster_sum(u64 v, const Row& r, DrawShared& sh, int buf) {
+  Sum s;
+  s.own = warp_sum(v);
+  if (r.lane < r.nrank) *peer(&sh.sums[buf][r.rank * kDrawWarps + r.warp], r.lane) = s.own;
+  cluster_barrier();
+  const int n = r.nrank * kDrawWarps, at = r.rank * kDrawWarps + r.warp;
+  u64 all = 0ull, before = 0ull;
+  for (int q = r.lane; q < n; q += 32) {
+    const u64 t = sh.sums[buf][q];
+    all += t;
+    if (q < at) before += t;
+  }
+  s.all = warp_sum(all);
+  s.before = warp_sum(before);
+  return s;
+}
+
+// Of the row's weights with sum s: the warp whose run holds the element at which
+// the cumulative weight passes `target` (< s.all) calls done(index, x) in one
+// thread.
+template <typename Row, typename W, typename Done>
+__device__ __forceinline__ void find_index(const Row& r, const Sum& s, u64 target, W&& weight,
+                                           Done&& done) {
+  if (target < s.before || target - s.before >= s.own) return;
+  u64 left = target - s.before;
+#pragma unroll 1
+  for (int32_t u0 = r.w_lo; u0 < r.w_hi; u0 += 32) {
+    const int32_t u = u0 + r.lane;
+    u64 own = 0ull;
+    uint4 q = make_uint4(0u, 0u, 0u, 0u);
+    if (u < r.w_hi) {
+      q = r.unit(u);
+#pragma unroll 1
+      for (int e = 0; e < Row::EPU; ++e) own += weight(Row::element(q, e), u * Row::EPU + e);
+    }
+    u64 incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (r.lane >= o) incl += t;
+    }
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, incl > left);
+    if (hit) {
+      if (r.lane == __ffs(hit) - 1) {
+        u64 c = incl - own;
+#pragma unroll 1
+        for (int e = 0; e < Row::EPU; ++e) {
+          const float x = Row::element(q, e);
+          c += weight(x, u * Row::EPU + e);
+          if (c > left) {
+            done(u * Row::EPU + e, x);
+            break;
+          }
+        }
+      }
+      return;
+    }
+    left -= __shfl_sync(0xFFFFFFFFu, incl, 31);
+  }
+}
+
+// The row's sum of the weights of the elements from `lowest` up.
+template <typename Row>
+__device__ __forceinline__ u64 sum_from(const Row& r, const WeightRow& w, uint32_t table,
+                                        float lowest) {
+  u64 sum = 0ull;
+  WeightSum part;
+  r.each_pair(
+      [&](float x0, float x1, int32_t) {
+        int32_t h[2], l[2];
+        weight_bits(x0 >= lowest ? x0 : -INFINITY, x1 >= lowest ? x1 : -INFINITY, w, table, h, l);
+        part.add(h, l);
+      },
+      [&](int n) { sum += part.take((uint32_t)n); });
+  return sum;
+}
+
+// Inclusive scan over the CTA of one count and one mass a thread.
+__device__ __forceinline__ void cta_scan(unsigned& c, u64& m, DrawShared& sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned tc = __shfl_up_sync(0xFFFFFFFFu, c, o);
+    const u64 tm = __shfl_up_sync(0xFFFFFFFFu, m, o);
+    if (lane >= o) {
+      c += tc;
+      m += tm;
+    }
+  }
+  if (lane == 31) {
+    sh.scan_c[warp] = c;
+    sh.scan_m[warp] = m;
+  }
+  __syncthreads();
+  unsigned bc = lane < warp ? sh.scan_c[lane] : 0u;
+  u64 bm = lane < warp ? sh.scan_m[lane] : 0ull;
+  c += __reduce_add_sync(0xFFFFFFFFu, bc);
+  m += warp_sum(bm);
+  __syncthreads();
+}
+
+// Thread t < 256 holds the totals (c, m) of digit 255 - t. The first digit from
+// the top at which the cumulative count reaches k_rem or the cumulative mass
+// m_rem (both at least 1), or -1; sh.above_* get the totals above it, sh.all_*
+// those of all digits. Called by every thread; ends with a barrier.
+__device__ __forceinline__ int find_digit(unsigned c, u64 m, unsigned k_rem, u64 m_rem,
+                                          DrawShared& sh) {
+  if (threadIdx.x == 0) sh.sel[0] = kDrawThreads;
+  unsigned ic = c;
+  u64 im = m;
+  cta_scan(ic, im, sh);
+  if (threadIdx.x < 256 &&
+      ((ic - c < k_rem && k_rem <= ic) || (im - m < m_rem && m_rem <= im)))
+    atomicMin(&sh.sel[0], (int)threadIdx.x);
+  __syncthreads();
+  const int at = sh.sel[0];
+  if ((int)threadIdx.x == at) {
+    sh.above_c = ic - c;
+    sh.above_m = im - m;
+  }
+  if (threadIdx.x == 255) {
+    sh.all_c = ic;
+    sh.all_m = im;
+  }
+  __syncthreads();
+  return at < 256 ? 255 - at : -1;
+}
+
+// The request whose row `b` is, written to sh.request (-1: none; the lowest
+// where malformed offsets give several).
+__device__ __forceinline__ int32_t find_request(const int64_t* offsets, int32_t n, int64_t b,
+                                                DrawShared& sh) {
+  if (threadIdx.x == 0) sh.request = INT32_MAX;
+  __syncthreads();
+  for (int32_t i = threadIdx.x; i < n; i += kDrawThreads)
+    if (__ldcg(offsets + i) <= b && b < __ldcg(offsets + i + 1)) atomicMin(&sh.request, i);
+  __syncthreads();
+  return sh.request == INT32_MAX ? -1 : sh.request;
+}
+
+// The lowest index of an element equal to M.
+template <typename Row>
+__device__ __forceinline__ int32_t first_equal(const Row& r, float M, DrawShared& sh) {
+  int32_t best = INT32_MAX;
+  for (int32_t u = r.w_lo + r.lane; u < r.w_hi && best == INT32_MAX; u += 32) {
+    const uint4 q = r.unit(u);
+    if (Row::largest(q) == M) {
+#pragma unroll
+      for (int e = Row::EPU - 1; e >= 0; --e)
+        if (Row::element(q, e) == M) best = u * Row::EPU + e;
+    }
+  }
+  best = __reduce_min_sync(0xFFFFFFFFu, best);
+  if (r.lane < r.nrank)
+    *peer(&sh.count[r.rank * kDrawWarps + r.warp], r.lane) = (unsigned)best;
+  cluster_barrier();
+  int32_t all = INT32_MAX;
+  for (int q = r.lane; q < r.nrank * kDrawWarps; q += 32) all = min(all, (int32_t)sh.count[q]);
+  return __reduce_min_sync(0xFFFFFFFFu, all);
+}
+
+// What K is cut by: the first `k` elements; those with less than m before
+// them, m somewhere in [m_lo, m_hi]; the logits from `floor` up.
+struct Cut {
+  unsigned k;
+  u64 m_lo, m_hi;
+  float floor;
+};
+
+// The CTA's lists as one, in their order, in rank 0's sh.row.list: `n_seg` lists
+// with lengths sh.count[], list s at own + (s % per) * stride of rank s / per.
+// Returns the number of entries, or -1 where a list or the whole runs over.
+__device__ __forceinline__ int gather(DrawShared& sh, int n_seg, int per, int stride) {
+  const int tid = threadIdx.x;
+  unsigned* off = reinterpret_cast<unsigned*>(sh.wmax);
+  unsigned c = tid < n_seg ? sh.count[tid] : 0u;
+  const bool bad = c > (unsigned)stride;
+  unsigned incl = bad ? 0u : c;
+  u64 none = 0ull;
+  cta_scan(incl, none, sh);
+  if (tid < n_seg) off[tid] = incl - (bad ? 0u : c);
+  if (tid == kDrawThreads - 1) sh.all_c = incl;
+  if (__syncthreads_or(bad ? 1 : 0) || sh.all_c > (unsigned)kRowList) return -1;
+  const int n = (int)sh.all_c;
+  for (int g = tid; g < n; g += kDrawThreads) {
+    int lo = 0, hi = n_seg;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (off[mid] <= (unsigned)g)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    sh.row.list[g] = peer(sh.own, lo / per)[(lo % per) * stride + (g - (int)off[lo])];
+  }
+  __syncthreads();
+  return n;
+}
+
+// Rank 0, on the n entries of sh.row.list, which are in [x_lo, x_hi] and come
+// after above_c elements of mass above_m: where K ends, in sh.key, sh.last and
+// sh.sum. False: it cannot be told. `complete`: the list holds all elements that
+// the floor leaves. Every thread calls it; w[] are the weights of its entries
+// (threadIdx.x * per + i).
+__device__ __forceinline__ bool settle(DrawShared& sh, int n, int per, const u64 (&w)[3],
+                                       unsigned above_c, u64 above_m, const Cut& cut, float x_lo,
+                                       float x_hi, bool complete) {
+  const int tid = threadIdx.x;
+  const float step = (float)(kListBins - 1) / (x_hi - x_lo);
+  auto bin_of = [&](float x) {
+    return max(0, min(kListBins - 1, (int)((x_hi - x) * step)));
+  };
+  sh.row.bin.mass[tid] = 0ull;
+  sh.row.bin.count[tid] = 0u;
+  if (tid == 0) {
+    sh.sel[0] = kListBins;
+    sh.sel[1] = 0;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int j = tid * per + i;
+    if (i < per && j < n) {
+      const int b = bin_of(__uint_as_float(sh.row.list[j].x));
+      atomicAdd(&sh.row.bin.count[b], 1u);
+      atomicAdd(&sh.row.bin.mass[b], w[i]);
+    }
+  }
+  __syncthreads();
+  const unsigned c = sh.row.bin.count[tid];
+  const u64 m = sh.row.bin.mass[tid];
+  unsigned ic = c;
+  u64 im = m;
+  cta_scan(ic, im, sh);
+  if (above_c + ic >= cut.k || above_m + im >= cut.m_lo) atomicMin(&sh.sel[0], tid);
+  if (tid == kListBins - 1) sh.all_m = above_m + im;
+  __syncthreads();
+  const int at = sh.sel[0];
+  if (at == kListBins) {  // K takes the whole list
+    if (tid == 0) {
+      sh.key = ordered_bits(x_lo);
+      sh.last = INT32_MAX;
+      sh.sum = sh.all_m;
+    }
+    __syncthreads();
+    return complete;
+  }
+  if (tid == at) {
+    sh.above_c = above_c + ic - c;
+    sh.above_m = above_m + im - m;
+    sh.all_c = c;
+  }
+  __syncthreads();
+  const unsigned in_bin = sh.all_c, before_c = sh.above_c;
+  const u64 before_m = sh.above_m;
+  if (in_bin > (unsigned)kLastBin) return false;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int j = tid * per + i;
+    if (i < per && j < n) {
+      const uint2 q = sh.row.list[j];
+      const float x = __uint_as_float(q.x);
+      if (bin_of(x) == at) {
+        Ranked e;
+        e.w = w[i];
+        e.key = ordered_bits(x);
+        e.idx = q.y;
+        sh.row.last[atomicAdd(&sh.sel[1], 1)] = e;
+      }
+    }
+  }
+  __syncthreads();
+  // K is a prefix of the bin's elements too: its last one has as many before it
+  // as there are others in K.
+  bool in = false;
+  unsigned rank = 0u;
+  u64 mass = before_m;
+  Ranked e{0ull, 0u, 0u};
+  if (tid < (int)in_bin) {
+    e = sh.row.last[tid];
+    for (unsigned j = 0; j < in_bin; ++j) {
+      const Ranked o = sh.row.last[j];
+      if (o.key > e.key || (o.key == e.key && o.idx < e.idx)) {
+        ++rank;
+        mass += o.w;
+      }
+    }
+    in = before_c + rank < cut.k && mass < cut.m_lo;
+  }
+  const unsigned taken = (unsigned)__syncthreads_count(in ? 1 : 0);
+  if (in && rank + 1u == taken) {
+    sh.key = e.key;
+    sh.last = (int32_t)e.idx;
+    sh.sum = mass + e.w;
+  }
+  __syncthreads();
+  // cut by the mass: the next element must be out for every m in question
+  return before_c + taken >= cut.k || sh.sum >= cut.m_hi;
+}
+
+// VERIFY: the row's set goes to p.sets[b], with the outcome of its draft's
+// test. Otherwise the draw is made and written.
+template <int DT, bool VEC, bool RESIDENT, bool VERIFY>
+__global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawParams p) {
+  using Row = RowCtx<DT, VEC, RESIDENT>;
+  constexpr int EPU = Row::EPU;
+  constexpr int ZB = KeyBits<DT>::kZB;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ DrawShared sh;
+  const int tid = threadIdx.x;
+
+  cluster_arrive();  // waited for before the first write to another CTA
+  Row r;
+  r.rank = (int)cg::this_cluster().block_rank();
+  r.nrank = p.cluster;
+  r.warp = tid >> 5;
+  r.lane = tid & 31;
+  const int64_t b = blockIdx.x / r.nrank;
+  if (tid < kExp2Entries) sh.table[tid] = exp2_entry(tid);
+  if (tid == 0) sh.own_n = 0u;
+  r.place(p, b, smem);
+  pdl_wait_then_release();
+
+  // The slice, in four parts, so that the maximum is formed as they arrive.
+  const int32_t units = max(0, (r.w_hi - r.w_lo - r.lane + 31) / 32);
+  const int32_t part = ((r.w_hi - r.w_lo + 31) / 32 + 3) / 4;
+  if constexpr (RESIDENT) {
+    const uint64_t pol = evict_first_policy();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      for (int32_t j = c * part; j < min(units, (c + 1) * part); ++j) {
+        const int32_t u = r.w_lo + r.lane + 32 * j;
+        const uint32_t dst = r.slice + (uint32_t)(u - r.u_lo) * 16u;
+        if (VEC && (u + 1) * EPU <= p.V)
+          cp_async16(dst, r.row + (size_t)u * 16, pol);
+        else
+          sts128(dst, load_unit<DT, VEC>(r.row, u, p.V, pol));
+      }
+      cp_async_commit();
+    }
+  }
+  // the settings of the row, or of its request
+  int64_t s = b;
+  if constexpr (VERIFY) s = find_request(p.offsets, p.n, b, sh);
+  const bool owned = s >= 0;  // the same in every CTA of the cluster
+  const float T = owned ? __ldcg(p.temperature + s) : 0.0f;
+  int32_t top_k = owned && p.top_k ? __ldcg(p.top_k + s) : 0;
+  const float top_p = owned && p.top_p ? __ldcg(p.top_p + s) : 1.0f;
+  const float min_p = owned && p.min_p ? __ldcg(p.min_p + s) : 0.0f;
+  const bool p_on = top_p < 1.0f && top_p > 0.0f;  // NaN: off
+  if (top_p <= 0.0f) top_k = 1;
+  const bool k_on = top_k >= 1;
+  const bool m_on = min_p > 0.0f && T > 0.0f && T < INFINITY;
+  if (m_on && tid == kDrawThreads - 1)
+    sh.floor_step = min_p < 1.0f ? (double)T * log((double)min_p) : 0.0;
+
+  // The largest logit (NaN counts as -inf).
+  float M = -INFINITY;
+  if constexpr (RESIDENT) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      cp_async_wait_upto(3 - c);
+      for (int32_t j = c * part; j < min(units, (c + 1) * part); ++j)
+        M = fmaxf(M, Row::largest(r.unit(r.w_lo + r.lane + 32 * j)));
+    }
+  } else {
+    for (int32_t j = 0; j < units; ++j)
+      M = fmaxf(M, Row::largest(r.unit(r.w_lo + r.lane + 32 * j)));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+  cluster_wait();  // every CTA of the cluster runs
+  if (!owned) return;
+  if (r.lane < r.nrank) *peer(&sh.wmax[r.rank * kDrawWarps + r.warp], r.lane) = M;
+  cluster_barrier();
+  for (int q = r.lane; q < r.nrank * kDrawWarps; q += 32) M = fmaxf(M, sh.wmax[q]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+
+  RowSet set;
+  set.sum = 1ull;
+  set.M = M;
+  set.key = 0u;
+  set.last = -1;
+  set.kind = kNothing;
+  set.accepted = 0;
+  set.request = (int32_t)s;
+  int buf = 0;
+  bool drawn = VERIFY;
+  if (M == -INFINITY) {
+    // no candidate
+  } else if (!(T > 0.0f) || M == INFINITY) {
+    // Greedy, or +inf takes all the mass.
+    set.kind = kOne;
+    set.last = first_equal(r, M, sh);
+  } else {
+    const WeightRow w = weight_row(M, T, p.drop);
+    const uint32_t table = smem_addr(sh.table);
+    // The lowest logit that K may hold: min_p's, and no element whose weight is
+    // zero, which is never drawn.
+    float floor_x = w.lowest;
+    if (m_on) {
+      // the smallest binary32 number from M + T ln(min_p) up
+      const double d = sh.floor_step;
+      const float dh = (float)d, dl = (float)(d - (double)dh);
+      float f = M + dh;
+      const float bb = f - M;
+      const float rest = ((M - (f - bb)) + (dh - bb)) + dl;
+      if (rest > 0.0f && f < M)
+        f = __int_as_float(__float_as_int(f) + (f > 0.0f ? 1 : f < 0.0f ? -1 : 0));
+      if (rest > 0.0f && f == 0.0f) f = 1.40129846e-45f;
+      floor_x = fminf(fmaxf(floor_x, f), M);
+    }
+    const uint32_t floor_key = ordered_bits(floor_x);
+    set.kind = kSet;
+    set.key = floor_key;
+    set.last = INT32_MAX;
+    set.sum = 0ull;
+    Cut cut;
+    cut.k = k_on ? (unsigned)top_k : 0xFFFFFFFFu;
+    cut.m_lo = cut.m_hi = ULLONG_MAX;
+    cut.floor = floor_x;
+    const u64 p_part = fraction_of(top_p);
+    bool settled = false;
+
+    if ((k_on || p_on || m_on) && !w.shift) {
+      // Short sets.
+      const float x_lo = fmaxf(floor_x, fmaf(-11.0903549f, T, M));  // 16 powers of two
+      const bool tails = p_on;
+      float tail = 0.0f;
+      unsigned mine = 0u;
+#pragma unroll 2
+      for (int32_t u0 = r.w_lo; u0 < r.w_hi; u0 += 32) {
+        const int32_t u = u0 + r.lane;
+        const bool valid = u < r.w_hi;
+        uint4 q = make_uint4(0u, 0u, 0u, 0u);
+        if (valid) q = r.unit(u);
+        const bool hit = valid && Row::largest(q) >= x_lo;
+        if (tails && valid) {
+          float t[EPU];
+#pragma unroll
+          for (int e = 0; e < EPU; ++e) {
+            const float x = Row::element(q, e);
+            t[e] = ex2_approx(fmaf(x, w.rh, -w.c));
+            if (hit && x >= x_lo) t[e] = 0.0f;
+          }
+#pragma unroll
+          for (int o = EPU / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int e = 0; e < o; ++e) t[e] += t[e + o];
+          tail += t[0];
+        }
+        if (__ballot_sync(0xFFFFFFFFu, hit)) {
+          unsigned c = 0u;
+          if (hit) {
+#pragma unroll
+            for (int e = 0; e < EPU; ++e) c += Row::element(q, e) >= x_lo ? 1u : 0u;
+          }
+          unsigned incl = c;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const unsigned t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (r.lane >= o) incl += t;
+          }
+          unsigned at = mine + incl - c;
+          if (hit) {
+#pragma unroll
+            for (int e = 0; e < EPU; ++e) {
+              const float x = Row::element(q, e);
+              if (x >= x_lo) {
+                if (at < (unsigned)kWarpList)
+                  sh.own[r.warp * kWarpList + at] =
+                      make_uint2(__float_as_uint(x), (uint32_t)(u * EPU + e));
+                ++at;
+              }
+            }
+          }
+          mine += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        }
+      }
+      // a NaN among the logits ends up in the tail: the list does not count then
+      const bool odd = __any_sync(0xFFFFFFFFu, !(tail >= 0.0f));
+      const u64 t = warp_sum(odd ? 0ull : __float2ull_rn(tail * 17592186044416.0f));
+      if (r.lane == 0) {
+        const int at = r.rank * kDrawWarps + r.warp;
+        *peer(&sh.count[at], 0) = odd ? 0xFFFFFFFFu : mine;
+        *peer(&sh.sums[buf][at], 0) = t;
+      }
+      cluster_barrier();
+      bool ok = false;
+      if (r.rank == 0) {
+        const int n = gather(sh, r.nrank * kDrawWarps, kDrawWarps, kWarpList);
+        if (n >= 0) {
+          const int per = (n + kDrawThreads - 1) / kDrawThreads;
+          u64 we[3] = {0ull, 0ull, 0ull}, own = 0ull;
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const int j = tid * per + i;
+            if (i < per && j < n) we[i] = weight_of(__uint_as_float(sh.row.list[j].x), w, table);
+            own += we[i];
+          }
+          u64 incl = own;
+          unsigned none = 0u;
+          cta_scan(none, incl, sh);
+          if (tid == kDrawThreads - 1) sh.all_m = incl;
+          __syncthreads();
+          const u64 listed = sh.all_m;
+          if (p_on) {
+            u64 rest = 0ull;
+            for (int q = r.lane; q < r.nrank * kDrawWarps; q += 32) rest += sh.sums[buf][q];
+            rest = warp_sum(rest);
+            // The binary32 tail: y is rounded to 2^-20 of 64 and its factor r to
+            // 2^-25 of |C| + 64, ex2 to 2^-22, the sums to 2^-24 a step; the fixed-point
+            // weights to half a unit each.
+            const float rel = (fabsf(w.c) + 192.0f + (float)part * 4.0f) * 5.9604645e-8f;
+            const u64 err = __float2ull_ru((float)rest * rel) + (u64)p.V;
+            cut.m_lo = ceil_part(p_part, listed + rest - min(rest, err));
+            cut.m_hi = ceil_part(p_part, listed + rest + err);
+            if (cut.m_lo < 1ull) cut.m_lo = 1ull;
+          }
+          const bool complete = x_lo == floor_x;
+          if (k_on || p_on) {
+            ok = settle(sh, n, per, we, 0u, 0ull, cut, x_lo, M, complete);
+          } else {
+            if (tid == 0) {
+              sh.key = floor_key;
+              sh.last = INT32_MAX;
+              sh.sum = listed;
+            }
+            __syncthreads();
+            ok = complete;
+          }
+          if (ok && !VERIFY) {
+            // The draw, in the list's order, which is the indices'.
+            const uint32_t key = sh.key;
+            const int32_t last = sh.last;
+            const u64 sum = sh.sum;
+            u64 kept = 0ull;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+              const int j = tid * per + i;
+              if (i < per && j < n) {
+                const uint2 q = sh.row.list[j];
+                const uint32_t kj = ordered_bits(__uint_as_float(q.x));
+                if (kj < key || (kj == key && (int32_t)q.y > last)) we[i] = 0ull;
+              }
+              kept += we[i];
+            }
+            const u64 target = __umul64hi(fraction_of(__ldcg(p.uniform + b)), sum);
+            u64 end = kept;
+            cta_scan(none, end, sh);
+            u64 c = end - kept;
+            if (target >= c && target < end) {
+#pragma unroll
+              for (int i = 0; i < 3; ++i) {
+                if (target >= c && target < c + we[i]) {
+                  const int j = tid * per + i;
+                  p.out_idx[b] = (int64_t)sh.row.list[j].y;
+                  if (p.out_logprob)
+                    p.out_logprob[b] = (float)log((double)we[i] / (double)sum);
+                }
+                c += we[i];
+              }
+            }
+          }
+        }
+        if (tid < r.nrank) *peer(&sh.settled, tid) = ok ? 1 : 0;
+      }
+      cluster_barrier();
+      settled = sh.settled != 0;
+      buf ^= 1;
+      if (settled) {
+        drawn = true;
+        if (VERIFY && r.rank == 0) {
+          set.key = sh.key;
+          set.last = sh.last;
+          set.sum = sh.sum;
+        }
+      }
+    }
+
+    Sum sums{0ull, 0ull, 0ull};  // of K's weights
+    bool summed = false;
+    if (!settled && !(k_on || p_on)) {
+      sums = cluster_sum(sum_from(r, w, table, floor_x), r, sh, buf);
+      set.sum = sums.all;
+      buf ^= 1;
+      settled = summed = true;
+    }
+
+    if (!settled) {
+      // Long sets. The histogram's steps run down 24 powers of two, or to the floor.
+      const float low = fmaxf(floor_x, fmaf(-16.6355324f, T, M));
+      const float step = (float)(kBins - 1) / (M - low);
+      for (int j = tid; j < kBins; j += kDrawThreads) sh.hist[j] = 0u;
+      __syncthreads();
+      r.each([&](float x, int32_t) {
+        if (x >= floor_x)
+          atomicAdd(&sh.hist[max(0, min(kBins - 1, (int)((M - x) * step)))], 1u);
+      });
+      cluster_barrier();
+      constexpr int kPer = kBins / kDrawThreads;
+      unsigned c[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) c[i] = 0u;
+      for (int q = 0; q < r.nrank; ++q) {
+        const uint4* from = reinterpret_cast<const uint4*>(peer(sh.hist, q)) + tid * (kPer / 4);
+#pragma unroll
+        for (int i = 0; i < kPer / 4; ++i) {
+          const uint4 v = from[i];
+          c[4 * i] += v.x;
+          c[4 * i + 1] += v.y;
+          c[4 * i + 2] += v.z;
+          c[4 * i + 3] += v.w;
+        }
+      }
+      // Counts, and masses as if every logit were in the middle of its step, in
+      // units of 2^-24: an estimate that the exact masses are held against.
+      const float drop = w.rh * w.scale / step;  // powers of two a step
+      unsigned own_c = 0u;
+      u64 own_m = 0ull;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        own_c += c[i];
+        own_m += __float2ull_rn((float)c[i] * ex2_approx(24.0f - (float)(tid * kPer + i) * drop -
+                                                         0.5f * drop));
+      }
+      unsigned end_c = own_c;
+      u64 end_m = own_m;
+      if (tid < 4) sh.sel[tid] = kBins;
+      cta_scan(end_c, end_m, sh);
+      if (tid == kDrawThreads - 1) sh.all_m = end_m;
+      __syncthreads();
+      const u64 est = __umul64hi(p_part, sh.all_m);
+      const u64 m0 = p_on ? est - est / 256ull : ULLONG_MAX, m1 = p_on ? est + est / 256ull : ULLONG_MAX;
+      unsigned cc = end_c - own_c;
+      u64 cm = end_m - own_m;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int bin = tid * kPer + i;
+        cc += c[i];
+        cm += __float2ull_rn((float)c[i] * ex2_approx(24.0f - (float)bin * drop - 0.5f * drop));
+        if (cc >= cut.k) atomicMin(&sh.sel[0], bin);
+        if (cm >= m0) atomicMin(&sh.sel[1], bin);
+        if (cm >= m1) atomicMin(&sh.sel[2], bin);
+      }
+      __syncthreads();
+      const int kb = sh.sel[0];
+      const int b0 = max(0, min(sh.sel[1] - 1, kb)), b1 = min(min(sh.sel[2] + 1, kb), kBins - 1);
+      // the elements before the bracket and up to its end
+      cc = end_c - own_c;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int bin = tid * kPer + i;
+        if (bin == b0) sh.above_c = cc;
+        cc += c[i];
+        if (bin == b1) sh.all_c = cc;
+      }
+      __syncthreads();
+      const unsigned above_c = b0 < kBins ? sh.above_c : 0u;
+      const bool none = b0 >= kBins;  // top_k alone, and more than there are
+      if (none || sh.all_c - above_c <= (unsigned)kRowList) {
+        // The exact masses, and the elements of the bracket.
+        const float f0 = (float)b0, f1 = b1 == kBins - 1 ? INFINITY : (float)(b1 + 1);
+        u64 above = 0ull, all = 0ull;
+        WeightSum pa, ps;
+        auto list = [&](float x, float v, int32_t i) {
+          if (x >= floor_x && v >= f0 && v < f1) {
+            const unsigned at = atomicAdd(&sh.own_n, 1u);
+            if (at < (unsigned)kCtaList) sh.own[at] = make_uint2(__float_as_uint(x), (uint32_t)i);
+          }
+        };
+        r.each_pair(
+            [&](float x0, float x1, int32_t i) {
+              const float v0 = (M - x0) * step, v1 = (M - x1) * step;
+              int32_t h[2], l[2];
+              weight_bits(x0, x1, w, table, h, l);
+              ps.add(h, l);
+              const bool a0 = v0 < f0 && x0 >= floor_x, a1 = v1 < f0 && x1 >= floor_x;
+              h[0] = a0 ? h[0] : kBitsH;
+              h[1] = a1 ? h[1] : kBitsH;
+              l[0] = a0 ? l[0] : kBitsL;
+              l[1] = a1 ? l[1] : kBitsL;
+              pa.add(h, l);
+              list(x0, v0, i);
+              list(x1, v1, i + 1);
+            },
+            [&](int n) {
+              above += pa.take((uint32_t)n);
+              all += ps.take((uint32_t)n);
+            });
+        const Sum sa = cluster_sum(above, r, sh, buf);
+        const Sum ss = cluster_sum(all, r, sh, buf ^ 1);  // its barrier orders the lists too
+        if (p_on) {
+          cut.m_lo = cut.m_hi = max(ceil_part(p_part, ss.all), 1ull);
+        }
+        if (tid == 0) *peer(&sh.count[r.rank], 0) = sh.own_n;
+        cluster_barrier();
+        if (r.rank == 0) {
+          bool ok = false;
+          if (none) {
+            if (tid == 0) {
+              sh.key = floor_key;
+              sh.last = INT32_MAX;
+              sh.sum = sa.all;
+            }
+            ok = true;
+          } else if (!(sa.all >= cut.m_lo)) {
+            const int n = gather(sh, r.nrank, 1, kCtaList);
+            if (n >= 0) {
+              const int per = (n + kDrawThreads - 1) / kDrawThreads;
+              u64 we[3] = {0ull, 0ull, 0ull};
+#pragma unroll
+              for (int i = 0; i < 3; ++i) {
+                const int j = tid * per + i;
+                if (i < per && j < n)
+                  we[i] = weight_of(__uint_as_float(sh.row.list[j].x), w, table);
+              }
+              float hi = -INFINITY, lo = INFINITY;
+              for (int j = tid; j < n; j += kDrawThreads) {
+                hi = fmaxf(hi, __uint_as_float(sh.row.list[j].x));
+                lo = fminf(lo, __uint_as_float(sh.row.list[j].x));
+              }
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) {
+                hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+                lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+              }
+              if (r.lane == 0) {
+                sh.scan_f[r.warp] = hi;
+                reinterpret_cast<float*>(sh.scan_m)[r.warp] = lo;
+              }
+              __syncthreads();
+              for (int j = 0; j < kDrawWarps; ++j) {
+                hi = fmaxf(hi, sh.scan_f[j]);
+                lo = fminf(lo, reinterpret_cast<const float*>(sh.scan_m)[j]);
+              }
+              __syncthreads();
+              ok = settle(sh, n, per, we, above_c, sa.all, cut, lo, hi, false);
+            }
+          }
+          __syncthreads();
+          if (tid < r.nrank) {
+            *peer(&sh.key, tid) = sh.key;
+            *peer(&sh.last, tid) = sh.last;
+            *peer(&sh.sum, tid) = sh.sum;
+            *peer(&sh.settled, tid) = ok ? 1 : 0;
+          }
+        }
+        cluster_barrier();
+        settled = sh.settled != 0;
+        if (settled) {
+          set.key = sh.key;
+          set.last = sh.last;
+          set.sum = sh.sum;
+          if constexpr (!VERIFY) {
+            // The warps' sums of K: what is above the bracket, and their
+            // elements of it that are in K.
+            const int at = r.rank * kDrawWarps;
+            if (r.lane == 0) sh.scan_m[r.warp] = sa.own;
+            __syncthreads();
+            const int n = none ? 0 : (int)sh.own_n;
+            for (int j = tid; j < n; j += kDrawThreads) {
+              const uint2 q = sh.own[j];
+              const float x = __uint_as_float(q.x);
+              const uint32_t key = ordered_bits(x);
+              if (key > set.key || (key == set.key && (int32_t)q.y <= set.last))
+                atomicAdd(&sh.scan_m[r.warp_of((int32_t)q.y)], weight_of(x, w, table));
+            }
+            __syncthreads();
+            sums = cluster_sum(r.lane == 0 ? sh.scan_m[r.warp] : 0ull, r, sh, buf);
+            buf ^= 1;
+            summed = true;
+            (void)at;
+          }
+        }
+      }
+    }
+
+    if (!settled) {
+      // A radix select.
+      if (p_on) {
+        const Sum all = cluster_sum(sum_from(r, w, table, w.lowest), r, sh, buf);
+        buf ^= 1;
+        cut.m_lo = max(ceil_part(p_part, all.all), 1ull);
+      }
+      unsigned k_rem = cut.k;
+      u64 m_rem = cut.m_lo;
+      const uint32_t low = floor_key >> ZB;
+      const int nb = 32 - __clz((ordered_bits(M) >> ZB) - low);
+      uint32_t prefix = 0u;
+      unsigned ties = 0u;
+      u64 above = 0ull;
+      int hb = 0;
+      bool reached = true;
+      cluster_barrier();  // the histograms take the place of what peers may still read
+      for (int hi = nb;;) {
+        const int lo = hi > 8 ? hi - 8 : 0;
+        if (tid < 256) {
+          sh.digit.count[hb][tid] = 0u;
+          sh.digit.mass[hb][tid] = 0ull;
+        }
+        __syncthreads();
+        r.each([&](float x, int32_t) {
+          if (!(x >= floor_x)) return;
+          const uint32_t rel = (ordered_bits(x) >> ZB) - low;
+          if (hi < 32 && (rel >> hi) != (prefix >> hi)) return;
+          const uint32_t d = (rel >> lo) & ((1u << (hi - lo)) - 1u);
+          atomicAdd(&sh.digit.count[hb][d], 1u);
+          atomicAdd(&sh.digit.mass[hb][d], weight_of(x, w, table));
+        });
+        cluster_barrier();
+        unsigned c = 0u;
+        u64 mass = 0ull;
+        if (tid < 256) {
+          const int dg = 255 - tid;
+          for (int q = 0; q < r.nrank; ++q) {
+            c += *peer(&sh.digit.count[hb][dg], q);
+            mass += *peer(&sh.digit.mass[hb][dg], q);
+          }
+        }
+        const int d = find_digit(c, mass, k_rem, m_rem, sh);
+        if (d < 0) {  // on the first level only: K is all that the floor leaves
+          set.sum = sh.all_m;
+          reached = false;
+          break;
+        }
+        k_rem -= sh.above_c;
+        m_rem -= sh.above_m;
+        above += sh.above_m;
+        prefix |= (uint32_t)d << lo;
+        if (tid == 255 - d) sh.sel[1] = (int)c;
+        __syncthreads();
+        ties = (unsigned)sh.sel[1];
+        hb ^= 1;
+        if (lo == 0) break;
+        hi = lo;
+      }
+      if (reached) {
+        // The entries on K's last key that K takes.
+        const uint32_t key = key_of_short<DT>(low + prefix);
+        const u64 each = weight_of(logit_of_key(key), w, table);
+        u64 take = k_rem;
+        if (each > 0ull) {
+          const u64 by_mass = m_rem / each + (m_rem % each != 0ull ? 1ull : 0ull);
+          if (by_mass < take) take = by_mass;
+        }
+        if (take < 1ull) take = 1ull;
+        set.key = key;
+        if (take < ties) {
+          auto tie = [&](float x, int32_t) {
+            return x >= floor_x && ordered_bits(x) == key ? 1ull : 0ull;
+          };
+          u64 n = 0ull;
+          r.each([&](float x, int32_t i) { n += tie(x, i); });
+          const Sum st = cluster_sum(n, r, sh, buf);
+          buf ^= 1;
+          find_index(r, st, take - 1ull, tie, [&](int32_t i, float) {
+            for (int q = 0; q < r.nrank; ++q) *peer(&sh.found, q) = i;
+          });
+          cluster_barrier();
+          set.last = sh.found;
+        } else {
+          take = ties;
+        }
+        set.sum = above + take * each;
+      }
+    }
+
+    auto weight = [&](float x, int32_t i) {
+      if (!(x >= floor_x)) return 0ull;
+      const uint32_t key = ordered_bits(x);
+      if (key < set.key || (key == set.key && i > set.last)) return 0ull;
+      return weight_of(x, w, table);
+    };
+    if constexpr (!VERIFY) {
+      if (!drawn) {
+        if (!summed) {
+          u64 own = 0ull;
+          r.each([&](float x, int32_t i) { own += weight(x, i); });
+          sums = cluster_sum(own, r, sh, buf);
+          buf ^= 1;
+        }
+        const u64 target = __umul64hi(fraction_of(__ldcg(p.uniform + b)), sums.all);
+        find_index(r, sums, target, weight, [&](int32_t i, float x) {
+          p.out_idx[b] = i;
+          if (p.out_logprob)
+            p.out_logprob[b] = (float)log((double)weight(x, i) / (double)sums.all);
+        });
+      }
+    } else if (r.rank == 0 && tid == 0) {
+      const int64_t t = __ldcg(p.draft + b);
+      if (b + 1 < __ldcg(p.offsets + s + 1) && b + 1 < p.B && t >= 0 && t < p.V) {
+        const float x = logit_at<DT>(r.row, t);
+        const float u = fminf(fmaxf(__ldcg(p.uniform + b), 0.0f), 0.999999940395355224609375f);
+        const float q = p.probs ? __ldcg(p.probs + b * p.probs_ld + t) : 1.0f;
+        const u64 wt = weight(x, (int32_t)t);
+        if (wt > 0ull && !((double)u * (double)q * (double)set.sum >= (double)wt)) set.accepted = 1;
+      }
+    }
+  }
+  if (r.rank == 0 && tid == 0) {
+    if constexpr (VERIFY) {
+      if (set.kind == kOne && b + 1 < __ldcg(p.offsets + s + 1) && b + 1 < p.B) {
+        // the set is one token: its draft passes for every u
+        set.accepted = __ldcg(p.draft + b) == (int64_t)set.last ? 1 : 0;
+      }
+      p.sets[b] = set;
+    } else if (set.kind != kSet) {
+      p.out_idx[b] = set.kind == kOne ? set.last : -1;
+      if (p.out_logprob) p.out_logprob[b] = set.kind == kOne ? 0.0f : -INFINITY;
+    }
+  }
+  cluster_barrier();  // no CTA leaves while another may reach its shared memory
+}
+
+// q s rounded to an integer, q clamped to [0, 1] (NaN: 0).
+__device__ __forceinline__ u64 times_probability(u64 s, float q) {
+  const u64 f = __float2ull_rn(fminf(fmaxf(q, 0.0f), 1.0f) * 9223372036854775808.0f);
+  const u64 hi = __umul64hi(f, s), lo = f * s;
+  return (hi << 1) + (lo >> 63) + ((lo >> 62) & 1ull);
+}
+
+// One cluster per request, after filter_set_kernel has written its rows' sets:
+// the accepted drafts, then the draw from the first row whose draft did not
+// pass (max(p - q, 0), or p without the draft where there are no draft
+// probabilities), or from p of the last row when all did.
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const DrawParams p) {
+  using Row = RowCtx<DT, VEC, false>;
+  __shared__ DrawShared sh;
+  const int tid = threadIdx.x;
+  cluster_arrive();
+  Row r;
+  r.rank = (int)cg::this_cluster().block_rank();
+  r.nrank = p.cluster;
+  r.warp = tid >> 5;
+  r.lane = tid & 31;
+  const int64_t i = blockIdx.x / r.nrank;
+  if (tid < kExp2Entries) sh.table[tid] = exp2_entry(tid);
+  if (tid == 0) sh.found = INT32_MAX;
+  pdl_wait_then_release();
+  __syncthreads();
+  cluster_wait();  // every CTA of the cluster runs
+  int64_t r0 = __ldcg(p.offsets + i), r1 = __ldcg(p.offsets + i + 1);
+  r0 = r0 > 0 ? r0 : 0;
+  r1 = r1 < p.B ? r1 : p.B;
+  if (r1 <= r0) {  // the same in every CTA of the cluster
+    if (r.rank == 0 && tid == 0) p.out_count[i] = 0;
+    return;
+  }
+  const int32_t rows = (int32_t)(r1 - r0);
+  for (int32_t j = tid; j < rows; j += kDrawThreads)
+    if (j == rows - 1 || __ldcg(&p.sets[r0 + j].accepted) == 0) {
+      atomicMin(&sh.found, j);
+      break;
+    }
+  __syncthreads();
+  const int64_t stop = r0 + sh.found;
+  const RowSet* from = p.sets + stop;
+  RowSet set;
+  set.sum = __ldcg(&from->sum);
+  set.M = __ldcg(&from->M);
+  set.key = __ldcg(&from->key);
+  set.last = __ldcg(&from->last);
+  set.kind = __ldcg(&from->kind);
+  if (r.rank == 0) {
+    for (int64_t b = r0 + tid; b < r1; b += kDrawThreads)
+      if (b != stop) p.out_idx[b] = b < stop ? __ldcg(p.draft + b) : -1;
+    if (tid == 0) {
+      p.out_count[i] = (int32_t)(stop - r0) + (set.kind != kNothing ? 1 : 0);
+      if (set.kind != kSet) p.out_idx[stop] = set.kind == kOne ? (int64_t)set.last : -1;
+    }
+  }
+  if (set.kind != kSet) return;  // the whole cluster
+
+  r.place(p, stop, nullptr);
+  const WeightRow w = weight_row(set.M, __ldcg(p.temperature + i), p.drop);
+  const uint32_t table = smem_addr(sh.table);
+  bool rest = stop != r1 - 1;
+  const int64_t draft = __ldcg(p.draft + stop);
+  const float* q = p.probs ? p.probs + stop * p.probs_ld : nullptr;
+  auto weight = [&](float x, int32_t at) {
+    if (!(x > -INFINITY)) return 0ull;
+    const uint32_t key = ordered_bits(x);
+    if (key < set.key || (key == set.key && at > set.last)) return 0ull;
+    if (rest && !q && at == draft) return 0ull;
+    const u64 full = weight_of(x, w, table);
+    if (!rest || !q) return full;
+    const u64 less = times_probability(set.sum, __ldg(q + at));
+    return full > less ? full - less : 0ull;
+  };
+  int buf = 0;
+  Sum sums;
+  for (;;) {
+    u64 own = 0ull;
+    r.each([&](float x, int32_t at) { own += weight(x, at); });
+    sums = cluster_sum(own, r, sh, buf);
+    buf ^= 1;
+    if (sums.all > 0ull || !rest) break;
+    rest = false;  // nothing is left of p - q: the draw is from p
+  }
+  const u64 target = __umul64hi(fraction_of(__ldcg(p.uniform_draw + i)), sums.all);
+  find_index(r, sums, target, weight, [&](int32_t at, float) { p.out_idx[stop] = at; });
+  cluster_barrier();
+}
+
+// The kernels of one dtype: (vec, resident, verify), or the verification's draw.
+template <int DT>
+void* draw_kernel_of(bool vec, bool resident, bool verify) {
+#define GSAMPLE_SET(V, R, F) \
+  if (vec == V && resident == R && verify == F) \
+    return reinterpret_cast<void*>(&filter_set_kernel<DT, V, R, F>);
+  GSAMPLE_SET(false, false, false)
+  GSAMPLE_SET(false, false, true)
+  GSAMPLE_SET(false, true, false)
+  GSAMPLE_SET(false, true, true)
+  GSAMPLE_SET(true, false, false)
+  GSAMPLE_SET(true, false, true)
+  GSAMPLE_SET(true, true, false)
+  GSAMPLE_SET(true, true, true)
+#undef GSAMPLE_SET
+  return nullptr;
+}
+
+template <int DT>
+void* verify_draw_kernel_of(bool vec) {
+  return vec ? reinterpret_cast<void*>(&verify_draw_kernel<DT, true>)
+             : reinterpret_cast<void*>(&verify_draw_kernel<DT, false>);
+}
+
+}  // namespace
+}  // namespace gsample

@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <cstdlib>
 #include <mutex>
 
 #include "gsample.h"
@@ -60,15 +61,37 @@ void fill_rows(const void* logits, gsample_dtype dtype, int64_t B, int64_t V, in
   p->V = (int32_t)V;
   const int epu = gsample::units_elems((int)dtype, vec);
   p->units_per_row = (int32_t)((V + epu - 1) / epu);
-  // A row's V weights of little more than 2^F at most stay below 2^63.
+  // A row's V weights of little more than 2^44 units at most stay below 2^63.
   int lg = 0;
   while ((int64_t(1) << lg) < V) ++lg;
-  p->fraction_bits = lg <= 18 ? 44 : 62 - lg;
+  p->drop = lg <= 18 ? 0 : lg - 18;
 }
 
-void set_cluster(int cluster, DrawParams* p) {
+// The cluster size for `rows` clusters: the largest (at most `most`, with at
+// least kUnitsPerCta units a CTA) whose clusters all run at once; else the
+// smallest whose slices fit in shared memory.
+void set_cluster(void* (*kernel)(int, bool, bool, int*), int dtype, bool vec, int64_t rows,
+                 int most, size_t limit, DrawParams* p) {
+  const int64_t nu = p->units_per_row;
+  int64_t top = (nu + kUnitsPerCta - 1) / kUnitsPerCta;
+  if (top > most) top = most;
+  int cluster = 0, fits = 0;
+  for (int c = (int)top; c >= 1; --c) {
+    const size_t smem = (size_t)((nu + c - 1) / c) * 16;
+    const bool resident = smem <= limit;
+    if (limit > 0 && !resident) break;
+    fits = c;
+    int threads = 0;
+    void* fn = kernel(dtype, vec, resident, &threads);
+    if (rows <= gsample::clusters_at_once(fn, threads, c, resident ? smem : 0)) {
+      cluster = c;
+      break;
+    }
+  }
+  if (cluster == 0) cluster = fits > 0 ? fits : (int)top;
+  if (const char* e = getenv("GS_CLUSTER")) cluster = atoi(e);
   p->cluster = cluster;
-  p->units_per_cta = (p->units_per_row + cluster - 1) / cluster;
+  p->units_per_cta = (int32_t)((nu + cluster - 1) / cluster);
 }
 
 }  // namespace
@@ -105,10 +128,7 @@ gsample_status gsample_filtered_categorical(const void* logits, gsample_dtype dt
   p.out_idx = out_idx;
   p.out_logprob = out_logprob;
   try {
-    set_cluster(gsample::plan_row_cluster(gsample::draw_kernel, (int)dtype, vec, B,
-                                          p.units_per_row, most, kUnitsPerCta,
-                                          gsample::draw_smem_limit()),
-                &p);
+    set_cluster(gsample::draw_kernel, (int)dtype, vec, B, most, gsample::draw_smem_limit(), &p);
   } catch (...) {
     return GSAMPLE_ERR_CUDA;
   }
@@ -166,16 +186,11 @@ gsample_status gsample_verify_drafts(const void* logits, gsample_dtype dtype, in
   p.sets = static_cast<gsample::RowSet*>(workspace);
   try {
     if (R > 0) {
-      set_cluster(gsample::plan_row_cluster(gsample::verify_kernel, (int)dtype, vec, R,
-                                            p.units_per_row, most, kUnitsPerCta,
-                                            gsample::draw_smem_limit()),
-                  &p);
+      set_cluster(gsample::verify_kernel, (int)dtype, vec, R, most, gsample::draw_smem_limit(), &p);
       st = launched(gsample::launch_draw(p, (int)dtype, vec, (cudaStream_t)stream));
       if (st != GSAMPLE_OK) return st;
     }
-    set_cluster(gsample::plan_row_cluster(gsample::verify_draw_kernel_fn, (int)dtype, vec, n,
-                                          p.units_per_row, most, kUnitsPerCta, 0),
-                &p);
+    set_cluster(gsample::verify_draw_kernel_fn, (int)dtype, vec, n, most, 0, &p);
   } catch (...) {
     return GSAMPLE_ERR_CUDA;
   }

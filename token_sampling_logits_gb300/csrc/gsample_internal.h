@@ -136,8 +136,8 @@ struct DrawParams {
   int32_t units_per_row;
   int32_t cluster;
   int32_t units_per_cta;
-  int32_t fraction_bits;  // F: weights are in units of 2^-F, a row's sum below 2^63
-  int32_t n;              // requests
+  int32_t drop;  // powers of two taken off the weights, so that a row's sum stays below 2^63
+  int32_t n;     // requests
   const float* temperature;
   const int32_t* top_k;  // nullptr: no top-k
   const float* top_p;    // nullptr: no top-p
@@ -255,10 +255,9 @@ cudaError_t launch_process(ProcessParams p, int dtype, int out_dtype, int sms,
 gsample_status check_logits(const void* logits, gsample_dtype dtype, int64_t B, int64_t V,
                             int64_t ld);
 gsample_status current_device_sms(int* sms);
-// For a kernel with one cluster per row: the cluster size for B rows of nu
-// units (may throw: the occupancies are kept in a map), and the load path.
-int plan_row_cluster(void* (*kernel)(int, bool, bool, int*), int dtype, bool vec, int64_t B,
-                     int64_t nu, int max_cluster, int64_t min_units, size_t smem_limit);
+// How many clusters of `cluster` CTAs of a kernel the device runs at once (may
+// throw: kept in a map), and whether rows take 128-bit loads.
+int clusters_at_once(void* fn, int threads, int cluster, size_t smem);
 bool wide_rows(const void* logits, gsample_dtype dtype, int64_t ld);
 // The sampler of gsample_gumbel_argmax (its checks, plan and launch), drawing
 // from constrained logits.

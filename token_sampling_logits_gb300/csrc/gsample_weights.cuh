@@ -4,16 +4,17 @@
 // Weights. A row's weights are e_i = 2^(x_i r - C), r = log2(e) / T, with C the
 // multiple of 1/256 nearest to M r (M the row's largest logit): one factor
 // away from exp((x_i - M) / T) for the whole row, which a draw does not see.
-// They are integers in units of 2^-F, so sums are exact, the same in any order
+// They are integers in units of 2^-44, so sums are exact, the same in any order
 // and for any split of the row, and cumulative sums compare exactly with a
 // target. 2^y is the table-driven form of P. T. P. Tang, "Table-driven
 // implementation of the exponential function in IEEE floating-point
 // arithmetic" (ACM TOMS 15(2), 1989), with a table of 256 steps and a cubic
-// for the rest: y = x r is kept as an unevaluated pair of binary32, the cubic
-// as 40 fraction bits. A weight is off by at most about 2^-39 of itself plus
-// half a unit 2^-F, and the errors of different elements are independent: with
-// binary32 weights a draw among 152K equal tokens would name a neighbour of
-// the right index in a few of a hundred rows.
+// for the rest, all of it on unevaluated pairs of binary32: two elements share
+// each instruction (fma.rn.f32x2), where 64-bit integers for the same number
+// of bits took 89 instructions an element. A weight is off by at most about
+// 2^-39 of itself plus half a unit, and the errors of different elements are
+// independent: with binary32 weights a draw among 152K equal tokens would name
+// a neighbour of the right index in a few of a hundred rows.
 #pragma once
 
 #include <cstdint>
@@ -21,10 +22,6 @@
 #include "gsample_device.cuh"
 
 namespace gsample {
-
-constexpr float kLog2eF = 1.4426950408889634f;
-constexpr double kLog2e64 = 1.4426950408889634074;
-constexpr double kLn2 = 0.69314718055994530942;
 
 // 2^(i/16) and 2^(i/256) in units of 2^-63: their products are the table.
 __constant__ unsigned long long kExp2Coarse[16] = {
@@ -39,76 +36,177 @@ __constant__ unsigned long long kExp2Fine[16] = {
     0x843A28C3ACDE4046ull, 0x8495EFB3303EFD30ull, 0x84F1F656379C1A29ull, 0x854E3CD8F9C8C95Dull};
 constexpr int kExp2Entries = 256;
 
-// Entry j of the table: 2^(j/256) in units of 2^-62.
-__device__ __forceinline__ unsigned long long exp2_entry(int j) {
-  return __umul64hi(kExp2Coarse[j >> 4], kExp2Fine[j & 15]);
+// Entry j of the table: 2^(j/256) as a pair of binary32.
+__device__ __forceinline__ float2 exp2_entry(int j) {
+  const unsigned long long v = __umul64hi(kExp2Coarse[j >> 4], kExp2Fine[j & 15]);  // 2^-62 units
+  const unsigned long long h = (v + (1ull << 38)) >> 39;                            // 2^-23 units
+  const long long rest = (long long)(v - (h << 39));
+  // (a low half of 0, that of 2^0, would not stand the exponents added below)
+  return make_float2((float)(uint32_t)h * 1.1920928955078125e-07f,
+                     rest ? (float)rest * 2.16840434497100886801e-19f : 2.8421709430404007e-14f);
 }
+
+// Two binary32 numbers that share an instruction.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ void split(F2 a, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+// a - b with b's sign flipped by the multiply of an fma: exact as a subtraction
+__device__ __forceinline__ F2 sub2(F2 a, F2 b) { return fma2(b, f2(-1.0f), a); }
 
 // Constants of a row's weights.
 struct WeightRow {
   float rh, rl;  // log2(e) / T as a pair
-  float base;    // subtracted from the logit first (0, or M where x r is too large to be split finely)
-  int32_t bias;  // what the bits of y + 49152 are for y = C, in steps of 1/256
-  int32_t unit;  // 62 - F
-  bool shift;
+  float M;
+  float lowest;  // logits below this (-inf and NaN too) have weight 0
+  float c;       // what is taken off y: the multiple of 1/256 nearest to M r, or 0
+  float scale;   // `shift`: a power of two that keeps x - M in range
+  int32_t bias;  // the bits of y + 49152 at y = C
+  bool shift;    // M is subtracted first: x r is too large to be split finely, or T so
+                 // large that `lowest` cannot stand in for -inf
 };
 
-// T > 0 and M finite. Temperatures below 2^-126 count as that. y is split on
-// the grid of 1/256 while it stays below 2^14; its rounding error (2^-48 of
-// it) asks for a smaller one.
-__device__ __forceinline__ WeightRow weight_row(float M, float T, int fraction_bits) {
-  constexpr int kMagicBits = 0x47400000;  // 49152.0f: adding it rounds to 1/256
-  const double r = kLog2e64 / (double)fmaxf(T, 1.17549435e-38f);
+constexpr int kMagicK = 0x47400000;           // 49152.0f: adding it rounds y to 1/256
+constexpr float kMagicH = 2.5f;               // rounds a weight in [0, 1.5) to 2^-22
+constexpr float kMagicL = 1.5f / 2097152.0f;  // rounds what that leaves to 2^-44
+constexpr float kLowestLogit = -3.402823466e38f;
+
+// T > 0 and M finite. Temperatures below 2^-126 count as that. `drop` powers
+// of two are taken off the weights (rows of more than 2^18 elements).
+__device__ __forceinline__ WeightRow weight_row(float M, float T, int drop) {
+  constexpr float kLog2eH = 1.44269502162933349609375f, kLog2eL = 1.9259629911266175e-08f;
   WeightRow w;
-  w.rh = (float)r;
-  w.rl = (float)(r - (double)w.rh);
-  const double c = (double)M * r;
-  w.shift = !(fabs(c) <= 512.0);
-  w.base = w.shift ? M : 0.0f;
-  w.bias = kMagicBits + (w.shift ? 0 : __double2int_rn(c * 256.0));
-  w.unit = 62 - fraction_bits;
+  T = fmaxf(T, 1.17549435e-38f);
+  w.scale = T > 1e30f ? 0.25f : 1.0f;
+  const float Ts = T * w.scale;
+  w.rh = w.rl = 0.0f;
+  if (T < INFINITY) {
+    const float q = __fdiv_rn(kLog2eH, Ts);
+    const float l = __fdiv_rn(__fadd_rn(__fmaf_rn(-q, Ts, kLog2eH), kLog2eL), Ts);
+    w.rh = __fadd_rn(q, l);
+    w.rl = __fsub_rn(l, __fsub_rn(w.rh, q));
+  }
+  w.M = M;
+  const float c = M * w.rh;
+  const float lowest = M - 42.0f * T;  // 60 powers of two below M
+  w.lowest = fmaxf(lowest, kLowestLogit);
+  w.shift = !(fabsf(c) <= 512.0f) || !(lowest >= kLowestLogit);
+  const int steps = w.shift ? 0 : __float2int_rn(c * 256.0f);
+  w.c = (float)steps * 0.00390625f + (float)drop;
+  w.bias = kMagicK + steps + drop * 256;
   return w;
 }
 
-// The weight of logit x <= M (-inf and NaN: 0) in units of 2^-F.
-// `table` is the shared-memory address of the 256 entries.
+// The weights of two logits x <= M: 2^-22 (h - the bits of kMagicH) + 2^-44
+// (l - the bits of kMagicL). `table` is the shared-memory address of the 256
+// entries. Products and differences of one value are formed from its negative
+// (n...), which rounds alike.
+__device__ __forceinline__ void weight_bits(float x0, float x1, const WeightRow& w, uint32_t table,
+                                            int32_t (&h)[2], int32_t (&l)[2]) {
+  const F2 neg = f2(-1.0f);
+  F2 x = f2(fmaxf(x0, w.lowest), fmaxf(x1, w.lowest)), xl = f2(0.0f);
+  bool z0 = true, z1 = true;
+  if (w.shift) {  // x - M as an exact pair
+    x = mul2(x, f2(w.scale));
+    const F2 m = f2(-w.M * w.scale), d = add2(x, m);
+    const F2 b = fma2(x, neg, d);
+    xl = add2(fma2(fma2(b, neg, d), neg, x), fma2(b, neg, m));
+    float d0, d1, l0, l1;
+    split(d, d0, d1);
+    split(xl, l0, l1);
+    z0 = x0 >= w.lowest && d0 * w.rh > -64.0f;
+    z1 = x1 >= w.lowest && d1 * w.rh > -64.0f;
+    x = f2(z0 ? d0 : 0.0f, z1 ? d1 : 0.0f);
+    xl = f2(z0 ? l0 : 0.0f, z1 ? l1 : 0.0f);
+  }
+  // y = x r as the pair (p, e)
+  const F2 rh = f2(w.rh), np = mul2(x, f2(-w.rh));
+  F2 e = fma2(x, f2(w.rl), fma2(x, rh, np));
+  if (w.shift) e = fma2(xl, rh, e);
+  // p = k / 256 + g0; y = k / 256 + g + ge
+  const F2 kf = fma2(np, neg, f2(49152.0f));
+  const F2 ng0 = add2(np, add2(kf, f2(-49152.0f)));
+  const F2 g = fma2(ng0, neg, e);
+  const F2 ge = fma2(add2(g, ng0), neg, e);
+  // 2^(g + ge) - 1 = a + t, a = g ln 2 to 24 bits
+  const F2 ln2h = f2(0.693147182464599609375f);
+  const F2 a = mul2(g, ln2h), na = mul2(g, f2(-0.693147182464599609375f));
+  F2 t = fma2(ge, ln2h, fma2(g, f2(-1.90465429995776793e-09f), fma2(g, ln2h, na)));
+  t = fma2(mul2(a, a), fma2(a, f2(1.0f / 6.0f), f2(0.5f)), t);
+  float kf0, kf1;
+  split(kf, kf0, kf1);
+  const int32_t k0 = __float_as_int(kf0) - w.bias, k1 = __float_as_int(kf1) - w.bias;
+  const uint2 t0 = lds64(table + ((uint32_t)k0 & 255u) * 8u);
+  const uint2 t1 = lds64(table + ((uint32_t)k1 & 255u) * 8u);
+  const int32_t n0 = (k0 >> 8) << 23, n1 = (k1 >> 8) << 23;  // added to the exponents
+  const F2 th = f2(__int_as_float((int32_t)t0.x + n0), __int_as_float((int32_t)t1.x + n1));
+  const F2 tl = f2(__int_as_float((int32_t)t0.y + n0), __int_as_float((int32_t)t1.y + n1));
+  // (th + tl) (1 + a + t) = v + lo
+  const F2 nu = mul2(th, na);
+  F2 lo = add2(fma2(tl, a, fma2(th, t, fma2(th, a, nu))), tl);
+  const F2 v = fma2(nu, neg, th);
+  lo = fma2(add2(nu, fma2(th, neg, v)), neg, lo);
+  const F2 vh = add2(add2(v, lo), f2(kMagicH));
+  const F2 vl = add2(add2(fma2(add2(vh, f2(-kMagicH)), neg, v), lo), f2(kMagicL));
+  float h0, h1, l0, l1;
+  split(vh, h0, h1);
+  split(vl, l0, l1);
+  h[0] = __float_as_int(z0 ? h0 : kMagicH);
+  h[1] = __float_as_int(z1 ? h1 : kMagicH);
+  l[0] = __float_as_int(z0 ? l0 : kMagicL);
+  l[1] = __float_as_int(z1 ? l1 : kMagicL);
+}
+
+constexpr int32_t kBitsH = 0x40200000;  // 2.5f
+constexpr int32_t kBitsL = 0x35400000;  // 1.5 * 2^-21
+
+// The weight of logit x <= M in units of 2^-44.
 __device__ __forceinline__ unsigned long long weight_of(float x, const WeightRow& w,
                                                         uint32_t table) {
-  float d = x, dl = 0.0f;
-  if (w.shift) {  // x - M as an exact pair
-    d = x - w.base;
-    const float b = d - x;
-    dl = (x - (d - b)) + (-w.base - b);
-  }
-  // y = d r as the pair (p, e)
-  float p = d * w.rh;
-  float e = fmaf(d, w.rl, fmaf(d, w.rh, -p));
-  if (w.shift) e = fmaf(dl, w.rh, e);
-  // p = k / 256 + g; an element far below (-inf, NaN) ends with a very negative k
-  p = fmaxf(p, -16000.0f);
-  const float kf = p + 49152.0f;
-  const int32_t k = __float_as_int(kf) - w.bias;
-  const int32_t s = w.unit - (k >> 8);
-  if (s > 63) return 0ull;
-  const float g0 = p - (kf - 49152.0f);
-  const float g = g0 + e;
-  const float ge = e - (g - g0);
-  // 2^g - 1 = a + t, a = g ln 2 to 24 bits
-  constexpr float kLn2h = 0.693147182464599609375f, kLn2l = (float)(kLn2 - 0.693147182464599609375);
-  const float a = g * kLn2h;
-  float t = fmaf(ge, kLn2h, fmaf(g, kLn2l, fmaf(g, kLn2h, -a)));
-  t = fmaf(a * a, fmaf(a, 1.0f / 6.0f, 0.5f), t);
-  // a + t in units of 2^-40: a to 2^-31, what that leaves joins t
-  constexpr float kA = 1.5f / 256.0f, kT = 1.5f / 131072.0f;
-  const float va = a + kA;
-  const float vt = t + (a - (va - kA)) + kT;
-  const int32_t q = ((__float_as_int(va) - __float_as_int(kA)) << 9) +
-                    (__float_as_int(vt) - __float_as_int(kT));
-  const uint2 tab = lds64(table + (uint32_t)(k & 255) * 8u);
-  const long long base = (long long)(((unsigned long long)tab.y << 32) | tab.x);
-  const long long v = base + (((long long)(int32_t)tab.y * (long long)q) >> 8);
-  return (((unsigned long long)v >> (s - 1)) + 1ull) >> 1;
+  int32_t h[2], l[2];
+  weight_bits(x, x, w, table, h, l);
+  return (unsigned long long)(((long long)(h[0] - kBitsH) << 22) + (long long)(l[0] - kBitsL));
 }
+
+// A sum of weights of a thread's elements: the two parts apart, in 32 bits,
+// joined before either can run over (at most 256 pairs).
+struct WeightSum {
+  uint32_t h = 0u, l = 0u;
+  __device__ __forceinline__ void add(const int32_t (&a)[2], const int32_t (&b)[2]) {
+    h += (uint32_t)a[0] + (uint32_t)a[1];
+    l += (uint32_t)b[0] + (uint32_t)b[1];
+  }
+  // `n`: elements added since the last call
+  __device__ __forceinline__ unsigned long long take(uint32_t n) {
+    const uint32_t sh = h - n * (uint32_t)kBitsH;
+    const int32_t sl = (int32_t)(l - n * (uint32_t)kBitsL);
+    h = l = 0u;
+    return ((unsigned long long)sh << 22) + (unsigned long long)(long long)sl;
+  }
+};
 
 // u in [0, 1) (smaller, or NaN: 0; larger: the largest below 1) in units of 2^-64.
 __device__ __forceinline__ unsigned long long fraction_of(float u) {
