@@ -33,6 +33,7 @@
 #include <cooperative_groups.h>
 
 #include <climits>
+#include <type_traits>
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -171,9 +172,13 @@ struct RowCtx {
     u_lo = min(p.units_per_row, rank * p.units_per_cta);
     u_hi = min(p.units_per_row, u_lo + p.units_per_cta);
     slice = smem_addr(smem);
+    run_of(warp, w_lo, w_hi);
+  }
+
+  __device__ __forceinline__ void run_of(int w, int32_t& lo, int32_t& hi) const {
     const int32_t n = u_hi - u_lo, per = (n + kDrawWarps - 1) / kDrawWarps;
-    w_lo = u_lo + min(n, warp * per);
-    w_hi = u_lo + min(n, (warp + 1) * per);
+    lo = u_lo + min(n, w * per);
+    hi = u_lo + min(n, (w + 1) * per);
   }
 
   // The warp that holds element i of this CTA's slice.
@@ -247,88 +252,17 @@ __device__ __forceinline__ u64 warp_sum(u64 v) {
   return v;
 }
 
-// The row's sum of v and what of it lies in the warps before this one; `own`
-// is this warp's. `buf` alternates between calls: a warp may still read one
-// call's sums while another writes the next one's.
-struct Sum {
-  u64 before, own, all;
-};
+// The row's sum of v; the warps' sums stay in sh.sums[buf]. `buf` alternates
+// between calls: a warp may still read one call's sums while another writes the
+// next one's.
 template <typename Row>
-__device__ __forceinline__ Sum cluster_sum(u64 v, const Row& r, DrawShared& sh, int buf) {
-  Sum s;
-  s.own = warp_sum(v);
-  if (r.lane < r.nrank) *peer(&sh.sums[buf][r.rank * kDrawWarps + r.warp], r.lane) = s.own;
+__device__ __forceinline__ u64 cluster_sum(u64 v, const Row& r, DrawShared& sh, int buf) {
+  v = warp_sum(v);
+  if (r.lane < r.nrank) *peer(&sh.sums[buf][r.rank * kDrawWarps + r.warp], r.lane) = v;
   cluster_barrier();
-  const int n = r.nrank * kDrawWarps, at = r.rank * kDrawWarps + r.warp;
-  u64 all = 0ull, before = 0ull;
-  for (int q = r.lane; q < n; q += 32) {
-    const u64 t = sh.sums[buf][q];
-    all += t;
-    if (q < at) before += t;
-  }
-  s.all = warp_sum(all);
-  s.before = warp_sum(before);
-  return s;
-}
-
-// Of the row's weights with sum s: the warp whose run holds the element at which
-// the cumulative weight passes `target` (< s.all) calls done(index, x) in one
-// thread.
-template <typename Row, typename W, typename Done>
-__device__ __forceinline__ void find_index(const Row& r, const Sum& s, u64 target, W&& weight,
-                                           Done&& done) {
-  if (target < s.before || target - s.before >= s.own) return;
-  u64 left = target - s.before;
-#pragma unroll 1
-  for (int32_t u0 = r.w_lo; u0 < r.w_hi; u0 += 32) {
-    const int32_t u = u0 + r.lane;
-    u64 own = 0ull;
-    uint4 q = make_uint4(0u, 0u, 0u, 0u);
-    if (u < r.w_hi) {
-      q = r.unit(u);
-#pragma unroll 1
-      for (int e = 0; e < Row::EPU; ++e) own += weight(Row::element(q, e), u * Row::EPU + e);
-    }
-    u64 incl = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const u64 t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-      if (r.lane >= o) incl += t;
-    }
-    const unsigned hit = __ballot_sync(0xFFFFFFFFu, incl > left);
-    if (hit) {
-      if (r.lane == __ffs(hit) - 1) {
-        u64 c = incl - own;
-#pragma unroll 1
-        for (int e = 0; e < Row::EPU; ++e) {
-          const float x = Row::element(q, e);
-          c += weight(x, u * Row::EPU + e);
-          if (c > left) {
-            done(u * Row::EPU + e, x);
-            break;
-          }
-        }
-      }
-      return;
-    }
-    left -= __shfl_sync(0xFFFFFFFFu, incl, 31);
-  }
-}
-
-// The row's sum of the weights of the elements from `lowest` up.
-template <typename Row>
-__device__ __forceinline__ u64 sum_from(const Row& r, const WeightRow& w, uint32_t table,
-                                        float lowest) {
-  u64 sum = 0ull;
-  WeightSum part;
-  r.each_pair(
-      [&](float x0, float x1, int32_t) {
-        int32_t h[2], l[2];
-        weight_bits(x0 >= lowest ? x0 : -INFINITY, x1 >= lowest ? x1 : -INFINITY, w, table, h, l);
-        part.add(h, l);
-      },
-      [&](int n) { sum += part.take((uint32_t)n); });
-  return sum;
+  u64 all = 0ull;
+  for (int q = r.lane; q < r.nrank * kDrawWarps; q += 32) all += sh.sums[buf][q];
+  return warp_sum(all);
 }
 
 // Inclusive scan over the CTA of one count and one mass a thread.
@@ -353,6 +287,105 @@ __device__ __forceinline__ void cta_scan(unsigned& c, u64& m, DrawShared& sh) {
   c += __reduce_add_sync(0xFFFFFFFFu, bc);
   m += warp_sum(bm);
   __syncthreads();
+}
+
+// The element at which the cumulative weight passes `target` (< the row's sum),
+// after cluster_sum(buf): the CTA that holds it scans the run of the warp that
+// held it, a unit a thread, and calls done(index, x, weight) in one thread.
+// pair(x0, x1, i, v) gives the weights of elements i and i + 1. Called by the
+// whole CTA.
+template <typename Row, typename W, typename Done>
+__device__ __forceinline__ void find_index(const Row& r, DrawShared& sh, int buf, u64 target,
+                                           W&& pair, Done&& done) {
+  // which warp: lane l adds the sums of eight of them
+  constexpr int kPer = kMaxSegments / 32;
+  const int n = r.nrank * kDrawWarps;
+  u64 own = 0ull;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) own += r.lane * kPer + j < n ? sh.sums[buf][r.lane * kPer + j] : 0ull;
+  u64 incl = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (r.lane >= o) incl += t;
+  }
+  const unsigned past = __ballot_sync(0xFFFFFFFFu, incl > target);
+  if (past == 0u) return;  // (target is below the sum)
+  const int l = __ffs(past) - 1;
+  u64 before = __shfl_sync(0xFFFFFFFFu, incl - own, l);
+  int at = l * kPer;
+  while (before + sh.sums[buf][at] <= target) before += sh.sums[buf][at++];
+  if (at / kDrawWarps != r.rank) return;
+  u64 left = target - before;
+  int32_t lo, hi;
+  r.run_of(at % kDrawWarps, lo, hi);
+  for (int32_t u0 = lo; u0 < hi; u0 += kDrawThreads) {
+    const int32_t u = u0 + (int)threadIdx.x;
+    u64 v[Row::EPU];
+    u64 sum = 0ull;
+    uint4 q = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int e = 0; e < Row::EPU; ++e) v[e] = 0ull;
+    if (u < hi) {
+      q = r.unit(u);
+#pragma unroll
+      for (int e = 0; e < Row::EPU; e += 2) {
+        u64 two[2];
+        pair(Row::element(q, e), Row::element(q, e + 1), u * Row::EPU + e, two);
+        v[e] = two[0];
+        v[e + 1] = two[1];
+        sum += two[0] + two[1];
+      }
+    }
+    u64 end = sum;
+    unsigned none = 0u;
+    cta_scan(none, end, sh);
+    u64 c = end - sum;
+    if (left >= c && left < end) {
+#pragma unroll
+      for (int e = 0; e < Row::EPU; ++e) {
+        if (left >= c && left < c + v[e]) done(u * Row::EPU + e, Row::element(q, e), v[e]);
+        c += v[e];
+      }
+    }
+    // what the units so far hold
+    if (threadIdx.x == kDrawThreads - 1) sh.all_m = end;
+    __syncthreads();
+    const u64 all = sh.all_m;
+    __syncthreads();
+    if (left < all) return;
+    left -= all;
+  }
+}
+
+// This thread's sum of the weights of the elements from `lowest` up.
+template <bool SHIFT, typename Row>
+__device__ __forceinline__ u64 sum_from(const Row& r, const WeightRow& w, uint32_t table,
+                                        float lowest) {
+  u64 sum = 0ull;
+  WeightSum part;
+  // an element below `lowest` counts as one below w.lowest, which weighs nothing
+  const bool all = !SHIFT && lowest <= w.lowest;
+  auto join = [&](int n) { sum += part.take((uint32_t)n); };
+  if (all) {
+    r.each_pair(
+        [&](float x0, float x1, int32_t) {
+          int32_t h[2], l[2];
+          weight_bits<SHIFT>(x0, x1, w, table, h, l);
+          part.add(h, l);
+        },
+        join);
+  } else {
+    r.each_pair(
+        [&](float x0, float x1, int32_t) {
+          int32_t h[2], l[2];
+          weight_bits<SHIFT>(x0 >= lowest ? x0 : -INFINITY, x1 >= lowest ? x1 : -INFINITY, w, table,
+                             h, l);
+          part.add(h, l);
+        },
+        join);
+  }
+  return sum;
 }
 
 // Thread t < 256 holds the totals (c, m) of digit 255 - t. The first digit from
@@ -680,8 +713,9 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
     bool settled = false;
 
     if ((k_on || p_on || m_on) && !w.shift) {
-      // Short sets.
-      const float x_lo = fmaxf(floor_x, fmaf(-11.0903549f, T, M));  // 16 powers of two
+      // Short sets: 16 powers of two down, and at low temperatures, where a
+      // top_k may reach further, 12 nats.
+      const float x_lo = fmaxf(floor_x, M - fmaxf(11.0903549f * T, 12.0f));
       const bool tails = p_on;
       float tail = 0.0f;
       unsigned mine = 0u;
@@ -835,18 +869,20 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
       }
     }
 
-    Sum sums{0ull, 0ull, 0ull};  // of K's weights
-    bool summed = false;
+    int summed = -1;  // the buffer with the warps' sums of K's weights
     if (!settled && !(k_on || p_on)) {
-      sums = cluster_sum(sum_from(r, w, table, floor_x), r, sh, buf);
-      set.sum = sums.all;
+      const u64 own = w.shift ? sum_from<true>(r, w, table, floor_x)
+                              : sum_from<false>(r, w, table, floor_x);
+      set.sum = cluster_sum(own, r, sh, buf);
+      summed = buf;
       buf ^= 1;
-      settled = summed = true;
+      settled = true;
     }
 
     if (!settled) {
-      // Long sets. The histogram's steps run down 24 powers of two, or to the floor.
-      const float low = fmaxf(floor_x, fmaf(-16.6355324f, T, M));
+      // Long sets. The histogram's steps run down 24 powers of two for a mass, to
+      // the floor for a count.
+      const float low = p_on ? fmaxf(floor_x, fmaf(-16.6355324f, T, M)) : floor_x;
       const float step = (float)(kBins - 1) / (M - low);
       for (int j = tid; j < kBins; j += kDrawThreads) sh.hist[j] = 0u;
       __syncthreads();
@@ -888,7 +924,8 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
       if (tid == kDrawThreads - 1) sh.all_m = end_m;
       __syncthreads();
       const u64 est = __umul64hi(p_part, sh.all_m);
-      const u64 m0 = p_on ? est - est / 256ull : ULLONG_MAX, m1 = p_on ? est + est / 256ull : ULLONG_MAX;
+      const u64 m0 = p_on ? est - est / 4096ull : ULLONG_MAX;
+      const u64 m1 = p_on ? est + est / 4096ull : ULLONG_MAX;
       unsigned cc = end_c - own_c;
       u64 cm = end_m - own_m;
 #pragma unroll
@@ -902,7 +939,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
       }
       __syncthreads();
       const int kb = sh.sel[0];
-      const int b0 = max(0, min(sh.sel[1] - 1, kb)), b1 = min(min(sh.sel[2] + 1, kb), kBins - 1);
+      const int b0 = min(sh.sel[1], kb), b1 = min(min(sh.sel[2], kb), kBins - 1);
       // the elements before the bracket and up to its end
       cc = end_c - own_c;
 #pragma unroll
@@ -918,7 +955,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
       if (none || sh.all_c - above_c <= (unsigned)kRowList) {
         // The exact masses, and the elements of the bracket.
         const float f0 = (float)b0, f1 = b1 == kBins - 1 ? INFINITY : (float)(b1 + 1);
-        u64 above = 0ull, all = 0ull;
+        u64 above = 0ull, all = 0ull, own_above = 0ull;
         WeightSum pa, ps;
         auto list = [&](float x, float v, int32_t i) {
           if (x >= floor_x && v >= f0 && v < f1) {
@@ -926,11 +963,12 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
             if (at < (unsigned)kCtaList) sh.own[at] = make_uint2(__float_as_uint(x), (uint32_t)i);
           }
         };
-        r.each_pair(
+        auto sweep = [&](auto shift) {
+          r.each_pair(
             [&](float x0, float x1, int32_t i) {
               const float v0 = (M - x0) * step, v1 = (M - x1) * step;
               int32_t h[2], l[2];
-              weight_bits(x0, x1, w, table, h, l);
+              weight_bits<decltype(shift)::value>(x0, x1, w, table, h, l);
               ps.add(h, l);
               const bool a0 = v0 < f0 && x0 >= floor_x, a1 = v1 < f0 && x1 >= floor_x;
               h[0] = a0 ? h[0] : kBitsH;
@@ -945,10 +983,16 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
               above += pa.take((uint32_t)n);
               all += ps.take((uint32_t)n);
             });
-        const Sum sa = cluster_sum(above, r, sh, buf);
-        const Sum ss = cluster_sum(all, r, sh, buf ^ 1);  // its barrier orders the lists too
+        };
+        if (w.shift)
+          sweep(std::true_type{});
+        else
+          sweep(std::false_type{});
+        own_above = warp_sum(above);
+        const u64 sa = cluster_sum(above, r, sh, buf);
+        const u64 ss = cluster_sum(all, r, sh, buf ^ 1);  // its barrier orders the lists too
         if (p_on) {
-          cut.m_lo = cut.m_hi = max(ceil_part(p_part, ss.all), 1ull);
+          cut.m_lo = cut.m_hi = max(ceil_part(p_part, ss), 1ull);
         }
         if (tid == 0) *peer(&sh.count[r.rank], 0) = sh.own_n;
         cluster_barrier();
@@ -958,10 +1002,10 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
             if (tid == 0) {
               sh.key = floor_key;
               sh.last = INT32_MAX;
-              sh.sum = sa.all;
+              sh.sum = sa;
             }
             ok = true;
-          } else if (!(sa.all >= cut.m_lo)) {
+          } else if (!(sa >= cut.m_lo)) {
             const int n = gather(sh, r.nrank, 1, kCtaList);
             if (n >= 0) {
               const int per = (n + kDrawThreads - 1) / kDrawThreads;
@@ -992,7 +1036,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
                 lo = fminf(lo, reinterpret_cast<const float*>(sh.scan_m)[j]);
               }
               __syncthreads();
-              ok = settle(sh, n, per, we, above_c, sa.all, cut, lo, hi, false);
+              ok = settle(sh, n, per, we, above_c, sa, cut, lo, hi, false);
             }
           }
           __syncthreads();
@@ -1012,8 +1056,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
           if constexpr (!VERIFY) {
             // The warps' sums of K: what is above the bracket, and their
             // elements of it that are in K.
-            const int at = r.rank * kDrawWarps;
-            if (r.lane == 0) sh.scan_m[r.warp] = sa.own;
+            if (r.lane == 0) sh.scan_m[r.warp] = own_above;
             __syncthreads();
             const int n = none ? 0 : (int)sh.own_n;
             for (int j = tid; j < n; j += kDrawThreads) {
@@ -1024,10 +1067,9 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
                 atomicAdd(&sh.scan_m[r.warp_of((int32_t)q.y)], weight_of(x, w, table));
             }
             __syncthreads();
-            sums = cluster_sum(r.lane == 0 ? sh.scan_m[r.warp] : 0ull, r, sh, buf);
+            cluster_sum(r.lane == 0 ? sh.scan_m[r.warp] : 0ull, r, sh, buf);
+            summed = buf;
             buf ^= 1;
-            summed = true;
-            (void)at;
           }
         }
       }
@@ -1036,9 +1078,11 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
     if (!settled) {
       // A radix select.
       if (p_on) {
-        const Sum all = cluster_sum(sum_from(r, w, table, w.lowest), r, sh, buf);
+        const u64 own = w.shift ? sum_from<true>(r, w, table, kLowestLogit)
+                                : sum_from<false>(r, w, table, kLowestLogit);
+        const u64 all = cluster_sum(own, r, sh, buf);
         buf ^= 1;
-        cut.m_lo = max(ceil_part(p_part, all.all), 1ull);
+        cut.m_lo = max(ceil_part(p_part, all), 1ull);
       }
       unsigned k_rem = cut.k;
       u64 m_rem = cut.m_lo;
@@ -1109,11 +1153,16 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
           };
           u64 n = 0ull;
           r.each([&](float x, int32_t i) { n += tie(x, i); });
-          const Sum st = cluster_sum(n, r, sh, buf);
+          cluster_sum(n, r, sh, buf);
+          find_index(r, sh, buf, take - 1ull,
+                     [&](float x0, float x1, int32_t i, u64(&v)[2]) {
+                       v[0] = tie(x0, i);
+                       v[1] = tie(x1, i + 1);
+                     },
+                     [&](int32_t i, float, u64) {
+                       for (int q = 0; q < r.nrank; ++q) *peer(&sh.found, q) = i;
+                     });
           buf ^= 1;
-          find_index(r, st, take - 1ull, tie, [&](int32_t i, float) {
-            for (int q = 0; q < r.nrank; ++q) *peer(&sh.found, q) = i;
-          });
           cluster_barrier();
           set.last = sh.found;
         } else {
@@ -1123,25 +1172,32 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
       }
     }
 
-    auto weight = [&](float x, int32_t i) {
-      if (!(x >= floor_x)) return 0ull;
+    auto kept = [&](float x, int32_t i) {
+      if (!(x >= floor_x)) return false;
       const uint32_t key = ordered_bits(x);
-      if (key < set.key || (key == set.key && i > set.last)) return 0ull;
-      return weight_of(x, w, table);
+      return key > set.key || (key == set.key && i <= set.last);
     };
     if constexpr (!VERIFY) {
       if (!drawn) {
-        if (!summed) {
+        auto pair = [&](float x0, float x1, int32_t i, u64(&v)[2]) {
+          weights_of(kept(x0, i) ? x0 : -INFINITY, kept(x1, i + 1) ? x1 : -INFINITY, w, table, v);
+        };
+        if (summed < 0) {
           u64 own = 0ull;
-          r.each([&](float x, int32_t i) { own += weight(x, i); });
-          sums = cluster_sum(own, r, sh, buf);
-          buf ^= 1;
+          r.each_pair(
+              [&](float x0, float x1, int32_t i) {
+                u64 v[2];
+                pair(x0, x1, i, v);
+                own += v[0] + v[1];
+              },
+              [](int) {});
+          cluster_sum(own, r, sh, buf);
+          summed = buf;
         }
-        const u64 target = __umul64hi(fraction_of(__ldcg(p.uniform + b)), sums.all);
-        find_index(r, sums, target, weight, [&](int32_t i, float x) {
+        const u64 target = __umul64hi(fraction_of(__ldcg(p.uniform + b)), set.sum);
+        find_index(r, sh, summed, target, pair, [&](int32_t i, float, u64 v) {
           p.out_idx[b] = i;
-          if (p.out_logprob)
-            p.out_logprob[b] = (float)log((double)weight(x, i) / (double)sums.all);
+          if (p.out_logprob) p.out_logprob[b] = (float)log((double)v / (double)set.sum);
         });
       }
     } else if (r.rank == 0 && tid == 0) {
@@ -1150,7 +1206,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
         const float x = logit_at<DT>(r.row, t);
         const float u = fminf(fmaxf(__ldcg(p.uniform + b), 0.0f), 0.999999940395355224609375f);
         const float q = p.probs ? __ldcg(p.probs + b * p.probs_ld + t) : 1.0f;
-        const u64 wt = weight(x, (int32_t)t);
+        const u64 wt = kept(x, (int32_t)t) ? weight_of(x, w, table) : 0ull;
         if (wt > 0ull && !((double)u * (double)q * (double)set.sum >= (double)wt)) set.accepted = 1;
       }
     }
@@ -1236,28 +1292,41 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Draw
   bool rest = stop != r1 - 1;
   const int64_t draft = __ldcg(p.draft + stop);
   const float* q = p.probs ? p.probs + stop * p.probs_ld : nullptr;
-  auto weight = [&](float x, int32_t at) {
-    if (!(x > -INFINITY)) return 0ull;
+  auto kept = [&](float x, int32_t at) {
+    if (!(x > -INFINITY)) return false;
     const uint32_t key = ordered_bits(x);
-    if (key < set.key || (key == set.key && at > set.last)) return 0ull;
-    if (rest && !q && at == draft) return 0ull;
-    const u64 full = weight_of(x, w, table);
-    if (!rest || !q) return full;
-    const u64 less = times_probability(set.sum, __ldg(q + at));
-    return full > less ? full - less : 0ull;
+    return (key > set.key || (key == set.key && at <= set.last)) && !(rest && !q && at == draft);
+  };
+  auto pair = [&](float x0, float x1, int32_t at, u64(&v)[2]) {
+    const bool k0 = kept(x0, at), k1 = kept(x1, at + 1);
+    v[0] = v[1] = 0ull;
+    if (!k0 && !k1) return;
+    weights_of(k0 ? x0 : -INFINITY, k1 ? x1 : -INFINITY, w, table, v);
+    if (rest && q) {
+      const u64 l0 = k0 ? times_probability(set.sum, __ldg(q + at)) : 0ull;
+      const u64 l1 = k1 ? times_probability(set.sum, __ldg(q + at + 1)) : 0ull;
+      v[0] = v[0] > l0 ? v[0] - l0 : 0ull;
+      v[1] = v[1] > l1 ? v[1] - l1 : 0ull;
+    }
   };
   int buf = 0;
-  Sum sums;
+  u64 all;
   for (;;) {
     u64 own = 0ull;
-    r.each([&](float x, int32_t at) { own += weight(x, at); });
-    sums = cluster_sum(own, r, sh, buf);
-    buf ^= 1;
-    if (sums.all > 0ull || !rest) break;
+    r.each_pair(
+        [&](float x0, float x1, int32_t at) {
+          u64 v[2];
+          pair(x0, x1, at, v);
+          own += v[0] + v[1];
+        },
+        [](int) {});
+    all = cluster_sum(own, r, sh, buf);
+    if (all > 0ull || !rest) break;
     rest = false;  // nothing is left of p - q: the draw is from p
+    buf ^= 1;
   }
-  const u64 target = __umul64hi(fraction_of(__ldcg(p.uniform_draw + i)), sums.all);
-  find_index(r, sums, target, weight, [&](int32_t at, float) { p.out_idx[stop] = at; });
+  const u64 target = __umul64hi(fraction_of(__ldcg(p.uniform_draw + i)), all);
+  find_index(r, sh, buf, target, pair, [&](int32_t at, float, u64) { p.out_idx[stop] = at; });
   cluster_barrier();
 }
 

@@ -74,8 +74,11 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
 }
-// a - b with b's sign flipped by the multiply of an fma: exact as a subtraction
-__device__ __forceinline__ F2 sub2(F2 a, F2 b) { return fma2(b, f2(-1.0f), a); }
+__device__ __forceinline__ F2 sub2(F2 a, F2 b) {
+  F2 r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
 
 // Constants of a row's weights.
 struct WeightRow {
@@ -124,16 +127,16 @@ __device__ __forceinline__ WeightRow weight_row(float M, float T, int drop) {
 // (l - the bits of kMagicL). `table` is the shared-memory address of the 256
 // entries. Products and differences of one value are formed from its negative
 // (n...), which rounds alike.
+template <bool SHIFT>
 __device__ __forceinline__ void weight_bits(float x0, float x1, const WeightRow& w, uint32_t table,
                                             int32_t (&h)[2], int32_t (&l)[2]) {
-  const F2 neg = f2(-1.0f);
   F2 x = f2(fmaxf(x0, w.lowest), fmaxf(x1, w.lowest)), xl = f2(0.0f);
   bool z0 = true, z1 = true;
-  if (w.shift) {  // x - M as an exact pair
+  if constexpr (SHIFT) {  // x - M as an exact pair
     x = mul2(x, f2(w.scale));
-    const F2 m = f2(-w.M * w.scale), d = add2(x, m);
-    const F2 b = fma2(x, neg, d);
-    xl = add2(fma2(fma2(b, neg, d), neg, x), fma2(b, neg, m));
+    const F2 m = f2(w.M * w.scale), d = sub2(x, m);
+    const F2 b = sub2(d, x);
+    xl = sub2(sub2(x, sub2(d, b)), add2(m, b));
     float d0, d1, l0, l1;
     split(d, d0, d1);
     split(xl, l0, l1);
@@ -145,12 +148,12 @@ __device__ __forceinline__ void weight_bits(float x0, float x1, const WeightRow&
   // y = x r as the pair (p, e)
   const F2 rh = f2(w.rh), np = mul2(x, f2(-w.rh));
   F2 e = fma2(x, f2(w.rl), fma2(x, rh, np));
-  if (w.shift) e = fma2(xl, rh, e);
+  if constexpr (SHIFT) e = fma2(xl, rh, e);
   // p = k / 256 + g0; y = k / 256 + g + ge
-  const F2 kf = fma2(np, neg, f2(49152.0f));
-  const F2 ng0 = add2(np, add2(kf, f2(-49152.0f)));
-  const F2 g = fma2(ng0, neg, e);
-  const F2 ge = fma2(add2(g, ng0), neg, e);
+  const F2 kf = sub2(f2(49152.0f), np);
+  const F2 ng0 = add2(np, sub2(kf, f2(49152.0f)));
+  const F2 g = sub2(e, ng0);
+  const F2 ge = sub2(e, add2(g, ng0));
   // 2^(g + ge) - 1 = a + t, a = g ln 2 to 24 bits
   const F2 ln2h = f2(0.693147182464599609375f);
   const F2 a = mul2(g, ln2h), na = mul2(g, f2(-0.693147182464599609375f));
@@ -167,10 +170,10 @@ __device__ __forceinline__ void weight_bits(float x0, float x1, const WeightRow&
   // (th + tl) (1 + a + t) = v + lo
   const F2 nu = mul2(th, na);
   F2 lo = add2(fma2(tl, a, fma2(th, t, fma2(th, a, nu))), tl);
-  const F2 v = fma2(nu, neg, th);
-  lo = fma2(add2(nu, fma2(th, neg, v)), neg, lo);
+  const F2 v = sub2(th, nu);
+  lo = sub2(lo, add2(nu, sub2(v, th)));
   const F2 vh = add2(add2(v, lo), f2(kMagicH));
-  const F2 vl = add2(add2(fma2(add2(vh, f2(-kMagicH)), neg, v), lo), f2(kMagicL));
+  const F2 vl = add2(add2(sub2(v, sub2(vh, f2(kMagicH))), lo), f2(kMagicL));
   float h0, h1, l0, l1;
   split(vh, h0, h1);
   split(vl, l0, l1);
@@ -183,12 +186,23 @@ __device__ __forceinline__ void weight_bits(float x0, float x1, const WeightRow&
 constexpr int32_t kBitsH = 0x40200000;  // 2.5f
 constexpr int32_t kBitsL = 0x35400000;  // 1.5 * 2^-21
 
-// The weight of logit x <= M in units of 2^-44.
+// The weights of two logits x <= M in units of 2^-44.
+__device__ __forceinline__ void weights_of(float x0, float x1, const WeightRow& w, uint32_t table,
+                                           unsigned long long (&v)[2]) {
+  int32_t h[2], l[2];
+  if (w.shift)
+    weight_bits<true>(x0, x1, w, table, h, l);
+  else
+    weight_bits<false>(x0, x1, w, table, h, l);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    v[i] = (unsigned long long)(((long long)(h[i] - kBitsH) << 22) + (long long)(l[i] - kBitsL));
+}
 __device__ __forceinline__ unsigned long long weight_of(float x, const WeightRow& w,
                                                         uint32_t table) {
-  int32_t h[2], l[2];
-  weight_bits(x, x, w, table, h, l);
-  return (unsigned long long)(((long long)(h[0] - kBitsH) << 22) + (long long)(l[0] - kBitsL));
+  unsigned long long v[2];
+  weights_of(x, x, w, table, v);
+  return v[0];
 }
 
 // A sum of weights of a thread's elements: the two parts apart, in 32 bits,
