@@ -111,13 +111,13 @@ int64_t elt_bytes(gsample_dtype dt) { return dt == GSAMPLE_F32 ? 4 : 2; }
 
 // How many clusters of `cluster` CTAs of `fn` (with `smem` bytes of dynamic
 // shared memory each) the device runs at once; cached per device, kernel,
-// cluster size and 16 KB step of shared memory.
-int active_clusters(void* fn, int threads, int cluster, size_t smem) {
+// cluster size and step of shared memory.
+int active_clusters(void* fn, int threads, int cluster, size_t smem, size_t step = 16384) {
   static std::map<std::tuple<int, void*, int, size_t>, int> cache;
-  const size_t bucket = (smem + 16383) / 16384;
+  const size_t bytes = (smem + step - 1) / step * step;
   int dev = 0;
   cudaGetDevice(&dev);
-  const auto key = std::make_tuple(dev, fn, cluster, bucket);
+  const auto key = std::make_tuple(dev, fn, cluster, bytes);
   {
     std::lock_guard<std::mutex> lock(g_mu);
     const auto it = cache.find(key);
@@ -126,7 +126,7 @@ int active_clusters(void* fn, int threads, int cluster, size_t smem) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)cluster);
   cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = bucket * 16384;
+  cfg.dynamicSmemBytes = bytes;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)cluster;
@@ -609,7 +609,7 @@ gsample_status current_device_sms(int* sms) {
 }
 
 int clusters_at_once(void* fn, int threads, int cluster, size_t smem) {
-  return active_clusters(fn, threads, cluster, smem);
+  return active_clusters(fn, threads, cluster, smem, 1024);
 }
 
 bool wide_rows(const void* logits, gsample_dtype dtype, int64_t ld) {

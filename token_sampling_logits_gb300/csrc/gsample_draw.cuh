@@ -59,6 +59,7 @@ constexpr int kRowList = 1280;                // entries of a row's list, at ran
 constexpr int kListBins = 512;
 constexpr int kLastBin = 384;                 // entries of a list's bin that are ranked
 constexpr int kBins = 4096;                   // steps of the histogram
+constexpr int64_t kOpenIndex = -2;            // out_idx of a row left to the second launch
 
 using u64 = unsigned long long;
 
@@ -181,6 +182,13 @@ struct RowCtx {
     hi = u_lo + min(n, (w + 1) * per);
   }
 
+  // The warp that holds element i of the row, counted over the cluster.
+  __device__ __forceinline__ int segment_of(int32_t i, int32_t units, int32_t per_cta) const {
+    const int32_t u = i / EPU, q = u / per_cta;
+    const int32_t n = min(per_cta, units - q * per_cta), per = (n + kDrawWarps - 1) / kDrawWarps;
+    return q * kDrawWarps + (u - q * per_cta) / per;
+  }
+
   // The warp that holds element i of this CTA's slice.
   __device__ __forceinline__ int warp_of(int32_t i) const {
     const int32_t per = (u_hi - u_lo + kDrawWarps - 1) / kDrawWarps;
@@ -192,7 +200,13 @@ struct RowCtx {
       return lds128(slice + (uint32_t)(u - u_lo) * 16u);
     } else {
       if constexpr (VEC) {
-        if ((u + 1) * EPU <= V) return __ldg(reinterpret_cast<const uint4*>(row) + u);
+        if ((u + 1) * EPU <= V) {
+          uint4 v;
+          asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                       : "l"(row + (size_t)u * 16));
+          return v;
+        }
       }
       return load_unit<DT, VEC>(row, u, V, 0ull);
     }
@@ -605,10 +619,18 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
   r.warp = tid >> 5;
   r.lane = tid & 31;
   const int64_t b = blockIdx.x / r.nrank;
+  if (p.phase == kLeftOver) {
+    pdl_wait_then_release();
+    const bool left = VERIFY ? __ldcg(&p.sets[b].kind) == kOpen : __ldcg(p.out_idx + b) == kOpenIndex;
+    if (!left) {  // the same in every CTA of the cluster
+      cluster_wait();
+      return;
+    }
+  }
   if (tid < kExp2Entries) sh.table[tid] = exp2_entry(tid);
   if (tid == 0) sh.own_n = 0u;
   r.place(p, b, smem);
-  pdl_wait_then_release();
+  if (p.phase != kLeftOver) pdl_wait_then_release();
 
   // The slice, in four parts, so that the maximum is formed as they arrive.
   const int32_t units = max(0, (r.w_hi - r.w_lo - r.lane + 31) / 32);
@@ -653,6 +675,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
         M = fmaxf(M, Row::largest(r.unit(r.w_lo + r.lane + 32 * j)));
     }
   } else {
+#pragma unroll 8
     for (int32_t j = 0; j < units; ++j)
       M = fmaxf(M, Row::largest(r.unit(r.w_lo + r.lane + 32 * j)));
   }
@@ -712,62 +735,84 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
     const u64 p_part = fraction_of(top_p);
     bool settled = false;
 
-    if ((k_on || p_on || m_on) && !w.shift) {
-      // Short sets: 16 powers of two down, and at low temperatures, where a
-      // top_k may reach further, 12 nats.
-      const float x_lo = fmaxf(floor_x, M - fmaxf(11.0903549f * T, 12.0f));
-      const bool tails = p_on;
+    const bool unfiltered = !(k_on || p_on || m_on);
+    if (!w.shift && !(VERIFY && unfiltered)) {
+      // Short sets: 12 powers of two down; for a top_k without a top_p, whose last
+      // elements may weigh next to nothing, 16, and 12 nats at low temperatures.
+      const bool tails = p_on || unfiltered;
+      const float x_lo =
+          fmaxf(floor_x, M - (tails ? 8.3177662f * T : fmaxf(11.0903549f * T, 12.0f)));
       float tail = 0.0f;
       unsigned mine = 0u;
-#pragma unroll 2
-      for (int32_t u0 = r.w_lo; u0 < r.w_hi; u0 += 32) {
-        const int32_t u = u0 + r.lane;
-        const bool valid = u < r.w_hi;
-        uint4 q = make_uint4(0u, 0u, 0u, 0u);
-        if (valid) q = r.unit(u);
-        const bool hit = valid && Row::largest(q) >= x_lo;
-        if (tails && valid) {
-          float t[EPU];
+      auto sweep = [&](auto with_tail) {
+        constexpr int kAhead = RESIDENT ? 1 : 3;
+        const F2 rh = f2(w.rh), nc = f2(-w.c);
+        uint4 next[kAhead];
 #pragma unroll
-          for (int e = 0; e < EPU; ++e) {
-            const float x = Row::element(q, e);
-            t[e] = ex2_approx(fmaf(x, w.rh, -w.c));
-            if (hit && x >= x_lo) t[e] = 0.0f;
-          }
-#pragma unroll
-          for (int o = EPU / 2; o > 0; o >>= 1)
-#pragma unroll
-            for (int e = 0; e < o; ++e) t[e] += t[e + o];
-          tail += t[0];
+        for (int i = 0; i < kAhead; ++i) {
+          next[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (r.w_lo + r.lane + 32 * i < r.w_hi) next[i] = r.unit(r.w_lo + r.lane + 32 * i);
         }
-        if (__ballot_sync(0xFFFFFFFFu, hit)) {
-          unsigned c = 0u;
-          if (hit) {
+        for (int32_t u0 = r.w_lo; u0 < r.w_hi; u0 += 32) {
+          const int32_t u = u0 + r.lane;
+          const bool valid = u < r.w_hi;
+          const uint4 q = next[0];
 #pragma unroll
-            for (int e = 0; e < EPU; ++e) c += Row::element(q, e) >= x_lo ? 1u : 0u;
-          }
-          unsigned incl = c;
+          for (int i = 0; i + 1 < kAhead; ++i) next[i] = next[i + 1];
+          if (u + 32 * kAhead < r.w_hi) next[kAhead - 1] = r.unit(u + 32 * kAhead);
+          const bool hit = valid && Row::largest(q) >= x_lo;
+          if constexpr (decltype(with_tail)::value) {
+            F2 t[EPU / 2];
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const unsigned t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-            if (r.lane >= o) incl += t;
-          }
-          unsigned at = mine + incl - c;
-          if (hit) {
+            for (int e = 0; e < EPU / 2; ++e) {
+              const F2 y = fma2(f2(Row::element(q, 2 * e), Row::element(q, 2 * e + 1)), rh, nc);
+              float y0, y1;
+              split(y, y0, y1);
+              t[e] = f2(ex2_approx(y0), ex2_approx(y1));
+            }
+            if (hit) {
 #pragma unroll
-            for (int e = 0; e < EPU; ++e) {
-              const float x = Row::element(q, e);
-              if (x >= x_lo) {
-                if (at < (unsigned)kWarpList)
-                  sh.own[r.warp * kWarpList + at] =
-                      make_uint2(__float_as_uint(x), (uint32_t)(u * EPU + e));
-                ++at;
+              for (int e = 0; e < EPU / 2; ++e) {
+                float t0, t1;
+                split(t[e], t0, t1);
+                t[e] = f2(Row::element(q, 2 * e) >= x_lo ? 0.0f : t0,
+                          Row::element(q, 2 * e + 1) >= x_lo ? 0.0f : t1);
               }
             }
+#pragma unroll
+            for (int o = EPU / 4; o > 0; o >>= 1)
+#pragma unroll
+              for (int e = 0; e < o; ++e) t[e] = add2(t[e], t[e + o]);
+            float t0, t1;
+            split(t[0], t0, t1);
+            tail += valid ? t0 + t1 : 0.0f;
           }
-          mine += __shfl_sync(0xFFFFFFFFu, incl, 31);
+          // the hits, a lane's unit at a time
+          unsigned lanes = __ballot_sync(0xFFFFFFFFu, hit);
+          while (lanes) {
+            const int l = __ffs(lanes) - 1;
+            lanes &= lanes - 1u;
+            uint4 s;
+            s.x = __shfl_sync(0xFFFFFFFFu, q.x, l);
+            s.y = __shfl_sync(0xFFFFFFFFu, q.y, l);
+            s.z = __shfl_sync(0xFFFFFFFFu, q.z, l);
+            s.w = __shfl_sync(0xFFFFFFFFu, q.w, l);
+            const float x = Row::element(s, r.lane & (EPU - 1));
+            const bool in = r.lane < EPU && x >= x_lo;
+            const unsigned who = __ballot_sync(0xFFFFFFFFu, in);
+            const unsigned at = mine + __popc(who & ((1u << r.lane) - 1u));
+            if (in && at < (unsigned)kWarpList)
+              sh.own[r.warp * kWarpList + at] =
+                  make_uint2(__float_as_uint(x), (uint32_t)((u0 + l) * EPU + r.lane));
+            mine += __popc(who);
+          }
+          if (mine > (unsigned)kWarpList) break;
         }
-      }
+      };
+      if (tails)
+        sweep(std::true_type{});
+      else
+        sweep(std::false_type{});
       // a NaN among the logits ends up in the tail: the list does not count then
       const bool odd = __any_sync(0xFFFFFFFFu, !(tail >= 0.0f));
       const u64 t = warp_sum(odd ? 0ull : __float2ull_rn(tail * 17592186044416.0f));
@@ -795,22 +840,110 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
           if (tid == kDrawThreads - 1) sh.all_m = incl;
           __syncthreads();
           const u64 listed = sh.all_m;
-          if (p_on) {
-            u64 rest = 0ull;
+          u64 rest = 0ull, err = 0ull;
+          if (tails) {
             for (int q = r.lane; q < r.nrank * kDrawWarps; q += 32) rest += sh.sums[buf][q];
             rest = warp_sum(rest);
             // The binary32 tail: y is rounded to 2^-20 of 64 and its factor r to
             // 2^-25 of |C| + 64, ex2 to 2^-22, the sums to 2^-24 a step; the fixed-point
             // weights to half a unit each.
             const float rel = (fabsf(w.c) + 192.0f + (float)part * 4.0f) * 5.9604645e-8f;
-            const u64 err = __float2ull_ru((float)rest * rel) + (u64)p.V;
-            cut.m_lo = ceil_part(p_part, listed + rest - min(rest, err));
+            err = __float2ull_ru((float)rest * rel) + (u64)p.V;
+          }
+          if (p_on) {
+            cut.m_lo = max(ceil_part(p_part, listed + rest - min(rest, err)), 1ull);
             cut.m_hi = ceil_part(p_part, listed + rest + err);
-            if (cut.m_lo < 1ull) cut.m_lo = 1ull;
           }
           const bool complete = x_lo == floor_x;
           if (k_on || p_on) {
             ok = settle(sh, n, per, we, 0u, 0ull, cut, x_lo, M, complete);
+          } else if (unfiltered) {
+            // All elements are K. The warp whose run u falls in is told by the
+            // listed weights and the tails; in it the weights are exact, and the
+            // element stands when u is further from its ends than the error of
+            // what lies before.
+            u64* run = sh.sums[buf];
+            const int segs = r.nrank * kDrawWarps;
+            // each warp's listed weights join its tail
+            u64 c = 0ull;
+            int last = -1;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+              const int j = tid * per + i;
+              if (i < per && j < n) {
+                const int at = r.segment_of((int32_t)sh.row.list[j].y, p.units_per_row, p.units_per_cta);
+                if (at != last && c) {
+                  atomicAdd(&run[last], c);
+                  c = 0ull;
+                }
+                last = at;
+                c += we[i];
+              }
+            }
+            if (c) atomicAdd(&run[last], c);
+            __syncthreads();
+            const u64 f = fraction_of(__ldcg(p.uniform + b));
+            const u64 sum = listed + rest;
+            const u64 t_lo = __umul64hi(f, sum - min(sum, err)), t_hi = __umul64hi(f, sum + err);
+            const u64 here = tid < segs ? run[tid] : 0ull;
+            u64 upto = here;
+            cta_scan(none, upto, sh);
+            if (tid == 0) sh.sel[0] = -1;
+            __syncthreads();
+            if (t_lo >= upto - here && t_lo < upto) {
+              sh.sel[0] = tid;
+              sh.above_m = upto - here;
+            }
+            __syncthreads();
+            const int at = sh.sel[0];
+            const u64 before = sh.above_m;
+            bool hit = false;
+            if (at >= 0 && err <= (sum >> 24)) {
+              RowCtx<DT, VEC, false> g;
+              g.row = r.row;
+              g.V = r.V;
+              const int32_t q0 = at / kDrawWarps * p.units_per_cta;
+              const int32_t qn = min(p.units_per_cta, p.units_per_row - q0);
+              const int32_t each = (qn + kDrawWarps - 1) / kDrawWarps;
+              const int32_t lo = q0 + min(qn, (at % kDrawWarps) * each);
+              const int32_t hi = q0 + min(qn, (at % kDrawWarps + 1) * each);
+              u64 base = before;
+              for (int32_t u0 = lo; u0 < hi; u0 += kDrawThreads) {
+                const int32_t u = u0 + tid;
+                uint4 q = make_uint4(0u, 0u, 0u, 0u);
+                u64 v[EPU], all = 0ull;
+#pragma unroll
+                for (int e = 0; e < EPU; ++e) v[e] = 0ull;
+                if (u < hi) {
+                  q = g.unit(u);
+#pragma unroll
+                  for (int e = 0; e < EPU; e += 2) {
+                    u64 two[2];
+                    weights_of(Row::element(q, e), Row::element(q, e + 1), w, table, two);
+                    v[e] = two[0];
+                    v[e + 1] = two[1];
+                    all += two[0] + two[1];
+                  }
+                }
+                u64 end = all;
+                cta_scan(none, end, sh);
+                u64 from = base + end - all;
+#pragma unroll
+                for (int e = 0; e < EPU; ++e) {
+                  if (v[e] > 0ull && from + err <= t_lo && t_hi + err < from + v[e]) {
+                    hit = true;
+                    p.out_idx[b] = u * EPU + e;
+                    if (p.out_logprob) p.out_logprob[b] = log_ratio(v[e], sum, table);
+                  }
+                  from += v[e];
+                }
+                if (tid == kDrawThreads - 1) sh.all_m = end;
+                __syncthreads();
+                base += sh.all_m;
+                __syncthreads();
+              }
+            }
+            ok = __syncthreads_or(hit ? 1 : 0) != 0;
           } else {
             if (tid == 0) {
               sh.key = floor_key;
@@ -820,7 +953,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
             __syncthreads();
             ok = complete;
           }
-          if (ok && !VERIFY) {
+          if (ok && !VERIFY && !unfiltered) {
             // The draw, in the list's order, which is the indices'.
             const uint32_t key = sh.key;
             const int32_t last = sh.last;
@@ -847,7 +980,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
                   const int j = tid * per + i;
                   p.out_idx[b] = (int64_t)sh.row.list[j].y;
                   if (p.out_logprob)
-                    p.out_logprob[b] = (float)log((double)we[i] / (double)sum);
+                    p.out_logprob[b] = log_ratio(we[i], sum, table);
                 }
                 c += we[i];
               }
@@ -869,6 +1002,17 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
       }
     }
 
+    if (p.phase == kShortOnly && !settled) {
+      // left to a second launch, whose clusters have more threads a row
+      if (tid == 0) {
+        if constexpr (VERIFY)
+          p.sets[b].kind = kOpen;
+        else
+          p.out_idx[b] = kOpenIndex;
+      }
+      cluster_barrier();
+      return;
+    }
     int summed = -1;  // the buffer with the warps' sums of K's weights
     if (!settled && !(k_on || p_on)) {
       const u64 own = w.shift ? sum_from<true>(r, w, table, floor_x)
@@ -1197,7 +1341,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
         const u64 target = __umul64hi(fraction_of(__ldcg(p.uniform + b)), set.sum);
         find_index(r, sh, summed, target, pair, [&](int32_t i, float, u64 v) {
           p.out_idx[b] = i;
-          if (p.out_logprob) p.out_logprob[b] = (float)log((double)v / (double)set.sum);
+          if (p.out_logprob) p.out_logprob[b] = log_ratio(v, set.sum, table);
         });
       }
     } else if (r.rank == 0 && tid == 0) {

@@ -67,6 +67,11 @@ void fill_rows(const void* logits, gsample_dtype dtype, int64_t B, int64_t V, in
   p->drop = lg <= 18 ? 0 : lg - 18;
 }
 
+void use_cluster(int cluster, DrawParams* p) {
+  p->cluster = cluster;
+  p->units_per_cta = (p->units_per_row + cluster - 1) / cluster;
+}
+
 // The cluster size for `rows` clusters: the largest (at most `most`, with at
 // least kUnitsPerCta units a CTA) whose clusters all run at once; else the
 // smallest whose slices fit in shared memory.
@@ -90,8 +95,31 @@ void set_cluster(void* (*kernel)(int, bool, bool, int*), int dtype, bool vec, in
   }
   if (cluster == 0) cluster = fits > 0 ? fits : (int)top;
   if (const char* e = getenv("GS_CLUSTER")) cluster = atoi(e);
-  p->cluster = cluster;
-  p->units_per_cta = (int32_t)((nu + cluster - 1) / cluster);
+  use_cluster(cluster, p);
+}
+
+// The rows' sets (verification) or draws. While clusters of two CTAs or more
+// for all rows run at once they take one launch; past that a launch with one CTA
+// a row settles the short sets, reading the row twice, and a second one with
+// clusters the rest.
+cudaError_t launch_sets(void* (*kernel)(int, bool, bool, int*), int dtype, bool vec, int64_t rows,
+                        int most, DrawParams* p, cudaStream_t stream) {
+  set_cluster(kernel, dtype, vec, rows, most, gsample::draw_smem_limit(), p);
+  int threads = 0;
+  const size_t smem = (size_t)p->units_per_cta * 16;
+  const bool resident = smem <= gsample::draw_smem_limit();
+  void* fn = kernel(dtype, vec, resident, &threads);
+  static const int force = getenv("GS_STREAM") ? atoi(getenv("GS_STREAM")) : -1;
+  const bool one = force >= 0 ? !force : rows <= gsample::clusters_at_once(fn, threads, p->cluster, resident ? smem : 0);
+  if (!one) {
+    DrawParams q = *p;
+    q.phase = gsample::kShortOnly;
+    use_cluster(1, &q);
+    const cudaError_t e = gsample::launch_draw(q, dtype, vec, stream);
+    if (e != cudaSuccess) return e;
+    p->phase = gsample::kLeftOver;
+  }
+  return gsample::launch_draw(*p, dtype, vec, stream);
 }
 
 }  // namespace
@@ -128,11 +156,11 @@ gsample_status gsample_filtered_categorical(const void* logits, gsample_dtype dt
   p.out_idx = out_idx;
   p.out_logprob = out_logprob;
   try {
-    set_cluster(gsample::draw_kernel, (int)dtype, vec, B, most, gsample::draw_smem_limit(), &p);
+    return launched(launch_sets(gsample::draw_kernel, (int)dtype, vec, B, most, &p,
+                                (cudaStream_t)stream));
   } catch (...) {
     return GSAMPLE_ERR_CUDA;
   }
-  return launched(gsample::launch_draw(p, (int)dtype, vec, (cudaStream_t)stream));
 }
 
 size_t gsample_verify_workspace_bytes(int64_t R) {
@@ -186,8 +214,8 @@ gsample_status gsample_verify_drafts(const void* logits, gsample_dtype dtype, in
   p.sets = static_cast<gsample::RowSet*>(workspace);
   try {
     if (R > 0) {
-      set_cluster(gsample::verify_kernel, (int)dtype, vec, R, most, gsample::draw_smem_limit(), &p);
-      st = launched(gsample::launch_draw(p, (int)dtype, vec, (cudaStream_t)stream));
+      st = launched(launch_sets(gsample::verify_kernel, (int)dtype, vec, R, most, &p,
+                                (cudaStream_t)stream));
       if (st != GSAMPLE_OK) return st;
     }
     set_cluster(gsample::verify_draw_kernel_fn, (int)dtype, vec, n, most, 0, &p);

@@ -128,6 +128,9 @@ cudaError_t launch_filter(const FilterParams& p, int dtype, bool vec, cudaStream
 // number, and the verification of drafts (sets != nullptr): settings per row,
 // or per request there.
 struct RowSet;
+// What a launch settles: every row; the rows with short sets alone; those that
+// such a launch left.
+enum DrawPhase : int32_t { kAllRows = 0, kShortOnly = 1, kLeftOver = 2 };
 struct DrawParams {
   const char* logits;
   int64_t ld_bytes;
@@ -138,6 +141,7 @@ struct DrawParams {
   int32_t units_per_cta;
   int32_t drop;  // powers of two taken off the weights, so that a row's sum stays below 2^63
   int32_t n;     // requests
+  DrawPhase phase;
   const float* temperature;
   const int32_t* top_k;  // nullptr: no top-k
   const float* top_p;    // nullptr: no top-p

@@ -222,6 +222,51 @@ struct WeightSum {
   }
 };
 
+// v > 0 as 2^(n / 256) times 1 + r, |r| < 2^-9, r as a pair.
+struct LogParts {
+  int32_t n;
+  float rh, rl;
+};
+__device__ __forceinline__ LogParts log_parts(unsigned long long v, uint32_t table) {
+  const int up = __clzll((long long)v);
+  v <<= up;  // 2^-63 units of a number in [1, 2)
+  const uint32_t top = (uint32_t)(v >> 40);  // 24 bits
+  const float mh = (float)top * 1.1920928955078125e-07f;
+  const float ml = (float)(uint32_t)((v >> 8) & 0xFFFFFFFFull) * 2.7755575615628914e-17f;
+  const int k = min(255, __float2int_rn(256.0f * __log2f(mh)));
+  const uint2 t = lds64(table + (uint32_t)k * 8u);
+  const float th = __uint_as_float(t.x), tl = __uint_as_float(t.y);
+  const float d = __fadd_rn(__fsub_rn(mh, th), 0.0f);  // exact
+  const float e = __fsub_rn(ml, tl);
+  const float rh = __fdividef(__fadd_rn(d, e), th);
+  // d + e - rh (th + tl), over th
+  float rest = __fmaf_rn(-rh, th, d);
+  rest = __fadd_rn(rest, e);
+  rest = __fmaf_rn(-rh, tl, rest);
+  return LogParts{(63 - up) * 256 + k, rh, __fdividef(rest, th)};
+}
+
+// ln(w / s), 0 < w <= s, rounded once (and off by at most 2^-40 before): by the
+// steps of the table, the rest of each number by its series (Tang, as above).
+__device__ __forceinline__ float log_ratio(unsigned long long w, unsigned long long s,
+                                           uint32_t table) {
+  if (w >= s) return 0.0f;
+  const LogParts a = log_parts(w, table), b = log_parts(s, table);
+  auto series = [](const LogParts& p) {  // ln(1 + r) - rh
+    const float q = p.rh * p.rh;
+    return fmaf(q, fmaf(p.rh, fmaf(p.rh, -0.25f, 1.0f / 3.0f), -0.5f), p.rl * (1.0f - p.rh));
+  };
+  // (n_a - n_b) ln2 / 256 as a pair, then the differences of the series
+  constexpr float ch = 0.0027076061815023422f, cl = -7.4400558592100308e-12f;
+  const float n = (float)(a.n - b.n);
+  const float p = n * ch, pl = fmaf(n, cl, fmaf(n, ch, -p));
+  const float d = a.rh - b.rh, db = d - a.rh;
+  const float dl = (a.rh - (d - db)) + (-b.rh - db);
+  const float sum = p + d, sb = sum - p;
+  const float sl = (p - (sum - sb)) + (d - sb);
+  return sum + (sl + (pl + (dl + (series(a) - series(b)))));
+}
+
 // u in [0, 1) (smaller, or NaN: 0; larger: the largest below 1) in units of 2^-64.
 __device__ __forceinline__ unsigned long long fraction_of(float u) {
   if (!(u > 0.0f)) return 0ull;
@@ -237,7 +282,7 @@ __device__ __forceinline__ unsigned long long ceil_part(unsigned long long f,
 
 // What a row draws from. kSet: the elements whose ordered key is above `key`,
 // and those equal to it up to index `last`, with weights as above and their sum.
-enum RowKind : int32_t { kNothing = 0, kOne = 1, kSet = 2 };
+enum RowKind : int32_t { kNothing = 0, kOne = 1, kSet = 2, kOpen = 3 };
 struct RowSet {
   unsigned long long sum;
   float M;
