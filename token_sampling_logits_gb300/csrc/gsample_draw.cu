@@ -111,11 +111,12 @@ int draw_max_cluster(int dtype, bool vec) {
   return size;
 }
 
-cudaError_t launch_draw(const DrawParams& p, int dtype, bool vec, cudaStream_t stream) {
+cudaError_t launch_draw(const DrawParams& p, int dtype, bool vec, int64_t clusters,
+                        cudaStream_t stream) {
   const size_t need = (size_t)p.units_per_cta * 16;
   const bool resident = need <= kDrawSmemLimit;
   void* fn = select_set(dtype, vec, resident, p.sets != nullptr);
-  return launch_rows(fn, p, p.B, resident ? need : 0, stream);
+  return launch_rows(fn, p, clusters, resident ? need : 0, stream);
 }
 
 cudaError_t launch_verify_draw(const DrawParams& p, int dtype, bool vec, cudaStream_t stream) {

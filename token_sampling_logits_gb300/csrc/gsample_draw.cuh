@@ -33,6 +33,7 @@
 #include <cooperative_groups.h>
 
 #include <climits>
+#include <cstddef>
 #include <type_traits>
 #include <cstdint>
 
@@ -56,6 +57,7 @@ constexpr int kMaxSegments = kDrawMaxCluster * kDrawWarps;
 constexpr int kWarpList = 64;                 // entries of a warp's list
 constexpr int kCtaList = kWarpList * kDrawWarps;
 constexpr int kRowList = 1280;                // entries of a row's list, at rank 0
+constexpr int kLandList = 768;
 constexpr int kListBins = 512;
 constexpr int kLastBin = 384;                 // entries of a list's bin that are ranked
 constexpr int kBins = 4096;                   // steps of the histogram
@@ -93,18 +95,20 @@ __device__ __forceinline__ float logit_of_key(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key);
 }
 
-struct Ranked {  // an element of the bin that K ends in
+struct alignas(16) Ranked {  // an element of the bin that K ends in
   u64 w;
   uint32_t key, idx;
 };
 
-struct DrawShared {
+struct alignas(16) DrawShared {
   float2 table[kExp2Entries];
   u64 sums[2][kMaxSegments];      // the warps' sums of the whole cluster (two buffers)
   float wmax[kMaxSegments];       // their maxima; then, at rank 0, offsets of their lists
   unsigned count[kMaxSegments];   // at rank 0: the lengths of their lists
+  unsigned landed_at[kMaxSegments];  // and where they landed
+  unsigned landed_n;
   union {
-    unsigned hist[kBins];
+    alignas(16) unsigned hist[kBins];  // read sixteen bytes at a time
     struct {
       uint2 list[kRowList];  // logit bits and index
       union {
@@ -113,6 +117,7 @@ struct DrawShared {
           unsigned count[kListBins];
         } bin;
         Ranked last[kLastBin];
+        uint2 landed[kLandList];  // as they come from the cluster's warps
       };
     } row;
     struct {
@@ -138,6 +143,8 @@ struct DrawShared {
   u64 sum;
 };
 
+static_assert(offsetof(DrawShared, hist) % 16 == 0, "the histogram is read as uint4");
+
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
@@ -159,7 +166,8 @@ __device__ __forceinline__ T* peer(T* p, int rank) {
 template <int DT, bool VEC, bool RESIDENT>
 struct RowCtx {
   using C = HCfg<DT, VEC>;
-  static constexpr int EPU = C::kEPU;
+  static constexpr int EPU = C::kEPU, kDT = DT;
+  static constexpr bool kVec = VEC, kResident = RESIDENT;
   static constexpr int kFlush = 256 / EPU;  // units between joins of a WeightSum
   const char* row;
   int32_t V, u_lo, u_hi;
@@ -463,11 +471,10 @@ __device__ __forceinline__ int32_t first_equal(const Row& r, float M, DrawShared
 }
 
 // What K is cut by: the first `k` elements; those with less than m before
-// them, m somewhere in [m_lo, m_hi]; the logits from `floor` up.
+// them, m somewhere in [m_lo, m_hi].
 struct Cut {
   unsigned k;
   u64 m_lo, m_hi;
-  float floor;
 };
 
 // The CTA's lists as one, in their order, in rank 0's sh.row.list: `n_seg` lists
@@ -498,6 +505,25 @@ __device__ __forceinline__ int gather(DrawShared& sh, int n_seg, int per, int st
   }
   __syncthreads();
   return n;
+}
+
+// The lists that landed at rank 0, in the order of their warps, in sh.row.list.
+// Returns the number of entries, or -1 where one did not fit.
+__device__ __forceinline__ int in_order(DrawShared& sh, int n_seg) {
+  const int tid = threadIdx.x;
+  const unsigned c = tid < n_seg ? sh.count[tid] : 0u;
+  const bool bad = c == 0xFFFFFFFFu;
+  unsigned incl = bad ? 0u : c;
+  u64 none = 0ull;
+  cta_scan(incl, none, sh);
+  if (tid == kDrawThreads - 1) sh.all_c = incl;
+  if (__syncthreads_or(bad ? 1 : 0)) return -1;
+  if (tid < n_seg) {
+    const unsigned from = sh.landed_at[tid], to = incl - c;
+    for (unsigned j = 0; j < c; ++j) sh.row.list[to + j] = sh.row.landed[from + j];
+  }
+  __syncthreads();
+  return (int)sh.all_c;
 }
 
 // Rank 0, on the n entries of sh.row.list, which are in [x_lo, x_hi] and come
@@ -601,418 +627,58 @@ __device__ __forceinline__ bool settle(DrawShared& sh, int n, int per, const u64
   return before_c + taken >= cut.k || sh.sum >= cut.m_hi;
 }
 
-// VERIFY: the row's set goes to p.sets[b], with the outcome of its draft's
-// test. Otherwise the draw is made and written.
-template <int DT, bool VEC, bool RESIDENT, bool VERIFY>
-__global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawParams p) {
-  using Row = RowCtx<DT, VEC, RESIDENT>;
-  constexpr int EPU = Row::EPU;
-  constexpr int ZB = KeyBits<DT>::kZB;
-  extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ DrawShared sh;
+// The sum of 2^(x r - c) over a unit, in binary32; t[] gets its terms.
+template <typename Row>
+__device__ __forceinline__ float unit_tail(const uint4& q, F2 rh, F2 rl, F2 nc,
+                                           F2 (&t)[Row::EPU / 2]) {
+#pragma unroll
+  for (int e = 0; e < Row::EPU / 2; ++e) {
+    const F2 x = f2(Row::element(q, 2 * e), Row::element(q, 2 * e + 1));
+    float y0, y1;
+    split(fma2(x, rl, fma2(x, rh, nc)), y0, y1);
+    t[e] = f2(ex2_approx(y0), ex2_approx(y1));
+  }
+  F2 s[Row::EPU / 2];
+#pragma unroll
+  for (int e = 0; e < Row::EPU / 2; ++e) s[e] = t[e];
+#pragma unroll
+  for (int o = Row::EPU / 4; o > 0; o >>= 1)
+#pragma unroll
+    for (int e = 0; e < o; ++e) s[e] = add2(s[e], s[e + o]);
+  float s0, s1;
+  split(s[0], s0, s1);
+  return s0 + s1;
+}
+
+// A binary32 sum with what its roundings left out.
+struct Tail {
+  float hi = 0.0f, lo = 0.0f;
+  __device__ __forceinline__ void add(float t) {
+    const float s = __fadd_rn(hi, t), b = __fsub_rn(s, hi);
+    lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(t, b));
+    hi = s;
+  }
+};
+
+// A row that its short list does not settle, by the whole cluster: *set, and the
+// draw (not VERIFY). top_k 0 and top_p 1: off.
+template <bool VERIFY, typename Row>
+__device__ __noinline__ void settle_long(const DrawParams& p, const Row& r, DrawShared& sh,
+                                         int64_t b, float M, float T, float floor_x, int32_t top_k,
+                                         float top_p, int buf, RowSet* out) {
+  constexpr int DT = Row::kDT, ZB = KeyBits<DT>::kZB;
   const int tid = threadIdx.x;
-
-  cluster_arrive();  // waited for before the first write to another CTA
-  Row r;
-  r.rank = (int)cg::this_cluster().block_rank();
-  r.nrank = p.cluster;
-  r.warp = tid >> 5;
-  r.lane = tid & 31;
-  const int64_t b = blockIdx.x / r.nrank;
-  if (p.phase == kLeftOver) {
-    pdl_wait_then_release();
-    const bool left = VERIFY ? __ldcg(&p.sets[b].kind) == kOpen : __ldcg(p.out_idx + b) == kOpenIndex;
-    if (!left) {  // the same in every CTA of the cluster
-      cluster_wait();
-      return;
-    }
-  }
-  if (tid < kExp2Entries) sh.table[tid] = exp2_entry(tid);
-  if (tid == 0) sh.own_n = 0u;
-  r.place(p, b, smem);
-  if (p.phase != kLeftOver) pdl_wait_then_release();
-
-  // The slice, in four parts, so that the maximum is formed as they arrive.
-  const int32_t units = max(0, (r.w_hi - r.w_lo - r.lane + 31) / 32);
-  const int32_t part = ((r.w_hi - r.w_lo + 31) / 32 + 3) / 4;
-  if constexpr (RESIDENT) {
-    const uint64_t pol = evict_first_policy();
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      for (int32_t j = c * part; j < min(units, (c + 1) * part); ++j) {
-        const int32_t u = r.w_lo + r.lane + 32 * j;
-        const uint32_t dst = r.slice + (uint32_t)(u - r.u_lo) * 16u;
-        if (VEC && (u + 1) * EPU <= p.V)
-          cp_async16(dst, r.row + (size_t)u * 16, pol);
-        else
-          sts128(dst, load_unit<DT, VEC>(r.row, u, p.V, pol));
-      }
-      cp_async_commit();
-    }
-  }
-  // the settings of the row, or of its request
-  int64_t s = b;
-  if constexpr (VERIFY) s = find_request(p.offsets, p.n, b, sh);
-  const bool owned = s >= 0;  // the same in every CTA of the cluster
-  const float T = owned ? __ldcg(p.temperature + s) : 0.0f;
-  int32_t top_k = owned && p.top_k ? __ldcg(p.top_k + s) : 0;
-  const float top_p = owned && p.top_p ? __ldcg(p.top_p + s) : 1.0f;
-  const float min_p = owned && p.min_p ? __ldcg(p.min_p + s) : 0.0f;
-  const bool p_on = top_p < 1.0f && top_p > 0.0f;  // NaN: off
-  if (top_p <= 0.0f) top_k = 1;
-  const bool k_on = top_k >= 1;
-  const bool m_on = min_p > 0.0f && T > 0.0f && T < INFINITY;
-  if (m_on && tid == kDrawThreads - 1)
-    sh.floor_step = min_p < 1.0f ? (double)T * log((double)min_p) : 0.0;
-
-  // The largest logit (NaN counts as -inf).
-  float M = -INFINITY;
-  if constexpr (RESIDENT) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      cp_async_wait_upto(3 - c);
-      for (int32_t j = c * part; j < min(units, (c + 1) * part); ++j)
-        M = fmaxf(M, Row::largest(r.unit(r.w_lo + r.lane + 32 * j)));
-    }
-  } else {
-#pragma unroll 8
-    for (int32_t j = 0; j < units; ++j)
-      M = fmaxf(M, Row::largest(r.unit(r.w_lo + r.lane + 32 * j)));
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-  cluster_wait();  // every CTA of the cluster runs
-  if (!owned) return;
-  if (r.lane < r.nrank) *peer(&sh.wmax[r.rank * kDrawWarps + r.warp], r.lane) = M;
-  cluster_barrier();
-  for (int q = r.lane; q < r.nrank * kDrawWarps; q += 32) M = fmaxf(M, sh.wmax[q]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-
-  RowSet set;
-  set.sum = 1ull;
-  set.M = M;
-  set.key = 0u;
-  set.last = -1;
-  set.kind = kNothing;
-  set.accepted = 0;
-  set.request = (int32_t)s;
-  int buf = 0;
-  bool drawn = VERIFY;
-  if (M == -INFINITY) {
-    // no candidate
-  } else if (!(T > 0.0f) || M == INFINITY) {
-    // Greedy, or +inf takes all the mass.
-    set.kind = kOne;
-    set.last = first_equal(r, M, sh);
-  } else {
-    const WeightRow w = weight_row(M, T, p.drop);
-    const uint32_t table = smem_addr(sh.table);
-    // The lowest logit that K may hold: min_p's, and no element whose weight is
-    // zero, which is never drawn.
-    float floor_x = w.lowest;
-    if (m_on) {
-      // the smallest binary32 number from M + T ln(min_p) up
-      const double d = sh.floor_step;
-      const float dh = (float)d, dl = (float)(d - (double)dh);
-      float f = M + dh;
-      const float bb = f - M;
-      const float rest = ((M - (f - bb)) + (dh - bb)) + dl;
-      if (rest > 0.0f && f < M)
-        f = __int_as_float(__float_as_int(f) + (f > 0.0f ? 1 : f < 0.0f ? -1 : 0));
-      if (rest > 0.0f && f == 0.0f) f = 1.40129846e-45f;
-      floor_x = fminf(fmaxf(floor_x, f), M);
-    }
-    const uint32_t floor_key = ordered_bits(floor_x);
-    set.kind = kSet;
-    set.key = floor_key;
-    set.last = INT32_MAX;
-    set.sum = 0ull;
-    Cut cut;
-    cut.k = k_on ? (unsigned)top_k : 0xFFFFFFFFu;
-    cut.m_lo = cut.m_hi = ULLONG_MAX;
-    cut.floor = floor_x;
-    const u64 p_part = fraction_of(top_p);
-    bool settled = false;
-
-    const bool unfiltered = !(k_on || p_on || m_on);
-    if (!w.shift && !(VERIFY && unfiltered)) {
-      // Short sets: 12 powers of two down; for a top_k without a top_p, whose last
-      // elements may weigh next to nothing, 16, and 12 nats at low temperatures.
-      const bool tails = p_on || unfiltered;
-      const float x_lo =
-          fmaxf(floor_x, M - (tails ? 8.3177662f * T : fmaxf(11.0903549f * T, 12.0f)));
-      float tail = 0.0f;
-      unsigned mine = 0u;
-      auto sweep = [&](auto with_tail) {
-        constexpr int kAhead = RESIDENT ? 1 : 3;
-        const F2 rh = f2(w.rh), nc = f2(-w.c);
-        uint4 next[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          next[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (r.w_lo + r.lane + 32 * i < r.w_hi) next[i] = r.unit(r.w_lo + r.lane + 32 * i);
-        }
-        for (int32_t u0 = r.w_lo; u0 < r.w_hi; u0 += 32) {
-          const int32_t u = u0 + r.lane;
-          const bool valid = u < r.w_hi;
-          const uint4 q = next[0];
-#pragma unroll
-          for (int i = 0; i + 1 < kAhead; ++i) next[i] = next[i + 1];
-          if (u + 32 * kAhead < r.w_hi) next[kAhead - 1] = r.unit(u + 32 * kAhead);
-          const bool hit = valid && Row::largest(q) >= x_lo;
-          if constexpr (decltype(with_tail)::value) {
-            F2 t[EPU / 2];
-#pragma unroll
-            for (int e = 0; e < EPU / 2; ++e) {
-              const F2 y = fma2(f2(Row::element(q, 2 * e), Row::element(q, 2 * e + 1)), rh, nc);
-              float y0, y1;
-              split(y, y0, y1);
-              t[e] = f2(ex2_approx(y0), ex2_approx(y1));
-            }
-            if (hit) {
-#pragma unroll
-              for (int e = 0; e < EPU / 2; ++e) {
-                float t0, t1;
-                split(t[e], t0, t1);
-                t[e] = f2(Row::element(q, 2 * e) >= x_lo ? 0.0f : t0,
-                          Row::element(q, 2 * e + 1) >= x_lo ? 0.0f : t1);
-              }
-            }
-#pragma unroll
-            for (int o = EPU / 4; o > 0; o >>= 1)
-#pragma unroll
-              for (int e = 0; e < o; ++e) t[e] = add2(t[e], t[e + o]);
-            float t0, t1;
-            split(t[0], t0, t1);
-            tail += valid ? t0 + t1 : 0.0f;
-          }
-          // the hits, a lane's unit at a time
-          unsigned lanes = __ballot_sync(0xFFFFFFFFu, hit);
-          while (lanes) {
-            const int l = __ffs(lanes) - 1;
-            lanes &= lanes - 1u;
-            uint4 s;
-            s.x = __shfl_sync(0xFFFFFFFFu, q.x, l);
-            s.y = __shfl_sync(0xFFFFFFFFu, q.y, l);
-            s.z = __shfl_sync(0xFFFFFFFFu, q.z, l);
-            s.w = __shfl_sync(0xFFFFFFFFu, q.w, l);
-            const float x = Row::element(s, r.lane & (EPU - 1));
-            const bool in = r.lane < EPU && x >= x_lo;
-            const unsigned who = __ballot_sync(0xFFFFFFFFu, in);
-            const unsigned at = mine + __popc(who & ((1u << r.lane) - 1u));
-            if (in && at < (unsigned)kWarpList)
-              sh.own[r.warp * kWarpList + at] =
-                  make_uint2(__float_as_uint(x), (uint32_t)((u0 + l) * EPU + r.lane));
-            mine += __popc(who);
-          }
-          if (mine > (unsigned)kWarpList) break;
-        }
-      };
-      if (tails)
-        sweep(std::true_type{});
-      else
-        sweep(std::false_type{});
-      // a NaN among the logits ends up in the tail: the list does not count then
-      const bool odd = __any_sync(0xFFFFFFFFu, !(tail >= 0.0f));
-      const u64 t = warp_sum(odd ? 0ull : __float2ull_rn(tail * 17592186044416.0f));
-      if (r.lane == 0) {
-        const int at = r.rank * kDrawWarps + r.warp;
-        *peer(&sh.count[at], 0) = odd ? 0xFFFFFFFFu : mine;
-        *peer(&sh.sums[buf][at], 0) = t;
-      }
-      cluster_barrier();
-      bool ok = false;
-      if (r.rank == 0) {
-        const int n = gather(sh, r.nrank * kDrawWarps, kDrawWarps, kWarpList);
-        if (n >= 0) {
-          const int per = (n + kDrawThreads - 1) / kDrawThreads;
-          u64 we[3] = {0ull, 0ull, 0ull}, own = 0ull;
-#pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            const int j = tid * per + i;
-            if (i < per && j < n) we[i] = weight_of(__uint_as_float(sh.row.list[j].x), w, table);
-            own += we[i];
-          }
-          u64 incl = own;
-          unsigned none = 0u;
-          cta_scan(none, incl, sh);
-          if (tid == kDrawThreads - 1) sh.all_m = incl;
-          __syncthreads();
-          const u64 listed = sh.all_m;
-          u64 rest = 0ull, err = 0ull;
-          if (tails) {
-            for (int q = r.lane; q < r.nrank * kDrawWarps; q += 32) rest += sh.sums[buf][q];
-            rest = warp_sum(rest);
-            // The binary32 tail: y is rounded to 2^-20 of 64 and its factor r to
-            // 2^-25 of |C| + 64, ex2 to 2^-22, the sums to 2^-24 a step; the fixed-point
-            // weights to half a unit each.
-            const float rel = (fabsf(w.c) + 192.0f + (float)part * 4.0f) * 5.9604645e-8f;
-            err = __float2ull_ru((float)rest * rel) + (u64)p.V;
-          }
-          if (p_on) {
-            cut.m_lo = max(ceil_part(p_part, listed + rest - min(rest, err)), 1ull);
-            cut.m_hi = ceil_part(p_part, listed + rest + err);
-          }
-          const bool complete = x_lo == floor_x;
-          if (k_on || p_on) {
-            ok = settle(sh, n, per, we, 0u, 0ull, cut, x_lo, M, complete);
-          } else if (unfiltered) {
-            // All elements are K. The warp whose run u falls in is told by the
-            // listed weights and the tails; in it the weights are exact, and the
-            // element stands when u is further from its ends than the error of
-            // what lies before.
-            u64* run = sh.sums[buf];
-            const int segs = r.nrank * kDrawWarps;
-            // each warp's listed weights join its tail
-            u64 c = 0ull;
-            int last = -1;
-#pragma unroll
-            for (int i = 0; i < 3; ++i) {
-              const int j = tid * per + i;
-              if (i < per && j < n) {
-                const int at = r.segment_of((int32_t)sh.row.list[j].y, p.units_per_row, p.units_per_cta);
-                if (at != last && c) {
-                  atomicAdd(&run[last], c);
-                  c = 0ull;
-                }
-                last = at;
-                c += we[i];
-              }
-            }
-            if (c) atomicAdd(&run[last], c);
-            __syncthreads();
-            const u64 f = fraction_of(__ldcg(p.uniform + b));
-            const u64 sum = listed + rest;
-            const u64 t_lo = __umul64hi(f, sum - min(sum, err)), t_hi = __umul64hi(f, sum + err);
-            const u64 here = tid < segs ? run[tid] : 0ull;
-            u64 upto = here;
-            cta_scan(none, upto, sh);
-            if (tid == 0) sh.sel[0] = -1;
-            __syncthreads();
-            if (t_lo >= upto - here && t_lo < upto) {
-              sh.sel[0] = tid;
-              sh.above_m = upto - here;
-            }
-            __syncthreads();
-            const int at = sh.sel[0];
-            const u64 before = sh.above_m;
-            bool hit = false;
-            if (at >= 0 && err <= (sum >> 24)) {
-              RowCtx<DT, VEC, false> g;
-              g.row = r.row;
-              g.V = r.V;
-              const int32_t q0 = at / kDrawWarps * p.units_per_cta;
-              const int32_t qn = min(p.units_per_cta, p.units_per_row - q0);
-              const int32_t each = (qn + kDrawWarps - 1) / kDrawWarps;
-              const int32_t lo = q0 + min(qn, (at % kDrawWarps) * each);
-              const int32_t hi = q0 + min(qn, (at % kDrawWarps + 1) * each);
-              u64 base = before;
-              for (int32_t u0 = lo; u0 < hi; u0 += kDrawThreads) {
-                const int32_t u = u0 + tid;
-                uint4 q = make_uint4(0u, 0u, 0u, 0u);
-                u64 v[EPU], all = 0ull;
-#pragma unroll
-                for (int e = 0; e < EPU; ++e) v[e] = 0ull;
-                if (u < hi) {
-                  q = g.unit(u);
-#pragma unroll
-                  for (int e = 0; e < EPU; e += 2) {
-                    u64 two[2];
-                    weights_of(Row::element(q, e), Row::element(q, e + 1), w, table, two);
-                    v[e] = two[0];
-                    v[e + 1] = two[1];
-                    all += two[0] + two[1];
-                  }
-                }
-                u64 end = all;
-                cta_scan(none, end, sh);
-                u64 from = base + end - all;
-#pragma unroll
-                for (int e = 0; e < EPU; ++e) {
-                  if (v[e] > 0ull && from + err <= t_lo && t_hi + err < from + v[e]) {
-                    hit = true;
-                    p.out_idx[b] = u * EPU + e;
-                    if (p.out_logprob) p.out_logprob[b] = log_ratio(v[e], sum, table);
-                  }
-                  from += v[e];
-                }
-                if (tid == kDrawThreads - 1) sh.all_m = end;
-                __syncthreads();
-                base += sh.all_m;
-                __syncthreads();
-              }
-            }
-            ok = __syncthreads_or(hit ? 1 : 0) != 0;
-          } else {
-            if (tid == 0) {
-              sh.key = floor_key;
-              sh.last = INT32_MAX;
-              sh.sum = listed;
-            }
-            __syncthreads();
-            ok = complete;
-          }
-          if (ok && !VERIFY && !unfiltered) {
-            // The draw, in the list's order, which is the indices'.
-            const uint32_t key = sh.key;
-            const int32_t last = sh.last;
-            const u64 sum = sh.sum;
-            u64 kept = 0ull;
-#pragma unroll
-            for (int i = 0; i < 3; ++i) {
-              const int j = tid * per + i;
-              if (i < per && j < n) {
-                const uint2 q = sh.row.list[j];
-                const uint32_t kj = ordered_bits(__uint_as_float(q.x));
-                if (kj < key || (kj == key && (int32_t)q.y > last)) we[i] = 0ull;
-              }
-              kept += we[i];
-            }
-            const u64 target = __umul64hi(fraction_of(__ldcg(p.uniform + b)), sum);
-            u64 end = kept;
-            cta_scan(none, end, sh);
-            u64 c = end - kept;
-            if (target >= c && target < end) {
-#pragma unroll
-              for (int i = 0; i < 3; ++i) {
-                if (target >= c && target < c + we[i]) {
-                  const int j = tid * per + i;
-                  p.out_idx[b] = (int64_t)sh.row.list[j].y;
-                  if (p.out_logprob)
-                    p.out_logprob[b] = log_ratio(we[i], sum, table);
-                }
-                c += we[i];
-              }
-            }
-          }
-        }
-        if (tid < r.nrank) *peer(&sh.settled, tid) = ok ? 1 : 0;
-      }
-      cluster_barrier();
-      settled = sh.settled != 0;
-      buf ^= 1;
-      if (settled) {
-        drawn = true;
-        if (VERIFY && r.rank == 0) {
-          set.key = sh.key;
-          set.last = sh.last;
-          set.sum = sh.sum;
-        }
-      }
-    }
-
-    if (p.phase == kShortOnly && !settled) {
-      // left to a second launch, whose clusters have more threads a row
-      if (tid == 0) {
-        if constexpr (VERIFY)
-          p.sets[b].kind = kOpen;
-        else
-          p.out_idx[b] = kOpenIndex;
-      }
-      cluster_barrier();
-      return;
-    }
+  const WeightRow w = weight_row(M, T, p.drop);
+  const uint32_t table = smem_addr(sh.table);
+  const bool k_on = top_k >= 1, p_on = top_p < 1.0f;
+  const uint32_t floor_key = ordered_bits(floor_x);
+  RowSet set = *out;
+  Cut cut;
+  cut.k = k_on ? (unsigned)top_k : 0xFFFFFFFFu;
+  cut.m_lo = cut.m_hi = ULLONG_MAX;
+  const u64 p_part = fraction_of(top_p);
+  bool settled = false;
+  {
     int summed = -1;  // the buffer with the warps' sums of K's weights
     if (!settled && !(k_on || p_on)) {
       const u64 own = w.shift ? sum_from<true>(r, w, table, floor_x)
@@ -1322,7 +988,6 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
       return key > set.key || (key == set.key && i <= set.last);
     };
     if constexpr (!VERIFY) {
-      if (!drawn) {
         auto pair = [&](float x0, float x1, int32_t i, u64(&v)[2]) {
           weights_of(kept(x0, i) ? x0 : -INFINITY, kept(x1, i + 1) ? x1 : -INFINITY, w, table, v);
         };
@@ -1343,15 +1008,441 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
           p.out_idx[b] = i;
           if (p.out_logprob) p.out_logprob[b] = log_ratio(v, set.sum, table);
         });
+    }
+  }
+  *out = set;
+}
+
+// Row b. VERIFY: its set goes to p.sets[b], with the outcome of its draft's
+// test. Otherwise the draw is made and written.
+template <bool VERIFY, typename Row>
+__device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShared& sh, void* smem,
+                                           int64_t b) {
+  constexpr int EPU = Row::EPU, DT = Row::kDT;
+  constexpr bool VEC = Row::kVec, RESIDENT = Row::kResident;
+  const int tid = threadIdx.x;
+  r.place(p, b, smem);
+  if (tid == 0) sh.own_n = 0u;
+
+  // The slice, in four parts, so that the first sweep works as they arrive.
+  const int32_t units = max(0, (r.w_hi - r.w_lo - r.lane + 31) / 32);
+  const int32_t part = ((r.w_hi - r.w_lo + 31) / 32 + 3) / 4;
+  if constexpr (RESIDENT) {
+    const uint64_t pol = evict_first_policy();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      for (int32_t j = c * part; j < min(units, (c + 1) * part); ++j) {
+        const int32_t u = r.w_lo + r.lane + 32 * j;
+        const uint32_t dst = r.slice + (uint32_t)(u - r.u_lo) * 16u;
+        if (VEC && (u + 1) * EPU <= p.V)
+          cp_async16(dst, r.row + (size_t)u * 16, pol);
+        else
+          sts128(dst, load_unit<DT, VEC>(r.row, u, p.V, pol));
       }
-    } else if (r.rank == 0 && tid == 0) {
+      cp_async_commit();
+    }
+  }
+  // the settings of the row, or of its request
+  int64_t s = b;
+  if constexpr (VERIFY) s = find_request(p.offsets, p.n, b, sh);
+  const bool owned = s >= 0;  // the same in every CTA of the cluster
+  const float T = owned ? __ldcg(p.temperature + s) : 0.0f;
+  int32_t top_k = owned && p.top_k ? __ldcg(p.top_k + s) : 0;
+  const float top_p = owned && p.top_p ? __ldcg(p.top_p + s) : 1.0f;
+  const float min_p = owned && p.min_p ? __ldcg(p.min_p + s) : 0.0f;
+  const bool p_on = top_p < 1.0f && top_p > 0.0f;  // NaN: off
+  if (top_p <= 0.0f) top_k = 1;
+  const bool k_on = top_k >= 1;
+  const bool m_on = min_p > 0.0f && T > 0.0f && T < INFINITY;
+  if (m_on && tid == kDrawThreads - 1)
+    sh.floor_step = min_p < 1.0f ? (double)T * log((double)min_p) : 0.0;
+
+  const bool unfiltered = !(k_on || p_on || m_on);
+  // Rows whose mass is asked for sum their weights in the first sweep, in
+  // binary32, relative to 2^c0: the largest of the warp's first logits, as a
+  // power of two. (The sum is over all; what is listed later comes off it.)
+  const bool tails = T > 0.0f && T < 1e30f && p.phase != kLeftOver && (p_on || (unfiltered && !VERIFY));
+  float scale, rh, rl;
+  weight_scale(T, scale, rh, rl);
+  // the same factor as a pair with a positive low half: -inf stays -inf
+  const float th = rh * 0.99999988079071044921875f, tl = (rh - th) + rl;
+  float c0 = 0.0f;
+  Tail tail;
+
+  // The largest logit (NaN counts as -inf).
+  float M = -INFINITY;
+  auto first = [&](auto with_tail) {
+    F2 t[EPU / 2];
+    if constexpr (RESIDENT) cp_async_wait_upto(3);
+    if constexpr (decltype(with_tail)::value) {
+      float m0 = units > 0 ? Row::largest(r.unit(r.w_lo + r.lane)) : -INFINITY;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m0 = fmaxf(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, o));
+      c0 = rintf(m0 * rh);
+      if (!(fabsf(c0) <= 512.0f)) c0 = 0.0f;
+    }
+    const F2 rh2 = f2(th), rl2 = f2(tl), nc = f2(-c0);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if constexpr (RESIDENT) cp_async_wait_upto(3 - c);
+#pragma unroll 2
+      for (int32_t j = c * part; j < min(units, (c + 1) * part); ++j) {
+        const uint4 q = r.unit(r.w_lo + r.lane + 32 * j);
+        M = fmaxf(M, Row::largest(q));
+        if constexpr (decltype(with_tail)::value) tail.add(unit_tail<Row>(q, rh2, rl2, nc, t));
+      }
+    }
+  };
+  if (tails)
+    first(std::true_type{});
+  else
+    first(std::false_type{});
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+  if (!owned) return;
+  if (r.lane < r.nrank) *peer(&sh.wmax[r.rank * kDrawWarps + r.warp], r.lane) = M;
+  if (tid == 0) sh.landed_n = 0u;
+  cluster_barrier();
+  for (int q = r.lane; q < r.nrank * kDrawWarps; q += 32) M = fmaxf(M, sh.wmax[q]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+
+  RowSet set;
+  set.sum = 1ull;
+  set.M = M;
+  set.key = 0u;
+  set.last = -1;
+  set.kind = kNothing;
+  set.accepted = 0;
+  set.request = (int32_t)s;
+  int buf = 0;
+  if (M == -INFINITY) {
+    // no candidate
+  } else if (!(T > 0.0f) || M == INFINITY) {
+    // Greedy, or +inf takes all the mass.
+    set.kind = kOne;
+    set.last = first_equal(r, M, sh);
+  } else {
+    const WeightRow w = weight_row(M, T, p.drop);
+    const uint32_t table = smem_addr(sh.table);
+    // The lowest logit that K may hold: min_p's, and no element whose weight is
+    // zero, which is never drawn.
+    float floor_x = w.lowest;
+    if (m_on) {
+      // the smallest binary32 number from M + T ln(min_p) up
+      const double d = sh.floor_step;
+      const float dh = (float)d, dl = (float)(d - (double)dh);
+      float f = M + dh;
+      const float bb = f - M;
+      const float rest = ((M - (f - bb)) + (dh - bb)) + dl;
+      if (rest > 0.0f && f < M)
+        f = __int_as_float(__float_as_int(f) + (f > 0.0f ? 1 : f < 0.0f ? -1 : 0));
+      if (rest > 0.0f && f == 0.0f) f = 1.40129846e-45f;
+      floor_x = fminf(fmaxf(floor_x, f), M);
+    }
+    const uint32_t floor_key = ordered_bits(floor_x);
+    set.kind = kSet;
+    set.key = floor_key;
+    set.last = INT32_MAX;
+    set.sum = 0ull;
+    Cut cut;
+    cut.k = k_on ? (unsigned)top_k : 0xFFFFFFFFu;
+    cut.m_lo = cut.m_hi = ULLONG_MAX;
+    const u64 p_part = fraction_of(top_p);
+    bool settled = false;
+
+    if (!w.shift && p.phase != kLeftOver && !(VERIFY && unfiltered)) {
+      // Short sets: 12 powers of two down; for a top_k without a top_p, whose last
+      // elements may weigh next to nothing, 16, and 12 nats at low temperatures.
+      const float x_lo =
+          fmaxf(floor_x, M - (tails ? 8.3177662f * T : fmaxf(11.0903549f * T, 12.0f)));
+      unsigned mine = 0u;
+      for (int32_t u0 = r.w_lo; u0 < r.w_hi; u0 += 32) {
+        const int32_t u = u0 + r.lane;
+        uint4 q = make_uint4(0u, 0u, 0u, 0u);
+        bool hit = false;
+        if (u < r.w_hi) {
+          q = r.unit(u);
+          hit = Row::largest(q) >= x_lo;
+        }
+        unsigned lanes = __ballot_sync(0xFFFFFFFFu, hit);
+        if (lanes == 0u) continue;
+        if (hit && tails) {
+          // the unit off the tail, and what is not listed of it on again
+          F2 t[EPU / 2];
+          const float all = unit_tail<Row>(q, f2(th), f2(tl), f2(-c0), t);
+          float left = 0.0f;
+#pragma unroll
+          for (int e = 0; e < EPU / 2; ++e) {
+            float t0, t1;
+            split(t[e], t0, t1);
+            left += Row::element(q, 2 * e) >= x_lo ? 0.0f : t0;
+            left += Row::element(q, 2 * e + 1) >= x_lo ? 0.0f : t1;
+          }
+          tail.add(-all);
+          tail.add(left);
+        }
+        // the hits, a lane's unit at a time
+        do {
+          const int l = __ffs(lanes) - 1;
+          lanes &= lanes - 1u;
+          uint4 s;
+          s.x = __shfl_sync(0xFFFFFFFFu, q.x, l);
+          s.y = __shfl_sync(0xFFFFFFFFu, q.y, l);
+          s.z = __shfl_sync(0xFFFFFFFFu, q.z, l);
+          s.w = __shfl_sync(0xFFFFFFFFu, q.w, l);
+          const float x = Row::element(s, r.lane & (EPU - 1));
+          const bool in = r.lane < EPU && x >= x_lo;
+          const unsigned who = __ballot_sync(0xFFFFFFFFu, in);
+          const unsigned at = mine + __popc(who & ((1u << r.lane) - 1u));
+          if (in && at < (unsigned)kWarpList)
+            sh.own[r.warp * kWarpList + at] =
+                make_uint2(__float_as_uint(x), (uint32_t)((u0 + l) * EPU + r.lane));
+          mine += __popc(who);
+        } while (lanes);
+        if (mine > (unsigned)kWarpList) break;
+      }
+      // To rank 0: the list, where it falls, and the tail in units of 2^-44. A NaN
+      // or an overflow makes the tail one; the list does not count then.
+      const float to_units = ex2_approx(c0 - w.c + 44.0f);
+      const float total = tail.hi + tail.lo;
+      const bool odd = __any_sync(0xFFFFFFFFu, !(fabsf(total) < INFINITY));
+      const u64 t = warp_sum(odd ? 0ull : __float2ull_rn(fmaxf(total, 0.0f) * to_units));
+      {
+        const int at = r.rank * kDrawWarps + r.warp;
+        bool fits = !odd && mine <= (unsigned)kWarpList;
+        unsigned to = 0u;
+        if (r.lane == 0 && fits && mine > 0u) to = atomicAdd(peer(&sh.landed_n, 0), mine);
+        to = __shfl_sync(0xFFFFFFFFu, to, 0);
+        fits = fits && to + mine <= (unsigned)kLandList;
+        __syncwarp();
+        if (fits)
+          for (unsigned j = r.lane; j < mine; j += 32)
+            *peer(&sh.row.landed[to + j], 0) = sh.own[r.warp * kWarpList + j];
+        if (r.lane == 0) {
+          *peer(&sh.count[at], 0) = fits ? mine : 0xFFFFFFFFu;
+          *peer(&sh.landed_at[at], 0) = to;
+          *peer(&sh.sums[buf][at], 0) = t;
+        }
+      }
+      if (p.phase == kShortOnly) {
+        // rank 0 goes on alone; the others make room for the next row's
+        cluster_arrive();
+        if (r.rank != 0) return;
+        cluster_wait();
+      } else {
+        cluster_barrier();
+      }
+      bool ok = false;
+      if (r.rank == 0) {
+        const int n = in_order(sh, r.nrank * kDrawWarps);
+        if (n >= 0) {
+          const int per = (n + kDrawThreads - 1) / kDrawThreads;
+          u64 we[3] = {0ull, 0ull, 0ull}, own = 0ull;
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const int j = tid * per + i;
+            if (i < per && j < n) we[i] = weight_of(__uint_as_float(sh.row.list[j].x), w, table);
+            own += we[i];
+          }
+          u64 incl = own;
+          unsigned none = 0u;
+          cta_scan(none, incl, sh);
+          if (tid == kDrawThreads - 1) sh.all_m = incl;
+          __syncthreads();
+          const u64 listed = sh.all_m;
+          u64 rest = 0ull, err = 0ull;
+          if (tails) {
+            for (int q = r.lane; q < r.nrank * kDrawWarps; q += 32) rest += sh.sums[buf][q];
+            rest = warp_sum(rest);
+            // The binary32 tail. In 2^-24 of a term: 23 for y, whose two roundings are
+            // of 2^-20 while |y| < 32 (terms below are less than the V units), 4 for
+            // ex2, 4 for the sum of a unit, 5 for its scale; then what the rounding of
+            // the low parts left of the terms that were listed, and half a unit for
+            // each fixed-point weight.
+            err = __float2ull_ru((float)rest * (40.0f * 5.9604645e-8f)) + (listed >> 34) + (u64)p.V;
+          }
+          if (p_on) {
+            cut.m_lo = max(ceil_part(p_part, listed + rest - min(rest, err)), 1ull);
+            cut.m_hi = ceil_part(p_part, listed + rest + err);
+          }
+          const bool complete = x_lo == floor_x;
+          if (k_on || p_on) {
+            ok = settle(sh, n, per, we, 0u, 0ull, cut, x_lo, M, complete);
+          } else if (unfiltered) {
+            // All elements are K. The warp whose run u falls in is told by the
+            // listed weights and the tails; in it the weights are exact, and the
+            // element stands when u is further from its ends than the error of
+            // what lies before.
+            u64* run = sh.sums[buf];
+            const int segs = r.nrank * kDrawWarps;
+            // each warp's listed weights join its tail
+            u64 c = 0ull;
+            int last = -1;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+              const int j = tid * per + i;
+              if (i < per && j < n) {
+                const int at = r.segment_of((int32_t)sh.row.list[j].y, p.units_per_row, p.units_per_cta);
+                if (at != last && c) {
+                  atomicAdd(&run[last], c);
+                  c = 0ull;
+                }
+                last = at;
+                c += we[i];
+              }
+            }
+            if (c) atomicAdd(&run[last], c);
+            __syncthreads();
+            const u64 f = fraction_of(__ldcg(p.uniform + b));
+            const u64 sum = listed + rest;
+            const u64 t_lo = __umul64hi(f, sum - min(sum, err)), t_hi = __umul64hi(f, sum + err);
+            const u64 here = tid < segs ? run[tid] : 0ull;
+            u64 upto = here;
+            cta_scan(none, upto, sh);
+            if (tid == 0) sh.sel[0] = -1;
+            __syncthreads();
+            if (t_lo >= upto - here && t_lo < upto) {
+              sh.sel[0] = tid;
+              sh.above_m = upto - here;
+            }
+            __syncthreads();
+            const int at = sh.sel[0];
+            const u64 before = sh.above_m;
+            bool hit = false;
+            if (at >= 0 && err <= (sum >> 24)) {
+              RowCtx<DT, VEC, false> g;
+              g.row = r.row;
+              g.V = r.V;
+              const int32_t q0 = at / kDrawWarps * p.units_per_cta;
+              const int32_t qn = min(p.units_per_cta, p.units_per_row - q0);
+              const int32_t each = (qn + kDrawWarps - 1) / kDrawWarps;
+              const int32_t lo = q0 + min(qn, (at % kDrawWarps) * each);
+              const int32_t hi = q0 + min(qn, (at % kDrawWarps + 1) * each);
+              u64 base = before;
+              for (int32_t u0 = lo; u0 < hi; u0 += kDrawThreads) {
+                const int32_t u = u0 + tid;
+                uint4 q = make_uint4(0u, 0u, 0u, 0u);
+                u64 v[EPU], all = 0ull;
+#pragma unroll
+                for (int e = 0; e < EPU; ++e) v[e] = 0ull;
+                if (u < hi) {
+                  q = g.unit(u);
+#pragma unroll
+                  for (int e = 0; e < EPU; e += 2) {
+                    u64 two[2];
+                    weights_of(Row::element(q, e), Row::element(q, e + 1), w, table, two);
+                    v[e] = two[0];
+                    v[e + 1] = two[1];
+                    all += two[0] + two[1];
+                  }
+                }
+                u64 end = all;
+                cta_scan(none, end, sh);
+                u64 from = base + end - all;
+#pragma unroll
+                for (int e = 0; e < EPU; ++e) {
+                  if (v[e] > 0ull && from + err <= t_lo && t_hi + err < from + v[e]) {
+                    hit = true;
+                    p.out_idx[b] = u * EPU + e;
+                    if (p.out_logprob) p.out_logprob[b] = log_ratio(v[e], sum, table);
+                  }
+                  from += v[e];
+                }
+                if (tid == kDrawThreads - 1) sh.all_m = end;
+                __syncthreads();
+                base += sh.all_m;
+                __syncthreads();
+              }
+            }
+            ok = __syncthreads_or(hit ? 1 : 0) != 0;
+          } else {
+            if (tid == 0) {
+              sh.key = floor_key;
+              sh.last = INT32_MAX;
+              sh.sum = listed;
+            }
+            __syncthreads();
+            ok = complete;
+          }
+          if (ok && !VERIFY && !unfiltered) {
+            // The draw, in the list's order, which is the indices'.
+            const uint32_t key = sh.key;
+            const int32_t last = sh.last;
+            const u64 sum = sh.sum;
+            u64 kept = 0ull;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+              const int j = tid * per + i;
+              if (i < per && j < n) {
+                const uint2 q = sh.row.list[j];
+                const uint32_t kj = ordered_bits(__uint_as_float(q.x));
+                if (kj < key || (kj == key && (int32_t)q.y > last)) we[i] = 0ull;
+              }
+              kept += we[i];
+            }
+            const u64 target = __umul64hi(fraction_of(__ldcg(p.uniform + b)), sum);
+            u64 end = kept;
+            cta_scan(none, end, sh);
+            u64 c = end - kept;
+            if (target >= c && target < end) {
+#pragma unroll
+              for (int i = 0; i < 3; ++i) {
+                if (target >= c && target < c + we[i]) {
+                  const int j = tid * per + i;
+                  p.out_idx[b] = (int64_t)sh.row.list[j].y;
+                  if (p.out_logprob)
+                    p.out_logprob[b] = log_ratio(we[i], sum, table);
+                }
+                c += we[i];
+              }
+            }
+          }
+        }
+        if (p.phase != kShortOnly && tid < r.nrank) *peer(&sh.settled, tid) = ok ? 1 : 0;
+      }
+      if (p.phase == kShortOnly) {
+        settled = ok;
+      } else {
+        cluster_barrier();
+        settled = sh.settled != 0;
+      }
+      buf ^= 1;
+      if (settled) {
+        if (VERIFY && r.rank == 0) {
+          set.key = sh.key;
+          set.last = sh.last;
+          set.sum = sh.sum;
+        }
+      }
+    }
+
+    if (p.phase == kShortOnly && !settled) {
+      // left to a second launch
+      if (r.rank == 0 && tid == 0) {
+        if constexpr (VERIFY)
+          p.sets[b].kind = kOpen;
+        else
+          p.out_idx[b] = kOpenIndex;
+      }
+      return;
+    }
+    if (!settled) {
+      settle_long<VERIFY>(p, r, sh, b, M, T, floor_x, k_on ? top_k : 0, p_on ? top_p : 1.0f, buf,
+                          &set);
+    }
+    if constexpr (VERIFY) {
+      if (r.rank == 0 && tid == 0) {
       const int64_t t = __ldcg(p.draft + b);
       if (b + 1 < __ldcg(p.offsets + s + 1) && b + 1 < p.B && t >= 0 && t < p.V) {
         const float x = logit_at<DT>(r.row, t);
         const float u = fminf(fmaxf(__ldcg(p.uniform + b), 0.0f), 0.999999940395355224609375f);
         const float q = p.probs ? __ldcg(p.probs + b * p.probs_ld + t) : 1.0f;
-        const u64 wt = kept(x, (int32_t)t) ? weight_of(x, w, table) : 0ull;
+        const uint32_t key = ordered_bits(x);
+        const bool kept = x >= floor_x && (key > set.key || (key == set.key && (int32_t)t <= set.last));
+        const u64 wt = kept ? weight_of(x, w, table) : 0ull;
         if (wt > 0ull && !((double)u * (double)q * (double)set.sum >= (double)wt)) set.accepted = 1;
+      }
       }
     }
   }
@@ -1367,7 +1458,40 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(const DrawP
       if (p.out_logprob) p.out_logprob[b] = set.kind == kOne ? 0.0f : -INFINITY;
     }
   }
-  cluster_barrier();  // no CTA leaves while another may reach its shared memory
+  // No CTA leaves while another may reach its shared memory. (In a kShortOnly
+  // launch none does from here on.)
+  if (p.phase != kShortOnly) cluster_barrier();
+}
+
+// One cluster a row; a kLeftOver launch has fewer, which take the rows that are
+// open in turn.
+template <int DT, bool VEC, bool RESIDENT, bool VERIFY>
+__global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(
+    const __grid_constant__ DrawParams p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ DrawShared sh;
+  cluster_arrive();
+  RowCtx<DT, VEC, RESIDENT> r;
+  r.rank = (int)cg::this_cluster().block_rank();
+  r.nrank = p.cluster;
+  r.warp = threadIdx.x >> 5;
+  r.lane = threadIdx.x & 31;
+  if (threadIdx.x < kExp2Entries) sh.table[threadIdx.x] = exp2_entry(threadIdx.x);
+  pdl_wait_then_release();
+  cluster_wait();  // every CTA of the cluster runs, before the first write to another
+  int64_t b = blockIdx.x / r.nrank;
+  if (p.phase != kLeftOver) {
+    settle_row<VERIFY>(p, r, sh, smem, b);
+    return;
+  }
+  for (; b < p.B; b += gridDim.x / r.nrank) {
+    // the same in every CTA of the cluster
+    const bool open = VERIFY ? __ldcg(&p.sets[b].kind) == kOpen : __ldcg(p.out_idx + b) == kOpenIndex;
+    if (open) {
+      __syncthreads();
+      settle_row<VERIFY>(p, r, sh, smem, b);
+    }
+  }
 }
 
 // q s rounded to an integer, q clamped to [0, 1] (NaN: 0).

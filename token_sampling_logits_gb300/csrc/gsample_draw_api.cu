@@ -98,28 +98,30 @@ void set_cluster(void* (*kernel)(int, bool, bool, int*), int dtype, bool vec, in
   use_cluster(cluster, p);
 }
 
-// The rows' sets (verification) or draws. While clusters of two CTAs or more
-// for all rows run at once they take one launch; past that a launch with one CTA
-// a row settles the short sets, reading the row twice, and a second one with
-// clusters the rest.
+// The rows' sets (verification) or draws: one launch while the rows' clusters all
+// run at once. Past that one launch settles the short sets, with the smallest
+// clusters, all but one CTA of which leave early; a second one, with the largest
+// clusters and as many as run at once, what is left.
 cudaError_t launch_sets(void* (*kernel)(int, bool, bool, int*), int dtype, bool vec, int64_t rows,
                         int most, DrawParams* p, cudaStream_t stream) {
-  set_cluster(kernel, dtype, vec, rows, most, gsample::draw_smem_limit(), p);
-  int threads = 0;
-  const size_t smem = (size_t)p->units_per_cta * 16;
-  const bool resident = smem <= gsample::draw_smem_limit();
-  void* fn = kernel(dtype, vec, resident, &threads);
-  static const int force = getenv("GS_STREAM") ? atoi(getenv("GS_STREAM")) : -1;
-  const bool one = force >= 0 ? !force : rows <= gsample::clusters_at_once(fn, threads, p->cluster, resident ? smem : 0);
-  if (!one) {
-    DrawParams q = *p;
-    q.phase = gsample::kShortOnly;
-    use_cluster(1, &q);
-    const cudaError_t e = gsample::launch_draw(q, dtype, vec, stream);
-    if (e != cudaSuccess) return e;
-    p->phase = gsample::kLeftOver;
-  }
-  return gsample::launch_draw(*p, dtype, vec, stream);
+  const size_t limit = gsample::draw_smem_limit();
+  auto at_once = [&](const DrawParams& q) {
+    int threads = 0;
+    const size_t smem = (size_t)q.units_per_cta * 16;
+    const bool resident = smem <= limit;
+    void* fn = kernel(dtype, vec, resident, &threads);
+    return gsample::clusters_at_once(fn, threads, q.cluster, resident ? smem : 0);
+  };
+  set_cluster(kernel, dtype, vec, rows, most, limit, p);
+  if (rows <= at_once(*p)) return gsample::launch_draw(*p, dtype, vec, rows, stream);
+  p->phase = gsample::kShortOnly;
+  const cudaError_t e = gsample::launch_draw(*p, dtype, vec, rows, stream);
+  if (e != cudaSuccess) return e;
+  DrawParams q = *p;
+  q.phase = gsample::kLeftOver;
+  set_cluster(kernel, dtype, vec, 1, most, limit, &q);
+  const int64_t n = at_once(q);
+  return gsample::launch_draw(q, dtype, vec, n < 1 ? 1 : n < rows ? n : rows, stream);
 }
 
 }  // namespace

@@ -163,7 +163,8 @@ void* verify_kernel(int dtype, bool vec, bool resident, int* threads);
 void* verify_draw_kernel_fn(int dtype, bool vec, bool resident, int* threads);
 size_t draw_smem_limit();
 int draw_max_cluster(int dtype, bool vec);
-cudaError_t launch_draw(const DrawParams& p, int dtype, bool vec, cudaStream_t stream);
+cudaError_t launch_draw(const DrawParams& p, int dtype, bool vec, int64_t clusters,
+                        cudaStream_t stream);
 cudaError_t launch_verify_draw(const DrawParams& p, int dtype, bool vec, cudaStream_t stream);
 
 cudaError_t launch_debug_weights(const float* x, int64_t n, float M, float T, uint64_t* out,

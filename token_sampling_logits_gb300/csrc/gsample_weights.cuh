@@ -97,24 +97,29 @@ constexpr float kMagicH = 2.5f;               // rounds a weight in [0, 1.5) to 
 constexpr float kMagicL = 1.5f / 2097152.0f;  // rounds what that leaves to 2^-44
 constexpr float kLowestLogit = -3.402823466e38f;
 
-// T > 0 and M finite. Temperatures below 2^-126 count as that. `drop` powers
-// of two are taken off the weights (rows of more than 2^18 elements).
-__device__ __forceinline__ WeightRow weight_row(float M, float T, int drop) {
+// T > 0. Temperatures below 2^-126 count as that.
+__device__ __forceinline__ void weight_scale(float T, float& scale, float& rh, float& rl) {
   constexpr float kLog2eH = 1.44269502162933349609375f, kLog2eL = 1.9259629911266175e-08f;
-  WeightRow w;
   T = fmaxf(T, 1.17549435e-38f);
-  w.scale = T > 1e30f ? 0.25f : 1.0f;
-  const float Ts = T * w.scale;
-  w.rh = w.rl = 0.0f;
+  scale = T > 1e30f ? 0.25f : 1.0f;
+  rh = rl = 0.0f;
   if (T < INFINITY) {
-    const float q = __fdiv_rn(kLog2eH, Ts);
-    const float l = __fdiv_rn(__fadd_rn(__fmaf_rn(-q, Ts, kLog2eH), kLog2eL), Ts);
-    w.rh = __fadd_rn(q, l);
-    w.rl = __fsub_rn(l, __fsub_rn(w.rh, q));
+    const float t = T * scale;
+    const float q = __fdiv_rn(kLog2eH, t);
+    const float l = __fdiv_rn(__fadd_rn(__fmaf_rn(-q, t, kLog2eH), kLog2eL), t);
+    rh = __fadd_rn(q, l);
+    rl = __fsub_rn(l, __fsub_rn(rh, q));
   }
+}
+
+// T > 0 and M finite. `drop` powers of two are taken off the weights (rows of
+// more than 2^18 elements).
+__device__ __forceinline__ WeightRow weight_row(float M, float T, int drop) {
+  WeightRow w;
+  weight_scale(T, w.scale, w.rh, w.rl);
   w.M = M;
   const float c = M * w.rh;
-  const float lowest = M - 42.0f * T;  // 60 powers of two below M
+  const float lowest = M - 42.0f * fmaxf(T, 1.17549435e-38f);  // 60 powers of two below M
   w.lowest = fmaxf(lowest, kLowestLogit);
   w.shift = !(fabsf(c) <= 512.0f) || !(lowest >= kLowestLogit);
   const int steps = w.shift ? 0 : __float2int_rn(c * 256.0f);
