@@ -7,9 +7,9 @@
 
 namespace gsample {
 
-void* draw_kernel_f32(bool vec, bool resident, bool verify);
-void* draw_kernel_bf16(bool vec, bool resident, bool verify);
-void* draw_kernel_f16(bool vec, bool resident, bool verify);
+void* draw_kernel_f32(bool vec, bool verify);
+void* draw_kernel_bf16(bool vec, bool verify);
+void* draw_kernel_f16(bool vec, bool verify);
 void* verify_draw_kernel_f32(bool vec);
 void* verify_draw_kernel_bf16(bool vec);
 void* verify_draw_kernel_f16(bool vec);
@@ -19,7 +19,7 @@ namespace {
 using u64 = unsigned long long;
 constexpr int kDrawThreads = 512;  // as in gsample_draw.cuh
 constexpr int kDrawMaxCluster = 16;
-constexpr size_t kDrawSmemLimit = 76 * 1024;  // of a slice: two CTAs an SM
+constexpr size_t kDrawSmemLimit = 160 * 1024;  // of the units' maxima
 
 __global__ void __launch_bounds__(256) debug_weights_kernel(const float* x, int64_t n, float M,
                                                             float T, u64* out) {
@@ -31,10 +31,10 @@ __global__ void __launch_bounds__(256) debug_weights_kernel(const float* x, int6
     out[j] = weight_of(x[j], w, smem_addr(tab));
 }
 
-void* select_set(int dtype, bool vec, bool resident, bool verify) {
-  return dtype == 0   ? draw_kernel_f32(vec, resident, verify)
-         : dtype == 1 ? draw_kernel_bf16(vec, resident, verify)
-                      : draw_kernel_f16(vec, resident, verify);
+void* select_set(int dtype, bool vec, bool verify) {
+  return dtype == 0   ? draw_kernel_f32(vec, verify)
+         : dtype == 1 ? draw_kernel_bf16(vec, verify)
+                      : draw_kernel_f16(vec, verify);
 }
 
 void* select_verify_draw(int dtype, bool vec) {
@@ -63,33 +63,19 @@ cudaError_t launch_rows(void* fn, const DrawParams& p, int64_t clusters, size_t 
 
 }  // namespace
 
-void* draw_kernel(int dtype, bool vec, bool resident, int* threads) {
-  *threads = kDrawThreads;
-  return select_set(dtype, vec, resident, false);
-}
-
-void* verify_kernel(int dtype, bool vec, bool resident, int* threads) {
-  *threads = kDrawThreads;
-  return select_set(dtype, vec, resident, true);
-}
-
-void* verify_draw_kernel_fn(int dtype, bool vec, bool, int* threads) {
-  *threads = kDrawThreads;
-  return select_verify_draw(dtype, vec);
-}
-
+void* draw_kernel(int dtype, bool vec, bool verify) { return select_set(dtype, vec, verify); }
+void* verify_draw_kernel_fn(int dtype, bool vec) { return select_verify_draw(dtype, vec); }
+int draw_threads() { return kDrawThreads; }
 size_t draw_smem_limit() { return kDrawSmemLimit; }
 
 // One-time per-device setup of the kernels of (dtype, vec): clusters of up to
-// 16 CTAs and the full shared-memory slice, then the largest cluster that the
-// device co-schedules.
+// 16 CTAs and the shared memory for the units' maxima, then the largest cluster
+// that the device co-schedules.
 int draw_max_cluster(int dtype, bool vec) {
   int size = kDrawMaxCluster;
-  for (int v = 0; v < 5; ++v) {
-    const bool res = v & 1;
-    void* fn = v == 4 ? select_verify_draw(dtype, vec)
-                      : select_set(dtype, vec, res, v >= 2);
-    const int smem = v < 4 && res ? (int)kDrawSmemLimit : 0;
+  for (int v = 0; v < 3; ++v) {
+    void* fn = v == 2 ? select_verify_draw(dtype, vec) : select_set(dtype, vec, v != 0);
+    const int smem = v < 2 ? (int)kDrawSmemLimit : 0;
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
       return 0;
@@ -113,10 +99,8 @@ int draw_max_cluster(int dtype, bool vec) {
 
 cudaError_t launch_draw(const DrawParams& p, int dtype, bool vec, int64_t clusters,
                         cudaStream_t stream) {
-  const size_t need = (size_t)p.units_per_cta * 16;
-  const bool resident = need <= kDrawSmemLimit;
-  void* fn = select_set(dtype, vec, resident, p.sets != nullptr);
-  return launch_rows(fn, p, clusters, resident ? need : 0, stream);
+  return launch_rows(select_set(dtype, vec, p.sets != nullptr), p, clusters,
+                     p.maxima ? draw_smem(p.units_per_cta) : 0, stream);
 }
 
 cudaError_t launch_verify_draw(const DrawParams& p, int dtype, bool vec, cudaStream_t stream) {

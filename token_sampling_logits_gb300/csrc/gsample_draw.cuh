@@ -38,6 +38,7 @@
 #include <cstdint>
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "gsample_internal.h"
 #include "gsample_slice.cuh"
@@ -145,11 +146,14 @@ struct alignas(16) DrawShared {
 
 static_assert(offsetof(DrawShared, hist) % 16 == 0, "the histogram is read as uint4");
 
+// Cluster barriers. Not the .aligned forms, which are undefined where the lanes of
+// a warp have not met again after a branch of their own.
 __device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_barrier() {
   cluster_arrive();
@@ -163,29 +167,32 @@ __device__ __forceinline__ T* peer(T* p, int rank) {
 }
 
 // One row's work within its cluster: the slice of this CTA and how to read it.
-template <int DT, bool VEC, bool RESIDENT>
+template <int DT, bool VEC>
 struct RowCtx {
   using C = HCfg<DT, VEC>;
   static constexpr int EPU = C::kEPU, kDT = DT;
-  static constexpr bool kVec = VEC, kResident = RESIDENT;
+  static constexpr bool kVec = VEC;
+  static constexpr bool kHalfMaxima = VEC && DT == 2;  // unit maxima as f16, else as bf16
   static constexpr int kFlush = 256 / EPU;  // units between joins of a WeightSum
   const char* row;
   int32_t V, u_lo, u_hi;
-  uint32_t slice;
   int rank, nrank, warp, lane;
   int32_t w_lo, w_hi;  // units of this warp
 
-  __device__ __forceinline__ void place(const DrawParams& p, int64_t b, void* smem) {
+  __device__ __forceinline__ void place(const DrawParams& p, int64_t b) {
     row = p.logits + b * p.ld_bytes;
     V = p.V;
     u_lo = min(p.units_per_row, rank * p.units_per_cta);
     u_hi = min(p.units_per_row, u_lo + p.units_per_cta);
-    slice = smem_addr(smem);
     run_of(warp, w_lo, w_hi);
   }
 
+  // A warp's run is a multiple of eight units, but for the last.
+  static __device__ __forceinline__ int32_t run_length(int32_t n) {
+    return ((n + kDrawWarps - 1) / kDrawWarps + 7) / 8 * 8;
+  }
   __device__ __forceinline__ void run_of(int w, int32_t& lo, int32_t& hi) const {
-    const int32_t n = u_hi - u_lo, per = (n + kDrawWarps - 1) / kDrawWarps;
+    const int32_t n = u_hi - u_lo, per = run_length(n);
     lo = u_lo + min(n, w * per);
     hi = u_lo + min(n, (w + 1) * per);
   }
@@ -193,31 +200,44 @@ struct RowCtx {
   // The warp that holds element i of the row, counted over the cluster.
   __device__ __forceinline__ int segment_of(int32_t i, int32_t units, int32_t per_cta) const {
     const int32_t u = i / EPU, q = u / per_cta;
-    const int32_t n = min(per_cta, units - q * per_cta), per = (n + kDrawWarps - 1) / kDrawWarps;
-    return q * kDrawWarps + (u - q * per_cta) / per;
+    return q * kDrawWarps + (u - q * per_cta) / run_length(min(per_cta, units - q * per_cta));
   }
 
   // The warp that holds element i of this CTA's slice.
   __device__ __forceinline__ int warp_of(int32_t i) const {
-    const int32_t per = (u_hi - u_lo + kDrawWarps - 1) / kDrawWarps;
-    return (i / EPU - u_lo) / per;
+    return (i / EPU - u_lo) / run_length(u_hi - u_lo);
   }
 
+  // The logits are read once from memory, and where a row is read again, from L2.
   __device__ __forceinline__ uint4 unit(int32_t u) const {
-    if constexpr (RESIDENT) {
-      return lds128(slice + (uint32_t)(u - u_lo) * 16u);
-    } else {
-      if constexpr (VEC) {
-        if ((u + 1) * EPU <= V) {
-          uint4 v;
-          asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                       : "l"(row + (size_t)u * 16));
-          return v;
-        }
+    if constexpr (VEC) {
+      if ((u + 1) * EPU <= V) {
+        uint4 v;
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(row + (size_t)u * 16));
+        return v;
       }
-      return load_unit<DT, VEC>(row, u, V, 0ull);
     }
+    return load_unit<DT, VEC>(row, u, V, 0ull);
+  }
+
+  static __device__ __forceinline__ uint4 no_unit() {  // all -inf
+    const uint32_t n = C::kF32Bits ? 0xFF800000u : DT == 1 ? 0xFF80FF80u : 0xFC00FC00u;
+    return make_uint4(n, n, n, n);
+  }
+
+  // A unit's largest element, rounded up to sixteen bits; and what it is at most.
+  static __device__ __forceinline__ uint32_t short_of(float x) {
+    if constexpr (kHalfMaxima) {
+      return __half_as_ushort(__float2half_ru(x));
+    } else {
+      const uint32_t b = __float_as_uint(x);
+      return (b & 0x80000000u ? b : b + 0xFFFFu) >> 16;
+    }
+  }
+  static __device__ __forceinline__ float of_short(uint32_t s) {
+    return half_to_f32<kHalfMaxima ? 2 : 1>(s);
   }
 
   static __device__ __forceinline__ float element(const uint4& r, int e) {
@@ -230,22 +250,31 @@ struct RowCtx {
       return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
                    fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
     } else {
+      return largest_short<DT>(r);
+    }
+  }
+  // The same of eight 16-bit numbers.
+  template <int D>
+  static __device__ __forceinline__ float largest_short(const uint4& r) {
+    {
       uint32_t m;
-      if constexpr (DT == 1)
+      if constexpr (D == 1)
         asm("{.reg .b32 a, b;\n max.bf16x2 a, %1, %2;\n max.bf16x2 b, %3, %4;\n max.bf16x2 %0, a, b;}"
             : "=r"(m) : "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w));
       else
         asm("{.reg .b32 a, b;\n max.f16x2 a, %1, %2;\n max.f16x2 b, %3, %4;\n max.f16x2 %0, a, b;}"
             : "=r"(m) : "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w));
-      return fmaxf(half_to_f32<DT>(m & 0xFFFFu), half_to_f32<DT>(m >> 16));
+      return fmaxf(half_to_f32<D>(m & 0xFFFFu), half_to_f32<D>(m >> 16));
     }
   }
 
   // f(x, i) on every element of this thread's units, in index order.
   template <typename F>
   __device__ __forceinline__ void each(F&& f) const {
+    uint4 next = w_lo + lane < w_hi ? unit(w_lo + lane) : no_unit();
     for (int32_t u = w_lo + lane; u < w_hi; u += 32) {
-      const uint4 r = unit(u);
+      const uint4 r = next;
+      if (u + 32 < w_hi) next = unit(u + 32);
 #pragma unroll
       for (int e = 0; e < EPU; ++e) f(element(r, e), u * EPU + e);
     }
@@ -255,8 +284,10 @@ struct RowCtx {
   template <typename F, typename G>
   __device__ __forceinline__ void each_pair(F&& f, G&& g) const {
     int n = 0;
+    uint4 next = w_lo + lane < w_hi ? unit(w_lo + lane) : no_unit();
     for (int32_t u = w_lo + lane; u < w_hi; u += 32) {
-      const uint4 r = unit(u);
+      const uint4 r = next;
+      if (u + 32 < w_hi) next = unit(u + 32);
 #pragma unroll
       for (int e = 0; e < EPU; e += 2) f(element(r, e), element(r, e + 1), u * EPU + e);
       if (++n == kFlush) {
@@ -336,7 +367,7 @@ __device__ __forceinline__ void find_index(const Row& r, DrawShared& sh, int buf
   const int l = __ffs(past) - 1;
   u64 before = __shfl_sync(0xFFFFFFFFu, incl - own, l);
   int at = l * kPer;
-  while (before + sh.sums[buf][at] <= target) before += sh.sums[buf][at++];
+  while (at + 1 < n && before + sh.sums[buf][at] <= target) before += sh.sums[buf][at++];
   if (at / kDrawWarps != r.rank) return;
   u64 left = target - before;
   int32_t lo, hi;
@@ -1016,31 +1047,14 @@ __device__ __noinline__ void settle_long(const DrawParams& p, const Row& r, Draw
 // Row b. VERIFY: its set goes to p.sets[b], with the outcome of its draft's
 // test. Otherwise the draw is made and written.
 template <bool VERIFY, typename Row>
-__device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShared& sh, void* smem,
-                                           int64_t b) {
+__device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShared& sh,
+                                           uint16_t* maxima, int64_t b) {
   constexpr int EPU = Row::EPU, DT = Row::kDT;
-  constexpr bool VEC = Row::kVec, RESIDENT = Row::kResident;
   const int tid = threadIdx.x;
-  r.place(p, b, smem);
-  if (tid == 0) sh.own_n = 0u;
-
-  // The slice, in four parts, so that the first sweep works as they arrive.
-  const int32_t units = max(0, (r.w_hi - r.w_lo - r.lane + 31) / 32);
-  const int32_t part = ((r.w_hi - r.w_lo + 31) / 32 + 3) / 4;
-  if constexpr (RESIDENT) {
-    const uint64_t pol = evict_first_policy();
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      for (int32_t j = c * part; j < min(units, (c + 1) * part); ++j) {
-        const int32_t u = r.w_lo + r.lane + 32 * j;
-        const uint32_t dst = r.slice + (uint32_t)(u - r.u_lo) * 16u;
-        if (VEC && (u + 1) * EPU <= p.V)
-          cp_async16(dst, r.row + (size_t)u * 16, pol);
-        else
-          sts128(dst, load_unit<DT, VEC>(r.row, u, p.V, pol));
-      }
-      cp_async_commit();
-    }
+  r.place(p, b);
+  if (tid == 0) {
+    sh.own_n = 0u;
+    sh.landed_n = 0u;
   }
   // the settings of the row, or of its request
   int64_t s = b;
@@ -1069,27 +1083,44 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
   float c0 = 0.0f;
   Tail tail;
 
-  // The largest logit (NaN counts as -inf).
+  if (!owned) return;
+
+  // The largest logit (NaN counts as -inf). A unit's own maximum is kept in
+  // sixteen bits, so that the units to list are found without the row: the
+  // second look at 304 KB of logits takes 38 KB of shared memory.
   float M = -INFINITY;
+  const bool listing = p.phase != kLeftOver && p.maxima;
   auto first = [&](auto with_tail) {
+    constexpr int kBatch = 4;
     F2 t[EPU / 2];
-    if constexpr (RESIDENT) cp_async_wait_upto(3);
-    if constexpr (decltype(with_tail)::value) {
-      float m0 = units > 0 ? Row::largest(r.unit(r.w_lo + r.lane)) : -INFINITY;
+    const F2 rh2 = f2(th), rl2 = f2(tl);
+    F2 nc = f2(0.0f);
+    const int32_t pad = r.u_lo + (r.w_hi - r.u_lo + 7) / 8 * 8;  // of the last run
+    for (int32_t u0 = r.w_lo; u0 < r.w_hi; u0 += 32 * kBatch) {
+      uint4 q[kBatch];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m0 = fmaxf(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, o));
-      c0 = rintf(m0 * rh);
-      if (!(fabsf(c0) <= 512.0f)) c0 = 0.0f;
-    }
-    const F2 rh2 = f2(th), rl2 = f2(tl), nc = f2(-c0);
+      for (int i = 0; i < kBatch; ++i) {
+        const int32_t u = u0 + 32 * i + r.lane;
+        q[i] = Row::no_unit();
+        if (u < r.w_hi) q[i] = r.unit(u);
+      }
+      if constexpr (decltype(with_tail)::value) {
+        if (u0 == r.w_lo) {
+          float m0 = Row::largest(q[0]);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if constexpr (RESIDENT) cp_async_wait_upto(3 - c);
-#pragma unroll 2
-      for (int32_t j = c * part; j < min(units, (c + 1) * part); ++j) {
-        const uint4 q = r.unit(r.w_lo + r.lane + 32 * j);
-        M = fmaxf(M, Row::largest(q));
-        if constexpr (decltype(with_tail)::value) tail.add(unit_tail<Row>(q, rh2, rl2, nc, t));
+          for (int o = 16; o > 0; o >>= 1) m0 = fmaxf(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, o));
+          c0 = rintf(m0 * rh);
+          if (!(fabsf(c0) <= 512.0f)) c0 = 0.0f;
+          nc = f2(-c0);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int32_t u = u0 + 32 * i + r.lane;
+        const float m = Row::largest(q[i]);
+        M = fmaxf(M, m);
+        if (listing && u < pad) maxima[u - r.u_lo] = (uint16_t)Row::short_of(fmaxf(m, -INFINITY));
+        if constexpr (decltype(with_tail)::value) tail.add(unit_tail<Row>(q[i], rh2, rl2, nc, t));
       }
     }
   };
@@ -1099,9 +1130,7 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
     first(std::false_type{});
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-  if (!owned) return;
   if (r.lane < r.nrank) *peer(&sh.wmax[r.rank * kDrawWarps + r.warp], r.lane) = M;
-  if (tid == 0) sh.landed_n = 0u;
   cluster_barrier();
   for (int q = r.lane; q < r.nrank * kDrawWarps; q += 32) M = fmaxf(M, sh.wmax[q]);
 #pragma unroll
@@ -1151,23 +1180,54 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
     const u64 p_part = fraction_of(top_p);
     bool settled = false;
 
-    if (!w.shift && p.phase != kLeftOver && !(VERIFY && unfiltered)) {
+    if (!w.shift && listing && !(VERIFY && unfiltered)) {
       // Short sets: 12 powers of two down; for a top_k without a top_p, whose last
       // elements may weigh next to nothing, 16, and 12 nats at low temperatures.
       const float x_lo =
           fmaxf(floor_x, M - (tails ? 8.3177662f * T : fmaxf(11.0903549f * T, 12.0f)));
-      unsigned mine = 0u;
-      for (int32_t u0 = r.w_lo; u0 < r.w_hi; u0 += 32) {
-        const int32_t u = u0 + r.lane;
+      // the units to list, in order
+      unsigned* todo = reinterpret_cast<unsigned*>(sh.row.list) + r.warp * kWarpList;
+      unsigned n_units = 0u;
+      for (int32_t u0 = r.w_lo; u0 < r.w_hi; u0 += 256) {
+        const int32_t u = u0 + r.lane * 8;
         uint4 q = make_uint4(0u, 0u, 0u, 0u);
         bool hit = false;
         if (u < r.w_hi) {
-          q = r.unit(u);
-          hit = Row::largest(q) >= x_lo;
+          q = lds128(smem_addr(maxima) + (uint32_t)(u - r.u_lo) * 2u);
+          hit = Row::template largest_short<Row::kHalfMaxima ? 2 : 1>(q) >= x_lo;
         }
-        unsigned lanes = __ballot_sync(0xFFFFFFFFu, hit);
-        if (lanes == 0u) continue;
-        if (hit && tails) {
+        if (__ballot_sync(0xFFFFFFFFu, hit) == 0u) continue;
+        unsigned in = 0u;
+        if (hit) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t s = word_of(q, e >> 1) >> ((e & 1) * 16) & 0xFFFFu;
+            in |= Row::of_short(s) >= x_lo ? 1u << e : 0u;
+          }
+        }
+        const unsigned c = __popc(in);
+        unsigned incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+          if (r.lane >= o) incl += t;
+        }
+        unsigned at = n_units + incl - c;
+        n_units += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        if (n_units > (unsigned)kWarpList) break;
+        for (; in; in &= in - 1u) todo[at++] = (unsigned)(u + __ffs(in) - 1);
+      }
+      __syncwarp();
+      // their elements, a unit a lane
+      unsigned mine = n_units > (unsigned)kWarpList ? kWarpList + 1u : 0u;
+      for (unsigned i0 = 0; i0 < n_units && mine <= (unsigned)kWarpList; i0 += 32) {
+        const bool some = i0 + r.lane < n_units;
+        const int32_t u = some ? (int32_t)todo[i0 + r.lane] : 0;
+        const uint4 q = some ? r.unit(u) : Row::no_unit();
+        unsigned c = 0u;
+#pragma unroll
+        for (int e = 0; e < EPU; ++e) c += Row::element(q, e) >= x_lo ? 1u : 0u;
+        if (tails && c) {
           // the unit off the tail, and what is not listed of it on again
           F2 t[EPU / 2];
           const float all = unit_tail<Row>(q, f2(th), f2(tl), f2(-c0), t);
@@ -1182,32 +1242,36 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
           tail.add(-all);
           tail.add(left);
         }
-        // the hits, a lane's unit at a time
-        do {
-          const int l = __ffs(lanes) - 1;
-          lanes &= lanes - 1u;
-          uint4 s;
-          s.x = __shfl_sync(0xFFFFFFFFu, q.x, l);
-          s.y = __shfl_sync(0xFFFFFFFFu, q.y, l);
-          s.z = __shfl_sync(0xFFFFFFFFu, q.z, l);
-          s.w = __shfl_sync(0xFFFFFFFFu, q.w, l);
-          const float x = Row::element(s, r.lane & (EPU - 1));
-          const bool in = r.lane < EPU && x >= x_lo;
-          const unsigned who = __ballot_sync(0xFFFFFFFFu, in);
-          const unsigned at = mine + __popc(who & ((1u << r.lane) - 1u));
-          if (in && at < (unsigned)kWarpList)
-            sh.own[r.warp * kWarpList + at] =
-                make_uint2(__float_as_uint(x), (uint32_t)((u0 + l) * EPU + r.lane));
-          mine += __popc(who);
-        } while (lanes);
-        if (mine > (unsigned)kWarpList) break;
+        unsigned incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+          if (r.lane >= o) incl += t;
+        }
+        unsigned at = mine + incl - c;
+        mine += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        if (mine <= (unsigned)kWarpList) {
+#pragma unroll
+          for (int e = 0; e < EPU; ++e) {
+            const float x = Row::element(q, e);
+            if (x >= x_lo)
+              sh.own[r.warp * kWarpList + at++] =
+                  make_uint2(__float_as_uint(x), (uint32_t)(u * EPU + e));
+          }
+        }
       }
-      // To rank 0: the list, where it falls, and the tail in units of 2^-44. A NaN
-      // or an overflow makes the tail one; the list does not count then.
-      const float to_units = ex2_approx(c0 - w.c + 44.0f);
-      const float total = tail.hi + tail.lo;
-      const bool odd = __any_sync(0xFFFFFFFFu, !(fabsf(total) < INFINITY));
-      const u64 t = warp_sum(odd ? 0ull : __float2ull_rn(fmaxf(total, 0.0f) * to_units));
+      // To rank 0: the list, where it falls, and the tail in units of 2^-44, exact
+      // up to the fraction of C. A NaN or an overflow makes the tail one; the list
+      // does not count then.
+      const float whole = floorf(w.c);
+      const float power = c0 - whole + 44.0f;
+      bool odd = !(fabsf(tail.hi) + fabsf(tail.lo) < INFINITY) || !(fabsf(power) <= 100.0f);
+      odd = __any_sync(0xFFFFFFFFu, odd);
+      const float to_units = __int_as_float(((int)(odd ? 0.0f : power) + 127) << 23);
+      long long sum = 0;
+      if (!odd) sum = __float2ll_rn(tail.hi * to_units) + __float2ll_rn(tail.lo * to_units);
+      sum = (long long)warp_sum((u64)sum);
+      const u64 t = sum > 0 ? __float2ull_rn((float)sum * ex2_approx(whole - w.c)) : 0ull;
       {
         const int at = r.rank * kDrawWarps + r.warp;
         bool fits = !odd && mine <= (unsigned)kWarpList;
@@ -1311,12 +1375,9 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
             const u64 before = sh.above_m;
             bool hit = false;
             if (at >= 0 && err <= (sum >> 24)) {
-              RowCtx<DT, VEC, false> g;
-              g.row = r.row;
-              g.V = r.V;
               const int32_t q0 = at / kDrawWarps * p.units_per_cta;
               const int32_t qn = min(p.units_per_cta, p.units_per_row - q0);
-              const int32_t each = (qn + kDrawWarps - 1) / kDrawWarps;
+              const int32_t each = Row::run_length(qn);
               const int32_t lo = q0 + min(qn, (at % kDrawWarps) * each);
               const int32_t hi = q0 + min(qn, (at % kDrawWarps + 1) * each);
               u64 base = before;
@@ -1327,7 +1388,7 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
 #pragma unroll
                 for (int e = 0; e < EPU; ++e) v[e] = 0ull;
                 if (u < hi) {
-                  q = g.unit(u);
+                  q = r.unit(u);
 #pragma unroll
                   for (int e = 0; e < EPU; e += 2) {
                     u64 two[2];
@@ -1465,13 +1526,13 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
 
 // One cluster a row; a kLeftOver launch has fewer, which take the rows that are
 // open in turn.
-template <int DT, bool VEC, bool RESIDENT, bool VERIFY>
+template <int DT, bool VEC, bool VERIFY>
 __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(
     const __grid_constant__ DrawParams p) {
-  extern __shared__ __align__(16) unsigned char smem[];
+  extern __shared__ __align__(16) uint16_t maxima[];
   __shared__ DrawShared sh;
   cluster_arrive();
-  RowCtx<DT, VEC, RESIDENT> r;
+  RowCtx<DT, VEC> r;
   r.rank = (int)cg::this_cluster().block_rank();
   r.nrank = p.cluster;
   r.warp = threadIdx.x >> 5;
@@ -1481,7 +1542,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(
   cluster_wait();  // every CTA of the cluster runs, before the first write to another
   int64_t b = blockIdx.x / r.nrank;
   if (p.phase != kLeftOver) {
-    settle_row<VERIFY>(p, r, sh, smem, b);
+    settle_row<VERIFY>(p, r, sh, maxima, b);
     return;
   }
   for (; b < p.B; b += gridDim.x / r.nrank) {
@@ -1489,7 +1550,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(
     const bool open = VERIFY ? __ldcg(&p.sets[b].kind) == kOpen : __ldcg(p.out_idx + b) == kOpenIndex;
     if (open) {
       __syncthreads();
-      settle_row<VERIFY>(p, r, sh, smem, b);
+      settle_row<VERIFY>(p, r, sh, maxima, b);
     }
   }
 }
@@ -1507,7 +1568,7 @@ __device__ __forceinline__ u64 times_probability(u64 s, float q) {
 // probabilities), or from p of the last row when all did.
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const DrawParams p) {
-  using Row = RowCtx<DT, VEC, false>;
+  using Row = RowCtx<DT, VEC>;
   __shared__ DrawShared sh;
   const int tid = threadIdx.x;
   cluster_arrive();
@@ -1554,7 +1615,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Draw
   }
   if (set.kind != kSet) return;  // the whole cluster
 
-  r.place(p, stop, nullptr);
+  r.place(p, stop);
   const WeightRow w = weight_row(set.M, __ldcg(p.temperature + i), p.drop);
   const uint32_t table = smem_addr(sh.table);
   bool rest = stop != r1 - 1;
@@ -1598,22 +1659,14 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Draw
   cluster_barrier();
 }
 
-// The kernels of one dtype: (vec, resident, verify), or the verification's draw.
+// The kernels of one dtype.
 template <int DT>
-void* draw_kernel_of(bool vec, bool resident, bool verify) {
-#define GSAMPLE_SET(V, R, F) \
-  if (vec == V && resident == R && verify == F) \
-    return reinterpret_cast<void*>(&filter_set_kernel<DT, V, R, F>);
-  GSAMPLE_SET(false, false, false)
-  GSAMPLE_SET(false, false, true)
-  GSAMPLE_SET(false, true, false)
-  GSAMPLE_SET(false, true, true)
-  GSAMPLE_SET(true, false, false)
-  GSAMPLE_SET(true, false, true)
-  GSAMPLE_SET(true, true, false)
-  GSAMPLE_SET(true, true, true)
-#undef GSAMPLE_SET
-  return nullptr;
+void* draw_kernel_of(bool vec, bool verify) {
+  if (vec)
+    return verify ? reinterpret_cast<void*>(&filter_set_kernel<DT, true, true>)
+                  : reinterpret_cast<void*>(&filter_set_kernel<DT, true, false>);
+  return verify ? reinterpret_cast<void*>(&filter_set_kernel<DT, false, true>)
+                : reinterpret_cast<void*>(&filter_set_kernel<DT, false, false>);
 }
 
 template <int DT>

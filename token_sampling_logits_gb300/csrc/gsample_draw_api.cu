@@ -72,55 +72,44 @@ void use_cluster(int cluster, DrawParams* p) {
   p->units_per_cta = (p->units_per_row + cluster - 1) / cluster;
 }
 
-// The cluster size for `rows` clusters: the largest (at most `most`, with at
-// least kUnitsPerCta units a CTA) whose clusters all run at once; else the
-// smallest whose slices fit in shared memory.
-void set_cluster(void* (*kernel)(int, bool, bool, int*), int dtype, bool vec, int64_t rows,
-                 int most, size_t limit, DrawParams* p) {
-  const int64_t nu = p->units_per_row;
+// The largest cluster size (at most `most`, with at least kUnitsPerCta units a
+// CTA) at which `rows` clusters run at once, else 1.
+int fitting_cluster(void* fn, bool maxima, int64_t rows, int most, const DrawParams& p) {
+  const int64_t nu = p.units_per_row;
   int64_t top = (nu + kUnitsPerCta - 1) / kUnitsPerCta;
   if (top > most) top = most;
-  int cluster = 0, fits = 0;
-  for (int c = (int)top; c >= 1; --c) {
-    const size_t smem = (size_t)((nu + c - 1) / c) * 16;
-    const bool resident = smem <= limit;
-    if (limit > 0 && !resident) break;
-    fits = c;
-    int threads = 0;
-    void* fn = kernel(dtype, vec, resident, &threads);
-    if (rows <= gsample::clusters_at_once(fn, threads, c, resident ? smem : 0)) {
-      cluster = c;
-      break;
-    }
+  for (int c = (int)top; c > 1; --c) {
+    const size_t smem = maxima ? gsample::draw_smem((int32_t)((nu + c - 1) / c)) : 0;
+    if (smem > gsample::draw_smem_limit()) break;
+    if (rows <= gsample::clusters_at_once(fn, gsample::draw_threads(), c, smem)) return c;
   }
-  if (cluster == 0) cluster = fits > 0 ? fits : (int)top;
-  if (const char* e = getenv("GS_CLUSTER")) cluster = atoi(e);
-  use_cluster(cluster, p);
+  return 1;
 }
 
-// The rows' sets (verification) or draws: one launch while the rows' clusters all
-// run at once. Past that one launch settles the short sets, with the smallest
-// clusters, all but one CTA of which leave early; a second one, with the largest
-// clusters and as many as run at once, what is left.
-cudaError_t launch_sets(void* (*kernel)(int, bool, bool, int*), int dtype, bool vec, int64_t rows,
-                        int most, DrawParams* p, cudaStream_t stream) {
+// The rows' sets (verification) or draws. With clusters of kOneLaunch CTAs or
+// more for all rows at once they take one launch. Otherwise one launch settles
+// the short sets, and a second one, with the largest clusters and as many as run
+// at once, what is left: a CTA or two would take long for a long row.
+constexpr int kOneLaunch = 4;
+cudaError_t launch_sets(int dtype, bool vec, int64_t rows, int most, DrawParams* p,
+                        cudaStream_t stream) {
+  void* fn = gsample::draw_kernel(dtype, vec, p->sets != nullptr);
   const size_t limit = gsample::draw_smem_limit();
-  auto at_once = [&](const DrawParams& q) {
-    int threads = 0;
-    const size_t smem = (size_t)q.units_per_cta * 16;
-    const bool resident = smem <= limit;
-    void* fn = kernel(dtype, vec, resident, &threads);
-    return gsample::clusters_at_once(fn, threads, q.cluster, resident ? smem : 0);
-  };
-  set_cluster(kernel, dtype, vec, rows, most, limit, p);
-  if (rows <= at_once(*p)) return gsample::launch_draw(*p, dtype, vec, rows, stream);
+  int c = fitting_cluster(fn, true, rows, most, *p);
+  if (const char* e = getenv("GS_CLUSTER")) c = atoi(e);
+  while (c < most && gsample::draw_smem((p->units_per_row + c - 1) / c) > limit) ++c;
+  use_cluster(c, p);
+  p->maxima = gsample::draw_smem(p->units_per_cta) <= limit;
+  static const int one = getenv("GS_ONE") ? atoi(getenv("GS_ONE")) : kOneLaunch;
+  if (c >= one || !p->maxima) return gsample::launch_draw(*p, dtype, vec, rows, stream);
   p->phase = gsample::kShortOnly;
   const cudaError_t e = gsample::launch_draw(*p, dtype, vec, rows, stream);
   if (e != cudaSuccess) return e;
   DrawParams q = *p;
   q.phase = gsample::kLeftOver;
-  set_cluster(kernel, dtype, vec, 1, most, limit, &q);
-  const int64_t n = at_once(q);
+  q.maxima = false;
+  use_cluster(fitting_cluster(fn, false, 1, most, q), &q);
+  const int64_t n = gsample::clusters_at_once(fn, gsample::draw_threads(), q.cluster, 0);
   return gsample::launch_draw(q, dtype, vec, n < 1 ? 1 : n < rows ? n : rows, stream);
 }
 
@@ -158,8 +147,7 @@ gsample_status gsample_filtered_categorical(const void* logits, gsample_dtype dt
   p.out_idx = out_idx;
   p.out_logprob = out_logprob;
   try {
-    return launched(launch_sets(gsample::draw_kernel, (int)dtype, vec, B, most, &p,
-                                (cudaStream_t)stream));
+    return launched(launch_sets((int)dtype, vec, B, most, &p, (cudaStream_t)stream));
   } catch (...) {
     return GSAMPLE_ERR_CUDA;
   }
@@ -216,11 +204,11 @@ gsample_status gsample_verify_drafts(const void* logits, gsample_dtype dtype, in
   p.sets = static_cast<gsample::RowSet*>(workspace);
   try {
     if (R > 0) {
-      st = launched(launch_sets(gsample::verify_kernel, (int)dtype, vec, R, most, &p,
-                                (cudaStream_t)stream));
+      st = launched(launch_sets((int)dtype, vec, R, most, &p, (cudaStream_t)stream));
       if (st != GSAMPLE_OK) return st;
     }
-    set_cluster(gsample::verify_draw_kernel_fn, (int)dtype, vec, n, most, 0, &p);
+    use_cluster(fitting_cluster(gsample::verify_draw_kernel_fn((int)dtype, vec), false, n, most, p),
+                &p);
   } catch (...) {
     return GSAMPLE_ERR_CUDA;
   }

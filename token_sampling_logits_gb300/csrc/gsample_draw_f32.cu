@@ -3,8 +3,8 @@
 
 namespace gsample {
 
-void* draw_kernel_f32(bool vec, bool resident, bool verify) {
-  return draw_kernel_of<0>(vec, resident, verify);
+void* draw_kernel_f32(bool vec, bool verify) {
+  return draw_kernel_of<0>(vec, verify);
 }
 
 void* verify_draw_kernel_f32(bool vec) { return verify_draw_kernel_of<0>(vec); }

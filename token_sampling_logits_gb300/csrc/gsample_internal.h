@@ -142,6 +142,7 @@ struct DrawParams {
   int32_t drop;  // powers of two taken off the weights, so that a row's sum stays below 2^63
   int32_t n;     // requests
   DrawPhase phase;
+  bool maxima;  // the units' maxima fit in shared memory
   const float* temperature;
   const int32_t* top_k;  // nullptr: no top-k
   const float* top_p;    // nullptr: no top-p
@@ -158,9 +159,11 @@ struct DrawParams {
   RowSet* sets;
   int32_t* out_count;
 };
-void* draw_kernel(int dtype, bool vec, bool resident, int* threads);
-void* verify_kernel(int dtype, bool vec, bool resident, int* threads);
-void* verify_draw_kernel_fn(int dtype, bool vec, bool resident, int* threads);
+void* draw_kernel(int dtype, bool vec, bool verify);
+void* verify_draw_kernel_fn(int dtype, bool vec);
+int draw_threads();
+// Shared memory for the maxima of a slice, two bytes a unit, and its limit.
+inline size_t draw_smem(int32_t units) { return ((size_t)units + 7) / 8 * 16; }
 size_t draw_smem_limit();
 int draw_max_cluster(int dtype, bool vec);
 cudaError_t launch_draw(const DrawParams& p, int dtype, bool vec, int64_t clusters,
