@@ -109,7 +109,10 @@ struct alignas(16) DrawShared {
   unsigned landed_at[kMaxSegments];  // and where they landed
   unsigned landed_n;
   union {
-    alignas(16) unsigned hist[kBins];  // read sixteen bytes at a time
+    alignas(16) struct {
+      unsigned hist[kBins];   // of this CTA; read sixteen bytes at a time
+      unsigned steps[kBins];  // of the row
+    };
     struct {
       uint2 list[kRowList];  // logit bits and index
       union {
@@ -732,20 +735,33 @@ __device__ __noinline__ void settle_long(const DrawParams& p, const Row& r, Draw
           atomicAdd(&sh.hist[max(0, min(kBins - 1, (int)((M - x) * step)))], 1u);
       });
       cluster_barrier();
+      // each CTA adds up its share of the steps and hands the sums to all
+      const int share = (kBins / 4 + r.nrank - 1) / r.nrank;
+      for (int j = tid; j < share; j += kDrawThreads) {
+        const int at = r.rank * share + j;
+        if (at < kBins / 4) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 4
+          for (int q = 0; q < r.nrank; ++q) {
+            const uint4 o = reinterpret_cast<const uint4*>(peer(sh.hist, q))[at];
+            v.x += o.x;
+            v.y += o.y;
+            v.z += o.z;
+            v.w += o.w;
+          }
+          for (int q = 0; q < r.nrank; ++q) reinterpret_cast<uint4*>(peer(sh.steps, q))[at] = v;
+        }
+      }
+      cluster_barrier();
       constexpr int kPer = kBins / kDrawThreads;
       unsigned c[kPer];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) c[i] = 0u;
-      for (int q = 0; q < r.nrank; ++q) {
-        const uint4* from = reinterpret_cast<const uint4*>(peer(sh.hist, q)) + tid * (kPer / 4);
-#pragma unroll
-        for (int i = 0; i < kPer / 4; ++i) {
-          const uint4 v = from[i];
-          c[4 * i] += v.x;
-          c[4 * i + 1] += v.y;
-          c[4 * i + 2] += v.z;
-          c[4 * i + 3] += v.w;
-        }
+      for (int i = 0; i < kPer / 4; ++i) {
+        const uint4 v = reinterpret_cast<const uint4*>(sh.steps)[tid * (kPer / 4) + i];
+        c[4 * i] = v.x;
+        c[4 * i + 1] = v.y;
+        c[4 * i + 2] = v.z;
+        c[4 * i + 3] = v.w;
       }
       // Counts, and masses as if every logit were in the middle of its step, in
       // units of 2^-24: an estimate that the exact masses are held against.

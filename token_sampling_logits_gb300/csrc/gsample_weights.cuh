@@ -191,8 +191,9 @@ __device__ __forceinline__ void weight_bits(float x0, float x1, const WeightRow&
 constexpr int32_t kBitsH = 0x40200000;  // 2.5f
 constexpr int32_t kBitsL = 0x35400000;  // 1.5 * 2^-21
 
-// The weights of two logits x <= M in units of 2^-44.
-__device__ __forceinline__ void weights_of(float x0, float x1, const WeightRow& w, uint32_t table,
+// The weights of two logits x <= M in units of 2^-44. (Out of line: where few
+// elements are weighed the instructions that are fetched count for more.)
+static __device__ __noinline__ void weights_of(float x0, float x1, const WeightRow& w, uint32_t table,
                                            unsigned long long (&v)[2]) {
   int32_t h[2], l[2];
   if (w.shift)
