@@ -136,6 +136,7 @@ struct alignas(16) DrawShared {
   int sel[4];
   unsigned above_c, all_c;
   u64 above_m, all_m;
+  u64 tail, tail_err, m_lo, m_hi;  // at rank 0
   double floor_step;     // T ln(min_p)
   int32_t found;         // written by the CTA that finds an index
   int32_t request;
@@ -550,12 +551,13 @@ __device__ __forceinline__ int in_order(DrawShared& sh, int n_seg) {
   unsigned incl = bad ? 0u : c;
   u64 none = 0ull;
   cta_scan(incl, none, sh);
+  unsigned* off = reinterpret_cast<unsigned*>(sh.wmax);
+  if (tid < n_seg) off[tid] = incl - (bad ? 0u : c);
   if (tid == kDrawThreads - 1) sh.all_c = incl;
   if (__syncthreads_or(bad ? 1 : 0)) return -1;
-  if (tid < n_seg) {
-    const unsigned from = sh.landed_at[tid], to = incl - c;
-    for (unsigned j = 0; j < c; ++j) sh.row.list[to + j] = sh.row.landed[from + j];
-  }
+  for (int s = tid >> 5; s < n_seg; s += kDrawWarps)
+    for (unsigned j = tid & 31; j < sh.count[s]; j += 32)
+      sh.row.list[off[s] + j] = sh.row.landed[sh.landed_at[s] + j];
   __syncthreads();
   return (int)sh.all_c;
 }
@@ -1107,29 +1109,36 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
   float M = -INFINITY;
   const bool listing = p.phase != kLeftOver && p.maxima;
   auto first = [&](auto with_tail) {
-    constexpr int kBatch = 4;
+    // two units at a time, and the next two on their way
+    constexpr int kBatch = 2;
     F2 t[EPU / 2];
     const F2 rh2 = f2(th), rl2 = f2(tl);
     F2 nc = f2(0.0f);
     const int32_t pad = r.u_lo + (r.w_hi - r.u_lo + 7) / 8 * 8;  // of the last run
-    for (int32_t u0 = r.w_lo; u0 < r.w_hi; u0 += 32 * kBatch) {
-      uint4 q[kBatch];
+    uint4 next[kBatch];
+    auto fetch = [&](int32_t u0) {
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int32_t u = u0 + 32 * i + r.lane;
-        q[i] = Row::no_unit();
-        if (u < r.w_hi) q[i] = r.unit(u);
+        next[i] = Row::no_unit();
+        if (u < r.w_hi) next[i] = r.unit(u);
       }
-      if constexpr (decltype(with_tail)::value) {
-        if (u0 == r.w_lo) {
-          float m0 = Row::largest(q[0]);
+    };
+    fetch(r.w_lo);
+    if constexpr (decltype(with_tail)::value) {
+      float m0 = Row::largest(next[0]);
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) m0 = fmaxf(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, o));
-          c0 = rintf(m0 * rh);
-          if (!(fabsf(c0) <= 512.0f)) c0 = 0.0f;
-          nc = f2(-c0);
-        }
-      }
+      for (int o = 16; o > 0; o >>= 1) m0 = fmaxf(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, o));
+      c0 = rintf(m0 * rh);
+      if (!(fabsf(c0) <= 512.0f)) c0 = 0.0f;
+      nc = f2(-c0);
+    }
+#pragma unroll 1
+    for (int32_t u0 = r.w_lo; u0 < r.w_hi; u0 += 32 * kBatch) {
+      uint4 q[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) q[i] = next[i];
+      fetch(u0 + 32 * kBatch);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int32_t u = u0 + 32 * i + r.lane;
@@ -1196,7 +1205,7 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
     const u64 p_part = fraction_of(top_p);
     bool settled = false;
 
-    if (!w.shift && listing && !(VERIFY && unfiltered)) {
+    if (!w.shift && listing && (tails || !(p_on || unfiltered))) {
       // Short sets: 12 powers of two down; for a top_k without a top_p, whose last
       // elements may weigh next to nothing, 16, and 12 nats at low temperatures.
       const float x_lo =
@@ -1331,20 +1340,31 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
           if (tid == kDrawThreads - 1) sh.all_m = incl;
           __syncthreads();
           const u64 listed = sh.all_m;
-          u64 rest = 0ull, err = 0ull;
           if (tails) {
-            for (int q = r.lane; q < r.nrank * kDrawWarps; q += 32) rest += sh.sums[buf][q];
-            rest = warp_sum(rest);
-            // The binary32 tail. In 2^-24 of a term: 23 for y, whose two roundings are
-            // of 2^-20 while |y| < 32 (terms below are less than the V units), 4 for
-            // ex2, 4 for the sum of a unit, 5 for its scale; then what the rounding of
-            // the low parts left of the terms that were listed, and half a unit for
-            // each fixed-point weight.
-            err = __float2ull_ru((float)rest * (40.0f * 5.9604645e-8f)) + (listed >> 34) + (u64)p.V;
+            if (r.warp == 0) {
+              u64 rest = 0ull;
+              for (int q = r.lane; q < r.nrank * kDrawWarps; q += 32) rest += sh.sums[buf][q];
+              rest = warp_sum(rest);
+              if (r.lane == 0) {
+                // The binary32 tail. In 2^-24 of a term: 23 for y, whose two roundings
+                // are of 2^-20 while |y| < 32 (terms below are less than the V units), 4
+                // for ex2, 4 for the sum of a unit, 6 for its scale; then what the rounding
+                // of the low parts left of the terms that were listed, and half a unit for
+                // each fixed-point weight.
+                const u64 err =
+                    __float2ull_ru((float)rest * (40.0f * 5.9604645e-8f)) + (listed >> 34) + (u64)p.V;
+                sh.tail = rest;
+                sh.tail_err = err;
+                sh.m_lo = max(ceil_part(p_part, listed + rest - min(rest, err)), 1ull);
+                sh.m_hi = ceil_part(p_part, listed + rest + err);
+              }
+            }
+            __syncthreads();
           }
+          const u64 rest = tails ? sh.tail : 0ull, err = tails ? sh.tail_err : 0ull;
           if (p_on) {
-            cut.m_lo = max(ceil_part(p_part, listed + rest - min(rest, err)), 1ull);
-            cut.m_hi = ceil_part(p_part, listed + rest + err);
+            cut.m_lo = sh.m_lo;
+            cut.m_hi = sh.m_hi;
           }
           const bool complete = x_lo == floor_x;
           if (k_on || p_on) {
@@ -1396,35 +1416,39 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
               const int32_t each = Row::run_length(qn);
               const int32_t lo = q0 + min(qn, (at % kDrawWarps) * each);
               const int32_t hi = q0 + min(qn, (at % kDrawWarps + 1) * each);
+              // (the error of the run's tail is part of err)
               u64 base = before;
+              const F2 th2 = f2(th), tl2 = f2(tl), nc = f2(-w.c);
+              constexpr float kUnits = 17592186044416.0f;
               for (int32_t u0 = lo; u0 < hi; u0 += kDrawThreads) {
                 const int32_t u = u0 + tid;
-                uint4 q = make_uint4(0u, 0u, 0u, 0u);
-                u64 v[EPU], all = 0ull;
-#pragma unroll
-                for (int e = 0; e < EPU; ++e) v[e] = 0ull;
+                uint4 q = Row::no_unit();
+                u64 all = 0ull;
                 if (u < hi) {
                   q = r.unit(u);
-#pragma unroll
-                  for (int e = 0; e < EPU; e += 2) {
-                    u64 two[2];
-                    weights_of(Row::element(q, e), Row::element(q, e + 1), w, table, two);
-                    v[e] = two[0];
-                    v[e + 1] = two[1];
-                    all += two[0] + two[1];
+                  F2 t[EPU / 2];
+                  const float tails_of = unit_tail<Row>(q, th2, tl2, nc, t);
+                  if (Row::largest(q) >= x_lo) {
+#pragma unroll 1
+                    for (int e = 0; e < EPU; ++e) all += weight_of(Row::element(q, e), w, table);
+                  } else {
+                    all = __float2ull_rn(tails_of * kUnits);
                   }
                 }
                 u64 end = all;
                 cta_scan(none, end, sh);
                 u64 from = base + end - all;
-#pragma unroll
-                for (int e = 0; e < EPU; ++e) {
-                  if (v[e] > 0ull && from + err <= t_lo && t_hi + err < from + v[e]) {
-                    hit = true;
-                    p.out_idx[b] = u * EPU + e;
-                    if (p.out_logprob) p.out_logprob[b] = log_ratio(v[e], sum, table);
+                if (t_lo >= from && t_lo < from + all) {
+#pragma unroll 1
+                  for (int e = 0; e < EPU; ++e) {
+                    const u64 v = weight_of(Row::element(q, e), w, table);
+                    if (from + err <= t_lo && t_hi + err < from + v) {
+                      hit = true;
+                      p.out_idx[b] = u * EPU + e;
+                      if (p.out_logprob) p.out_logprob[b] = log_ratio(v, sum, table);
+                    }
+                    from += v;
                   }
-                  from += v[e];
                 }
                 if (tid == kDrawThreads - 1) sh.all_m = end;
                 __syncthreads();
@@ -1571,11 +1595,19 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(
   }
 }
 
-// q s rounded to an integer, q clamped to [0, 1] (NaN: 0).
-__device__ __forceinline__ u64 times_probability(u64 s, float q) {
-  const u64 f = __float2ull_rn(fminf(fmaxf(q, 0.0f), 1.0f) * 9223372036854775808.0f);
-  const u64 hi = __umul64hi(f, s), lo = f * s;
-  return (hi << 1) + (lo >> 63) + ((lo >> 62) & 1ull);
+// What of a weight exceeds q S: S as the pair (sh, sl) in units of 2^-44 of its
+// own, q clamped to [0, 1] (NaN: 0), the product rounded to 2^-44 the way the
+// weights are.
+__device__ __forceinline__ u64 left_of(u64 w, float q, float sh, float sl) {
+  q = fminf(fmaxf(q, 0.0f), 1.0f);
+  const float p = q * sh;
+  if (!(p < 1.25f)) return 0ull;  // weights are below that
+  const float e = fmaf(q, sl, fmaf(q, sh, -p));
+  const float vh = (p + e) + kMagicH;
+  const float vl = (__fsub_rn(p, __fsub_rn(vh, kMagicH)) + e) + kMagicL;
+  const long long less = ((long long)(__float_as_int(vh) - kBitsH) << 22) +
+                         (long long)(__float_as_int(vl) - kBitsL);
+  return (long long)w > less ? w - (u64)less : 0ull;
 }
 
 // One cluster per request, after filter_set_kernel has written its rows' sets:
@@ -1642,29 +1674,50 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Draw
     const uint32_t key = ordered_bits(x);
     return (key > set.key || (key == set.key && at <= set.last)) && !(rest && !q && at == draft);
   };
-  auto pair = [&](float x0, float x1, int32_t at, u64(&v)[2]) {
+  // S 2^-44 as a pair
+  const u64 top = set.sum >> 30 << 30;
+  const float s_hi = (float)top * 5.684341886080802e-14f;
+  const float s_lo = (float)(long long)(set.sum - (u64)__float2ull_rn((float)top)) * 5.684341886080802e-14f;
+  auto weigh = [&](float x0, float x1, int32_t at, u64(&v)[2], auto inlined) {
     const bool k0 = kept(x0, at), k1 = kept(x1, at + 1);
     v[0] = v[1] = 0ull;
     if (!k0 && !k1) return;
-    weights_of(k0 ? x0 : -INFINITY, k1 ? x1 : -INFINITY, w, table, v);
-    if (rest && q) {
-      const u64 l0 = k0 ? times_probability(set.sum, __ldg(q + at)) : 0ull;
-      const u64 l1 = k1 ? times_probability(set.sum, __ldg(q + at + 1)) : 0ull;
-      v[0] = v[0] > l0 ? v[0] - l0 : 0ull;
-      v[1] = v[1] > l1 ? v[1] - l1 : 0ull;
+    x0 = k0 ? x0 : -INFINITY;
+    x1 = k1 ? x1 : -INFINITY;
+    if constexpr (decltype(inlined)::value) {
+      int32_t h[2], l[2];
+      weight_bits<false>(x0, x1, w, table, h, l);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        v[e] = (u64)(((long long)(h[e] - kBitsH) << 22) + (long long)(l[e] - kBitsL));
+    } else {
+      weights_of(x0, x1, w, table, v);
     }
+    if (rest && q) {
+      if (k0) v[0] = left_of(v[0], __ldg(q + at), s_hi, s_lo);
+      if (k1) v[1] = left_of(v[1], __ldg(q + at + 1), s_hi, s_lo);
+    }
+  };
+  auto pair = [&](float x0, float x1, int32_t at, u64(&v)[2]) {
+    weigh(x0, x1, at, v, std::false_type{});
   };
   int buf = 0;
   u64 all;
   for (;;) {
     u64 own = 0ull;
-    r.each_pair(
-        [&](float x0, float x1, int32_t at) {
-          u64 v[2];
-          pair(x0, x1, at, v);
-          own += v[0] + v[1];
-        },
-        [](int) {});
+    auto sweep = [&](auto inlined) {
+      r.each_pair(
+          [&](float x0, float x1, int32_t at) {
+            u64 v[2];
+            weigh(x0, x1, at, v, inlined);
+            own += v[0] + v[1];
+          },
+          [](int) {});
+    };
+    if (w.shift)
+      sweep(std::false_type{});
+    else
+      sweep(std::true_type{});
     all = cluster_sum(own, r, sh, buf);
     if (all > 0ull || !rest) break;
     rest = false;  // nothing is left of p - q: the draw is from p
