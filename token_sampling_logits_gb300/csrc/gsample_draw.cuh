@@ -643,6 +643,7 @@ __device__ __forceinline__ bool settle(DrawShared& sh, int n, int per, const u64
   Ranked e{0ull, 0u, 0u};
   if (tid < (int)in_bin) {
     e = sh.row.last[tid];
+#pragma unroll 4
     for (unsigned j = 0; j < in_bin; ++j) {
       const Ranked o = sh.row.last[j];
       if (o.key > e.key || (o.key == e.key && o.idx < e.idx)) {
@@ -1093,7 +1094,7 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
   // Rows whose mass is asked for sum their weights in the first sweep, in
   // binary32, relative to 2^c0: the largest of the warp's first logits, as a
   // power of two. (The sum is over all; what is listed later comes off it.)
-  const bool tails = T > 0.0f && T < 1e30f && p.phase != kLeftOver && (p_on || (unfiltered && !VERIFY));
+  const bool tails = T > 0.0f && T < 1e30f && p.phase != kLeftOver && (p_on || unfiltered);
   float scale, rh, rl;
   weight_scale(T, scale, rh, rl);
   // the same factor as a pair with a positive low half: -inf stays -inf
@@ -1203,13 +1204,41 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
     cut.k = k_on ? (unsigned)top_k : 0xFFFFFFFFu;
     cut.m_lo = cut.m_hi = ULLONG_MAX;
     const u64 p_part = fraction_of(top_p);
-    bool settled = false;
+    bool settled = false, tested = false;
 
     if (!w.shift && listing && (tails || !(p_on || unfiltered))) {
       // Short sets: 12 powers of two down; for a top_k without a top_p, whose last
       // elements may weigh next to nothing, 16, and 12 nats at low temperatures.
-      const float x_lo =
-          fmaxf(floor_x, M - (tails ? 8.3177662f * T : fmaxf(11.0903549f * T, 12.0f)));
+      float x_lo = fmaxf(floor_x, M - (tails ? 8.3177662f * T : fmaxf(11.0903549f * T, 12.0f)));
+      if (k_on && !p_on) {
+        // Not more than a top_k needs: units enough for it hold as many elements, so
+        // the largest top_k of this CTA are among those from the threshold up.
+        float hi = M;
+#pragma unroll 1
+        for (int tries = 0; tries < 8; ++tries) {
+          const float mid = tries == 0 ? x_lo : 0.5f * (x_lo + hi);
+          // (a maximum is rounded up: above the next number of sixteen bits it is above mid)
+          const float over = Row::of_short(Row::short_of(mid));
+          unsigned c = 0u;
+          for (int32_t u = r.w_lo + r.lane * 8; u < r.w_hi; u += 256) {
+            const uint4 q = lds128(smem_addr(maxima) + (uint32_t)(u - r.u_lo) * 2u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              c += Row::of_short(word_of(q, e >> 1) >> ((e & 1) * 16) & 0xFFFFu) > over ? 1u : 0u;
+          }
+          u64 none = 0ull;
+          cta_scan(c, none, sh);
+          if (tid == kDrawThreads - 1) sh.all_c = c;
+          __syncthreads();
+          c = sh.all_c;
+          __syncthreads();
+          if (c >= cut.k)
+            x_lo = mid;
+          else
+            hi = mid;
+          if (tries == 0 ? c <= 256u : c >= cut.k && c <= 2u * cut.k + 64u) break;
+        }
+      }
       // the units to list, in order
       unsigned* todo = reinterpret_cast<unsigned*>(sh.row.list) + r.warp * kWarpList;
       unsigned n_units = 0u;
@@ -1369,6 +1398,36 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
           const bool complete = x_lo == floor_x;
           if (k_on || p_on) {
             ok = settle(sh, n, per, we, 0u, 0ull, cut, x_lo, M, complete);
+          } else if (unfiltered && VERIFY) {
+            // The mass is known to err: enough for the draft's test, unless u q S
+            // and the draft's weight are that close. (The sum itself, which the draw may
+            // need, is formed there: 0 stands for it.)
+            if (tid == 0) {
+              sh.sel[2] = 1;
+              sh.sel[3] = 0;
+              const int64_t d = __ldcg(p.draft + b);
+              if (b + 1 < __ldcg(p.offsets + s + 1) && b + 1 < p.B && d >= 0 && d < p.V) {
+                const float u = fminf(fmaxf(__ldcg(p.uniform + b), 0.0f), 0.999999940395355224609375f);
+                const float q = p.probs ? __ldcg(p.probs + b * p.probs_ld + d) : 1.0f;
+                const u64 wd = weight_of(logit_at<DT>(r.row, d), w, table);
+                const u64 sum = listed + rest;
+                const double uq = (double)u * (double)q;
+                const bool least = uq * (double)(sum - min(sum, err)) >= (double)wd;
+                const bool most = uq * (double)(sum + err) >= (double)wd;
+                sh.sel[2] = wd == 0ull || least == most;
+                sh.sel[3] = wd > 0ull && !most;
+              }
+            }
+            __syncthreads();
+            ok = sh.sel[2] != 0;
+            tested = true;
+            set.accepted = sh.sel[3];
+            if (tid == 0) {
+              sh.key = floor_key;
+              sh.last = INT32_MAX;
+              sh.sum = 0ull;
+            }
+            __syncthreads();
           } else if (unfiltered) {
             // All elements are K. The warp whose run u falls in is told by the
             // listed weights and the tails; in it the weights are exact, and the
@@ -1529,11 +1588,13 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
       return;
     }
     if (!settled) {
+      tested = false;
+      set.accepted = 0;
       settle_long<VERIFY>(p, r, sh, b, M, T, floor_x, k_on ? top_k : 0, p_on ? top_p : 1.0f, buf,
                           &set);
     }
     if constexpr (VERIFY) {
-      if (r.rank == 0 && tid == 0) {
+      if (r.rank == 0 && tid == 0 && !tested) {
       const int64_t t = __ldcg(p.draft + b);
       if (b + 1 < __ldcg(p.offsets + s + 1) && b + 1 < p.B && t >= 0 && t < p.V) {
         const float x = logit_at<DT>(r.row, t);
@@ -1585,12 +1646,17 @@ __global__ void __launch_bounds__(kDrawThreads, 2) filter_set_kernel(
     settle_row<VERIFY>(p, r, sh, maxima, b);
     return;
   }
-  for (; b < p.B; b += gridDim.x / r.nrank) {
-    // the same in every CTA of the cluster
-    const bool open = VERIFY ? __ldcg(&p.sets[b].kind) == kOpen : __ldcg(p.out_idx + b) == kOpenIndex;
-    if (open) {
+  // 32 rows' flags at a time; every warp of the cluster sees the same ones (a row's
+  // is written behind barriers that come after all have read it)
+  const int64_t step = gridDim.x / r.nrank;
+  for (; b < p.B; b += 32 * step) {
+    const int64_t at = b + r.lane * step;
+    bool mine = false;
+    if (at < p.B)
+      mine = VERIFY ? __ldcg(&p.sets[at].kind) == kOpen : __ldcg(p.out_idx + at) == kOpenIndex;
+    for (unsigned open = __ballot_sync(0xFFFFFFFFu, mine); open; open &= open - 1u) {
       __syncthreads();
-      settle_row<VERIFY>(p, r, sh, maxima, b);
+      settle_row<VERIFY>(p, r, sh, maxima, b + (__ffs(open) - 1) * step);
     }
   }
 }
@@ -1674,6 +1740,13 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Draw
     const uint32_t key = ordered_bits(x);
     return (key > set.key || (key == set.key && at <= set.last)) && !(rest && !q && at == draft);
   };
+  int buf = 0;
+  if (rest && q && set.sum == 0ull) {  // of a row without filter, not formed yet
+    const u64 own = w.shift ? sum_from<true>(r, w, table, kLowestLogit)
+                            : sum_from<false>(r, w, table, kLowestLogit);
+    set.sum = cluster_sum(own, r, sh, buf);
+    buf ^= 1;
+  }
   // S 2^-44 as a pair
   const u64 top = set.sum >> 30 << 30;
   const float s_hi = (float)top * 5.684341886080802e-14f;
@@ -1701,7 +1774,6 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Draw
   auto pair = [&](float x0, float x1, int32_t at, u64(&v)[2]) {
     weigh(x0, x1, at, v, std::false_type{});
   };
-  int buf = 0;
   u64 all;
   for (;;) {
     u64 own = 0ull;
