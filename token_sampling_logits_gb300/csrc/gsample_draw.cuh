@@ -60,7 +60,6 @@ constexpr int kCtaList = kWarpList * kDrawWarps;
 constexpr int kRowList = 1280;                // entries of a row's list, at rank 0
 constexpr int kLandList = 768;
 constexpr int kListBins = 512;
-constexpr int kLastBin = 384;                 // entries of a list's bin that are ranked
 constexpr int kBins = 4096;                   // steps of the histogram
 constexpr int64_t kOpenIndex = -2;            // out_idx of a row left to the second launch
 
@@ -120,7 +119,7 @@ struct alignas(16) DrawShared {
           u64 mass[kListBins];
           unsigned count[kListBins];
         } bin;
-        Ranked last[kLastBin];
+        Ranked last[kRowList];
         uint2 landed[kLandList];  // as they come from the cluster's warps
       };
     } row;
@@ -618,7 +617,6 @@ __device__ __forceinline__ bool settle(DrawShared& sh, int n, int per, const u64
   __syncthreads();
   const unsigned in_bin = sh.all_c, before_c = sh.above_c;
   const u64 before_m = sh.above_m;
-  if (in_bin > (unsigned)kLastBin) return false;
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
     const int j = tid * per + i;
@@ -637,27 +635,39 @@ __device__ __forceinline__ bool settle(DrawShared& sh, int n, int per, const u64
   __syncthreads();
   // K is a prefix of the bin's elements too: its last one has as many before it
   // as there are others in K.
-  bool in = false;
-  unsigned rank = 0u;
-  u64 mass = before_m;
-  Ranked e{0ull, 0u, 0u};
-  if (tid < (int)in_bin) {
-    e = sh.row.last[tid];
+  unsigned taken = 0u, rank[3];
+  u64 mass[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int at_e = tid + i * kDrawThreads;
+    bool in = false;
+    rank[i] = 0xFFFFFFFFu;
+    mass[i] = before_m;
+    if (i > 0 && in_bin <= (unsigned)(i * kDrawThreads)) continue;
+    if (at_e < (int)in_bin) {
+      const Ranked e = sh.row.last[at_e];
+      unsigned before = 0u;
 #pragma unroll 4
-    for (unsigned j = 0; j < in_bin; ++j) {
-      const Ranked o = sh.row.last[j];
-      if (o.key > e.key || (o.key == e.key && o.idx < e.idx)) {
-        ++rank;
-        mass += o.w;
+      for (unsigned j = 0; j < in_bin; ++j) {
+        const Ranked o = sh.row.last[j];
+        if (o.key > e.key || (o.key == e.key && o.idx < e.idx)) {
+          ++before;
+          mass[i] += o.w;
+        }
       }
+      in = before_c + before < cut.k && mass[i] < cut.m_lo;
+      if (in) rank[i] = before;
     }
-    in = before_c + rank < cut.k && mass < cut.m_lo;
+    taken += (unsigned)__syncthreads_count(in ? 1 : 0);
   }
-  const unsigned taken = (unsigned)__syncthreads_count(in ? 1 : 0);
-  if (in && rank + 1u == taken) {
-    sh.key = e.key;
-    sh.last = (int32_t)e.idx;
-    sh.sum = mass + e.w;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    if (rank[i] != 0xFFFFFFFFu && rank[i] + 1u == taken) {
+      const Ranked e = sh.row.last[tid + i * kDrawThreads];
+      sh.key = e.key;
+      sh.last = (int32_t)e.idx;
+      sh.sum = mass[i] + e.w;
+    }
   }
   __syncthreads();
   // cut by the mass: the next element must be out for every m in question
@@ -1735,10 +1745,9 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Draw
   bool rest = stop != r1 - 1;
   const int64_t draft = __ldcg(p.draft + stop);
   const float* q = p.probs ? p.probs + stop * p.probs_ld : nullptr;
+  const float least = logit_of_key(set.key);  // K's smallest logit
   auto kept = [&](float x, int32_t at) {
-    if (!(x > -INFINITY)) return false;
-    const uint32_t key = ordered_bits(x);
-    return (key > set.key || (key == set.key && at <= set.last)) && !(rest && !q && at == draft);
+    return (x > least || (x == least && at <= set.last)) && !(rest && !q && at == draft);
   };
   int buf = 0;
   if (rest && q && set.sum == 0ull) {  // of a row without filter, not formed yet
@@ -1778,13 +1787,18 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Draw
   for (;;) {
     u64 own = 0ull;
     auto sweep = [&](auto inlined) {
-      r.each_pair(
-          [&](float x0, float x1, int32_t at) {
-            u64 v[2];
-            weigh(x0, x1, at, v, inlined);
-            own += v[0] + v[1];
-          },
-          [](int) {});
+      uint4 next = r.w_lo + r.lane < r.w_hi ? r.unit(r.w_lo + r.lane) : Row::no_unit();
+      for (int32_t u = r.w_lo + r.lane; u < r.w_hi; u += 32) {
+        const uint4 c = next;
+        if (u + 32 < r.w_hi) next = r.unit(u + 32);
+        if (!(Row::largest(c) >= least)) continue;
+#pragma unroll
+        for (int e = 0; e < Row::EPU; e += 2) {
+          u64 v[2];
+          weigh(Row::element(c, e), Row::element(c, e + 1), u * Row::EPU + e, v, inlined);
+          own += v[0] + v[1];
+        }
+      }
     };
     if (w.shift)
       sweep(std::false_type{});

@@ -207,8 +207,13 @@ gsample_status gsample_verify_drafts(const void* logits, gsample_dtype dtype, in
       st = launched(launch_sets((int)dtype, vec, R, most, &p, (cudaStream_t)stream));
       if (st != GSAMPLE_OK) return st;
     }
-    use_cluster(fitting_cluster(gsample::verify_draw_kernel_fn((int)dtype, vec), false, n, most, p),
-                &p);
+    // Eight CTAs a request at least: most draws are over in 3 us, and those from a
+    // whole vocabulary are what the launch waits for.
+    int c = fitting_cluster(gsample::verify_draw_kernel_fn((int)dtype, vec), false, n, most, p);
+    const int64_t wide = (p.units_per_row + kUnitsPerCta - 1) / kUnitsPerCta;
+    if (c < 8) c = wide < 8 ? (int)wide : 8;
+    if (c > most) c = most;
+    use_cluster(c, &p);
   } catch (...) {
     return GSAMPLE_ERR_CUDA;
   }
