@@ -1760,7 +1760,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Draw
   const u64 top = set.sum >> 30 << 30;
   const float s_hi = (float)top * 5.684341886080802e-14f;
   const float s_lo = (float)(long long)(set.sum - (u64)__float2ull_rn((float)top)) * 5.684341886080802e-14f;
-  auto weigh = [&](float x0, float x1, int32_t at, u64(&v)[2], auto inlined) {
+  auto weigh = [&](float x0, float x1, int32_t at, float q0, float q1, u64(&v)[2], auto inlined) {
     const bool k0 = kept(x0, at), k1 = kept(x1, at + 1);
     v[0] = v[1] = 0ull;
     if (!k0 && !k1) return;
@@ -1776,13 +1776,17 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Draw
       weights_of(x0, x1, w, table, v);
     }
     if (rest && q) {
-      if (k0) v[0] = left_of(v[0], __ldg(q + at), s_hi, s_lo);
-      if (k1) v[1] = left_of(v[1], __ldg(q + at + 1), s_hi, s_lo);
+      v[0] = left_of(v[0], q0, s_hi, s_lo);
+      v[1] = left_of(v[1], q1, s_hi, s_lo);
     }
   };
   auto pair = [&](float x0, float x1, int32_t at, u64(&v)[2]) {
-    weigh(x0, x1, at, v, std::false_type{});
+    const bool some = rest && q;
+    const float q0 = some && at < p.V ? __ldg(q + at) : 0.0f;
+    const float q1 = some && at + 1 < p.V ? __ldg(q + at + 1) : 0.0f;
+    weigh(x0, x1, at, q0, q1, v, std::false_type{});
   };
+  const bool q_wide = q && ((uintptr_t)q & 15u) == 0;
   u64 all;
   for (;;) {
     u64 own = 0ull;
@@ -1792,10 +1796,30 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Draw
         const uint4 c = next;
         if (u + 32 < r.w_hi) next = r.unit(u + 32);
         if (!(Row::largest(c) >= least)) continue;
+        const int32_t at = u * Row::EPU;
+        float qs[Row::EPU];
+#pragma unroll
+        for (int e = 0; e < Row::EPU; ++e) qs[e] = 0.0f;
+        if (rest && q) {
+          if (q_wide && at + Row::EPU <= p.V) {
+#pragma unroll
+            for (int e = 0; e < Row::EPU; e += 4) {
+              const float4 f = __ldg(reinterpret_cast<const float4*>(q + at + e));
+              qs[e] = f.x;
+              qs[e + 1] = f.y;
+              qs[e + 2] = f.z;
+              qs[e + 3] = f.w;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < Row::EPU; ++e)
+              if (at + e < p.V) qs[e] = __ldg(q + at + e);
+          }
+        }
 #pragma unroll
         for (int e = 0; e < Row::EPU; e += 2) {
           u64 v[2];
-          weigh(Row::element(c, e), Row::element(c, e + 1), u * Row::EPU + e, v, inlined);
+          weigh(Row::element(c, e), Row::element(c, e + 1), at + e, qs[e], qs[e + 1], v, inlined);
           own += v[0] + v[1];
         }
       }

@@ -17,7 +17,9 @@ namespace {
 constexpr int kPageThreads = 1024;
 constexpr int kPageWarps = kPageThreads / 32;
 constexpr int kMapThreads = 256;
-constexpr int kMapTokens = 2048;  // slot-map entries of a CTA
+constexpr int kMapTokens = 1024;  // slot-map entries of a CTA
+constexpr int kMapOffsets = 1025;
+constexpr int kTableCols = 1024;  // table columns of a CTA at a time
 
 // The list of request i, clipped to [0, total).
 struct List {
@@ -167,53 +169,66 @@ __global__ void __launch_bounds__(kPageThreads) pages_extend_kernel(const PageAr
 
 // The slot map and the batch's block table, from the state after the
 // extension: the first `map_ctas` CTAs take kMapTokens entries of the map each,
-// the others the table.
+// the others kTableCols columns of one request's table at a time. What a request
+// is gets read once a CTA (a division and four dependent loads an entry took
+// 12 us for 256 tables of 2049 columns, this 5), and a token finds its request
+// among offsets in shared memory.
 __global__ void __launch_bounds__(kMapThreads) pages_map_kernel(const PageArgs s,
                                                                 const ExtendArgs a) {
+  __shared__ int64_t offsets[kMapOffsets];
   pdl_wait_then_release();
+  const uint32_t page = (uint32_t)s.page_size;
   if (blockIdx.x < (unsigned)a.map_ctas) {
+    const bool near = a.offsets && a.n + 1 <= kMapOffsets;
+    if (near) {
+      for (int64_t i = threadIdx.x; i <= a.n; i += kMapThreads) offsets[i] = __ldcg(a.offsets + i);
+      __syncthreads();
+    }
+    auto offset = [&](int64_t i) { return near ? offsets[i] : __ldcg(a.offsets + i); };
     const int64_t t0 = (int64_t)blockIdx.x * kMapTokens;
     const int64_t t1 = min(t0 + kMapTokens, a.total);
     for (int64_t t = t0 + threadIdx.x; t < t1; t += kMapThreads) {
       int64_t i = t, at = t;
       if (a.offsets) {
+        if (t < offset(0) || t >= offset(a.n)) continue;
         int64_t lo = 0, hi = a.n;
-        if (t < __ldcg(a.offsets) || t >= __ldcg(a.offsets + a.n)) continue;
         while (hi - lo > 1) {
           const int64_t mid = (lo + hi) >> 1;
-          if (__ldcg(a.offsets + mid) <= t)
+          if (offset(mid) <= t)
             lo = mid;
           else
             hi = mid;
         }
         i = lo;
-        const List l = list_of(a.offsets, a.total, i);
-        if (t < l.at || t >= l.at + l.count) continue;
-        at = l.at;
+        at = min(max(offset(i), (int64_t)0), a.total);
+        if (t < at || t >= min(max(offset(i + 1), at), a.total)) continue;
       }
       const int32_t start = __ldcg(a.out_start + i);
+      const int64_t row = a.slot ? (int64_t)__ldcg(a.slot + i) : i;
       int64_t where = -1;
       if (start >= 0) {
-        const int64_t row = a.slot ? (int64_t)__ldcg(a.slot + i) : i;
-        const int64_t position = start + (t - at);
-        const int64_t c = position / s.page_size;
-        where = (int64_t)__ldcg(s.table + row * s.ld + c) * s.page_size +
-                (position - c * s.page_size);
+        const uint32_t position = (uint32_t)start + (uint32_t)(t - at);  // below 2^31
+        const uint32_t c = position / page;
+        where = (int64_t)__ldcg(s.table + row * s.ld + c) * page + (position - c * page);
       }
       a.out_slot_map[t] = where;
     }
   } else {
-    const int64_t step = (int64_t)(gridDim.x - a.map_ctas) * kMapThreads;
-    const int64_t all = a.n * a.table_cols;
-    for (int64_t j = (int64_t)(blockIdx.x - a.map_ctas) * kMapThreads + threadIdx.x; j < all;
-         j += step) {
-      const int64_t i = j / a.table_cols, c = j - i * a.table_cols;
-      int32_t page = -1;
-      if (__ldcg(a.out_start + i) >= 0) {
-        const int64_t row = a.slot ? (int64_t)__ldcg(a.slot + i) : i;
-        if (c < pages_of(length_of(s, row), s.page_size)) page = __ldcg(s.table + row * s.ld + c);
-      }
-      a.out_table[i * a.table_ld + c] = page;
+    const uint32_t chunks = (uint32_t)((a.table_cols + kTableCols - 1) / kTableCols);
+    const int64_t all = a.n * chunks;
+    for (int64_t j = blockIdx.x - a.map_ctas; j < all; j += gridDim.x - a.map_ctas) {
+      const int64_t i = j / chunks;
+      const int64_t c0 = (j - i * chunks) * kTableCols;
+      const int64_t c1 = min(c0 + kTableCols, a.table_cols);
+      const int32_t start = __ldcg(a.out_start + i);
+      const int64_t row = a.slot ? (int64_t)__ldcg(a.slot + i) : i;
+      const int64_t count = list_of(a.offsets, a.total, i).count;
+      const int64_t held = start >= 0 ? ((uint32_t)start + (uint32_t)count + page - 1) / page : 0;
+      const int32_t* from = s.table + (start >= 0 ? row * s.ld : 0);
+      int32_t* to = a.out_table + i * a.table_ld;
+#pragma unroll 4
+      for (int64_t c = c0 + threadIdx.x; c < c1; c += kMapThreads)
+        to[c] = c < held ? __ldcg(from + c) : -1;
     }
   }
 }
@@ -303,8 +318,7 @@ cudaError_t launch_pages_extend(const PageArgs& s, ExtendArgs a, int sms, cudaSt
   cudaError_t e = launch(pages_extend_kernel, 1u, kPageThreads, bitmap_bytes(s, a.slot), stream, s, a);
   if (e != cudaSuccess) return e;
   a.map_ctas = (int32_t)((a.total + kMapTokens - 1) / kMapTokens);
-  const int64_t cells = a.n * a.table_cols;
-  int64_t table_ctas = (cells + kMapThreads * 8 - 1) / (kMapThreads * 8);
+  int64_t table_ctas = a.n * ((a.table_cols + kTableCols - 1) / kTableCols);
   if (table_ctas > (int64_t)sms * 8) table_ctas = (int64_t)sms * 8;
   if (a.map_ctas + table_ctas == 0) return cudaSuccess;
   return launch(pages_map_kernel, (unsigned)(a.map_ctas + table_ctas), kMapThreads, 0, stream, s, a);
