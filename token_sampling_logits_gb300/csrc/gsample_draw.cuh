@@ -737,17 +737,27 @@ __device__ __noinline__ void settle_long(const DrawParams& p, const Row& r, Draw
     }
 
     if (!settled) {
-      // Long sets. The histogram's steps run down 24 powers of two for a mass, to
+      // Long sets. The histogram's steps run down 32 powers of two for a mass (what
+      // lies below counts as nothing: V 2^-32 of the largest weight at most), to
       // the floor for a count.
-      const float low = p_on ? fmaxf(floor_x, fmaf(-16.6355324f, T, M)) : floor_x;
+      const float low = p_on ? fmaxf(floor_x, fmaf(-22.1807098f, T, M)) : floor_x;
       const float step = (float)(kBins - 1) / (M - low);
       for (int j = tid; j < kBins; j += kDrawThreads) sh.hist[j] = 0u;
       __syncthreads();
+      // The first four powers of two are weighed exactly: a few heavy elements, whose
+      // places in their steps would not average out.
+      const float drop = w.rh * w.scale / step;  // powers of two a step
+      const int heavy = (int)fminf(4.0f / drop, (float)kBins);
+      u64 head = 0ull;
       r.each([&](float x, int32_t) {
-        if (x >= floor_x)
-          atomicAdd(&sh.hist[max(0, min(kBins - 1, (int)((M - x) * step)))], 1u);
+        if (x >= floor_x) {
+          const int at = max(0, min(kBins - 1, (int)((M - x) * step)));
+          atomicAdd(&sh.hist[at], 1u);
+          if (at < heavy) head += weight_of(x, w, table);
+        }
       });
-      cluster_barrier();
+      head = cluster_sum(head, r, sh, buf);  // (its barrier ends the histograms)
+      buf ^= 1;
       // each CTA adds up its share of the steps and hands the sums to all
       const int share = (kBins / 4 + r.nrank - 1) / r.nrank;
       for (int j = tid; j < share; j += kDrawThreads) {
@@ -777,35 +787,46 @@ __device__ __noinline__ void settle_long(const DrawParams& p, const Row& r, Draw
         c[4 * i + 3] = v.w;
       }
       // Counts, and masses as if every logit were in the middle of its step, in
-      // units of 2^-24: an estimate that the exact masses are held against.
-      const float drop = w.rh * w.scale / step;  // powers of two a step
+      // units of 2^-32: an estimate that the exact masses are held against.
+      const float top = (w.shift ? 0.0f : fmaf(M, w.rh, -w.c)) + 32.0f - 0.5f * drop;
+      auto middle = [&](int bin, unsigned n) {
+        return __float2ull_rn((float)n * ex2_approx(top - (float)bin * drop));
+      };
       unsigned own_c = 0u;
-      u64 own_m = 0ull;
+      u64 own_m = 0ull, own_h = 0ull;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
+        const u64 m = middle(tid * kPer + i, c[i]);
         own_c += c[i];
-        own_m += __float2ull_rn((float)c[i] * ex2_approx(24.0f - (float)(tid * kPer + i) * drop -
-                                                         0.5f * drop));
+        own_m += m;
+        if (tid * kPer + i < heavy) own_h += m;
       }
+      unsigned none_c = 0u;
+      u64 mid_head = own_h;
+      cta_scan(none_c, mid_head, sh);
+      if (tid == kDrawThreads - 1) sh.above_m = mid_head;
       unsigned end_c = own_c;
       u64 end_m = own_m;
       if (tid < 4) sh.sel[tid] = kBins;
       cta_scan(end_c, end_m, sh);
       if (tid == kDrawThreads - 1) sh.all_m = end_m;
       __syncthreads();
-      const u64 est = __umul64hi(p_part, sh.all_m);
-      const u64 m0 = p_on ? est - est / 4096ull : ULLONG_MAX;
-      const u64 m1 = p_on ? est + est / 4096ull : ULLONG_MAX;
+      // what the exact head has over its estimate, added past it
+      const u64 more = (head >> 12) - sh.above_m;  // (may be below 0)
+      const u64 est = __umul64hi(p_part, sh.all_m + more);
+      const u64 m0 = p_on ? est - est / 2048ull : ULLONG_MAX;
+      const u64 m1 = p_on ? est + est / 2048ull : ULLONG_MAX;
       unsigned cc = end_c - own_c;
       u64 cm = end_m - own_m;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int bin = tid * kPer + i;
         cc += c[i];
-        cm += __float2ull_rn((float)c[i] * ex2_approx(24.0f - (float)bin * drop - 0.5f * drop));
+        cm += middle(bin, c[i]);
+        const u64 upto = bin + 1 >= heavy ? cm + more : cm;
         if (cc >= cut.k) atomicMin(&sh.sel[0], bin);
-        if (cm >= m0) atomicMin(&sh.sel[1], bin);
-        if (cm >= m1) atomicMin(&sh.sel[2], bin);
+        if (upto >= m0) atomicMin(&sh.sel[1], bin);
+        if (upto >= m1) atomicMin(&sh.sel[2], bin);
       }
       __syncthreads();
       const int kb = sh.sel[0];
@@ -1218,8 +1239,8 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
 
     if (!w.shift && listing && (tails || !(p_on || unfiltered))) {
       // Short sets: 12 powers of two down; for a top_k without a top_p, whose last
-      // elements may weigh next to nothing, 16, and 12 nats at low temperatures.
-      float x_lo = fmaxf(floor_x, M - (tails ? 8.3177662f * T : fmaxf(11.0903549f * T, 12.0f)));
+      // elements may weigh next to nothing, 24, and 24 nats at low temperatures.
+      float x_lo = fmaxf(floor_x, M - (tails ? 8.3177662f * T : fmaxf(16.6355324f * T, 24.0f)));
       if (k_on && !p_on) {
         // Not more than a top_k needs: units enough for it hold as many elements, so
         // the largest top_k of this CTA are among those from the threshold up.
