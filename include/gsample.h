@@ -426,8 +426,8 @@ gsample_status gsample_constrained_gumbel_argmax(const void* logits, gsample_dty
  *     above: the largest below 1). top_k, top_p, min_p: device arrays of B
  *     entries; any may be NULL (that filter off).
  *   - out_logprob: device float[B] or NULL: log(e_i / sum over K) of the drawn
- *     token, natural, rounded once; 0 for greedy rows, -inf for a row without
- *     candidates (out_idx -1).
+ *     token, natural, rounded once (without a filter it may be off by 2^-24 before
+ *     that); 0 for greedy rows, -inf for a row without candidates (out_idx -1).
  *   - T <= 0 or NaN: greedy. +inf logits: the lowest such index. T = +inf: all
  *     candidates weigh the same. Temperatures below 2^-126 count as that.
  *   - Weights are fixed-point numbers with 44 fraction bits (fewer past V =
@@ -436,7 +436,8 @@ gsample_status gsample_constrained_gumbel_argmax(const void* logits, gsample_dty
  *     one only where u or a filter's border lies within about 1e-11 of the mass
  *     from a boundary. An element whose weight is below 2^-45 is never drawn.
  *   - Layout, alignment, errors and asynchrony as gsample_gumbel_argmax; B up
- *     to (2^31 - 1) / 16. No workspace. */
+ *     to (2^31 - 1) / 16. No workspace. One or two launches (between them out_idx
+ *     holds negative marks). */
 gsample_status gsample_filtered_categorical(const void* logits, gsample_dtype dtype, int64_t B,
                                             int64_t V, int64_t ld, const float* temperature,
                                             const float* uniform, const int32_t* top_k,
@@ -476,7 +477,7 @@ size_t gsample_verify_workspace_bytes(int64_t R);
  *     without rows).
  *   - workspace: device buffer of gsample_verify_workspace_bytes(R) bytes,
  *     16-byte aligned, with any contents; launches in flight at the same time
- *     must not share one. Two launches.
+ *     must not share one. Two or three launches.
  * Temperatures <= 0, special values, precision, layout, validation and
  * asynchrony as gsample_filtered_categorical; R and n up to (2^31 - 1) / 16. */
 gsample_status gsample_verify_drafts(const void* logits, gsample_dtype dtype, int64_t R, int64_t V,

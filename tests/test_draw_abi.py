@@ -146,6 +146,26 @@ def test_the_python_layer_refuses_cpu_tensors():
         gs.PageState(i.view(2, 2), i[:2], i, i[:1], 16)
 
 
+def test_the_kernels_wait_before_they_may_exit():
+    """As every kernel of the library (tests/test_launch_order.py), those of the
+    shared header: the first wait comes before the first return."""
+    import os
+    import re
+
+    from token_sampling_logits_gb300 import build
+
+    text = open(os.path.join(build.CSRC, "gsample_draw.cuh")).read()
+    text = re.sub(r"//[^\n]*", " ", text)
+    found = 0
+    for m in re.finditer(r"__global__ void __launch_bounds__\([^)]*\)\s*(\w+)\(", text):
+        body = text[text.index("{", m.end()):]
+        wait, leave = body.index("pdl_wait_then_release()"), body.index("return;")
+        assert wait < leave, m.group(1)
+        assert "__ldcg" not in body[:wait] and "__ldg" not in body[:wait]
+        found += 1
+    assert found == 2
+
+
 # ---- the definitions ------------------------------------------------------------
 def test_the_filter_set_of_a_small_row():
     x = np.log([0.4, 0.1, 0.3, 0.1, 0.1]).astype(np.float32)

@@ -434,3 +434,84 @@ def test_verify_in_a_graph_and_workspaces():
         gs.verify_drafts(x, D, O, Td, u, d, workspace=ws[:64])
     with pytest.raises(ValueError):
         gs.verify_drafts(x, D, O, Td, u, d, probs=torch.zeros(8, 1999, device="cuda"))
+
+
+# ---- long rows, several streams, many requests ------------------------------------
+@pytest.mark.parametrize("dtype,V,B", [("f32", 6000011, 1), ("bf16", 524309, 3)])
+def test_long_rows(dtype, V, B):
+    """Vocabularies past 2^18 take powers of two off their weights; past the shared
+    memory for the units' maxima no list is made."""
+    rng = np.random.default_rng(V)
+    x, h = logits(rng, B, V, dtype)
+    T, u = np.full(B, 0.9, np.float32), rng.random(B).astype(np.float32)
+    for f in [(None, None, None), (np.full(B, 40, np.int32), None, None),
+              (None, np.full(B, 0.7, np.float32), None), (None, None, np.full(B, 0.2, np.float32))]:
+        idx, lp = draw(x, T, u, *f)
+        # a unit of the weights is 2^-44 of the largest one times the powers taken off
+        tol = 2.0 ** -38 + V * 2.0 ** -44 * max(1, 2.0 ** math.ceil(math.log2(V) - 18))
+        check_rows(h, T, u, *f, idx, lp, tol=tol)
+
+
+@pytest.mark.parametrize("B", [305, 333, 1200])
+def test_batches_past_one_wave_with_long_sets_among_them(B):
+    rng = np.random.default_rng(B)
+    V = 16384
+    x, h = logits(rng, B, V, "bf16", sd=2.5)
+    T = rng.uniform(0.6, 1.2, B).astype(np.float32)
+    T[::37] = 8.0  # nuclei of thousands
+    p = np.full(B, 0.95, np.float32)
+    k = np.where(np.arange(B) % 5 == 0, 3000, 0).astype(np.int32)
+    u = rng.random(B).astype(np.float32)
+    idx, lp = draw(x, T, u, k, p)
+    some = np.unique(np.concatenate([np.arange(0, B, 37), np.arange(0, B, 25), [B - 1]]))
+    check_rows(h[some], T[some], u[some], k[some], p[some], None, idx[some], lp[some])
+
+
+def test_equal_logits_at_the_end_of_long_sets():
+    """More equal logits than a list holds, in rows that differ elsewhere."""
+    rng = np.random.default_rng(31)
+    B, V = 6, 40000
+    x = torch.from_numpy(rng.integers(0, 6, (B, V)).astype(np.float32)).cuda()
+    h = x.cpu().numpy()
+    u = rng.random(B).astype(np.float32)
+    for T in (0.3, 1.0, 5.0):
+        for f in [(np.full(B, 9000, np.int32), None, None), (None, np.full(B, 0.6, np.float32), None),
+                  (np.full(B, 20000, np.int32), np.full(B, 0.9, np.float32), np.full(B, 1e-3, np.float32))]:
+            idx, lp = draw(x, np.full(B, T, np.float32), u, *f)
+            check_rows(h, np.full(B, T), u, *f, idx, lp)
+
+
+def test_two_streams_at_once():
+    rng = np.random.default_rng(77)
+    x, h = logits(rng, 400, 20000, "bf16", sd=2.5)
+    T, u = np.full(400, 0.9, np.float32), rng.random(400).astype(np.float32)
+    Td, U = dev(T), dev(u)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = []
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(gs.filtered_categorical(x, Td, U, top_p=0.9))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    some = np.arange(0, 400, 20)
+    check_rows(h[some], T[some], u[some], None, np.full(20, 0.9), None, outs[0].cpu().numpy()[some], None)
+
+
+def test_verify_many_requests():
+    """More rows than run at once, with filters and without, drafts of all kinds."""
+    rng = np.random.default_rng(41)
+    n, V = 130, 9000
+    offsets = request_rows(rng, n, 5)
+    R = int(offsets[-1])
+    x, h = logits(rng, R, V, "bf16", sd=2.5)
+    draft = np.where(rng.random(R) < 0.6, h.argmax(1), rng.integers(-1, V + 1, R)).astype(np.int64)
+    e = np.exp(h + rng.standard_normal(h.shape).astype(np.float32) * 0.5)
+    q = (e / e.sum(1, keepdims=True)).astype(np.float32)
+    T, k, p, m = settings(rng, n)
+    u, d = rng.random(R).astype(np.float32), rng.random(n).astype(np.float32)
+    for qd, qh in ((None, None), (dev(q), q)):
+        for f in ((None, None, None), (k, p, m)):
+            out, count = run_verify(x, draft, offsets, T, u, d, qd, *f)
+            check_verify(h, draft, offsets, T, u, d, qh, *f, out, count)

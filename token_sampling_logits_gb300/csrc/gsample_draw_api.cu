@@ -6,7 +6,6 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <cstdlib>
 #include <mutex>
 
 #include "gsample.h"
@@ -89,19 +88,22 @@ int fitting_cluster(void* fn, bool maxima, int64_t rows, int most, const DrawPar
 // The rows' sets (verification) or draws. With clusters of kOneLaunch CTAs or
 // more for all rows at once they take one launch. Otherwise one launch settles
 // the short sets, and a second one, with the largest clusters and as many as run
-// at once, what is left: a CTA or two would take long for a long row.
+// at once, what is left: a CTA or two would take long for a long row. Measured at
+// V = 151936 bf16: 256 rows with one long one 92 us so, 195 with the long row on
+// one CTA (62 us without one; the second launch finds nothing in 4 us); 64 long
+// rows 91 us in one launch with four CTAs a row, 290 in two. Leaving the last 16
+// of 320 rows, which the first launch takes a second wave for, to the second as
+// well made 95 us 114.
 constexpr int kOneLaunch = 4;
 cudaError_t launch_sets(int dtype, bool vec, int64_t rows, int most, DrawParams* p,
                         cudaStream_t stream) {
   void* fn = gsample::draw_kernel(dtype, vec, p->sets != nullptr);
   const size_t limit = gsample::draw_smem_limit();
   int c = fitting_cluster(fn, true, rows, most, *p);
-  if (const char* e = getenv("GS_CLUSTER")) c = atoi(e);
   while (c < most && gsample::draw_smem((p->units_per_row + c - 1) / c) > limit) ++c;
   use_cluster(c, p);
   p->maxima = gsample::draw_smem(p->units_per_cta) <= limit;
-  static const int one = getenv("GS_ONE") ? atoi(getenv("GS_ONE")) : kOneLaunch;
-  if (c >= one || !p->maxima) return gsample::launch_draw(*p, dtype, vec, rows, stream);
+  if (c >= kOneLaunch || !p->maxima) return gsample::launch_draw(*p, dtype, vec, rows, stream);
   p->phase = gsample::kShortOnly;
   const cudaError_t e = gsample::launch_draw(*p, dtype, vec, rows, stream);
   if (e != cudaSuccess) return e;
