@@ -119,6 +119,7 @@ struct alignas(16) DrawShared {
   unsigned count[kMaxSegments];   // at rank 0: the lengths of their lists
   unsigned landed_at[kMaxSegments];  // and where they landed
   unsigned landed_n;
+  unsigned near[256], near_all[256];  // units near the maximum, of this CTA and of the row
   union {
     alignas(16) struct {
       unsigned hist[kBins];   // of this CTA; read sixteen bytes at a time
@@ -144,7 +145,7 @@ struct alignas(16) DrawShared {
   u64 scan_m[kDrawWarps];
   float scan_f[kDrawWarps];
   unsigned scan_c[kDrawWarps];
-  int sel[4];
+  int sel[8];
   unsigned above_c, all_c;
   u64 above_m, all_m;
   u64 tail, tail_err, m_lo, m_hi;  // at rank 0
@@ -253,6 +254,12 @@ struct RowCtx {
   }
   static __device__ __forceinline__ float of_short(uint32_t s) {
     return half_to_f32<kHalfMaxima ? 2 : 1>(s);
+  }
+  // What it is at least: the same where the logits have sixteen bits, else the next
+  // number down.
+  static __device__ __forceinline__ float at_least(uint32_t s) {
+    if constexpr (!C::kF32Bits) return of_short(s);
+    return of_short(s == 0u ? 0x8001u : s & 0x8000u ? s + 1u : s - 1u);
   }
 
   static __device__ __forceinline__ float element(const uint4& r, int e) {
@@ -819,15 +826,16 @@ __device__ __noinline__ void settle_long(const DrawParams& p, const Row& r, Draw
       if (tid == kDrawThreads - 1) sh.above_m = mid_head;
       unsigned end_c = own_c;
       u64 end_m = own_m;
-      if (tid < 4) sh.sel[tid] = kBins;
+      if (tid < 8) sh.sel[tid] = kBins;
       cta_scan(end_c, end_m, sh);
       if (tid == kDrawThreads - 1) sh.all_m = end_m;
       __syncthreads();
       // what the exact head has over its estimate, added past it
       const u64 more = (head >> 12) - sh.above_m;  // (may be below 0)
       const u64 est = __umul64hi(p_part, sh.all_m + more);
-      const u64 m0 = p_on ? est - est / 2048ull : ULLONG_MAX;
-      const u64 m1 = p_on ? est + est / 2048ull : ULLONG_MAX;
+      // The estimate errs by 2e-4 of itself in a row of a hundred (1e-5 in the median):
+      // a bracket of 2^-11 either way, or where that holds too many of a quarter.
+      const u64 wide = p_on ? est >> 11 : 0ull, slim = wide >> 2;
       unsigned cc = end_c - own_c;
       u64 cm = end_m - own_m;
 #pragma unroll
@@ -837,23 +845,36 @@ __device__ __noinline__ void settle_long(const DrawParams& p, const Row& r, Draw
         cm += middle(bin, c[i]);
         const u64 upto = bin + 1 >= heavy ? cm + more : cm;
         if (cc >= cut.k) atomicMin(&sh.sel[0], bin);
-        if (upto >= m0) atomicMin(&sh.sel[1], bin);
-        if (upto >= m1) atomicMin(&sh.sel[2], bin);
+        if (p_on) {
+          if (upto + wide >= est) atomicMin(&sh.sel[1], bin);
+          if (upto >= est + wide) atomicMin(&sh.sel[2], bin);
+          if (upto + slim >= est) atomicMin(&sh.sel[3], bin);
+          if (upto >= est + slim) atomicMin(&sh.sel[4], bin);
+        }
       }
       __syncthreads();
       const int kb = sh.sel[0];
-      const int b0 = min(sh.sel[1], kb), b1 = min(min(sh.sel[2], kb), kBins - 1);
-      // the elements before the bracket and up to its end
-      cc = end_c - own_c;
+      int b0 = 0, b1 = 0;
+      unsigned above_c = 0u;
+#pragma unroll 1
+      for (int s = 1; s < 5; s += 2) {
+        b0 = min(sh.sel[s], kb);
+        b1 = min(min(sh.sel[s + 1], kb), kBins - 1);
+        // the elements before the bracket and up to its end
+        cc = end_c - own_c;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int bin = tid * kPer + i;
-        if (bin == b0) sh.above_c = cc;
-        cc += c[i];
-        if (bin == b1) sh.all_c = cc;
+        for (int i = 0; i < kPer; ++i) {
+          const int bin = tid * kPer + i;
+          if (bin == b0) sh.above_c = cc;
+          cc += c[i];
+          if (bin == b1) sh.all_c = cc;
+        }
+        __syncthreads();
+        above_c = b0 < kBins ? sh.above_c : 0u;
+        const bool enough = sh.all_c - above_c <= (unsigned)kRowList;
+        if (enough) break;
+        if (s == 1) __syncthreads();  // the second bracket takes their place
       }
-      __syncthreads();
-      const unsigned above_c = b0 < kBins ? sh.above_c : 0u;
       const bool none = b0 >= kBins;  // top_k alone, and more than there are
       if (none || sh.all_c - above_c <= (unsigned)kRowList) {
         // The exact masses, and the elements of the bracket.
@@ -1114,6 +1135,7 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
   constexpr int EPU = Row::EPU, DT = Row::kDT;
   const int tid = threadIdx.x;
   r.place(p, b);
+  if (tid < 256) sh.near[tid] = sh.near_all[tid] = 0u;
   if (tid == 0) {
     sh.own_n = 0u;
     sh.landed_n = 0u;
@@ -1254,32 +1276,42 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
       // elements may weigh next to nothing, 24, and 24 nats at low temperatures.
       float x_lo = fmaxf(floor_x, M - (tails ? 8.3177662f * T : fmaxf(16.6355324f * T, 24.0f)));
       if (k_on && !p_on) {
-        // Not more than a top_k needs: units enough for it hold as many elements, so
-        // the largest top_k of this CTA are among those from the threshold up.
-        float hi = M;
-#pragma unroll 1
-        for (int tries = 0; tries < 8; ++tries) {
-          const float mid = tries == 0 ? x_lo : 0.5f * (x_lo + hi);
-          // (a maximum is rounded up: above the next number of sixteen bits it is above mid)
-          const float over = Row::of_short(Row::short_of(mid));
-          unsigned c = 0u;
-          for (int32_t u = r.w_lo + r.lane * 8; u < r.w_hi; u += 256) {
-            const uint4 q = lds128(smem_addr(maxima) + (uint32_t)(u - r.u_lo) * 2u);
+        // Not more than a top_k needs. The units by what their maxima are at least, in
+        // 256 steps over the cluster: those down to the step in which the count
+        // reaches top_k hold as many elements.
+        const float step = 255.0f / (M - x_lo);
+        for (int32_t u = r.w_lo + r.lane * 8; u < r.w_hi; u += 256) {
+          const uint4 q = lds128(smem_addr(maxima) + (uint32_t)(u - r.u_lo) * 2u);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              c += Row::of_short(word_of(q, e >> 1) >> ((e & 1) * 16) & 0xFFFFu) > over ? 1u : 0u;
+          for (int e = 0; e < 8; ++e) {
+            const float v = Row::at_least(word_of(q, e >> 1) >> ((e & 1) * 16) & 0xFFFFu);
+            if (v >= x_lo) atomicAdd(&sh.near[max(0, min(255, (int)((M - v) * step)))], 1u);
           }
-          u64 none = 0ull;
-          cta_scan(c, none, sh);
-          if (tid == kDrawThreads - 1) sh.all_c = c;
-          __syncthreads();
-          c = sh.all_c;
-          __syncthreads();
-          if (c >= cut.k)
-            x_lo = mid;
-          else
-            hi = mid;
-          if (tries == 0 ? c <= 256u : c >= cut.k && c <= 2u * cut.k + 64u) break;
+        }
+        __syncthreads();
+        if (tid < 256) {
+          const unsigned c = sh.near[tid];
+          if (c)
+            for (int q = 0; q < r.nrank; ++q) atomicAdd(peer(&sh.near_all[tid], q), c);
+        }
+        cluster_barrier();
+        unsigned c = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c += sh.near_all[r.lane * 8 + i];
+        unsigned incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+          if (r.lane >= o) incl += t;
+        }
+        const unsigned past = __ballot_sync(0xFFFFFFFFu, incl >= cut.k);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          unsigned upto = __shfl_sync(0xFFFFFFFFu, incl - c, l);
+          int at = l * 8;
+          while (at < l * 8 + 7 && upto + sh.near_all[at] < cut.k) upto += sh.near_all[at++];
+          // (a little below the step's end, whatever the roundings)
+          if (at < 255) x_lo = fmaxf(x_lo, M - ((float)at + 1.01f) / step);
         }
       }
       // the units to list, in order
