@@ -515,3 +515,35 @@ def test_verify_many_requests():
         for f in ((None, None, None), (k, p, m)):
             out, count = run_verify(x, draft, offsets, T, u, d, qd, *f)
             check_verify(h, draft, offsets, T, u, d, qh, *f, out, count)
+
+
+def test_outliers_far_above_their_warps_first_logits():
+    """Rows whose maximum lies many powers of two above what a warp reads first."""
+    rng = np.random.default_rng(55)
+    B, V = 40, 30000
+    x, h = logits(rng, B, V, "f32", sd=1.0)
+    x[:, 29990:29996] += torch.linspace(20, 45, B, device="cuda")[:, None]
+    x[::4, :] *= 0.2
+    h = x.cpu().numpy()
+    u = rng.random(B).astype(np.float32)
+    for T in (0.2, 0.6, 1.0):
+        for f in [(None, None, None), (None, np.full(B, 0.97, np.float32), None),
+                  (np.full(B, 30, np.int32), None, None)]:
+            idx, lp = draw(x, np.full(B, T, np.float32), u, *f)
+            check_rows(h, np.full(B, T), u, *f, idx, lp)
+
+
+def test_verify_of_one_token_sets_and_no_rows():
+    """Greedy rows take their draft unless u q is 1 or more; a call without rows."""
+    x = torch.zeros(4, 50, device="cuda")
+    x[:, 7] = 1.0
+    offsets, draft = np.array([0, 2, 4], np.int64), np.array([7, 0, 7, 0], np.int64)
+    q = np.zeros((4, 50), np.float32)
+    q[0, 7], q[2, 7] = 1.0, 4.0
+    u, d = np.full(4, 0.5, np.float32), np.full(2, 0.5, np.float32)
+    out, count = run_verify(x, draft, offsets, np.zeros(2, np.float32), u, d, dev(q))
+    assert out.tolist() == [7, 7, 7, -1] and count.tolist() == [2, 1]
+    check_verify(x.cpu().numpy(), draft, offsets, np.zeros(2), u, d, q, None, None, None, out, count)
+    tokens, count = gs.verify_drafts(x[:0], dev(draft[:0]), dev(np.zeros(4, np.int64)), 1.0,
+                                     dev(u[:0]), torch.zeros(3, device="cuda"))
+    assert tokens.numel() == 0 and count.tolist() == [0, 0, 0]

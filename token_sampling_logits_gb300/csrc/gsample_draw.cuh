@@ -561,20 +561,25 @@ __device__ __forceinline__ int gather(DrawShared& sh, int n_seg, int per, int st
 }
 
 // The lists that landed at rank 0, in the order of their warps, in sh.row.list.
-// Returns the number of entries, or -1 where one did not fit.
-__device__ __forceinline__ int in_order(DrawShared& sh, int n_seg) {
+// Returns the number of entries, or -1 where one did not fit; *coarse: some
+// warp's tail is.
+constexpr unsigned kCoarse = 1u << 30;
+__device__ __forceinline__ int in_order(DrawShared& sh, int n_seg, bool* coarse) {
   const int tid = threadIdx.x;
-  const unsigned c = tid < n_seg ? sh.count[tid] : 0u;
+  unsigned c = tid < n_seg ? sh.count[tid] : 0u;
   const bool bad = c == 0xFFFFFFFFu;
+  const bool rough = !bad && (c & kCoarse);
+  c &= kCoarse - 1u;
   unsigned incl = bad ? 0u : c;
   u64 none = 0ull;
   cta_scan(incl, none, sh);
   unsigned* off = reinterpret_cast<unsigned*>(sh.wmax);
   if (tid < n_seg) off[tid] = incl - (bad ? 0u : c);
   if (tid == kDrawThreads - 1) sh.all_c = incl;
+  *coarse = __syncthreads_or(rough ? 1 : 0) != 0;
   if (__syncthreads_or(bad ? 1 : 0)) return -1;
   for (int s = tid >> 5; s < n_seg; s += kDrawWarps)
-    for (unsigned j = tid & 31; j < sh.count[s]; j += 32)
+    for (unsigned j = tid & 31; j < (sh.count[s] & (kCoarse - 1u)); j += 32)
       sh.row.list[off[s] + j] = sh.row.landed[sh.landed_at[s] + j];
   __syncthreads();
   return (int)sh.all_c;
@@ -1394,7 +1399,9 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
       // does not count then.
       const float whole = floorf(w.c);
       const float power = c0 - whole + 44.0f;
-      bool odd = !(fabsf(tail.hi) + fabsf(tail.lo) < INFINITY) || !(fabsf(power) <= 100.0f);
+      bool odd = !(fabsf(tail.hi) + fabsf(tail.lo) < INFINITY) || !(fabsf(c0 - whole) <= 76.0f);
+      // y is rounded more coarsely where 2^c0 is far below the largest weight
+      const unsigned coarse = c0 < whole - 40.0f ? kCoarse : 0u;
       odd = __any_sync(0xFFFFFFFFu, odd);
       const float to_units = __int_as_float(((int)(odd ? 0.0f : power) + 127) << 23);
       long long sum = 0;
@@ -1413,7 +1420,7 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
           for (unsigned j = r.lane; j < mine; j += 32)
             *peer(&sh.row.landed[to + j], 0) = sh.own[r.warp * kWarpList + j];
         if (r.lane == 0) {
-          *peer(&sh.count[at], 0) = fits ? mine : 0xFFFFFFFFu;
+          *peer(&sh.count[at], 0) = fits ? mine | coarse : 0xFFFFFFFFu;
           *peer(&sh.landed_at[at], 0) = to;
           *peer(&sh.sums[buf][at], 0) = t;
         }
@@ -1428,7 +1435,8 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
       }
       bool ok = false;
       if (r.rank == 0) {
-        const int n = in_order(sh, r.nrank * kDrawWarps);
+        bool rough = false;
+        const int n = in_order(sh, r.nrank * kDrawWarps, &rough);
         if (n >= 0) {
           const int per = (n + kDrawThreads - 1) / kDrawThreads;
           u64 we[3] = {0ull, 0ull, 0ull}, own = 0ull;
@@ -1451,12 +1459,14 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
               rest = warp_sum(rest);
               if (r.lane == 0) {
                 // The binary32 tail. In 2^-24 of a term: 23 for y, whose two roundings
-                // are of 2^-20 while |y| < 32 (terms below are less than the V units), 4
-                // for ex2, 4 for the sum of a unit, 6 for its scale; then what the rounding
-                // of the low parts left of the terms that were listed, and half a unit for
-                // each fixed-point weight.
-                const u64 err =
-                    __float2ull_ru((float)rest * (40.0f * 5.9604645e-8f)) + (listed >> 34) + (u64)p.V;
+                // are of 2^-20 while |y| < 32 (46 where 2^c0 lies more than 40 powers
+                // below the largest weight: |y| < 64; terms below either are less than the
+                // V units), 4 for ex2, 4 for the sum of a unit, 6 for its scale; then what
+                // the rounding of the low parts left of the terms that were listed, and
+                // half a unit for each fixed-point weight.
+                const float rel = rough ? 64.0f : 40.0f;
+                const u64 err = __float2ull_ru((float)rest * (rel * 5.9604645e-8f)) +
+                                (listed >> 34) + (u64)p.V;
                 sh.tail = rest;
                 sh.tail_err = err;
                 sh.m_lo = max(ceil_part(p_part, listed + rest - min(rest, err)), 1ull);
@@ -1686,8 +1696,12 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
   if (r.rank == 0 && tid == 0) {
     if constexpr (VERIFY) {
       if (set.kind == kOne && b + 1 < __ldcg(p.offsets + s + 1) && b + 1 < p.B) {
-        // the set is one token: its draft passes for every u
-        set.accepted = __ldcg(p.draft + b) == (int64_t)set.last ? 1 : 0;
+        // the set is one token: its draft passes for every u (and q up to 1)
+        const float u = fminf(fmaxf(__ldcg(p.uniform + b), 0.0f), 0.999999940395355224609375f);
+        const int64_t d = __ldcg(p.draft + b);
+        const bool same = d == (int64_t)set.last;
+        const float q = same && p.probs ? __ldcg(p.probs + b * p.probs_ld + d) : 1.0f;
+        set.accepted = same && !((double)u * (double)q >= 1.0) ? 1 : 0;
       }
       p.sets[b] = set;
     } else if (set.kind != kSet) {
