@@ -377,7 +377,8 @@ __device__ __forceinline__ void find_index(const Row& r, DrawShared& sh, int buf
   const int n = r.nrank * kDrawWarps;
   u64 own = 0ull;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) own += r.lane * kPer + j < n ? sh.sums[buf][r.lane * kPer + j] : 0ull;
+  for (int j = 0; j < kPer; ++j)
+    own += r.lane * kPer + j < n ? sh.sums[buf][r.lane * kPer + j] : 0ull;
   u64 incl = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -749,151 +750,150 @@ __device__ __noinline__ void settle_long(const DrawParams& p, const Row& r, Draw
   cut.m_lo = cut.m_hi = ULLONG_MAX;
   const u64 p_part = fraction_of(top_p);
   bool settled = false;
-  {
-    int summed = -1;  // the buffer with the warps' sums of K's weights
-    if (!settled && !(k_on || p_on)) {
-      const u64 own = w.shift ? sum_from<true>(r, w, table, floor_x)
-                              : sum_from<false>(r, w, table, floor_x);
-      set.sum = cluster_sum(own, r, sh, buf);
-      summed = buf;
-      buf ^= 1;
-      settled = true;
-    }
+  int summed = -1;  // the buffer with the warps' sums of K's weights
+  if (!(k_on || p_on)) {
+    const u64 own = w.shift ? sum_from<true>(r, w, table, floor_x)
+                            : sum_from<false>(r, w, table, floor_x);
+    set.sum = cluster_sum(own, r, sh, buf);
+    summed = buf;
+    buf ^= 1;
+    settled = true;
+  }
 
-    if (!settled) {
-      // Long sets. The histogram's steps run down 32 powers of two for a mass (what
-      // lies below counts as nothing: V 2^-32 of the largest weight at most), to
-      // the floor for a count.
-      const float low = p_on ? fmaxf(floor_x, fmaf(-22.1807098f, T, M)) : floor_x;
-      const float step = (float)(kBins - 1) / (M - low);
-      for (int j = tid; j < kBins; j += kDrawThreads) sh.hist[j] = 0u;
-      __syncthreads();
-      // The first four powers of two are weighed exactly: a few heavy elements, whose
-      // places in their steps would not average out.
-      const float drop = w.rh * w.scale / step;  // powers of two a step
-      const int heavy = (int)fminf(4.0f / drop, (float)kBins);
-      u64 head = 0ull;
-      r.each([&](float x, int32_t) {
-        if (x >= floor_x) {
-          const int at = max(0, min(kBins - 1, (int)((M - x) * step)));
-          atomicAdd(&sh.hist[at], 1u);
-          if (at < heavy) head += weight_of(x, w, table);
-        }
-      });
-      head = cluster_sum(head, r, sh, buf);  // (its barrier ends the histograms)
-      buf ^= 1;
-      // each CTA adds up its share of the steps and hands the sums to all
-      const int share = (kBins / 4 + r.nrank - 1) / r.nrank;
-      for (int j = tid; j < share; j += kDrawThreads) {
-        const int at = r.rank * share + j;
-        if (at < kBins / 4) {
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (!settled) {
+    // Long sets. The histogram's steps run down 32 powers of two for a mass (what
+    // lies below counts as nothing: V 2^-32 of the largest weight at most), to
+    // the floor for a count.
+    const float low = p_on ? fmaxf(floor_x, fmaf(-22.1807098f, T, M)) : floor_x;
+    const float step = (float)(kBins - 1) / (M - low);
+    for (int j = tid; j < kBins; j += kDrawThreads) sh.hist[j] = 0u;
+    __syncthreads();
+    // The first four powers of two are weighed exactly: a few heavy elements, whose
+    // places in their steps would not average out.
+    const float drop = w.rh * w.scale / step;  // powers of two a step
+    const int heavy = (int)fminf(4.0f / drop, (float)kBins);
+    u64 head = 0ull;
+    r.each([&](float x, int32_t) {
+      if (x >= floor_x) {
+        const int at = max(0, min(kBins - 1, (int)((M - x) * step)));
+        atomicAdd(&sh.hist[at], 1u);
+        if (at < heavy) head += weight_of(x, w, table);
+      }
+    });
+    head = cluster_sum(head, r, sh, buf);  // (its barrier ends the histograms)
+    buf ^= 1;
+    // each CTA adds up its share of the steps and hands the sums to all
+    const int share = (kBins / 4 + r.nrank - 1) / r.nrank;
+    for (int j = tid; j < share; j += kDrawThreads) {
+      const int at = r.rank * share + j;
+      if (at < kBins / 4) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 4
-          for (int q = 0; q < r.nrank; ++q) {
-            const uint4 o = reinterpret_cast<const uint4*>(peer(sh.hist, q))[at];
-            v.x += o.x;
-            v.y += o.y;
-            v.z += o.z;
-            v.w += o.w;
-          }
-          for (int q = 0; q < r.nrank; ++q) reinterpret_cast<uint4*>(peer(sh.steps, q))[at] = v;
+        for (int q = 0; q < r.nrank; ++q) {
+          const uint4 o = reinterpret_cast<const uint4*>(peer(sh.hist, q))[at];
+          v.x += o.x;
+          v.y += o.y;
+          v.z += o.z;
+          v.w += o.w;
         }
+        for (int q = 0; q < r.nrank; ++q) reinterpret_cast<uint4*>(peer(sh.steps, q))[at] = v;
       }
-      cluster_barrier();
-      constexpr int kPer = kBins / kDrawThreads;
-      unsigned c[kPer];
+    }
+    cluster_barrier();
+    constexpr int kPer = kBins / kDrawThreads;
+    unsigned c[kPer];
 #pragma unroll
-      for (int i = 0; i < kPer / 4; ++i) {
-        const uint4 v = reinterpret_cast<const uint4*>(sh.steps)[tid * (kPer / 4) + i];
-        c[4 * i] = v.x;
-        c[4 * i + 1] = v.y;
-        c[4 * i + 2] = v.z;
-        c[4 * i + 3] = v.w;
-      }
-      // Counts, and masses as if every logit were in the middle of its step, in
-      // units of 2^-32: an estimate that the exact masses are held against.
-      const float top = (w.shift ? 0.0f : fmaf(M, w.rh, -w.c)) + 32.0f - 0.5f * drop;
-      auto middle = [&](int bin, unsigned n) {
-        return __float2ull_rn((float)n * ex2_approx(top - (float)bin * drop));
-      };
-      unsigned own_c = 0u;
-      u64 own_m = 0ull, own_h = 0ull;
+    for (int i = 0; i < kPer / 4; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(sh.steps)[tid * (kPer / 4) + i];
+      c[4 * i] = v.x;
+      c[4 * i + 1] = v.y;
+      c[4 * i + 2] = v.z;
+      c[4 * i + 3] = v.w;
+    }
+    // Counts, and masses as if every logit were in the middle of its step, in
+    // units of 2^-32: an estimate that the exact masses are held against.
+    const float top = (w.shift ? 0.0f : fmaf(M, w.rh, -w.c)) + 32.0f - 0.5f * drop;
+    auto middle = [&](int bin, unsigned n) {
+      return __float2ull_rn((float)n * ex2_approx(top - (float)bin * drop));
+    };
+    unsigned own_c = 0u;
+    u64 own_m = 0ull, own_h = 0ull;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const u64 m = middle(tid * kPer + i, c[i]);
-        own_c += c[i];
-        own_m += m;
-        if (tid * kPer + i < heavy) own_h += m;
+    for (int i = 0; i < kPer; ++i) {
+      const u64 m = middle(tid * kPer + i, c[i]);
+      own_c += c[i];
+      own_m += m;
+      if (tid * kPer + i < heavy) own_h += m;
+    }
+    unsigned none_c = 0u;
+    u64 mid_head = own_h;
+    cta_scan(none_c, mid_head, sh);
+    if (tid == kDrawThreads - 1) sh.above_m = mid_head;
+    unsigned end_c = own_c;
+    u64 end_m = own_m;
+    if (tid < 8) sh.sel[tid] = kBins;
+    cta_scan(end_c, end_m, sh);
+    if (tid == kDrawThreads - 1) sh.all_m = end_m;
+    __syncthreads();
+    // what the exact head has over its estimate, added past it
+    const u64 more = (head >> 12) - sh.above_m;  // (may be below 0)
+    const u64 est = __umul64hi(p_part, sh.all_m + more);
+    // The estimate errs by 2e-4 of itself in a row of a hundred (1e-5 in the median):
+    // a bracket of 2^-11 either way, or where that holds too many of a quarter.
+    const u64 wide = p_on ? est >> 11 : 0ull, slim = wide >> 2;
+    unsigned cc = end_c - own_c;
+    u64 cm = end_m - own_m;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int bin = tid * kPer + i;
+      cc += c[i];
+      cm += middle(bin, c[i]);
+      const u64 upto = bin + 1 >= heavy ? cm + more : cm;
+      if (cc >= cut.k) atomicMin(&sh.sel[0], bin);
+      if (p_on) {
+        if (upto + wide >= est) atomicMin(&sh.sel[1], bin);
+        if (upto >= est + wide) atomicMin(&sh.sel[2], bin);
+        if (upto + slim >= est) atomicMin(&sh.sel[3], bin);
+        if (upto >= est + slim) atomicMin(&sh.sel[4], bin);
       }
-      unsigned none_c = 0u;
-      u64 mid_head = own_h;
-      cta_scan(none_c, mid_head, sh);
-      if (tid == kDrawThreads - 1) sh.above_m = mid_head;
-      unsigned end_c = own_c;
-      u64 end_m = own_m;
-      if (tid < 8) sh.sel[tid] = kBins;
-      cta_scan(end_c, end_m, sh);
-      if (tid == kDrawThreads - 1) sh.all_m = end_m;
-      __syncthreads();
-      // what the exact head has over its estimate, added past it
-      const u64 more = (head >> 12) - sh.above_m;  // (may be below 0)
-      const u64 est = __umul64hi(p_part, sh.all_m + more);
-      // The estimate errs by 2e-4 of itself in a row of a hundred (1e-5 in the median):
-      // a bracket of 2^-11 either way, or where that holds too many of a quarter.
-      const u64 wide = p_on ? est >> 11 : 0ull, slim = wide >> 2;
-      unsigned cc = end_c - own_c;
-      u64 cm = end_m - own_m;
+    }
+    __syncthreads();
+    const int kb = sh.sel[0];
+    int b0 = 0, b1 = 0;
+    unsigned above_c = 0u;
+#pragma unroll 1
+    for (int s = 1; s < 5; s += 2) {
+      b0 = min(sh.sel[s], kb);
+      b1 = min(min(sh.sel[s + 1], kb), kBins - 1);
+      // the elements before the bracket and up to its end
+      cc = end_c - own_c;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int bin = tid * kPer + i;
+        if (bin == b0) sh.above_c = cc;
         cc += c[i];
-        cm += middle(bin, c[i]);
-        const u64 upto = bin + 1 >= heavy ? cm + more : cm;
-        if (cc >= cut.k) atomicMin(&sh.sel[0], bin);
-        if (p_on) {
-          if (upto + wide >= est) atomicMin(&sh.sel[1], bin);
-          if (upto >= est + wide) atomicMin(&sh.sel[2], bin);
-          if (upto + slim >= est) atomicMin(&sh.sel[3], bin);
-          if (upto >= est + slim) atomicMin(&sh.sel[4], bin);
-        }
+        if (bin == b1) sh.all_c = cc;
       }
       __syncthreads();
-      const int kb = sh.sel[0];
-      int b0 = 0, b1 = 0;
-      unsigned above_c = 0u;
-#pragma unroll 1
-      for (int s = 1; s < 5; s += 2) {
-        b0 = min(sh.sel[s], kb);
-        b1 = min(min(sh.sel[s + 1], kb), kBins - 1);
-        // the elements before the bracket and up to its end
-        cc = end_c - own_c;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int bin = tid * kPer + i;
-          if (bin == b0) sh.above_c = cc;
-          cc += c[i];
-          if (bin == b1) sh.all_c = cc;
+      above_c = b0 < kBins ? sh.above_c : 0u;
+      const bool enough = sh.all_c - above_c <= (unsigned)kRowList;
+      if (enough) break;
+      if (s == 1) __syncthreads();  // the second bracket takes their place
+    }
+    const bool none = b0 >= kBins;  // top_k alone, and more than there are
+    if (none || sh.all_c - above_c <= (unsigned)kRowList) {
+      // The exact masses, and the elements of the bracket.
+      const float f0 = (float)b0, f1 = b1 == kBins - 1 ? INFINITY : (float)(b1 + 1);
+      u64 above = 0ull, all = 0ull, own_above = 0ull;
+      WeightSum pa, ps;
+      auto list = [&](float x, float v, int32_t i) {
+        if (x >= floor_x && v >= f0 && v < f1) {
+          const unsigned at = atomicAdd(&sh.own_n, 1u);
+          if (at < (unsigned)kCtaList) sh.own[at] = make_uint2(__float_as_uint(x), (uint32_t)i);
         }
-        __syncthreads();
-        above_c = b0 < kBins ? sh.above_c : 0u;
-        const bool enough = sh.all_c - above_c <= (unsigned)kRowList;
-        if (enough) break;
-        if (s == 1) __syncthreads();  // the second bracket takes their place
-      }
-      const bool none = b0 >= kBins;  // top_k alone, and more than there are
-      if (none || sh.all_c - above_c <= (unsigned)kRowList) {
-        // The exact masses, and the elements of the bracket.
-        const float f0 = (float)b0, f1 = b1 == kBins - 1 ? INFINITY : (float)(b1 + 1);
-        u64 above = 0ull, all = 0ull, own_above = 0ull;
-        WeightSum pa, ps;
-        auto list = [&](float x, float v, int32_t i) {
-          if (x >= floor_x && v >= f0 && v < f1) {
-            const unsigned at = atomicAdd(&sh.own_n, 1u);
-            if (at < (unsigned)kCtaList) sh.own[at] = make_uint2(__float_as_uint(x), (uint32_t)i);
-          }
-        };
-        auto sweep = [&](auto shift) {
-          r.each_pair(
+      };
+      auto sweep = [&](auto shift) {
+        r.each_pair(
             [&](float x0, float x1, int32_t i) {
               const float v0 = (M - x0) * step, v1 = (M - x1) * step;
               int32_t h[2], l[2];
@@ -912,222 +912,221 @@ __device__ __noinline__ void settle_long(const DrawParams& p, const Row& r, Draw
               above += pa.take((uint32_t)n);
               all += ps.take((uint32_t)n);
             });
-        };
-        if (w.shift)
-          sweep(std::true_type{});
-        else
-          sweep(std::false_type{});
-        own_above = warp_sum(above);
-        const u64 sa = cluster_sum(above, r, sh, buf);
-        const u64 ss = cluster_sum(all, r, sh, buf ^ 1);  // its barrier orders the lists too
-        if (p_on) {
-          cut.m_lo = cut.m_hi = max(ceil_part(p_part, ss), 1ull);
+      };
+      if (w.shift)
+        sweep(std::true_type{});
+      else
+        sweep(std::false_type{});
+      own_above = warp_sum(above);
+      const u64 sa = cluster_sum(above, r, sh, buf);
+      const u64 ss = cluster_sum(all, r, sh, buf ^ 1);  // its barrier orders the lists too
+      if (p_on) {
+        cut.m_lo = cut.m_hi = max(ceil_part(p_part, ss), 1ull);
+      }
+      if (tid == 0) *peer(&sh.count[r.rank], 0) = sh.own_n;
+      cluster_barrier();
+      if (r.rank == 0) {
+        bool ok = false;
+        if (none) {
+          if (tid == 0) {
+            sh.key = floor_key;
+            sh.last = INT32_MAX;
+            sh.sum = sa;
+          }
+          ok = true;
+        } else if (!(sa >= cut.m_lo)) {
+          const int n = gather(sh, r.nrank, 1, kCtaList);
+          if (n >= 0) {
+            const int per = (n + kDrawThreads - 1) / kDrawThreads;
+            u64 we[3] = {0ull, 0ull, 0ull};
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+              const int j = tid * per + i;
+              if (i < per && j < n)
+                we[i] = weight_of(__uint_as_float(sh.row.list[j].x), w, table);
+            }
+            float hi = -INFINITY, lo = INFINITY;
+            for (int j = tid; j < n; j += kDrawThreads) {
+              hi = fmaxf(hi, __uint_as_float(sh.row.list[j].x));
+              lo = fminf(lo, __uint_as_float(sh.row.list[j].x));
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+              hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+              lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+            }
+            if (r.lane == 0) {
+              sh.scan_f[r.warp] = hi;
+              reinterpret_cast<float*>(sh.scan_m)[r.warp] = lo;
+            }
+            __syncthreads();
+            for (int j = 0; j < kDrawWarps; ++j) {
+              hi = fmaxf(hi, sh.scan_f[j]);
+              lo = fminf(lo, reinterpret_cast<const float*>(sh.scan_m)[j]);
+            }
+            __syncthreads();
+            ok = settle(sh, n, per, we, above_c, sa, cut, lo, hi, false);
+          }
         }
-        if (tid == 0) *peer(&sh.count[r.rank], 0) = sh.own_n;
-        cluster_barrier();
-        if (r.rank == 0) {
-          bool ok = false;
-          if (none) {
-            if (tid == 0) {
-              sh.key = floor_key;
-              sh.last = INT32_MAX;
-              sh.sum = sa;
-            }
-            ok = true;
-          } else if (!(sa >= cut.m_lo)) {
-            const int n = gather(sh, r.nrank, 1, kCtaList);
-            if (n >= 0) {
-              const int per = (n + kDrawThreads - 1) / kDrawThreads;
-              u64 we[3] = {0ull, 0ull, 0ull};
-#pragma unroll
-              for (int i = 0; i < 3; ++i) {
-                const int j = tid * per + i;
-                if (i < per && j < n)
-                  we[i] = weight_of(__uint_as_float(sh.row.list[j].x), w, table);
-              }
-              float hi = -INFINITY, lo = INFINITY;
-              for (int j = tid; j < n; j += kDrawThreads) {
-                hi = fmaxf(hi, __uint_as_float(sh.row.list[j].x));
-                lo = fminf(lo, __uint_as_float(sh.row.list[j].x));
-              }
-#pragma unroll
-              for (int o = 16; o > 0; o >>= 1) {
-                hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
-                lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-              }
-              if (r.lane == 0) {
-                sh.scan_f[r.warp] = hi;
-                reinterpret_cast<float*>(sh.scan_m)[r.warp] = lo;
-              }
-              __syncthreads();
-              for (int j = 0; j < kDrawWarps; ++j) {
-                hi = fmaxf(hi, sh.scan_f[j]);
-                lo = fminf(lo, reinterpret_cast<const float*>(sh.scan_m)[j]);
-              }
-              __syncthreads();
-              ok = settle(sh, n, per, we, above_c, sa, cut, lo, hi, false);
-            }
+        __syncthreads();
+        if (tid < r.nrank) {
+          *peer(&sh.key, tid) = sh.key;
+          *peer(&sh.last, tid) = sh.last;
+          *peer(&sh.sum, tid) = sh.sum;
+          *peer(&sh.settled, tid) = ok ? 1 : 0;
+        }
+      }
+      cluster_barrier();
+      settled = sh.settled != 0;
+      if (settled) {
+        set.key = sh.key;
+        set.last = sh.last;
+        set.sum = sh.sum;
+        if constexpr (!VERIFY) {
+          // The warps' sums of K: what is above the bracket, and their
+          // elements of it that are in K.
+          if (r.lane == 0) sh.scan_m[r.warp] = own_above;
+          __syncthreads();
+          const int n = none ? 0 : (int)sh.own_n;
+          for (int j = tid; j < n; j += kDrawThreads) {
+            const uint2 q = sh.own[j];
+            const float x = __uint_as_float(q.x);
+            const uint32_t key = ordered_bits(x);
+            if (key > set.key || (key == set.key && (int32_t)q.y <= set.last))
+              atomicAdd(&sh.scan_m[r.warp_of((int32_t)q.y)], weight_of(x, w, table));
           }
           __syncthreads();
-          if (tid < r.nrank) {
-            *peer(&sh.key, tid) = sh.key;
-            *peer(&sh.last, tid) = sh.last;
-            *peer(&sh.sum, tid) = sh.sum;
-            *peer(&sh.settled, tid) = ok ? 1 : 0;
-          }
-        }
-        cluster_barrier();
-        settled = sh.settled != 0;
-        if (settled) {
-          set.key = sh.key;
-          set.last = sh.last;
-          set.sum = sh.sum;
-          if constexpr (!VERIFY) {
-            // The warps' sums of K: what is above the bracket, and their
-            // elements of it that are in K.
-            if (r.lane == 0) sh.scan_m[r.warp] = own_above;
-            __syncthreads();
-            const int n = none ? 0 : (int)sh.own_n;
-            for (int j = tid; j < n; j += kDrawThreads) {
-              const uint2 q = sh.own[j];
-              const float x = __uint_as_float(q.x);
-              const uint32_t key = ordered_bits(x);
-              if (key > set.key || (key == set.key && (int32_t)q.y <= set.last))
-                atomicAdd(&sh.scan_m[r.warp_of((int32_t)q.y)], weight_of(x, w, table));
-            }
-            __syncthreads();
-            cluster_sum(r.lane == 0 ? sh.scan_m[r.warp] : 0ull, r, sh, buf);
-            summed = buf;
-            buf ^= 1;
-          }
-        }
-      }
-    }
-
-    if (!settled) {
-      // A radix select.
-      if (p_on) {
-        const u64 own = w.shift ? sum_from<true>(r, w, table, kLowestLogit)
-                                : sum_from<false>(r, w, table, kLowestLogit);
-        const u64 all = cluster_sum(own, r, sh, buf);
-        buf ^= 1;
-        cut.m_lo = max(ceil_part(p_part, all), 1ull);
-      }
-      unsigned k_rem = cut.k;
-      u64 m_rem = cut.m_lo;
-      const uint32_t low = floor_key >> ZB;
-      const int nb = 32 - __clz((ordered_bits(M) >> ZB) - low);
-      uint32_t prefix = 0u;
-      unsigned ties = 0u;
-      u64 above = 0ull;
-      int hb = 0;
-      bool reached = true;
-      cluster_barrier();  // the histograms take the place of what peers may still read
-      for (int hi = nb;;) {
-        const int lo = hi > 8 ? hi - 8 : 0;
-        if (tid < 256) {
-          sh.digit.count[hb][tid] = 0u;
-          sh.digit.mass[hb][tid] = 0ull;
-        }
-        __syncthreads();
-        r.each([&](float x, int32_t) {
-          if (!(x >= floor_x)) return;
-          const uint32_t rel = (ordered_bits(x) >> ZB) - low;
-          if (hi < 32 && (rel >> hi) != (prefix >> hi)) return;
-          const uint32_t d = (rel >> lo) & ((1u << (hi - lo)) - 1u);
-          atomicAdd(&sh.digit.count[hb][d], 1u);
-          atomicAdd(&sh.digit.mass[hb][d], weight_of(x, w, table));
-        });
-        cluster_barrier();
-        unsigned c = 0u;
-        u64 mass = 0ull;
-        if (tid < 256) {
-          const int dg = 255 - tid;
-          for (int q = 0; q < r.nrank; ++q) {
-            c += *peer(&sh.digit.count[hb][dg], q);
-            mass += *peer(&sh.digit.mass[hb][dg], q);
-          }
-        }
-        const int d = find_digit(c, mass, k_rem, m_rem, sh);
-        if (d < 0) {  // on the first level only: K is all that the floor leaves
-          set.sum = sh.all_m;
-          reached = false;
-          break;
-        }
-        k_rem -= sh.above_c;
-        m_rem -= sh.above_m;
-        above += sh.above_m;
-        prefix |= (uint32_t)d << lo;
-        if (tid == 255 - d) sh.sel[1] = (int)c;
-        __syncthreads();
-        ties = (unsigned)sh.sel[1];
-        hb ^= 1;
-        if (lo == 0) break;
-        hi = lo;
-      }
-      if (reached) {
-        // The entries on K's last key that K takes.
-        const uint32_t key = key_of_short<DT>(low + prefix);
-        const u64 each = weight_of(logit_of_key(key), w, table);
-        u64 take = k_rem;
-        if (each > 0ull) {
-          const u64 by_mass = m_rem / each + (m_rem % each != 0ull ? 1ull : 0ull);
-          if (by_mass < take) take = by_mass;
-        }
-        if (take < 1ull) take = 1ull;
-        set.key = key;
-        if (take < ties) {
-          auto tie = [&](float x, int32_t) {
-            return x >= floor_x && ordered_bits(x) == key ? 1ull : 0ull;
-          };
-          u64 n = 0ull;
-          r.each([&](float x, int32_t i) { n += tie(x, i); });
-          cluster_sum(n, r, sh, buf);
-          find_index(r, sh, buf, take - 1ull,
-                     [&](float x0, float x1, int32_t i, u64(&v)[2]) {
-                       v[0] = tie(x0, i);
-                       v[1] = tie(x1, i + 1);
-                     },
-                     [&](int32_t i, float, u64) {
-                       for (int q = 0; q < r.nrank; ++q) *peer(&sh.found, q) = i;
-                     });
-          buf ^= 1;
-          cluster_barrier();
-          set.last = sh.found;
-        } else {
-          take = ties;
-        }
-        set.sum = above + take * each;
-      }
-    }
-
-    auto kept = [&](float x, int32_t i) {
-      if (!(x >= floor_x)) return false;
-      const uint32_t key = ordered_bits(x);
-      return key > set.key || (key == set.key && i <= set.last);
-    };
-    if constexpr (!VERIFY) {
-        auto pair = [&](float x0, float x1, int32_t i, u64(&v)[2]) {
-          weights_of(kept(x0, i) ? x0 : -INFINITY, kept(x1, i + 1) ? x1 : -INFINITY, w, table, v);
-        };
-        if (summed < 0) {
-          u64 own = 0ull;
-          r.each_pair(
-              [&](float x0, float x1, int32_t i) {
-                u64 v[2];
-                pair(x0, x1, i, v);
-                own += v[0] + v[1];
-              },
-              [](int) {});
-          cluster_sum(own, r, sh, buf);
+          cluster_sum(r.lane == 0 ? sh.scan_m[r.warp] : 0ull, r, sh, buf);
           summed = buf;
+          buf ^= 1;
         }
-        const u64 target = __umul64hi(fraction_of(__ldcg(p.uniform + b)), set.sum);
-        find_index(r, sh, summed, target, pair, [&](int32_t i, float, u64 v) {
-          p.out_idx[b] = i;
-          if (p.out_logprob) p.out_logprob[b] = log_ratio(v, set.sum, table);
-        });
+      }
     }
+  }
+
+  if (!settled) {
+    // A radix select.
+    if (p_on) {
+      const u64 own = w.shift ? sum_from<true>(r, w, table, kLowestLogit)
+                              : sum_from<false>(r, w, table, kLowestLogit);
+      const u64 all = cluster_sum(own, r, sh, buf);
+      buf ^= 1;
+      cut.m_lo = max(ceil_part(p_part, all), 1ull);
+    }
+    unsigned k_rem = cut.k;
+    u64 m_rem = cut.m_lo;
+    const uint32_t low = floor_key >> ZB;
+    const int nb = 32 - __clz((ordered_bits(M) >> ZB) - low);
+    uint32_t prefix = 0u;
+    unsigned ties = 0u;
+    u64 above = 0ull;
+    int hb = 0;
+    bool reached = true;
+    cluster_barrier();  // the histograms take the place of what peers may still read
+    for (int hi = nb;;) {
+      const int lo = hi > 8 ? hi - 8 : 0;
+      if (tid < 256) {
+        sh.digit.count[hb][tid] = 0u;
+        sh.digit.mass[hb][tid] = 0ull;
+      }
+      __syncthreads();
+      r.each([&](float x, int32_t) {
+        if (!(x >= floor_x)) return;
+        const uint32_t rel = (ordered_bits(x) >> ZB) - low;
+        if (hi < 32 && (rel >> hi) != (prefix >> hi)) return;
+        const uint32_t d = (rel >> lo) & ((1u << (hi - lo)) - 1u);
+        atomicAdd(&sh.digit.count[hb][d], 1u);
+        atomicAdd(&sh.digit.mass[hb][d], weight_of(x, w, table));
+      });
+      cluster_barrier();
+      unsigned c = 0u;
+      u64 mass = 0ull;
+      if (tid < 256) {
+        const int dg = 255 - tid;
+        for (int q = 0; q < r.nrank; ++q) {
+          c += *peer(&sh.digit.count[hb][dg], q);
+          mass += *peer(&sh.digit.mass[hb][dg], q);
+        }
+      }
+      const int d = find_digit(c, mass, k_rem, m_rem, sh);
+      if (d < 0) {  // on the first level only: K is all that the floor leaves
+        set.sum = sh.all_m;
+        reached = false;
+        break;
+      }
+      k_rem -= sh.above_c;
+      m_rem -= sh.above_m;
+      above += sh.above_m;
+      prefix |= (uint32_t)d << lo;
+      if (tid == 255 - d) sh.sel[1] = (int)c;
+      __syncthreads();
+      ties = (unsigned)sh.sel[1];
+      hb ^= 1;
+      if (lo == 0) break;
+      hi = lo;
+    }
+    if (reached) {
+      // The entries on K's last key that K takes.
+      const uint32_t key = key_of_short<DT>(low + prefix);
+      const u64 each = weight_of(logit_of_key(key), w, table);
+      u64 take = k_rem;
+      if (each > 0ull) {
+        const u64 by_mass = m_rem / each + (m_rem % each != 0ull ? 1ull : 0ull);
+        if (by_mass < take) take = by_mass;
+      }
+      if (take < 1ull) take = 1ull;
+      set.key = key;
+      if (take < ties) {
+        auto tie = [&](float x, int32_t) {
+          return x >= floor_x && ordered_bits(x) == key ? 1ull : 0ull;
+        };
+        u64 n = 0ull;
+        r.each([&](float x, int32_t i) { n += tie(x, i); });
+        cluster_sum(n, r, sh, buf);
+        find_index(r, sh, buf, take - 1ull,
+                   [&](float x0, float x1, int32_t i, u64(&v)[2]) {
+                     v[0] = tie(x0, i);
+                     v[1] = tie(x1, i + 1);
+                   },
+                   [&](int32_t i, float, u64) {
+                     for (int q = 0; q < r.nrank; ++q) *peer(&sh.found, q) = i;
+                   });
+        buf ^= 1;
+        cluster_barrier();
+        set.last = sh.found;
+      } else {
+        take = ties;
+      }
+      set.sum = above + take * each;
+    }
+  }
+
+  auto kept = [&](float x, int32_t i) {
+    if (!(x >= floor_x)) return false;
+    const uint32_t key = ordered_bits(x);
+    return key > set.key || (key == set.key && i <= set.last);
+  };
+  if constexpr (!VERIFY) {
+    auto pair = [&](float x0, float x1, int32_t i, u64(&v)[2]) {
+      weights_of(kept(x0, i) ? x0 : -INFINITY, kept(x1, i + 1) ? x1 : -INFINITY, w, table, v);
+    };
+    if (summed < 0) {
+      u64 own = 0ull;
+      r.each_pair(
+          [&](float x0, float x1, int32_t i) {
+            u64 v[2];
+            pair(x0, x1, i, v);
+            own += v[0] + v[1];
+          },
+          [](int) {});
+      cluster_sum(own, r, sh, buf);
+      summed = buf;
+    }
+    const u64 target = __umul64hi(fraction_of(__ldcg(p.uniform + b)), set.sum);
+    find_index(r, sh, summed, target, pair, [&](int32_t i, float, u64 v) {
+      p.out_idx[b] = i;
+      if (p.out_logprob) p.out_logprob[b] = log_ratio(v, set.sum, table);
+    });
   }
   *out = set;
 }
@@ -1527,7 +1526,8 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
             for (int i = 0; i < 3; ++i) {
               const int j = tid * per + i;
               if (i < per && j < n) {
-                const int at = r.segment_of((int32_t)sh.row.list[j].y, p.units_per_row, p.units_per_cta);
+                const int at =
+                    r.segment_of((int32_t)sh.row.list[j].y, p.units_per_row, p.units_per_cta);
                 if (at != last && c) {
                   atomicAdd(&run[last], c);
                   c = 0ull;
@@ -1680,16 +1680,18 @@ __device__ __forceinline__ void settle_row(const DrawParams& p, Row& r, DrawShar
     }
     if constexpr (VERIFY) {
       if (r.rank == 0 && tid == 0 && !tested) {
-      const int64_t t = __ldcg(p.draft + b);
-      if (b + 1 < __ldcg(p.offsets + s + 1) && b + 1 < p.B && t >= 0 && t < p.V) {
-        const float x = logit_at<DT>(r.row, t);
-        const float u = fminf(fmaxf(__ldcg(p.uniform + b), 0.0f), 0.999999940395355224609375f);
-        const float q = p.probs ? __ldcg(p.probs + b * p.probs_ld + t) : 1.0f;
-        const uint32_t key = ordered_bits(x);
-        const bool kept = x >= floor_x && (key > set.key || (key == set.key && (int32_t)t <= set.last));
-        const u64 wt = kept ? weight_of(x, w, table) : 0ull;
-        if (wt > 0ull && !((double)u * (double)q * (double)set.sum >= (double)wt)) set.accepted = 1;
-      }
+        const int64_t d = __ldcg(p.draft + b);
+        if (b + 1 < __ldcg(p.offsets + s + 1) && b + 1 < p.B && d >= 0 && d < p.V) {
+          const float x = logit_at<DT>(r.row, d);
+          const float u = fminf(fmaxf(__ldcg(p.uniform + b), 0.0f), 0.999999940395355224609375f);
+          const float q = p.probs ? __ldcg(p.probs + b * p.probs_ld + d) : 1.0f;
+          const uint32_t key = ordered_bits(x);
+          const bool kept =
+              x >= floor_x && (key > set.key || (key == set.key && (int32_t)d <= set.last));
+          const u64 wd = kept ? weight_of(x, w, table) : 0ull;
+          if (wd > 0ull && !((double)u * (double)q * (double)set.sum >= (double)wd))
+            set.accepted = 1;
+        }
       }
     }
   }
@@ -1838,7 +1840,8 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Draw
   // S 2^-44 as a pair
   const u64 top = set.sum >> 30 << 30;
   const float s_hi = (float)top * 5.684341886080802e-14f;
-  const float s_lo = (float)(long long)(set.sum - (u64)__float2ull_rn((float)top)) * 5.684341886080802e-14f;
+  const float s_lo =
+      (float)(long long)(set.sum - (u64)__float2ull_rn((float)top)) * 5.684341886080802e-14f;
   auto weigh = [&](float x0, float x1, int32_t at, float q0, float q1, u64(&v)[2], auto inlined) {
     const bool k0 = kept(x0, at), k1 = kept(x1, at + 1);
     v[0] = v[1] = 0ull;
